@@ -70,7 +70,9 @@ typedef enum {
   SDPA_ERR_MISALIGNED = 3,       /* a base pointer breaks the alignment rule */
   SDPA_ERR_WORKSPACE_TOO_SMALL = 4,
   SDPA_ERR_CUDA = 5,             /* a CUDA runtime call or launch failed */
-  SDPA_ERR_TIMEOUT = 6           /* a device-side wait gave up (status word) */
+  SDPA_ERR_TIMEOUT = 6,          /* a device-side wait gave up (status word) */
+  SDPA_ERR_PAGE_TABLE = 7        /* a page number outside the cache was met
+                                    (status word; paged entry points) */
 } sdpa_status_t;
 
 /* Kernel paths.  The launcher picks one from the shape alone: one query row
@@ -297,9 +299,10 @@ SDPA_API const char* sdpa_status_string(sdpa_status_t status);
 
 /*
  * sdpa_device_status — synchronise `stream`, then read and clear the device
- * status word that kernels set when one of their bounded waits gives up.
- * Returns SDPA_OK, SDPA_ERR_TIMEOUT, or SDPA_ERR_CUDA if the synchronisation
- * itself failed.  The status word is per device and shared by all streams.
+ * status word that kernels set when one of their bounded waits gives up or a
+ * page table names a page outside the cache.  Returns SDPA_OK,
+ * SDPA_ERR_TIMEOUT, SDPA_ERR_PAGE_TABLE, or SDPA_ERR_CUDA if the
+ * synchronisation itself failed.  The status word is per device and shared by all streams.
  */
 SDPA_API sdpa_status_t sdpa_device_status(void* stream);
 
@@ -327,13 +330,21 @@ SDPA_API uint64_t sdpa_debug_set_wait_limit_ns(uint64_t ns);
  *  SDPA_DEBUG_DECODE_VECTOR   1: head_dim-64/128 fp16/bf16 decode on the
  *                             vector path instead of the tensor-core pass
  *                             (default 0)
+ *  SDPA_DEBUG_PAGED_SIMT      1: fp16/bf16 sdpa_paged_forward and
+ *                             sdpa_paged_scores on the CUDA-core kernels
+ *                             (default 0)
+ *  SDPA_DEBUG_PAGED_CTAS      CTAs that share the work of sdpa_paged_forward
+ *                             and sdpa_paged_scores (0: the plan's; at most
+ *                             the plan's)
  */
 typedef enum {
   SDPA_DEBUG_DECODE_SPLITS = 0,
   SDPA_DEBUG_DECODE_CLUSTER = 1,
   SDPA_DEBUG_DECODE_DROP_LAST = 2,
   SDPA_DEBUG_PREFILL_SPLIT = 3,
-  SDPA_DEBUG_DECODE_VECTOR = 4
+  SDPA_DEBUG_DECODE_VECTOR = 4,
+  SDPA_DEBUG_PAGED_SIMT = 5,
+  SDPA_DEBUG_PAGED_CTAS = 6
 } sdpa_debug_option_t;
 SDPA_API int sdpa_debug_set_option(int option, int value);
 
@@ -379,6 +390,148 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
                                                    const void* q, const void* k,
                                                    const void* v, void* o, float* lse,
                                                    void* stream);
+
+/* ------------------------------------------------------- paged KV cache ---
+ * Keys and values of many sequences in pages of a shared pool, as a serving
+ * loop keeps them: each step writes the new tokens' K and V rows
+ * (sdpa_paged_write), attends from the new tokens over everything cached
+ * (sdpa_paged_forward), may add up the attention weight that each cached key
+ * received (sdpa_paged_scores) and, when a sequence outgrows its budget,
+ * drops the keys of least accumulated weight (sdpa_paged_evict).
+ *
+ * Conventions shared by the four calls
+ *  - The cache: k_pages and v_pages are [num_pages, Hkv, page_size, D] by
+ *    shape with element strides k_stride / v_stride = {page, head, row} (D
+ *    contiguous), so that both storage orders, rows before heads
+ *    ([page][row][head][D]) and heads before rows, are served.  Position p of
+ *    sequence b is row p % page_size of page
+ *    page_table[b * page_table_stride + p / page_size] (device int32, at
+ *    most max_pages entries a sequence).  Entries that no position below the
+ *    sequence's length uses are not read.  An entry outside [0, num_pages)
+ *    reads as zero keys and values (written rows are dropped) and sets the
+ *    device status word to SDPA_ERR_PAGE_TABLE.
+ *  - seq_lens_kv: device int32 [num_seqs], the keys of each sequence with its
+ *    new tokens included (clamped to [0, max_pages * page_size]).
+ *  - New tokens are packed: q is [num_tokens, Hq, D] with element strides
+ *    q_stride = {token, head}; the tokens of sequence b are rows
+ *    [cu_seqlens_q[b], cu_seqlens_q[b + 1]) (device int32 [num_seqs + 1],
+ *    non-decreasing, clamped to [0, num_tokens]).  cu_seqlens_q NULL: one
+ *    token a sequence, row b.  They are the sequence's last positions: token
+ *    i of nq sits at position nk - nq + i.  Rows past the last sequence's end
+ *    belong to none: their rows of o and lse are left as they were.
+ *  - causal nonzero (the usual case): a token sees the keys at and before
+ *    its own position; zero: every key of its sequence.  A token that sees
+ *    no key (nq > nk) gives o = 0 and lse = -inf, or the sink.
+ *  - head_dim 64 or 128; fp32, fp16, bf16; any Hq that Hkv divides; page_size
+ *    >= 1.  fp16/bf16 with page_size a multiple of 8 run on the tensor cores,
+ *    everything else on fp32 CUDA-core kernels.
+ *  - Base pointers 16-byte aligned, row strides multiples of 16 bytes; o must
+ *    not overlap the inputs.  flags and reserved fields must be 0.
+ *  - Asynchronous on `stream`, nothing allocated, results independent of
+ *    timing (fixed summation order).  Host-side errors as for sdpa_forward.
+ *    Two calls that overlap on the GPU must not share a workspace.
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_tokens;    /* rows of q (and of the new k and v) */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;         /* sdpa_dtype_t of q, o and the cache */
+  float scale;
+  int32_t causal;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t max_pages;
+  uint32_t flags;        /* 0 */
+  const int32_t* page_table;
+  int64_t page_table_stride;   /* elements between sequences */
+  const int32_t* cu_seqlens_q; /* or NULL */
+  const int32_t* seq_lens_kv;
+  const float* sinks;          /* NULL or float32 [Hq] (sdpa_paged_forward) */
+  int64_t q_stride[2];
+  int64_t o_stride[2];
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+} sdpa_paged_params_t;
+
+/*
+ * sdpa_paged_write — copy the new tokens' key and value rows into the cache.
+ *  k, v: [num_tokens, Hkv, D] with element strides k_new_stride and
+ *      v_new_stride = {token, head}.  Token i of sequence b goes to position
+ *      nk - nq + i; a token whose position is negative or past max_pages *
+ *      page_size is not written.  num_q_heads, scale, causal, sinks, q_stride
+ *      and o_stride are not used.
+ */
+SDPA_API sdpa_status_t sdpa_paged_write(const sdpa_paged_params_t* params, const void* k,
+                                        const void* v, const int64_t* k_new_stride,
+                                        const int64_t* v_new_stride, void* k_pages,
+                                        void* v_pages, void* stream);
+
+/*
+ * sdpa_paged_workspace_size — bytes of device workspace that
+ * sdpa_paged_forward and sdpa_paged_scores need for this problem (partial
+ * results of work that is shared among CTAs; a function of the head sizes,
+ * the token count and the device, not of the lengths); 0 for an invalid
+ * problem or one with nothing to compute.
+ */
+SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params_t* params);
+
+/*
+ * sdpa_paged_forward — attention of the new tokens over the paged cache.
+ *  q: [num_tokens, Hq, D]; o: the same shape, strides o_stride.
+ *  lse: NULL or float32 [num_tokens, Hq], dense, natural-log units.
+ *  workspace: at least sdpa_paged_workspace_size(params) bytes, 256-byte
+ *      aligned; contents need no initialisation.
+ */
+SDPA_API sdpa_status_t sdpa_paged_forward(const sdpa_paged_params_t* params, const void* q,
+                                          const void* k_pages, const void* v_pages, void* o,
+                                          float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/*
+ * sdpa_paged_scores — add the attention weight that every cached key receives
+ * from the new tokens:
+ *     scores[b, kvh, j] += sum over the tokens i of sequence b that see key j
+ *                          and the query heads h of kvh of
+ *                          exp(scale * q_i,h . k_j - lse_i,h)
+ *  lse: float32 [num_tokens, Hq] as sdpa_paged_forward left it (with sinks,
+ *      if any, in it).  scores: float32, element (b, kvh, j) at b *
+ *      score_stride[0] + kvh * score_stride[1] + j for j < score_len; keys at
+ *      or past score_len and scores at or past a sequence's length are left
+ *      alone.  A row whose lse is -inf adds nothing.  v_stride, o_stride and
+ *      sinks are not used.
+ */
+SDPA_API sdpa_status_t sdpa_paged_scores(const sdpa_paged_params_t* params, const void* q,
+                                         const void* k_pages, const float* lse, float* scores,
+                                         const int64_t* score_stride, int32_t score_len,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sdpa_paged_evict — cut every sequence longer than `keep` (>= 1) back to
+ * `keep` keys per kv head: its newest min(recent, keep) keys stay, and of the
+ * others those of largest score (ties to the lower position; NaN counts as
+ * -inf, 0 and -0 tie).  The kept rows of K and V move, in order, to positions
+ * 0, 1, ... of the sequence's own pages; the heads choose independently.
+ * Sequences of at most `keep` keys stay as they are.
+ *  scores: float32 [num_seqs, Hkv, score_len] as for sdpa_paged_scores; keys
+ *      at or past score_len count as score 0.
+ *  scores_out: NULL or the kept keys' scores in their new places, 0 behind
+ *      them up to score_len; may be `scores` itself.
+ *  kept: int32 [num_seqs, Hkv, keep], dense: the old positions, ascending, -1
+ *      behind the last.
+ *  seq_lens_out: NULL or int32 [num_seqs], min(length, keep); may be
+ *      params->seq_lens_kv itself.
+ * The pages that a sequence longer than `keep` uses below position `keep`
+ * are rewritten, so no other sequence may share them, and no page may appear
+ * twice among a sequence's own.  num_tokens, num_q_heads, scale, causal,
+ * cu_seqlens_q, sinks, q_stride and o_stride are not used.
+ */
+SDPA_API sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* params, int32_t keep,
+                                        int32_t recent, void* k_pages, void* v_pages,
+                                        const float* scores, float* scores_out,
+                                        const int64_t* score_stride, int32_t score_len,
+                                        int32_t* kept, int32_t* seq_lens_out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,7 @@ SDPA_FLAG_BOOL_MASK = 0x2
 SDPA_FLAG_STRIDES = 0x4
 STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARGUMENT", 2: "SDPA_ERR_UNSUPPORTED",
           3: "SDPA_ERR_MISALIGNED", 4: "SDPA_ERR_WORKSPACE_TOO_SMALL", 5: "SDPA_ERR_CUDA",
-          6: "SDPA_ERR_TIMEOUT"}
+          6: "SDPA_ERR_TIMEOUT", 7: "SDPA_ERR_PAGE_TABLE"}
 KERNELS = {0: "none", 1: "prefill_tc", 2: "prefill_f32", 3: "decode_splitkv", 4: "no_keys",
            5: "prefill_tc_f32"}
 
@@ -31,11 +31,13 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_select_kernel", "sdpa_forward", "sdpa_st
            "sdpa_device_status", "sdpa_debug_set_wait_limit_ns", "sdpa_abi_version",
            "sdpa_forward_decode_noalloc", "sdpa_last_launch_count",
            "sdpa_backward_workspace_size", "sdpa_backward", "sdpa_debug_set_option",
-           "sdpa_host_staging_size", "sdpa_forward_host")
+           "sdpa_host_staging_size", "sdpa_forward_host", "sdpa_paged_write",
+           "sdpa_paged_workspace_size", "sdpa_paged_forward", "sdpa_paged_scores",
+           "sdpa_paged_evict")
 
 # sdpa_debug_option_t
 DEBUG_OPTIONS = {"decode_splits": 0, "decode_cluster": 1, "decode_drop_last": 2,
-                 "prefill_split": 3, "decode_vector": 4}
+                 "prefill_split": 3, "decode_vector": 4, "paged_simt": 5, "paged_ctas": 6}
 
 
 class SdpaParams(ctypes.Structure):
@@ -51,6 +53,21 @@ class SdpaParams(ctypes.Structure):
                 ("seq_lens_kv", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 3),
                 ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
                 ("o_stride", ctypes.c_int64 * 3)]
+
+
+class SdpaPagedParams(ctypes.Structure):
+    """Mirror of sdpa_paged_params_t."""
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64),
+                ("cu_seqlens_q", ctypes.c_void_p), ("seq_lens_kv", ctypes.c_void_p),
+                ("sinks", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
+                ("o_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3)]
 
 
 class SdpaError(RuntimeError):
@@ -102,6 +119,19 @@ def load_library(path: str = LIB_PATH):
             lib.sdpa_backward.argtypes = [P] + [ctypes.c_void_p] * 10 + [ctypes.c_size_t,
                                                                          ctypes.c_void_p]
             lib.sdpa_backward.restype = ctypes.c_int
+            PP, vp = ctypes.POINTER(SdpaPagedParams), ctypes.c_void_p
+            lib.sdpa_paged_write.argtypes = [PP] + [vp] * 7
+            lib.sdpa_paged_write.restype = ctypes.c_int
+            lib.sdpa_paged_workspace_size.argtypes = [PP]
+            lib.sdpa_paged_workspace_size.restype = ctypes.c_size_t
+            lib.sdpa_paged_forward.argtypes = [PP] + [vp] * 6 + [ctypes.c_size_t, vp]
+            lib.sdpa_paged_forward.restype = ctypes.c_int
+            lib.sdpa_paged_scores.argtypes = [PP] + [vp] * 5 + [ctypes.c_int32, vp,
+                                                                ctypes.c_size_t, vp]
+            lib.sdpa_paged_scores.restype = ctypes.c_int
+            lib.sdpa_paged_evict.argtypes = [PP, ctypes.c_int32, ctypes.c_int32] + [vp] * 5 + [
+                ctypes.c_int32] + [vp] * 3
+            lib.sdpa_paged_evict.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -484,3 +514,256 @@ def sdpa_forward_host(q, k, v, scale=None, causal=False, mask=None, sinks=None, 
     if st != 0:
         raise SdpaError(st, sdpa_status_string(st))
     return out, lse
+
+
+# ------------------------------------------------------------ paged KV cache
+def _check(cond, what, kind=ValueError):
+    if not cond:
+        raise kind(what)
+
+
+class _PagedCall:
+    """The arguments that the paged calls share, checked and in an
+    SdpaPagedParams, and the device and stream that the call runs on."""
+
+    def __init__(self, first, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream):
+        torch = self.torch = _torch()
+        int32 = torch.int32
+        _check(first.is_cuda, "tensors must be CUDA tensors")
+        dev = self.device = first.device
+        p = self.params = SdpaPagedParams()
+        _check(k_pages.dim() == 4 and k_pages.device == dev and k_pages.stride(3) == 1,
+               "k_pages must be [pages, kv heads, page_size, D] on the same device with a "
+               "contiguous last dimension")
+        p.num_pages, p.num_kv_heads, p.page_size, p.head_dim = shape = k_pages.shape
+        p.k_stride[:] = k_pages.stride()[:3]
+        if v_pages is not None:
+            _check(v_pages.shape == shape and v_pages.device == dev and v_pages.stride(3) == 1,
+                   "v_pages must have k_pages' shape and device and a contiguous last dimension")
+            _check(v_pages.dtype == k_pages.dtype, "k_pages and v_pages must share a dtype",
+                   TypeError)
+            p.v_stride[:] = v_pages.stride()[:3]
+        p.dtype = dtype_code(k_pages.dtype)
+        B = p.num_seqs = seq_lens_kv.numel()
+        _check(seq_lens_kv.dtype == int32 and seq_lens_kv.device == dev
+               and seq_lens_kv.is_contiguous(),
+               "seq_lens_kv must be a contiguous int32 CUDA tensor", TypeError)
+        _check(page_table.dtype == int32 and page_table.device == dev,
+               "page_table must be an int32 CUDA tensor", TypeError)
+        _check(page_table.dim() == 2 and page_table.shape[0] == B
+               and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
+               "page_table must be [sequences, pages] with contiguous rows")
+        p.max_pages = page_table.shape[1]
+        p.page_table = page_table.data_ptr()
+        p.page_table_stride = page_table.stride(0)
+        p.seq_lens_kv = seq_lens_kv.data_ptr()
+        if cu_seqlens_q is not None:
+            _check(cu_seqlens_q.dtype == int32 and cu_seqlens_q.device == dev
+                   and cu_seqlens_q.is_contiguous() and cu_seqlens_q.numel() == B + 1,
+                   "cu_seqlens_q must be a contiguous int32 CUDA tensor of sequences + 1 "
+                   "elements", TypeError)
+            p.cu_seqlens_q = cu_seqlens_q.data_ptr()
+        p.scale = 1.0
+        self.stream = stream
+
+    def queries(self, q, scale, causal, sinks=None):
+        p = self.params
+        _check(q.dim() == 3 and q.shape[2] == p.head_dim and q.stride(2) == 1,
+               "q must be [tokens, heads, D] with a contiguous last dimension")
+        _check(dtype_code(q.dtype) == p.dtype, "q and the cache must share a dtype", TypeError)
+        p.num_tokens, p.num_q_heads = q.shape[:2]
+        p.q_stride[:] = q.stride()[:2]
+        p.scale = 1.0 / math.sqrt(p.head_dim) if scale is None else scale
+        p.causal = 1 if causal else 0
+        if sinks is not None:
+            _check(sinks.dtype == self.torch.float32 and sinks.device == self.device
+                   and sinks.numel() == q.shape[1] and sinks.is_contiguous(),
+                   "sinks must be a contiguous float32 CUDA tensor with Hq elements", TypeError)
+            p.sinks = sinks.data_ptr()
+
+    def lse_ptr(self, lse):
+        _check(lse.dtype == self.torch.float32 and lse.device == self.device
+               and tuple(lse.shape) == (self.params.num_tokens, self.params.num_q_heads)
+               and lse.is_contiguous(), "lse must be a contiguous float32 [tokens, Hq] tensor")
+        return lse.data_ptr()
+
+    def scores(self, scores, what="scores"):
+        p = self.params
+        _check(scores.dtype == self.torch.float32 and scores.device == self.device
+               and scores.dim() == 3 and tuple(scores.shape[:2]) == (p.num_seqs, p.num_kv_heads)
+               and (scores.shape[2] <= 1 or scores.stride(2) == 1),
+               "%s must be a float32 CUDA tensor [sequences, kv heads, positions] with "
+               "contiguous rows" % what)
+        return (ctypes.c_int64 * 2)(*scores.stride()[:2])
+
+    def run(self, make, call):
+        """make(): allocations, on the call's stream; call(lib, stream)."""
+        torch, dev = self.torch, self.device
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.run(make, call)
+        if self.stream is None:
+            stream = torch.cuda.current_stream(dev).cuda_stream
+            made = make()
+        else:  # a raw stream handle: what is allocated here belongs to that stream
+            stream = self.stream
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+                made = make()
+        st = call(load_library(), made, stream)
+        if st != 0:
+            raise SdpaError(st, sdpa_status_string(st))
+        return made
+
+    def workspace(self, workspace):
+        """A workspace of the call's own: calls on other streams, and graphs
+        captured from it, share none."""
+        if workspace is None:
+            n = load_library().sdpa_paged_workspace_size(ctypes.byref(self.params))
+            return self.torch.empty(n, dtype=self.torch.uint8, device=self.device)
+        _check(workspace.device == self.device and workspace.is_contiguous(),
+               "workspace must be a contiguous CUDA tensor on the same device")
+        return workspace
+
+
+def sdpa_paged_workspace_size(params) -> int:
+    """Bytes of workspace that sdpa_paged_forward and sdpa_paged_scores need
+    for a SdpaPagedParams."""
+    return int(load_library().sdpa_paged_workspace_size(ctypes.byref(params)))
+
+
+def sdpa_paged_write(k, v, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q=None,
+                     stream=None):
+    """Copy the new tokens' keys and values into a paged KV cache.
+
+    k, v: [T, Hkv, D] packed new tokens.  k_pages, v_pages: [pages, Hkv,
+    page_size, D] by shape, any strides with a contiguous last dimension (a
+    [pages, page_size, Hkv, D] tensor through .transpose(1, 2), for instance).
+    page_table: int32 [B, columns], position p of sequence b in page
+    page_table[b, p // page_size].  seq_lens_kv: int32 [B], keys of each
+    sequence with its new tokens, which are its last ones.  cu_seqlens_q:
+    int32 [B + 1], sequence b's tokens are rows cu[b] .. cu[b + 1]; None: one
+    token a sequence.  Rows past the last sequence are not written.
+    """
+    c = _PagedCall(k, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream)
+    p = c.params
+    for t in (k, v):
+        _check(t.dim() == 3 and tuple(t.shape[1:]) == (p.num_kv_heads, p.head_dim)
+               and t.stride(2) == 1 and t.device == c.device and t.shape[0] == k.shape[0],
+               "k and v must be [tokens, kv heads, D] on the same device with a contiguous last "
+               "dimension")
+        _check(t.dtype == k_pages.dtype, "k, v and the cache must share a dtype", TypeError)
+    p.num_tokens = k.shape[0]
+    st2 = ctypes.c_int64 * 2
+    ks, vs = st2(*k.stride()[:2]), st2(*v.stride()[:2])
+    c.run(lambda: None, lambda lib, _, stream: lib.sdpa_paged_write(
+        ctypes.byref(p), k.data_ptr(), v.data_ptr(), ks, vs, k_pages.data_ptr(),
+        v_pages.data_ptr(), stream))
+
+
+def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q=None,
+                       scale=None, causal=True, sinks=None, out=None, lse=None, return_lse=True,
+                       workspace=None, stream=None):
+    """O (and LSE) of the new tokens' attention over a paged KV cache.
+
+    q: [T, Hq, D] packed new tokens (already in the cache: see
+    sdpa_paged_write); the cache arguments as for sdpa_paged_write.  causal:
+    a token sees the keys up to its own position (else all of its
+    sequence's).  sinks: None or float32 [Hq].  scale defaults to 1/sqrt(D).
+    out: [T, Hq, D] and lse: float32 [T, Hq]; rows past the last sequence are
+    left as they are.  workspace: a uint8 tensor of
+    sdpa_paged_workspace_size bytes (one is allocated otherwise).  float32,
+    float16, bfloat16; D 64 or 128.  Returns (out, lse) or out.
+    """
+    c = _PagedCall(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream)
+    c.queries(q, scale, causal, sinks)
+    p, torch = c.params, c.torch
+    if out is not None:
+        _check(out.shape == q.shape and out.dtype == q.dtype and out.device == c.device
+               and out.stride(2) == 1, "out must be like q with a contiguous last dimension")
+    if lse is not None:
+        c.lse_ptr(lse)
+
+    def make():
+        o = torch.empty_like(q) if out is None else out
+        ls = lse
+        if ls is None and return_lse:
+            ls = torch.empty(q.shape[:2], dtype=torch.float32, device=c.device)
+        return o, ls, c.workspace(workspace)
+
+    def call(lib, made, stream):
+        o, ls, ws = made
+        p.o_stride[:] = o.stride()[:2]
+        return lib.sdpa_paged_forward(ctypes.byref(p), q.data_ptr(), k_pages.data_ptr(),
+                                      v_pages.data_ptr(), o.data_ptr(),
+                                      None if ls is None else ls.data_ptr(), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), stream)
+
+    o, ls, _ = c.run(make, call)
+    return (o, ls) if return_lse else o
+
+
+def sdpa_paged_scores(q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqlens_q=None,
+                      scale=None, causal=True, workspace=None, stream=None):
+    """Add the attention weight that each cached key receives from the new
+    tokens to `scores` (float32 [B, Hkv, positions], in place, returned): the
+    sum over the tokens that see the key and the query heads of its kv head of
+    exp(scale * q . k - lse).
+
+    q and the cache arguments as given to sdpa_paged_forward, lse its second
+    result.
+    """
+    c = _PagedCall(q, k_pages, None, page_table, seq_lens_kv, cu_seqlens_q, stream)
+    c.queries(q, scale, causal)
+    ss = c.scores(scores)
+    lp = c.lse_ptr(lse)
+    c.run(lambda: c.workspace(workspace), lambda lib, ws, stream: lib.sdpa_paged_scores(
+        ctypes.byref(c.params), q.data_ptr(), k_pages.data_ptr(), lp, scores.data_ptr(), ss,
+        scores.shape[2], ws.data_ptr(), ws.numel() * ws.element_size(), stream))
+    return scores
+
+
+def sdpa_paged_evict(k_pages, v_pages, scores, page_table, seq_lens_kv, keep, recent=0,
+                     scores_out=None, seq_lens_out=None, kept=None, stream=None):
+    """Cut every sequence longer than `keep` back to `keep` keys per kv head:
+    its newest min(recent, keep) keys stay, and of the others those of largest
+    score (ties to the lower position).  The kept rows of the cache move to
+    positions 0, 1, ... of the sequence's own pages, in place; those pages
+    must not be shared with another sequence.
+
+    scores: float32 [B, Hkv, positions] as from sdpa_paged_scores.  Returns
+    (kept, seq_lens, scores): the old positions int32 [B, Hkv, keep] (-1
+    behind the last), the new lengths int32 [B], and the kept keys' scores in
+    their new places (0 behind them).  scores_out and seq_lens_out may be
+    `scores` and `seq_lens_kv` themselves.
+    """
+    c = _PagedCall(k_pages, k_pages, v_pages, page_table, seq_lens_kv, None, stream)
+    p, torch = c.params, c.torch
+    ss = c.scores(scores)
+    keep = int(keep)
+    _check(keep >= 1 and recent >= 0, "keep must be at least 1 and recent at least 0")
+    if scores_out is not None:
+        _check(scores_out.shape == scores.shape and scores_out.stride() == scores.stride(),
+               "scores_out must have the shape and strides of scores")
+        c.scores(scores_out, "scores_out")
+    for t, n, what in ((seq_lens_out, p.num_seqs, "seq_lens_out"),
+                       (kept, p.num_seqs * p.num_kv_heads * keep, "kept")):
+        _check(t is None or (t.dtype == torch.int32 and t.device == c.device
+                             and t.is_contiguous() and t.numel() == n),
+               "%s must be a contiguous int32 CUDA tensor of %d elements" % (what, n))
+
+    def make():
+        kp = kept
+        if kp is None:
+            kp = torch.empty((p.num_seqs, p.num_kv_heads, keep), dtype=torch.int32,
+                             device=c.device)
+        sl = torch.empty_like(seq_lens_kv) if seq_lens_out is None else seq_lens_out
+        so = scores_out
+        if so is None:
+            so = torch.empty_strided(scores.shape, scores.stride(), dtype=torch.float32,
+                                     device=c.device)
+        return kp, sl, so
+
+    return c.run(make, lambda lib, m, stream: lib.sdpa_paged_evict(
+        ctypes.byref(p), keep, int(recent), k_pages.data_ptr(), v_pages.data_ptr(),
+        scores.data_ptr(), m[2].data_ptr(), ss, scores.shape[2], m[0].data_ptr(),
+        m[1].data_ptr(), stream))

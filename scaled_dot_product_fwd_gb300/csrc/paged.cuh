@@ -1,0 +1,367 @@
+// paged.cuh — what the kernels over the paged KV cache share: their
+// arguments, the lengths of a sequence, and the division of the work.
+//
+// Division of the work.  The units of a call are (sequence, kv head, block):
+// a block of query rows for attention, a run of keys for the score sums.  A
+// unit takes a number of equal steps (key tiles, or query chunks) that
+// follows from the lengths and the causal rule, and the lengths are known on
+// the device only.  So every CTA computes the whole call's cost (kUnitCost +
+// steps per unit, summed per sequence in closed form), takes its equal share
+// of the line of all units, finds where it begins, and walks on from there.
+// A unit that crosses the end of a share is finished by the next CTAs: each
+// leaves a partial result in the workspace (slot 1 of the CTA that began the
+// unit, slot 0 of those that continue it) and a merge kernel joins them in
+// order.  Every CTA is busy equally long whatever the lengths, the workspace
+// has a fixed size, and the summation order depends on the lengths alone.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "sdpa.h"
+
+namespace gb300 {
+namespace paged {
+
+constexpr int kStatusPageTable = 7;  // SDPA_ERR_PAGE_TABLE
+constexpr int kUnitCost = 2;         // fixed cost of a unit, in steps
+
+struct Args {
+  int B, T, Hq, Hkv, G;
+  int causal;
+  int num_pages, page_size, max_pages;
+  int cap;  // max_pages * page_size, at most 2^30
+  const int* table;
+  long long table_stride;
+  const int* cu;    // or nullptr: one token a sequence
+  const int* lens;
+  const float* sinks;
+  long long qs[2], os[2], ks[3], vs[3];
+  float sl2;  // scale * log2(e)
+  // Query heads of a kv head are taken `gu` at a time (the whole group when
+  // it fits a tile's rows), `nsub` times; a tile of `rows` rows holds w =
+  // rows / gu tokens, row r = token r / gu, head r % gu.
+  int gu, nsub, w;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  float* ws;   // partial results (see the kernels)
+  int* desc;   // [CTAs][kDesc]: the unit that a CTA began and did not finish
+  int nctas;
+  // score sums
+  float* scores;
+  long long ss[2];
+  int score_len;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+// Descriptor of a cut unit, written by the CTA that began it: partial
+// results it has (0: this CTA cut none), sequence, head unit, block, first
+// token row, query tokens, keys.
+constexpr int kDesc = 8;
+
+// First packed row, new tokens and keys of a sequence.
+struct Seq {
+  int q0, nq, nk;
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  if (a.cu) {
+    s.q0 = min(max(a.cu[b], 0), a.T);
+    s.nq = min(max(a.cu[b + 1], s.q0), a.T) - s.q0;
+  } else {
+    s.q0 = min(b, a.T);
+    s.nq = b < a.T ? 1 : 0;
+  }
+  s.nk = min(max(a.lens[b], 0), a.cap);
+  return s;
+}
+
+// sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0 and m >= 1:
+// whole parts of a and b are summed directly, and what is left counts the
+// lattice points under a line, which swaps the roles of a and m (the steps
+// of Euclid's algorithm).
+__host__ __device__ inline long long floor_sum(long long n, long long m, long long a,
+                                               long long b) {
+  long long r = 0;
+  while (n > 0) {
+    r += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return r;
+}
+
+// Steps of the units of one (sequence, kv head).  Attention: block j holds
+// `w` tokens and reads the key tiles of `tile` keys up to its last visible
+// key.
+struct AttendUnits {
+  int w, lg, causal;  // tiles of 2^lg keys
+  __host__ __device__ int count(int nq, int nk) const { return (nq + w - 1) / w; }
+  __host__ __device__ int steps(int nq, int nk, int j) const {
+    int lim = nk;
+    if (causal) {
+      const long long last = static_cast<long long>(j + 1) * w;
+      lim = last < nq ? nk - nq + static_cast<int>(last) : nk;
+    }
+    return lim <= 0 ? 0 : (lim + (1 << lg) - 1) >> lg;
+  }
+  // steps of the blocks before j
+  __host__ __device__ long long before(int nq, int nk, int j) const {
+    if (j <= 0) return 0;
+    if (!causal) return static_cast<long long>(j) * steps(nq, nk, 0);
+    const int n = count(nq, nk);
+    long long r = 0;
+    int full = j;  // blocks that hold w tokens
+    if (j >= n) {
+      full = n - 1;
+      r = steps(nq, nk, n - 1);
+    }
+    if (full > 0) {
+      const int off = nk - nq;
+      const int i0 = off + w > 0 ? 0 : -off / w;  // first block that sees a key
+      if (full > i0)
+        r += floor_sum(full - i0, 1LL << lg, w,
+                       off + static_cast<long long>(i0 + 1) * w + (1 << lg) - 1);
+    }
+    return r;
+  }
+};
+// Score sums: unit j holds 2^lg keys and reads the chunks of `w` tokens
+// (times nsub head groups) from the first that sees one of its keys.
+struct ScoreUnits {
+  int w, lg, causal, nsub;
+  __host__ __device__ int count(int nq, int nk) const {
+    return nq > 0 ? (nk + (1 << lg) - 1) >> lg : 0;
+  }
+  __host__ __device__ int first(int nq, int nk, int j) const {
+    const int d = (j << lg) - (nk - nq);
+    return causal && d > 0 ? d / w : 0;
+  }
+  __host__ __device__ int steps(int nq, int nk, int j) const {
+    return ((nq + w - 1) / w - first(nq, nk, j)) * nsub;
+  }
+  __host__ __device__ long long before(int nq, int nk, int j) const {
+    if (j <= 0) return 0;
+    long long r = static_cast<long long>(j) * ((nq + w - 1) / w);
+    if (causal) {
+      const int off = nk - nq;
+      const int i0 = off > 0 ? (off + (1 << lg) - 1) >> lg : 0;  // first j with a cut
+      if (j > i0) r -= floor_sum(j - i0, w, 1LL << lg, (static_cast<long long>(i0) << lg) - off);
+    }
+    return r * nsub;
+  }
+};
+
+// One unit of a CTA's share, and the steps [s0, s1) of it that are the CTA's.
+struct Unit {
+  int b, h, j;
+  Seq s;
+  int steps, s0, s1;
+  long long pos;  // position of its step 0 on the line
+  __device__ bool whole() const { return s0 == 0 && s1 == steps; }
+  __device__ int slot() const { return s0 > 0 ? 0 : 1; }
+};
+
+// A CTA's share [begin, end) of the line and where it begins (shared memory;
+// made once by plan_share, then every role walks it with Walk).
+struct Share {
+  long long begin, end, size;
+  long long pos;  // start of the first unit
+  int b, h, j;    // the first unit (b = B: none)
+};
+
+// Units whose cost reaches into the share, in order.
+template <typename Units>
+struct Walk {
+  Units u;
+  long long pos;
+  int b, h, j, n;
+  Seq s;
+  __device__ Walk(const Args& a, const Units& units, const Share& sh) : u(units) {
+    b = sh.b;
+    h = sh.h;
+    j = sh.j;
+    pos = sh.pos;
+    n = 0;
+    s = Seq{0, 0, 0};
+    if (b < a.B) {
+      s = seq_of(a, b);
+      n = u.count(s.nq, s.nk);
+    }
+  }
+  // heads: units of one sequence and block number (kv heads, times nsub)
+  __device__ bool next(const Args& a, const Share& sh, int heads, Unit* out) {
+    while (b < a.B && pos < sh.end) {
+      if (j >= n) {
+        j = 0;
+        if (++h >= heads || n == 0) {
+          h = 0;
+          if (++b >= a.B) return false;
+          s = seq_of(a, b);
+          n = u.count(s.nq, s.nk);
+        }
+        continue;
+      }
+      out->b = b;
+      out->h = h;
+      out->j = j;
+      out->s = s;
+      const int steps = u.steps(s.nq, s.nk, j);
+      const long long p0 = pos + kUnitCost;
+      const long long lo = sh.begin - p0, hi = sh.end - p0;
+      out->steps = steps;
+      out->s0 = lo <= 0 ? 0 : lo >= steps ? steps : static_cast<int>(lo);
+      out->s1 = hi <= 0 ? 0 : hi >= steps ? steps : static_cast<int>(hi);
+      out->pos = p0;
+      const bool mine = steps == 0 ? pos >= sh.begin : out->s1 > out->s0;
+      pos = p0 + steps;
+      ++j;
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
+// Divide the line among the grid's CTAs and find this CTA's share.  Every
+// thread of the CTA calls it (kThreads of them, whole warps); `scratch`
+// holds kThreads / 32 + 1 numbers.  Ends with a CTA barrier.
+template <int kThreads, typename Units>
+__device__ void plan_share(const Args& a, const Units& u, int heads, int min_share,
+                           long long* scratch, Share* sh) {
+  const int tid = threadIdx.x;
+  const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  auto cost = [&](int b) {
+    const Seq s = seq_of(a, b);
+    const int n = u.count(s.nq, s.nk);
+    return (u.before(s.nq, s.nk, n) + static_cast<long long>(n) * kUnitCost) * heads;
+  };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += cost(b);
+  long long incl = mine;  // inclusive scan over the threads
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, d);
+    if ((tid & 31) >= d) incl += t;
+  }
+  if ((tid & 31) == 31) scratch[tid >> 5] = incl;
+  __syncthreads();
+  if (tid == 0) {
+    long long run = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      const long long t = scratch[i];
+      scratch[i] = run;
+      run += t;
+    }
+    scratch[kThreads / 32] = run;
+    sh->b = a.B;
+    sh->h = 0;
+    sh->j = 0;
+    sh->pos = run;
+  }
+  __syncthreads();
+  incl += scratch[tid >> 5];
+  const long long total = scratch[kThreads / 32];
+  long long size = (total + gridDim.x - 1) / gridDim.x;
+  if (size < min_share) size = min_share;
+  const long long begin = size * blockIdx.x;
+  const long long end = begin + size < total ? begin + size : total;
+  if (tid == 0) {
+    sh->begin = begin;
+    sh->end = end;
+    sh->size = size;
+  }
+  long long pos = incl - mine;
+  if (begin < total && begin >= pos && begin < incl) {
+    for (int b = b0; b < b1; ++b) {
+      const long long c = cost(b);
+      if (begin < pos + c) {
+        const Seq s = seq_of(a, b);
+        const int n = u.count(s.nq, s.nk);
+        const long long per_head = c / heads;
+        const int h = static_cast<int>((begin - pos) / per_head);
+        pos += h * per_head;
+        // last block that starts at or before `begin`
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          const long long at =
+              pos + u.before(s.nq, s.nk, mid) + static_cast<long long>(mid) * kUnitCost;
+          if (at <= begin) lo = mid; else hi = mid - 1;
+        }
+        sh->b = b;
+        sh->h = h;
+        sh->j = lo;
+        sh->pos = pos + u.before(s.nq, s.nk, lo) + static_cast<long long>(lo) * kUnitCost;
+        break;
+      }
+      pos += c;
+    }
+  }
+  __syncthreads();
+}
+
+// Partial results that a unit has: the CTAs from the one that holds its
+// first step to the one that holds its last.
+__device__ __forceinline__ int pieces_of(const Unit& u, const Share& sh) {
+  return static_cast<int>((u.pos + u.steps - 1) / sh.size - u.pos / sh.size) + 1;
+}
+
+// Page of position p, or -1 (and the status word set) where the table names
+// none of the cache's.
+__device__ __forceinline__ int page_of(const Args& a, int b, int p) {
+  const int page = a.table[b * a.table_stride + p / a.page_size];
+  if (page < 0 || page >= a.num_pages) {
+    atomicExch(a.status, kStatusPageTable);
+    return -1;
+  }
+  return page;
+}
+
+}  // namespace paged
+
+// Launchers (host side).  `a` holds the problem and the workspace; the
+// attention and score launchers fill in the tile's rows (gu, nsub, w).
+sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
+sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
+                                       const LaunchEnv& env);
+sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
+                                 int tiles, cudaStream_t stream);
+sdpa_status_t launch_paged_scores_merge(const paged::Args& a, int tile_keys,
+                                        cudaStream_t stream);
+sdpa_status_t launch_paged_write(const paged::Args& a, int row_bytes, const void* k,
+                                 const void* v, const int64_t* kn, const int64_t* vn,
+                                 void* k_pages, void* v_pages, int elem, cudaStream_t stream);
+sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, int keep,
+                                 int recent, void* k_pages, void* v_pages, const float* scores,
+                                 float* scores_out, const int64_t* ss, int score_len, int* kept,
+                                 int* lens_out, cudaStream_t stream);
+
+namespace paged {
+// Heads per tile and tokens per tile of `rows` query rows.
+inline void fit_rows(Args& a, int rows) {
+  a.nsub = (a.G + rows - 1) / rows;
+  a.gu = (a.G + a.nsub - 1) / a.nsub;
+  a.w = rows / a.gu;
+}
+// Largest tile whose partial results a CTA may leave, in query rows (two
+// 128-row tiles) and in keys (score sums).
+constexpr int kMaxRows = 256;
+constexpr int kMaxKeys = 256;
+}  // namespace paged
+
+}  // namespace gb300

@@ -1,0 +1,399 @@
+// paged_cache.cu — the paged KV cache's own operators: writing the new
+// tokens' rows into their pages, and eviction by accumulated attention
+// weight.  Both only move bytes: bound by HBM.
+//
+// Write: one warp a token; its lanes bring the token's K and V rows (all kv
+// heads) with 16-byte loads, issued before the warp looks its sequence up.
+//
+// Eviction, two kernels:
+//  - select (a CTA per (sequence, kv head)): the threshold weight is the
+//    keep'-th largest of the candidates, found digit by digit (8 bits each)
+//    from histograms of the weights' order-preserving integer form; then one
+//    ordered pass over the positions writes the kept ones (above the
+//    threshold, the first of those equal to it, and the newest) in ascending
+//    order by a scan, and the weights' new places.
+//  - move (a CTA per (sequence, kv head), K or V, 128-byte slice of the
+//    rows): row kept[i] goes to row i.  kept[i] >= i, and the sources of a
+//    chunk lie behind the destinations of every earlier chunk, so a CTA that
+//    takes the chunks in order, loads the next one early and writes a chunk
+//    only when every thread has its rows in registers, moves in place
+//    without losing a row.
+#include <cuda_runtime.h>
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace {
+
+// ------------------------------------------------------------------- write
+constexpr int kWriteWarps = 8;
+
+struct WriteArgs {
+  Args a;
+  const char* k;
+  const char* v;
+  char* kp;
+  char* vp;
+  long long kn[2], vn[2];  // byte strides of the new rows (token, head)
+  long long kb[3], vb[3];  // byte strides of the cache (page, head, row)
+  int pieces;              // 16-byte pieces of a row (a power of two)
+  int lg;                  // its log2
+};
+
+// Sequence of packed row t: the last b with cu[b] <= t, found by the warp 32
+// ways at a time; -1 where t belongs to none.
+__device__ __forceinline__ int find_seq(const Args& a, int t, int lane) {
+  if (!a.cu) return t < a.B ? t : -1;
+  int lo = 0, n = a.B;  // candidates lo .. lo + n - 1, cu[lo] <= t wanted
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && (i == 0 || a.cu[lo + i] <= t);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return a.cu[lo] <= t && t < a.cu[lo + 1] ? lo : -1;
+}
+
+__global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const WriteArgs w) {
+  const Args& a = w.a;
+  const int lane = threadIdx.x & 31;
+  const long long tt = static_cast<long long>(blockIdx.x) * kWriteWarps + (threadIdx.x >> 5);
+  if (tt >= a.T) return;
+  const int t = static_cast<int>(tt);
+  const int total = a.Hkv << w.lg;  // 16-byte pieces of a token
+  const char* ksrc = w.k + t * w.kn[0];
+  const char* vsrc = w.v + t * w.vn[0];
+  constexpr int U = 4;
+  uint4 kr[U], vr[U];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = base + i * 32 + lane;
+      if (x < total) {
+        const int h = x >> w.lg, c = x & (w.pieces - 1);
+        kr[i] = *reinterpret_cast<const uint4*>(ksrc + h * w.kn[1] + c * 16);
+        vr[i] = *reinterpret_cast<const uint4*>(vsrc + h * w.vn[1] + c * 16);
+      }
+    }
+  };
+  load(0);
+  const int b = find_seq(a, t, lane);
+  if (b < 0) return;
+  const Seq s = seq_of(a, b);
+  const int pos = s.nk - s.nq + (t - s.q0);
+  if (pos < 0 || pos >= s.nk) return;
+  const int page = page_of(a, b, pos);
+  if (page < 0) return;
+  const int row = pos % a.page_size;
+  char* kdst = w.kp + page * w.kb[0] + row * w.kb[2];
+  char* vdst = w.vp + page * w.vb[0] + row * w.vb[2];
+  for (int base = 0; base < total; base += 32 * U) {
+    if (base > 0) load(base);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int x = base + i * 32 + lane;
+      if (x < total) {
+        const int h = x >> w.lg, c = x & (w.pieces - 1);
+        *reinterpret_cast<uint4*>(kdst + h * w.kb[1] + c * 16) = kr[i];
+        *reinterpret_cast<uint4*>(vdst + h * w.vb[1] + c * 16) = vr[i];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- eviction
+struct EvictArgs {
+  Args a;
+  int keep, recent;
+  const float* scores;
+  float* scores_out;
+  long long ss[2];
+  int score_len;
+  int* kept;
+  int* lens_out;
+  char* kp;
+  char* vp;
+  long long kb[3], vb[3];  // byte strides of the cache (page, head, row)
+  int slices;              // 128-byte slices of a row
+};
+
+// Integer whose order is the weights' order: sign bit flipped for positive
+// numbers, all bits for negative ones; NaN as -inf, -0 as 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) x = -INFINITY;
+  if (x == 0.f) x = 0.f;
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int kSelT = 1024;
+
+__global__ void __launch_bounds__(kSelT) paged_evict_select_kernel(const EvictArgs e) {
+  const Args& a = e.a;
+  const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+  const int nk = min(max(a.lens[b], 0), a.cap);
+  int* kept = e.kept + static_cast<size_t>(blockIdx.x) * e.keep;
+  const float* sc = e.scores + b * e.ss[0] + h * e.ss[1];
+  float* out = e.scores_out ? e.scores_out + b * e.ss[0] + h * e.ss[1] : nullptr;
+  if (nk <= e.keep) {  // nothing to evict
+    for (int i = tid; i < e.keep; i += kSelT) kept[i] = i < nk ? i : -1;
+    if (out) {
+      if (out != sc)
+        for (int i = tid; i < min(nk, e.score_len); i += kSelT) out[i] = sc[i];
+      for (int i = nk + tid; i < e.score_len; i += kSelT) out[i] = 0.f;
+    }
+    return;
+  }
+  const int rec = min(e.recent, e.keep);
+  const int cand = nk - rec;    // positions below it compete
+  int want = e.keep - rec;      // for these places
+  auto weight = [&](int i) { return i < e.score_len ? sc[i] : 0.f; };
+
+  // the want-th largest key, from its top digit down
+  __shared__ int hist[256];
+  __shared__ int warp_sum[32];
+  __shared__ uint32_t s_digit;
+  __shared__ int s_want;
+  uint32_t prefix = 0, mask = 0;
+  if (want > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int i0 = 0; i0 < cand; i0 += kSelT) {
+        const int i = i0 + tid;
+        uint32_t key = 0;
+        bool in = i < cand;
+        if (in) {
+          key = order_key(weight(i));
+          in = (key & mask) == prefix;
+        }
+        // lanes of one digit add up before the shared-memory atomic: weights
+        // share their top digits
+        const uint32_t digit = (key >> shift) & 255u;
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : 256u);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      }
+      __syncthreads();
+      if (warp == 0) {  // suffix sums: lane holds digits 255 - 8 lane .. 248 - 8 lane
+        int c[8], sum = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          c[k] = hist[255 - 8 * lane - k];
+          sum += c[k];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += t;
+        }
+        int before = incl - sum;
+        if (before < want && want <= incl) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (before < want && want <= before + c[k]) {
+              s_digit = static_cast<uint32_t>(255 - 8 * lane - k);
+              s_want = want - before;
+            }
+            before += c[k];
+          }
+        }
+      }
+      __syncthreads();
+      prefix |= s_digit << shift;
+      mask |= 255u << shift;
+      want = s_want;
+    }
+  }
+  // `want` keys equal to the threshold are kept, the first ones.  Every
+  // position in order: place = kept before it (those above the threshold or
+  // recent, and of the equal ones at most `want`).
+  const bool none = e.keep == rec;  // only the newest stay
+  int run_gt = 0, run_eq = 0;
+  for (int i0 = 0; i0 < nk; i0 += kSelT) {
+    const int i = i0 + tid;
+    bool gt = false, eq = false;
+    float x = 0.f;
+    if (i < nk) {
+      x = weight(i);
+      if (i >= cand) {
+        gt = true;
+      } else if (!none) {
+        const uint32_t key = order_key(x);
+        gt = key > prefix;
+        eq = key == prefix;
+      }
+    }
+    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    const uint32_t lt = (1u << lane) - 1u;
+    int before = __popc(bg & lt) | (__popc(be & lt) << 16);
+    if (lane == 0) warp_sum[warp] = __popc(bg) | (__popc(be) << 16);
+    __syncthreads();  // (every weight of this chunk is read: `out` may be `sc`)
+    int w = warp_sum[lane];
+    int incl = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += t;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    before += __shfl_sync(0xffffffffu, incl - w, warp);
+    const int ng = run_gt + (before & 0xffff), ne = run_eq + (before >> 16);
+    if (gt || (eq && ne < want)) {
+      const int place = ng + min(ne, want);
+      kept[place] = i;
+      if (out && place < e.score_len) out[place] = x;
+    }
+    run_gt += total & 0xffff;
+    run_eq += total >> 16;
+    __syncthreads();
+  }
+  if (out)
+    for (int i = e.keep + tid; i < e.score_len; i += kSelT) out[i] = 0.f;
+}
+
+constexpr int kMoveT = 256;
+constexpr int kMoveRows = 4;                        // rows of a thread in a chunk
+constexpr int kMoveChunk = kMoveRows * kMoveT / 8;  // rows of a chunk (8 threads a slice)
+
+__global__ void __launch_bounds__(kMoveT) paged_evict_move_kernel(const EvictArgs e) {
+  const Args& a = e.a;
+  griddep_wait();
+  int x = blockIdx.x;
+  const int slice = x % e.slices;
+  x /= e.slices;
+  const bool is_v = x & 1;
+  const int bh = x >> 1;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int* kept = e.kept + static_cast<size_t>(bh) * e.keep;
+  if (h == 0 && slice == 0 && !is_v && threadIdx.x == 0 && e.lens_out)
+    e.lens_out[b] = min(min(max(a.lens[b], 0), a.cap), e.keep);
+  const long long* st = is_v ? e.vb : e.kb;
+  char* base = (is_v ? e.vp : e.kp) + h * st[1] + slice * 128 + (threadIdx.x & 7) * 16;
+  const int r0 = threadIdx.x >> 3;
+  struct Chunk {
+    uint4 data[kMoveRows];
+    char* dst[kMoveRows];  // nullptr: nothing to move
+  };
+  // rows [i0, i0 + kMoveChunk): issue the loads
+  auto load = [&](int i0, Chunk& c) {
+    int src[kMoveRows];
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int i = i0 + r0 + k * (kMoveT / 8);
+      src[k] = i < e.keep ? kept[i] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int i = i0 + r0 + k * (kMoveT / 8);
+      c.dst[k] = nullptr;
+      c.data[k] = make_uint4(0, 0, 0, 0);
+      if (src[k] > i) {  // (a row that stays needs no move)
+        const int ps = page_of(a, b, src[k]), pd = page_of(a, b, i);
+        if (ps >= 0 && pd >= 0) {
+          c.data[k] = *reinterpret_cast<const uint4*>(base + ps * st[0] +
+                                                      (src[k] % a.page_size) * st[2]);
+          c.dst[k] = base + pd * st[0] + (i % a.page_size) * st[2];
+        }
+      }
+    }
+  };
+  auto store = [&](Chunk& c) {
+    // every row of the chunk is in registers before any thread writes
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k)
+      asm volatile("" : "+r"(c.data[k].x), "+r"(c.data[k].y), "+r"(c.data[k].z),
+                        "+r"(c.data[k].w) : : "memory");
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k)
+      if (c.dst[k]) *reinterpret_cast<uint4*>(c.dst[k]) = c.data[k];
+  };
+  Chunk c0, c1;
+  load(0, c0);
+  for (int i0 = 0; i0 < e.keep; i0 += 2 * kMoveChunk) {
+    load(i0 + kMoveChunk, c1);
+    store(c0);
+    if (i0 + kMoveChunk >= e.keep) break;
+    load(i0 + 2 * kMoveChunk, c0);
+    store(c1);
+  }
+}
+
+}  // namespace
+}  // namespace paged
+
+sdpa_status_t launch_paged_write(const paged::Args& a, int row_bytes, const void* k,
+                                 const void* v, const int64_t* kn, const int64_t* vn,
+                                 void* k_pages, void* v_pages, int elem,
+                                 cudaStream_t stream) {
+  using namespace paged;
+  WriteArgs w;
+  w.a = a;
+  w.k = static_cast<const char*>(k);
+  w.v = static_cast<const char*>(v);
+  w.kp = static_cast<char*>(k_pages);
+  w.vp = static_cast<char*>(v_pages);
+  for (int i = 0; i < 2; ++i) {
+    w.kn[i] = kn[i] * elem;
+    w.vn[i] = vn[i] * elem;
+  }
+  for (int i = 0; i < 3; ++i) {
+    w.kb[i] = a.ks[i] * elem;
+    w.vb[i] = a.vs[i] * elem;
+  }
+  w.pieces = row_bytes / 16;
+  w.lg = 0;
+  while ((1 << w.lg) < w.pieces) ++w.lg;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.T) + kWriteWarps - 1) /
+                                              kWriteWarps);
+  paged_write_kernel<<<grid, kWriteWarps * 32, 0, stream>>>(w);
+  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, int keep,
+                                 int recent, void* k_pages, void* v_pages, const float* scores,
+                                 float* scores_out, const int64_t* ss, int score_len, int* kept,
+                                 int* lens_out, cudaStream_t stream) {
+  using namespace paged;
+  EvictArgs e;
+  e.a = a;
+  e.keep = keep;
+  e.recent = recent;
+  e.scores = scores;
+  e.scores_out = scores_out;
+  e.ss[0] = ss[0];
+  e.ss[1] = ss[1];
+  e.score_len = score_len;
+  e.kept = kept;
+  e.lens_out = lens_out;
+  e.kp = static_cast<char*>(k_pages);
+  e.vp = static_cast<char*>(v_pages);
+  for (int i = 0; i < 3; ++i) {
+    e.kb[i] = a.ks[i] * elem;
+    e.vb[i] = a.vs[i] * elem;
+  }
+  e.slices = row_bytes / 128;
+  const unsigned bh = static_cast<unsigned>(a.B) * a.Hkv;
+  paged_evict_select_kernel<<<bh, kSelT, 0, stream>>>(e);
+  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(bh * 2 * e.slices);
+  cfg.blockDim = dim3(kMoveT);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_evict_move_kernel, e) == cudaSuccess ? SDPA_OK
+                                                                             : SDPA_ERR_CUDA;
+}
+
+}  // namespace gb300

@@ -35,8 +35,8 @@ constexpr int kMaxDecodeRowsTc = 2;   // the same where a tensor-core prefill ex
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
 // test hooks (sdpa_debug_set_option), indexed by sdpa_debug_option_t
-constexpr int kDebugOptions = 5;
-std::atomic<int> g_debug[kDebugOptions] = {{0}, {1}, {0}, {-1}, {0}};
+constexpr int kDebugOptions = 7;
+std::atomic<int> g_debug[kDebugOptions] = {{0}, {1}, {0}, {-1}, {0}, {0}, {0}};
 thread_local int g_last_launches = 0;
 std::mutex g_dev_mutex;
 int* g_status_ptr[kMaxDevices] = {};
@@ -198,6 +198,7 @@ const char* sdpa_status_string(sdpa_status_t s) {
     case SDPA_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case SDPA_ERR_CUDA: return "CUDA error";
     case SDPA_ERR_TIMEOUT: return "device wait timed out";
+    case SDPA_ERR_PAGE_TABLE: return "page table names a page outside the cache";
     default: return "unknown status";
   }
 }
