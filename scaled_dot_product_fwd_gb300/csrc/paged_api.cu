@@ -154,6 +154,25 @@ sdpa_status_t enter(const sdpa_paged_params_t& p, void* ws, size_t ws_bytes, voi
   return SDPA_OK;
 }
 
+// Whether a problem runs on the tensor cores: a 16-bit type, pages of whole
+// groups of 8 rows (the 128-byte-swizzled tiles' unit), strides that a tensor
+// map takes, and a positive scale (the softmax takes its maximum over the raw
+// scores).
+bool tc_fits(const sdpa_paged_params_t& p, bool values) {
+  if (p.dtype == SDPA_F32 || p.page_size % 8 != 0 || p.num_pages < 1 || !(p.scale > 0.f))
+    return false;
+  if (debug_option(SDPA_DEBUG_PAGED_SIMT) == 1) return false;  // test hook
+  const int64_t kv[3] = {p.num_pages, p.num_kv_heads, p.page_size};
+  const int64_t qn[2] = {p.num_tokens, p.num_q_heads};
+  for (int i = 0; i < 3; ++i)
+    for (const int64_t* s : {p.k_stride, p.v_stride})
+      if ((s == p.k_stride || values) && kv[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t(1) << 38)))
+        return false;
+  for (int i = 0; i < 2; ++i)
+    if (qn[i] > 1 && (p.q_stride[i] <= 0 || p.q_stride[i] >= (int64_t(1) << 38))) return false;
+  return true;
+}
+
 bool no_rows(const sdpa_paged_params_t& p) {
   return p.num_seqs == 0 || p.num_tokens == 0 || p.num_q_heads == 0;
 }
@@ -219,7 +238,11 @@ sdpa_status_t sdpa_paged_forward(const sdpa_paged_params_t* p, const void* q,
   a.v = v_pages;
   a.o = o;
   a.lse = lse;
-  st = launch_paged_simt(a, p->head_dim, p->dtype, env);
+  if (!tc_fits(*p, true))
+    st = launch_paged_simt(a, p->head_dim, p->dtype, env);
+  else
+    st = p->head_dim == 64 ? launch_paged_tc_d64(a, p->dtype, env)
+                           : launch_paged_tc_d128(a, p->dtype, env);
   if (st == SDPA_OK) set_last_launches(2);
   return st;
 }

@@ -1,0 +1,640 @@
+// paged_tc.cuh — attention of packed new tokens over the paged KV cache for
+// fp16/bf16, head_dim 64/128, on the 5th-generation tensor cores: the kernel
+// and its launch, instantiated per head size in paged_tc_d64.cu and
+// paged_tc_d128.cu.
+//
+// The rows of a 128-row query tile are (token, query head) pairs of one kv
+// head: w = 128 / gu tokens times gu heads, row = token * gu + head, which a
+// TMA box of w tokens x gu heads lays down in that order.  So the tokens and
+// heads that read the same keys share every K and V tile, a single token
+// included, and one kernel serves prompt chunks and decode steps.  The work is
+// divided as paged.cuh describes (equal shares of all key tiles of all units,
+// cut units merged after).
+//
+// Two forms:
+//  NT = 2  (sequences of more than 128 rows on average): a unit is two query
+//          tiles that share each K/V tile; S_0 | S_1 | O_0 | O_1 in TMEM, and
+//          the softmax of one tile overlaps the products of the other.  Bound
+//          by the softmax warps and the tensor pipe.
+//  NT = 1  (decode and short chunks): one query tile; S is double-buffered
+//          over the key tiles (S_j+1 is computed while the softmax works on
+//          S_j), three 64 KB K/V stages in flight at head_dim 128.  Bound by
+//          HBM: few rows are live, and warps without one do no arithmetic.
+//
+// Key tiles are 128 keys in boxes of R = gcd(page_size, 128) rows, each
+// inside a page; one lane of the producer warp looks up and loads each box.
+// Boxes past the sequence's length are not loaded.  What the last tile holds
+// behind it (a page's rows of no sequence yet: anything, NaN included) is kept
+// out of the results: such scores are replaced by -inf, the value product
+// stops at the last group of 16 keys in use, and the rows of that group past
+// the length are zeroed in shared memory before it.
+//
+// Warp roles and the issue loop (a whole warp in step, no shared-memory access
+// between MMAs, named barriers) are those of the prefill kernel
+// (prefill_tc.cuh), whose softmax arithmetic this one uses: p = 2^(s * scale *
+// log2e - m) against a reference max m that moves only when a row sum passes
+// 2^15, so P stays in the exact range of fp16 and bf16.
+#pragma once
+
+#include <atomic>
+
+#include "paged.cuh"
+#include "prefill_tc.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace {
+
+template <int D, int NT>
+struct TcCfg {
+  static constexpr int CB = D / 64;        // 128-byte column blocks of a row
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int NS = NT == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 6 : 3);  // stages
+  static constexpr int STAGE = 2 * TILE;   // K_j, V_j
+  static constexpr int RING_OFF = NT * TILE;
+  static constexpr int BAR_OFF = RING_OFF + NS * STAGE;
+  // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain
+  static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int SOFT_WARPS = 4 * NT;
+  static constexpr int WARPS = SOFT_WARPS + 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+  static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
+  static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
+  static constexpr int UNIT_OFF =
+      WALK_OFF + WARPS * static_cast<int>(sizeof(Walk<AttendUnits>));
+  static constexpr int SMEM = UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr uint32_t s_col(int i) { return static_cast<uint32_t>(i * 128); }
+  static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(256 + t * D); }
+  static constexpr int SLOT = 128 * NT * (D + 2);  // floats of a partial result
+};
+
+constexpr uint32_t kPBar = 1;  // + t: softmax warps of tile t with the MMA warp
+constexpr uint32_t kKBar = 3;  // stage helper with the MMA warp
+
+// What a role needs of a unit.
+struct TileGeo {
+  int nt;       // active query tiles
+  int s0;       // first key tile
+  int n[2];     // key tiles of each query tile, from s0
+  int nmax;     // key tiles loaded
+  int nk;
+};
+template <int NT>
+__device__ __forceinline__ TileGeo tile_geo(const Args& a, const Unit& u) {
+  TileGeo g;
+  g.s0 = u.s0;
+  g.nk = u.s.nk;
+  g.nmax = u.s1 - u.s0;
+  const int tok0 = u.j * a.w * NT;
+  g.nt = NT == 2 && tok0 + a.w < u.s.nq ? 2 : 1;
+  g.n[0] = g.n[1] = g.nmax;
+  if (NT == 2 && a.causal && g.nt == 2) {  // the first tile may see fewer keys
+    const int lim = max(0, u.s.nk - u.s.nq + tok0 + a.w);
+    g.n[0] = max(0, min(u.s1, (lim + 127) >> 7) - u.s0);
+  }
+  return g;
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const Args a, const int box_rows) {
+  using C = TcCfg<D, NT>;
+  using E = Elem<BF16>;
+  using T = typename E::T;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + C::RING_OFF;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
+  uint64_t* empty = full + C::NS;
+  uint64_t* s_full = empty + C::NS;
+  uint64_t* o_done = s_full + 2;
+  uint64_t* pv_done = o_done + 2;
+  uint64_t* drain = pv_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  Share* sh = reinterpret_cast<Share*>(smem + C::SHARE_OFF);
+  constexpr int kLoad = C::SOFT_WARPS, kMma = kLoad + 1, kHelp = kLoad + 2;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoad && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // query rows that no box writes stay zero: finite scores that nobody reads
+  if (a.gu * a.w < 128) {
+    for (int i = threadIdx.x; i < NT * C::TILE / 16; i += C::THREADS)
+      reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_shared();
+  }
+  tc_fence_before();
+  griddep_launch_dependents();
+  griddep_wait();
+  const AttendUnits units{a.w * NT, 7, a.causal};
+  const int heads = a.Hkv * a.nsub;
+  plan_share<C::THREADS>(a, units, heads, 2,
+                         reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{a.wait_ns, abort_flag, a.status};
+  // Each warp walks the share on its own; the walk's state lives in shared
+  // memory, so that it holds no registers between units.
+  using W = Walk<AttendUnits>;
+  W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
+  Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
+  if (lane == 0) *walk = W(a, units, *sh);
+  auto next = [&]() {
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = walk->next(a, *sh, heads, unit);
+    return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
+  };
+  int last_use[C::NS];  // producer: last fill of each stage (-1: none)
+#pragma unroll
+  for (int s = 0; s < C::NS; ++s) last_use[s] = -1;
+  int last_q = -1;
+
+  if (warp >= C::SOFT_WARPS) {
+    if constexpr (NT == 2) setmaxnreg_dec<kControlRegs>();
+    if (warp == kLoad) {
+      // ---------------------------------------------------------- producer
+      const int nbox = 128 / box_rows;
+      const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * 128u;
+      int g = 0;
+      bool ok = true;
+      for (int it = 0; ok && next(); ++it) {
+        const Unit u = *unit;
+        const TileGeo tg = tile_geo<NT>(a, u);
+        const int kvh = u.h / a.nsub, sub = u.h % a.nsub;
+        // page of this lane's box of key tile t (num_pages, which reads as
+        // zero, where the table names none; -1: past the length)
+        auto lookup = [&](int t, int* row) {
+          const int key = t * 128 + lane * box_rows;
+          if (lane >= nbox || key >= u.s.nk) return -1;
+          const int page = page_of(a, u.b, key);
+          *row = key % a.page_size;
+          return page < 0 ? a.num_pages : page;
+        };
+        int row = 0;
+        int page = lookup(tg.s0, &row);
+        if (lane == 0) {
+          if (it > 0) ok = mbar_wait(q_empty, (it - 1) & 1, wc);
+          if (ok) {
+            last_q = it;
+            mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tg.nt * C::CB * a.gu * a.w * 128));
+            for (int t = 0; t < tg.nt; ++t)
+              for (int cb = 0; cb < C::CB; ++cb)
+                tma_load_4d(sQ + t * C::TILE + cb * 128 * 128, &tmQ, q_full, cb * 64,
+                            kvh * a.G + sub * a.gu, u.s.q0 + (u.j * NT + t) * a.w, 0);
+          }
+        }
+        for (int j = 0; j < tg.nmax; ++j, ++g) {
+          const int s = g % C::NS, use = g / C::NS;
+          const int boxes = min(nbox, (u.s.nk - (tg.s0 + j) * 128 + box_rows - 1) / box_rows);
+          if (lane == 0) {
+            if (ok && use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, wc);
+            if (ok) mbar_arrive_expect_tx(&full[s], 2u * C::CB * box_bytes * boxes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (page >= 0) {
+            uint8_t* dst = sRing + s * C::STAGE + lane * box_bytes;
+#pragma unroll
+            for (int cb = 0; cb < C::CB; ++cb)
+              tma_load_4d(dst + cb * 128 * 128, &tmK, &full[s], cb * 64, row, kvh, page);
+#pragma unroll
+            for (int cb = 0; cb < C::CB; ++cb)
+              tma_load_4d(dst + C::TILE + cb * 128 * 128, &tmV, &full[s], cb * 64, row, kvh,
+                          page);
+          }
+          last_use[s] = use;
+          if (j + 1 < tg.nmax) page = lookup(tg.s0 + j + 1, &row);
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+    } else if (warp == kMma) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
+      constexpr uint32_t idO = idesc_f16(BF16, 128, D, false, true);
+      const uint64_t q_desc = sdesc(smem_addr(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = sdesc(smem_addr(sRing), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = sdesc(smem_addr(sRing) + C::TILE, 128 * 128, 1024, kSwizzle128B);
+      const uint32_t qk_hi = static_cast<uint32_t>(q_desc >> 32);
+      const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc);
+      const uint32_t k_lo = static_cast<uint32_t>(k_desc);
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc);
+      auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+      // S (columns of slot i) = Q_t K^T of the g-th loaded tile
+      auto issue_s = [&](int t, int i, int g) {
+        const uint32_t qd = q_lo + static_cast<uint32_t>((t * C::TILE) >> 4);
+        const uint32_t kd = k_lo + static_cast<uint32_t>(((g % C::NS) * C::STAGE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+          mma_f16_ss_elect(tmem + C::s_col(i), desc(qk_hi, qd + off), desc(qk_hi, kd + off), idS,
+                           kk > 0 ? 1u : 0u, 1u);
+        }
+      };
+      // O_t += P V of the g-th loaded tile, P in slot i, keys in groups of 16
+      auto issue_pv = [&](int t, int i, int g, bool first, int groups) {
+        const uint32_t vd = v_lo + static_cast<uint32_t>(((g % C::NS) * C::STAGE) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16_ts_elect(tmem + C::o_col(t), tmem + C::s_col(i) + kk * 8,
+                           desc(v_hi, vd + ((kk * 16 * 128) >> 4)), idO,
+                           (!first || kk > 0) ? 1u : 0u, kk < groups ? 1u : 0u);
+      };
+      int g0 = 0;
+      while (next()) {
+        const TileGeo tg = tile_geo<NT>(a, *unit);
+        auto groups = [&](int j) { return min(8, (tg.nk - (tg.s0 + j) * 128 + 15) >> 4); };
+        named_bar_sync(kKBar, 64);  // Q and the first stage have landed
+        tc_fence_after();
+        if constexpr (NT == 2) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= tg.nt) continue;
+            if (tg.n[t] == 0) {
+              mma_commit_elect(&o_done[t], 1u);
+            } else {
+              issue_s(t, t, g0);
+              mma_commit_elect(&s_full[t], 1u);
+            }
+          }
+          if (tg.nmax <= 1) mma_commit_elect(q_empty, 1u);
+          for (int j = 0; j < tg.nmax; ++j) {
+            bool waited = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t >= tg.nt || j >= tg.n[t]) continue;
+              named_bar_sync(kPBar + t, 32 * 5);
+              tc_fence_after();
+              issue_pv(t, t, g0 + j, j == 0, groups(j));
+              if (j + 1 < tg.n[t]) {
+                if (!waited) {
+                  named_bar_sync(kKBar, 64);
+                  waited = true;
+                }
+                issue_s(t, t, g0 + j + 1);
+                mma_commit_elect(&s_full[t], 1u);
+              } else {
+                mma_commit_elect(&o_done[t], 1u);
+              }
+            }
+            if (j == tg.nmax - 2) mma_commit_elect(q_empty, 1u);
+            mma_commit_elect(&empty[(g0 + j) % C::NS], 1u);
+          }
+        } else {
+          if (tg.nmax == 0) {
+            mma_commit_elect(&o_done[0], 1u);
+            mma_commit_elect(q_empty, 1u);
+          } else {
+            issue_s(0, g0 & 1, g0);
+            mma_commit_elect(&s_full[g0 & 1], 1u);
+            if (tg.nmax > 1) {
+              named_bar_sync(kKBar, 64);
+              tc_fence_after();
+              issue_s(0, (g0 + 1) & 1, g0 + 1);
+              mma_commit_elect(&s_full[(g0 + 1) & 1], 1u);
+            }
+            if (tg.nmax <= 2) mma_commit_elect(q_empty, 1u);
+            for (int j = 0; j < tg.nmax; ++j) {
+              const int g = g0 + j;
+              named_bar_sync(kPBar, 32 * 5);
+              tc_fence_after();
+              issue_pv(0, g & 1, g, j == 0, groups(j));
+              mma_commit_elect(pv_done, 1u);
+              mma_commit_elect(&empty[g % C::NS], 1u);
+              if (j + 2 < tg.nmax) {
+                named_bar_sync(kKBar, 64);
+                tc_fence_after();
+                issue_s(0, g & 1, g + 2);
+                mma_commit_elect(&s_full[g & 1], 1u);
+                if (j + 3 == tg.nmax) mma_commit_elect(q_empty, 1u);
+              }
+            }
+            mma_commit_elect(&o_done[0], 1u);
+          }
+        }
+        g0 += tg.nmax;
+      }
+      // every MMA issued by this warp completes before TMEM is freed
+      mma_commit_elect(drain, 1u);
+      if (lane == 0) drain_wait(drain, 0, kDrainNs);
+      __syncwarp();
+    } else if (warp == kHelp) {
+      // ------------------------------------------------------ stage helper
+      // Waits for each stage, zeroes the last tile's value rows between the
+      // length and the end of its group of 16 keys, and passes the stage on
+      // (same count of meetings on both sides, also after a failed wait).
+      bool ok = true;
+      int g0 = 0;
+      for (int it = 0; next(); ++it) {
+        const TileGeo tg = tile_geo<NT>(a, *unit);
+        // one meeting for Q and the first stage, then one for every further stage
+        for (int j = 0; j < max(tg.nmax, 1); ++j) {
+          if (j == 0) ok = ok && mbar_wait(q_full, static_cast<uint32_t>(it & 1), wc);
+          if (j < tg.nmax) {
+            const int g = g0 + j;
+            ok = ok && mbar_wait(&full[g % C::NS], static_cast<uint32_t>((g / C::NS) & 1), wc);
+            const int keys = tg.nk - (tg.s0 + j) * 128;
+            if (keys < 128 && (keys & 15)) {
+              uint8_t* v = sRing + (g % C::NS) * C::STAGE + C::TILE;
+              const int rows = 16 - (keys & 15);
+              for (int i = lane; i < rows * C::CB * 8; i += 32) {
+                const int cb = i / (rows * 8), x = i % (rows * 8);
+                reinterpret_cast<uint4*>(v + cb * 128 * 128 + keys * 128)[x] =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_shared();
+            }
+            __syncwarp();
+          }
+          named_bar_sync(kKBar, 64);
+        }
+        g0 += tg.nmax;
+      }
+    }
+  } else {
+    if constexpr (NT == 2) setmaxnreg_inc<kSoftmaxRegs>();
+    // --------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + lane_off + C::o_col(t);
+    bool ok = true;
+    int g0 = 0;   // steps of earlier units (NT = 2: of this tile)
+    int oph = 0;  // phases of o_done[t] consumed
+    bool began = false;  // this CTA wrote its descriptor
+    while (next()) {
+      const TileGeo tg = tile_geo<NT>(a, *unit);
+      if (t >= tg.nt) continue;
+      const int tok0 = (unit->j * NT + t) * a.w;  // first token of the tile
+      const int nq = unit->s.nq;
+      const int tok = tok0 + r / a.gu;
+      // rows of this warp that exist
+      const bool live = (warp & 3) * 32 < min(a.w, nq - tok0) * a.gu;
+      // visible keys of the row, counted from the piece's first key
+      const int limit =
+          (a.causal ? min(tg.nk, tg.nk - nq + tok + 1) : tg.nk) - tg.s0 * 128;
+      float m = -INFINITY, l = 0.f;
+      const int n = tg.n[t];
+      for (int j = 0; j < n; ++j) {
+        const int g = g0 + j;
+        const int slot = NT == 2 ? t : g & 1;
+        const uint32_t tS = tmem + lane_off + C::s_col(slot);
+        if (live) {
+          ok = __all_sync(0xffffffffu,
+                          ok && mbar_wait(&s_full[slot], (NT == 2 ? g : g >> 1) & 1, wc));
+          if (ok) {
+            tc_fence_after();
+            uint32_t s[128];
+            __syncwarp();
+            tmem_ld4x32_sync(tS, tS + 32, tS + 64, tS + 96,
+                             *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                             *reinterpret_cast<uint32_t(*)[32]>(&s[32]),
+                             *reinterpret_cast<uint32_t(*)[32]>(&s[64]),
+                             *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+            const int vis = limit - j * 128;  // visible keys of the row in this tile
+            if (__any_sync(0xffffffffu, vis < 128)) {
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                if (i >= vis) s[i] = 0xff800000u;  // -inf
+            }
+            float alpha = 1.f, rs;
+            uint32_t pk[64];
+            bool resc = !(m > -INFINITY);
+            if (!resc) {
+              softmax_pairs<BF16, 128>(s, a.sl2, m, pk, rs);
+              resc = !(rs <= kFusedSumLimit);
+            }
+            if (resc) {
+              const float mx = row_max_raw(s) * a.sl2;  // -inf: no visible key
+              if (mx > -INFINITY) {
+                alpha = ex2(m - mx);  // 0 when m = -inf
+                m = mx;
+              }
+              softmax_pairs<BF16, 128>(s, a.sl2, m == -INFINITY ? 0.f : m, pk, rs);
+            }
+            __syncwarp();
+            l = l * alpha + rs;
+            // O_t through step j - 1 (NT = 2: complete, the commit behind
+            // s_full tracks it); rescaled where a row's max moved
+            if (j > 0 && __any_sync(0xffffffffu, resc)) {
+              if constexpr (NT == 1) {
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (g - 1) & 1, wc));
+                tc_fence_after();
+              }
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t ob[32];
+                tmem_ld32_sync(tO + c * 32, ob);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  ob[i] = __float_as_uint(__uint_as_float(ob[i]) * alpha);
+                tmem_st32(tO + c * 32, ob);
+              }
+            }
+            tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        // hand P_j to the MMA warp; met every step, also after a failed wait
+        named_bar_sync(kPBar + (NT == 2 ? t : 0), 32 * 5);
+      }
+      ok = ok && mbar_wait(&o_done[t], static_cast<uint32_t>(oph & 1), wc);
+      ok = __all_sync(0xffffffffu, ok);
+      g0 += n;
+      ++oph;
+      // ------------------------------------------------------------ epilogue
+      const bool whole = unit->whole();
+      if (!whole && unit->s0 == 0 && threadIdx.x == 0) {
+        int* d = a.desc + blockIdx.x * kDesc;
+        d[0] = pieces_of(*unit, *sh);
+        d[1] = unit->b;
+        d[2] = unit->h;
+        d[3] = unit->j;
+        d[4] = unit->s.q0;
+        d[5] = nq;
+        began = true;
+      }
+      if (!ok || !live) continue;
+      const int sub = unit->h % a.nsub;
+      const int e = sub * a.gu + r % a.gu;
+      const bool row_ok = r < a.w * a.gu && tok < nq && e < a.G;
+      tc_fence_after();
+      __syncwarp();
+      if (!whole) {
+        // unnormalised O (relative to 2^m), m and l
+        float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + unit->slot()) * C::SLOT;
+        float* orow = slot + (t * 128 + r) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ob[32];
+          tmem_ld32_sync(tO + c * 32, ob);
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(orow + c * 32)[i] =
+                  make_uint4(ob[4 * i], ob[4 * i + 1], ob[4 * i + 2], ob[4 * i + 3]);
+          }
+        }
+        if (row_ok) {
+          slot[NT * 128 * D + t * 128 + r] = m;
+          slot[NT * 128 * (D + 1) + t * 128 + r] = l;
+        }
+      } else {
+        const int hq = (unit->h / a.nsub) * a.G + e;
+        float f = 1.f;
+        const float own = l;
+        if (a.sinks && row_ok) {
+          const float sk = a.sinks[hq] * kLog2e;
+          const float mn = fmaxf(m, sk);
+          f = ex2(m - mn);
+          l = l * f + ex2(sk - mn);
+          m = mn;
+        }
+        const float inv = own != 0.f ? f / l : 0.f;
+        const long long q = unit->s.q0 + tok;
+        T* orow = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ob[32];
+          tmem_ld32_sync(tO + c * 32, ob);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            // (a row that saw no key: O may never have been written)
+            const float x0 = own != 0.f ? __uint_as_float(ob[2 * i]) * inv : 0.f;
+            const float x1 = own != 0.f ? __uint_as_float(ob[2 * i + 1]) * inv : 0.f;
+            w[i] = E::pack(x0, x1);
+          }
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<uint4*>(orow + c * 32)[i] =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+        if (row_ok && a.lse) a.lse[q * a.Hq + hq] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+    if (threadIdx.x == 0 && !began) a.desc[blockIdx.x * kDesc] = 0;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (warp == kLoad && lane == 0 && *abort_flag) {
+    // a role gave up: every copy the producer issued lands before the CTA exits
+    if (last_q >= 0) drain_wait(q_full, static_cast<uint32_t>(last_q & 1), kDrainNs);
+    for (int s = 0; s < C::NS; ++s)
+      if (last_use[s] >= 0) drain_wait(&full[s], last_use[s] & 1, kDrainNs);
+  }
+}
+
+template <int D, bool BF16, int NT>
+sdpa_status_t launch_tc_impl(Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                             const CUtensorMap& tv, int box_rows, const LaunchEnv& env) {
+  using C = TcCfg<D, NT>;
+  auto kern = paged_tc_kernel<D, BF16, NT>;
+  // The setmaxnreg split must fit the registers the kernel is launched with
+  // (an increase beyond them would wait forever).
+  static std::atomic<uint64_t> ready{0};  // devices on which this holds and is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load() & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SDPA_ERR_CUDA;
+    const long have = static_cast<long>((fa.numRegs + 7) & ~7) * C::THREADS;
+    const long need = 32L * (C::SOFT_WARPS * static_cast<long>(kSoftmaxRegs) + 4L * kControlRegs);
+    if (NT == 2 && have < need) return SDPA_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return SDPA_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, box_rows) != cudaSuccess)
+    return SDPA_ERR_CUDA;
+  return launch_paged_merge(a, D, BF16 ? SDPA_BF16 : SDPA_F16, 128, NT, env.stream);
+}
+
+template <int D>
+sdpa_status_t launch_tc(Args a, int dtype, const LaunchEnv& env) {
+  fit_rows(a, 128);
+  const bool bf16 = dtype == SDPA_BF16;
+  const CUtensorMapDataType dt =
+      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  int box_rows = 128;  // gcd(page_size, 128)
+  while (a.page_size % box_rows) box_rows >>= 1;
+  CUtensorMap tq, tk, tv;
+  // A stride of a dimension of one element is never followed: any valid one.
+  auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
+  if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
+                           static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
+      !encode_tiled_4d(&tk, dt, a.k, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
+                       st(a.ks[2], a.page_size), st(a.ks[1], a.Hkv), st(a.ks[0], a.num_pages)) ||
+      !encode_tiled_4d(&tv, dt, a.v, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
+                       st(a.vs[2], a.page_size), st(a.vs[1], a.Hkv), st(a.vs[0], a.num_pages)))
+    return SDPA_ERR_CUDA;
+  // more than 128 rows a sequence and head unit on average: two tiles a unit
+  const bool two = static_cast<long long>(a.T) * a.gu > 128LL * a.B;
+  if (bf16)
+    return two ? launch_tc_impl<D, true, 2>(a, tq, tk, tv, box_rows, env)
+               : launch_tc_impl<D, true, 1>(a, tq, tk, tv, box_rows, env);
+  return two ? launch_tc_impl<D, false, 2>(a, tq, tk, tv, box_rows, env)
+             : launch_tc_impl<D, false, 1>(a, tq, tk, tv, box_rows, env);
+}
+
+}  // namespace
+}  // namespace paged
+
+}  // namespace gb300
