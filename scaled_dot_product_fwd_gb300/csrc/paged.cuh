@@ -341,6 +341,8 @@ sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
                                        const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d128(paged::Args a, int dtype, const LaunchEnv& env);
+sdpa_status_t launch_paged_scores_tc(paged::Args a, int head_dim, int dtype,
+                                     const LaunchEnv& env);
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
                                  int tiles, cudaStream_t stream);
 sdpa_status_t launch_paged_scores_merge(const paged::Args& a, int tile_keys,

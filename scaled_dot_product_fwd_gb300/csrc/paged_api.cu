@@ -273,7 +273,8 @@ sdpa_status_t sdpa_paged_scores(const sdpa_paged_params_t* p, const void* q,
   a.ss[0] = score_stride[0];
   a.ss[1] = score_stride[1];
   a.score_len = score_len;
-  st = launch_paged_scores_simt(a, p->head_dim, p->dtype, env);
+  st = tc_fits(*p, false) ? launch_paged_scores_tc(a, p->head_dim, p->dtype, env)
+                          : launch_paged_scores_simt(a, p->head_dim, p->dtype, env);
   if (st == SDPA_OK) set_last_launches(2);
   return st;
 }

@@ -1,0 +1,513 @@
+// paged_scores_tc.cu — accumulated attention weights over the paged KV cache
+// on the 5th-generation tensor cores (fp16/bf16, head_dim 64/128):
+//     scores[key] += sum over rows of 2^(S^T[key, row] * scale*log2e - lse2[row])
+// with S^T = K Q^T, 128 keys on the lanes of TMEM and a chunk of query rows
+// (tokens x heads of the kv head) on its columns.  A thread owns a key: it
+// reads its row of S^T, subtracts the rows' log-sum-exp (shared memory, the
+// same address for a whole warp), and adds the exponentials up in registers
+// over all chunks, so no value crosses lanes and nothing is added atomically.
+//
+// A unit is 256 keys (two TMEM tiles, one a warpgroup): each query chunk that
+// is brought in meets both, which halves the query traffic out of L2.  Its
+// steps are the chunks of w tokens x gu heads that see a key of it, and the
+// work is divided among the CTAs as paged.cuh describes.  The K tiles of two
+// units and three query chunks are in flight (head_dim 128); S^T is
+// double-buffered, so the products of a step run while the exponentials of
+// the one before do.  Chunks: bound by the exponentials (128 x 256 a step,
+// about 1100 clk at the measured 30 a clk and SM, against 1024 clk of
+// products at head_dim 128).  Single tokens: the chunk has R = 16 columns
+// and K streams once, bound by HBM.
+//
+// Rows that do not exist (past the sequence's tokens, another head's) take no
+// part: their limit is 0, and a chunk that holds one, or a key that some row
+// does not see, takes the path with a comparison for every column.  Keys past
+// the length produce sums that are never written.
+#include <atomic>
+
+#include "paged.cuh"
+#include "prefill_tc.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace {
+
+constexpr int kUnitKeys = 256;
+constexpr int kLgUnit = 8;
+constexpr int kNL = 4;  // slots of the rows' log-sum-exp
+
+template <int D, int R>
+struct ScCfg {
+  static constexpr int CB = D / 64;
+  static constexpr int TILE = 128 * D * 2;  // a key tile
+  static constexpr int QTILE = R * D * 2;   // a query chunk
+  // units whose keys are in flight, and query chunks
+  static constexpr int NK = R == 16 ? (D == 64 ? 6 : 3) : 2;
+  static constexpr int NQS = R == 16 ? 4 : (D == 64 ? 6 : 2);
+  static constexpr int Q_OFF = NK * 2 * TILE;
+  static constexpr int BAR_OFF = Q_OFF + NQS * QTILE;
+  // k_full[NK], k_empty[NK], q_full[NQS], q_empty[NQS], s_full[2 tiles][2],
+  // l_full[kNL], l_empty[kNL], drain
+  static constexpr int NBARS = 2 * NK + 2 * NQS + 4 + 2 * kNL + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int WARPS = 12;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+  static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
+  static constexpr int MIN_OFF = SCRATCH_OFF + (WARPS + 1) * 8;  // int[kNL]
+  static constexpr int WALK_OFF = (MIN_OFF + kNL * 4 + 15) / 16 * 16;
+  static constexpr int UNIT_OFF = WALK_OFF + WARPS * static_cast<int>(sizeof(Walk<ScoreUnits>));
+  // per slot: -lse2[R], then the rows' limits [R]
+  static constexpr int LSE_OFF =
+      (UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;
+  static constexpr int SMEM = LSE_OFF + kNL * R * 8 + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+template <int R>
+__device__ __forceinline__ void load_cols(uint32_t t0, uint32_t (&s)[R]) {
+  if constexpr (R == 128) {
+    tmem_ld4x32_sync(t0, t0 + 32, t0 + 64, t0 + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                     *reinterpret_cast<uint32_t(*)[32]>(&s[32]),
+                     *reinterpret_cast<uint32_t(*)[32]>(&s[64]),
+                     *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+  } else {
+    static_assert(R == 16, "columns of a chunk");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]),
+          "=r"(s[7]), "=r"(s[8]), "=r"(s[9]), "=r"(s[10]), "=r"(s[11]), "=r"(s[12]),
+          "=r"(s[13]), "=r"(s[14]), "=r"(s[15])
+        : "r"(t0)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+// named barriers: kBarS + 2 t + buffer: the warps of key tile t have read
+// that buffer of S^T; kBarQ: stage helper with the MMA warp
+constexpr uint32_t kBarS = 1;
+constexpr uint32_t kBarQ = 5;
+
+template <int D, bool BF16, int R>
+__global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
+    paged_scores_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                           const __grid_constant__ CUtensorMap tmK, const Args a,
+                           const int box_rows) {
+  using C = ScCfg<D, R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sK = smem;
+  uint8_t* sQ = smem + C::Q_OFF;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* k_empty = k_full + C::NK;
+  uint64_t* q_full = k_empty + C::NK;
+  uint64_t* q_empty = q_full + C::NQS;
+  uint64_t* s_full = q_empty + C::NQS;  // [tile][buffer]
+  uint64_t* l_full = s_full + 4;
+  uint64_t* l_empty = l_full + kNL;
+  uint64_t* drain = l_empty + kNL;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  Share* sh = reinterpret_cast<Share*>(smem + C::SHARE_OFF);
+  int* sMin = reinterpret_cast<int*>(smem + C::MIN_OFF);
+  float* sLse = reinterpret_cast<float*>(smem + C::LSE_OFF);
+  constexpr int kLoad = 8, kMma = 9, kHelp = 10, kLse = 11;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NQS; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < kNL; ++i) {
+      mbar_init(&l_full[i], 32);
+      mbar_init(&l_empty[i], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoad && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  // rows of a chunk that no box writes stay zero (finite scores)
+  if (a.gu * a.w < R) {
+    for (int i = threadIdx.x; i < C::NQS * C::QTILE / 16; i += C::THREADS)
+      reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_shared();
+  }
+  tc_fence_before();
+  griddep_launch_dependents();
+  griddep_wait();
+  const ScoreUnits units{a.w, kLgUnit, a.causal, a.nsub};
+  plan_share<C::THREADS>(a, units, a.Hkv, 2,
+                         reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{a.wait_ns, abort_flag, a.status};
+  using W = Walk<ScoreUnits>;
+  W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
+  Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
+  if (lane == 0) *walk = W(a, units, *sh);
+  auto next = [&]() {
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = walk->next(a, *sh, a.Hkv, unit);
+    return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
+  };
+  // the two key tiles of unit j, or one where the length ends in the first
+  auto tiles_of = [&](const Unit& u) { return u.s.nk - u.j * kUnitKeys > 128 ? 2 : 1; };
+  int k_fills = 0, q_fills = 0;  // producer: fills of the two rings so far
+
+  if (warp == kLoad) {
+    // ------------------------------------------------------------ producer
+    const int nbox = 128 / box_rows;
+    const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * 128u;
+    bool ok = true;
+    int ku = 0, g = 0;  // units, steps
+    while (ok && next()) {
+      const Unit u = *unit;
+      const int first = units.first(u.s.nq, u.s.nk, u.j);
+      // this lane's box: of tile lane / nbox
+      const int key = u.j * kUnitKeys + lane * box_rows;
+      int page = -1, row = 0;
+      if (lane < 2 * nbox && key < u.s.nk) {
+        page = page_of(a, u.b, key);
+        row = key % a.page_size;
+        if (page < 0) page = a.num_pages;  // reads as zero
+      }
+      const int boxes = min(2 * nbox, (u.s.nk - u.j * kUnitKeys + box_rows - 1) / box_rows);
+      const int ks = ku % C::NK;
+      if (lane == 0) {
+        if (ku >= C::NK) ok = mbar_wait(&k_empty[ks], ((ku / C::NK) - 1) & 1, wc);
+        if (ok) mbar_arrive_expect_tx(&k_full[ks], C::CB * box_bytes * boxes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      if (page >= 0) {
+        uint8_t* dst = sK + (ks * 2 + lane / nbox) * C::TILE + (lane % nbox) * box_bytes;
+#pragma unroll
+        for (int cb = 0; cb < C::CB; ++cb)
+          tma_load_4d(dst + cb * 128 * 128, &tmK, &k_full[ks], cb * 64, row, u.h, page);
+      }
+      ++ku;
+      k_fills = ku;
+      if (lane == 0) {
+        for (int t = u.s0; t < u.s1 && ok; ++t, ++g) {
+          const int qs = g % C::NQS;
+          if (g >= C::NQS) ok = mbar_wait(&q_empty[qs], ((g / C::NQS) - 1) & 1, wc);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(C::CB * a.gu * a.w * 128));
+          const int tok = u.s.q0 + (first + t / a.nsub) * a.w;
+          const int head = u.h * a.G + (t % a.nsub) * a.gu;
+          for (int cb = 0; cb < C::CB; ++cb)
+            tma_load_4d(sQ + qs * C::QTILE + cb * R * 128, &tmQ, &q_full[qs], cb * 64, head,
+                        tok, 0);
+          q_fills = g + 1;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+  } else if (warp == kMma) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t idS = idesc_f16(BF16, 128, R, false, false);
+    const uint64_t k_desc = sdesc(smem_addr(sK), 16, 1024, kSwizzle128B);
+    const uint64_t q_desc = sdesc(smem_addr(sQ), 16, 1024, kSwizzle128B);
+    const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);
+    const uint32_t k_lo = static_cast<uint32_t>(k_desc);
+    const uint32_t q_lo = static_cast<uint32_t>(q_desc);
+    auto desc = [&](uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+    int ku = 0, g = 0;
+    int uses[4] = {0, 0, 0, 0};  // of each (tile, buffer)
+    while (next()) {
+      const int nt = tiles_of(*unit), n = unit->s1 - unit->s0;
+      for (int t = 0; t < n; ++t, ++g) {
+        named_bar_sync(kBarQ, 64);  // the chunk (and the unit's keys) have landed
+        tc_fence_after();
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          if (kt >= nt) continue;
+          const int buf = 2 * kt + (g & 1);
+          // the buffer's previous scores have been read
+          if ((g & 1) ? uses[2 * kt + 1]++ : uses[2 * kt]++) {
+            named_bar_sync(kBarS + buf, 160);
+            tc_fence_after();
+          }
+          const uint32_t kd = k_lo + static_cast<uint32_t>((((ku % C::NK) * 2 + kt) * C::TILE) >> 4);
+          const uint32_t qd = q_lo + static_cast<uint32_t>(((g % C::NQS) * C::QTILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ko = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+            const uint32_t qo = ((kk >> 2) * (R * 128) + (kk & 3) * 32) >> 4;
+            mma_f16_ss_elect(tmem + buf * 128, desc(kd + ko), desc(qd + qo), idS,
+                             kk > 0 ? 1u : 0u, 1u);
+          }
+          mma_commit_elect(&s_full[buf], 1u);
+        }
+        mma_commit_elect(&q_empty[g % C::NQS], 1u);
+      }
+      mma_commit_elect(&k_empty[ku % C::NK], 1u);
+      ++ku;
+    }
+    // meet the last readers of each buffer
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (uses[i] > 0) named_bar_sync(kBarS + i, 160);
+    mma_commit_elect(drain, 1u);
+    if (lane == 0) drain_wait(drain, 0, kDrainNs);
+    __syncwarp();
+  } else if (warp == kHelp) {
+    // -------------------------------------------------------- stage helper
+    bool ok = true;
+    int ku = 0, g = 0;
+    while (next()) {
+      ok = ok && mbar_wait(&k_full[ku % C::NK], static_cast<uint32_t>((ku / C::NK) & 1), wc);
+      const int n = unit->s1 - unit->s0;
+      for (int t = 0; t < n; ++t, ++g) {
+        ok = ok && mbar_wait(&q_full[g % C::NQS], static_cast<uint32_t>((g / C::NQS) & 1), wc);
+        __syncwarp();
+        named_bar_sync(kBarQ, 64);
+      }
+      ++ku;
+    }
+  } else if (warp == kLse) {
+    // ------------------------------------- the rows' log-sum-exp and limits
+    bool ok = true;
+    int g = 0;
+    while (ok && next()) {
+      const Unit u = *unit;
+      const int first = units.first(u.s.nq, u.s.nk, u.j);
+      for (int t = u.s0; t < u.s1 && ok; ++t, ++g) {
+        const int slot = g % kNL;
+        float* dst = sLse + slot * 2 * R;
+        const int tok0 = (first + t / a.nsub) * a.w, sub = t % a.nsub;
+        float v[(R + 31) / 32];
+        int lim[(R + 31) / 32];
+        int mn = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < (R + 31) / 32; ++i) {
+          const int r = i * 32 + lane;
+          v[i] = -INFINITY;
+          lim[i] = 0;
+          if (r < a.gu * a.w) {
+            const int tok = tok0 + r / a.gu, e = sub * a.gu + r % a.gu;
+            if (tok < u.s.nq && e < a.G) {
+              const float x =
+                  a.lse[static_cast<size_t>(u.s.q0 + tok) * a.Hq + u.h * a.G + e] * kLog2e;
+              v[i] = x == -INFINITY ? x : -x;  // a row that saw nothing adds nothing
+              lim[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
+            }
+            mn = min(mn, lim[i]);
+          }
+        }
+        mn = __reduce_min_sync(0xffffffffu, mn);
+        if (g >= kNL) ok = __all_sync(0xffffffffu, mbar_wait(&l_empty[slot], ((g / kNL) - 1) & 1, wc));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < (R + 31) / 32; ++i) {
+          const int r = i * 32 + lane;
+          if (r < R) {
+            dst[r] = v[i];
+            reinterpret_cast<int*>(dst)[R + r] = lim[i];
+          }
+        }
+        if (lane == 0) sMin[slot] = mn;
+        mbar_arrive(&l_full[slot]);
+      }
+    }
+  } else {
+    // -------------------------------------------------------- exponentials
+    const int kt = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool ok = true;
+    int g = 0;
+    int ph[2] = {0, 0};  // phases of s_full consumed, per buffer
+    bool began = false;
+    while (next()) {
+      const int key = unit->j * kUnitKeys + kt * 128 + r;
+      const int n = unit->s1 - unit->s0;
+      const bool mine = kt < tiles_of(*unit);
+      const bool whole = unit->whole();
+      float* dst = a.scores + unit->b * a.ss[0] + unit->h * a.ss[1] + key;
+      const bool live = mine && key < unit->s.nk && key < a.score_len;
+      float old = 0.f;
+      if (live && whole) old = *dst;  // on its way while the scores are computed
+      float sum = 0.f;
+      for (int t = 0; t < n; ++t, ++g) {
+        const int slot = g % kNL;
+        ok = ok && mbar_wait(&l_full[slot], static_cast<uint32_t>((g / kNL) & 1), wc);
+        if (mine) {
+          const int buf = 2 * kt + (g & 1);
+          const int p = (g & 1) ? ph[1]++ : ph[0]++;
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], static_cast<uint32_t>(p & 1), wc));
+          uint32_t s[R];
+          if (ok) {
+            tc_fence_after();
+            __syncwarp();
+            load_cols<R>(t0 + buf * 128, s);
+            tc_fence_before();
+          }
+          named_bar_arrive(kBarS + buf, 160);
+          if (ok) {
+            const float* nl = sLse + slot * 2 * R;
+            const int* lim = reinterpret_cast<const int*>(nl) + R;
+            const uint64_t SL = f2_pack(a.sl2, a.sl2);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            if (__all_sync(0xffffffffu, key < sMin[slot])) {
+#pragma unroll
+              for (int i = 0; i < R; i += 4) {
+                const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
+                const uint64_t x0 = f2_fma(
+                    f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), SL,
+                    f2_pack(l4.x, l4.y));
+                const uint64_t x1 = f2_fma(
+                    f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), SL,
+                    f2_pack(l4.z, l4.w));
+                float e0, e1, e2, e3;
+                f2_unpack(x0, e0, e1);
+                f2_unpack(x1, e2, e3);
+                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], f2_pack(ex2(e0), ex2(e1)));
+                acc[((i >> 1) + 1) & 3] =
+                    f2_add(acc[((i >> 1) + 1) & 3], f2_pack(ex2(e2), ex2(e3)));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < R; i += 4) {
+                const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
+                const int4 m4 = *reinterpret_cast<const int4*>(lim + i);
+                const float e0 = ex2(fmaf(__uint_as_float(s[i]), a.sl2, l4.x));
+                const float e1 = ex2(fmaf(__uint_as_float(s[i + 1]), a.sl2, l4.y));
+                const float e2 = ex2(fmaf(__uint_as_float(s[i + 2]), a.sl2, l4.z));
+                const float e3 = ex2(fmaf(__uint_as_float(s[i + 3]), a.sl2, l4.w));
+                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], f2_pack(key < m4.x ? e0 : 0.f,
+                                                                      key < m4.y ? e1 : 0.f));
+                acc[((i >> 1) + 1) & 3] =
+                    f2_add(acc[((i >> 1) + 1) & 3],
+                           f2_pack(key < m4.z ? e2 : 0.f, key < m4.w ? e3 : 0.f));
+              }
+            }
+            const uint64_t x = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+            float x0, x1;
+            f2_unpack(x, x0, x1);
+            sum += x0 + x1;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_empty[slot]);
+      }
+      if (!whole && unit->s0 == 0 && threadIdx.x == 0) {
+        int* d = a.desc + blockIdx.x * kDesc;
+        d[0] = pieces_of(*unit, *sh);
+        d[1] = unit->b;
+        d[2] = unit->h;
+        d[3] = unit->j;
+        d[6] = unit->s.nk;
+        began = true;
+      }
+      if (ok && live) {
+        if (whole)
+          *dst = old + sum;
+        else
+          a.ws[static_cast<size_t>(blockIdx.x * 2 + unit->slot()) * kUnitKeys + kt * 128 + r] =
+              sum;
+      }
+    }
+    if (threadIdx.x == 0 && !began) a.desc[blockIdx.x * kDesc] = 0;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (warp == kLoad && lane == 0 && *abort_flag) {
+    // a role gave up: every copy the producer issued lands before the CTA exits
+    for (int i = max(0, k_fills - C::NK); i < k_fills; ++i)
+      drain_wait(&k_full[i % C::NK], static_cast<uint32_t>((i / C::NK) & 1), kDrainNs);
+    for (int i = max(0, q_fills - C::NQS); i < q_fills; ++i)
+      drain_wait(&q_full[i % C::NQS], static_cast<uint32_t>((i / C::NQS) & 1), kDrainNs);
+  }
+}
+
+template <int D, bool BF16, int R>
+sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
+                        int box_rows, const LaunchEnv& env) {
+  using C = ScCfg<D, R>;
+  auto kern = paged_scores_tc_kernel<D, BF16, R>;
+  static std::atomic<uint64_t> ready{0};  // devices on which the attribute is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load() & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return SDPA_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, a, box_rows) != cudaSuccess) return SDPA_ERR_CUDA;
+  return launch_paged_scores_merge(a, kUnitKeys, env.stream);
+}
+
+template <int D>
+sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
+  // single tokens: 16 columns hold a sequence's rows
+  const bool few = a.G <= 16 && static_cast<long long>(a.T) * a.G <= 16LL * a.B;
+  fit_rows(a, few ? 16 : 128);
+  const bool bf16 = dtype == SDPA_BF16;
+  const CUtensorMapDataType dt =
+      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  int box_rows = 128;  // gcd(page_size, 128)
+  while (a.page_size % box_rows) box_rows >>= 1;
+  CUtensorMap tq, tk;
+  // a stride of a dimension of one element is never followed: any valid one
+  auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
+  if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
+                           static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
+      !encode_tiled_4d(&tk, dt, a.k, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
+                       st(a.ks[2], a.page_size), st(a.ks[1], a.Hkv), st(a.ks[0], a.num_pages)))
+    return SDPA_ERR_CUDA;
+  if (few)
+    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, box_rows, env)
+                : launch_sc<D, false, 16>(a, tq, tk, box_rows, env);
+  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, box_rows, env)
+              : launch_sc<D, false, 128>(a, tq, tk, box_rows, env);
+}
+
+}  // namespace
+}  // namespace paged
+
+sdpa_status_t launch_paged_scores_tc(paged::Args a, int head_dim, int dtype,
+                                     const LaunchEnv& env) {
+  return head_dim == 64 ? paged::launch_scores<64>(a, dtype, env)
+                        : paged::launch_scores<128>(a, dtype, env);
+}
+
+}  // namespace gb300
