@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -320,17 +321,26 @@ def sdpa_last_launch_count() -> int:
 _ws_cache = {}
 
 
+_torch_module = None
+_dtype_codes = {}
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported on first use (the C ABI needs none of it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _dtype_codes.update({torch.float32: SDPA_F32, torch.float16: SDPA_F16,
+                             torch.bfloat16: SDPA_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: SDPA_F32, torch.float16: SDPA_F16, torch.bfloat16: SDPA_BF16}
-    if t not in m:
+    _torch()
+    if t not in _dtype_codes:
         raise TypeError("unsupported dtype %s" % t)
-    return m[t]
+    return _dtype_codes[t]
 
 
 def _workspace(nbytes: int, device):
@@ -517,112 +527,140 @@ def sdpa_forward_host(q, k, v, scale=None, causal=False, mask=None, sinks=None, 
 
 
 # ------------------------------------------------------------ paged KV cache
-def _check(cond, what, kind=ValueError):
-    if not cond:
-        raise kind(what)
+# SdpaPagedParams as one struct.pack call: filling the ctypes fields one by one
+# costs several times as much, and single-token calls are bound by the host.
+_PAGED = struct.Struct("<6ifi3iIQqQQQ10q")
+_STRIDE2 = ctypes.c_int64 * 2
+_paged_fn = {}
+_paged_ws = {}
 
 
-class _PagedCall:
-    """The arguments that the paged calls share, checked and in an
-    SdpaPagedParams, and the device and stream that the call runs on."""
+def _paged_call(name):
+    """The C entry point taking the packed parameters as bytes."""
+    fn = _paged_fn.get(name)
+    if fn is None:
+        lib = load_library()
+        typed = getattr(lib, name)
+        fn = type(typed)((name, lib))
+        fn.argtypes = [ctypes.c_char_p] + typed.argtypes[1:]
+        fn.restype = typed.restype
+        _paged_fn[name] = fn
+    return fn
 
-    def __init__(self, first, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream):
-        torch = self.torch = _torch()
-        int32 = torch.int32
-        _check(first.is_cuda, "tensors must be CUDA tensors")
-        dev = self.device = first.device
-        p = self.params = SdpaPagedParams()
-        _check(k_pages.dim() == 4 and k_pages.device == dev and k_pages.stride(3) == 1,
-               "k_pages must be [pages, kv heads, page_size, D] on the same device with a "
-               "contiguous last dimension")
-        p.num_pages, p.num_kv_heads, p.page_size, p.head_dim = shape = k_pages.shape
-        p.k_stride[:] = k_pages.stride()[:3]
-        if v_pages is not None:
-            _check(v_pages.shape == shape and v_pages.device == dev and v_pages.stride(3) == 1,
-                   "v_pages must have k_pages' shape and device and a contiguous last dimension")
-            _check(v_pages.dtype == k_pages.dtype, "k_pages and v_pages must share a dtype",
-                   TypeError)
-            p.v_stride[:] = v_pages.stride()[:3]
-        p.dtype = dtype_code(k_pages.dtype)
-        B = p.num_seqs = seq_lens_kv.numel()
-        _check(seq_lens_kv.dtype == int32 and seq_lens_kv.device == dev
-               and seq_lens_kv.is_contiguous(),
-               "seq_lens_kv must be a contiguous int32 CUDA tensor", TypeError)
-        _check(page_table.dtype == int32 and page_table.device == dev,
-               "page_table must be an int32 CUDA tensor", TypeError)
-        _check(page_table.dim() == 2 and page_table.shape[0] == B
-               and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-               "page_table must be [sequences, pages] with contiguous rows")
-        p.max_pages = page_table.shape[1]
-        p.page_table = page_table.data_ptr()
-        p.page_table_stride = page_table.stride(0)
-        p.seq_lens_kv = seq_lens_kv.data_ptr()
-        if cu_seqlens_q is not None:
-            _check(cu_seqlens_q.dtype == int32 and cu_seqlens_q.device == dev
-                   and cu_seqlens_q.is_contiguous() and cu_seqlens_q.numel() == B + 1,
-                   "cu_seqlens_q must be a contiguous int32 CUDA tensor of sequences + 1 "
-                   "elements", TypeError)
-            p.cu_seqlens_q = cu_seqlens_q.data_ptr()
-        p.scale = 1.0
-        self.stream = stream
 
-    def queries(self, q, scale, causal, sinks=None):
-        p = self.params
-        _check(q.dim() == 3 and q.shape[2] == p.head_dim and q.stride(2) == 1,
-               "q must be [tokens, heads, D] with a contiguous last dimension")
-        _check(dtype_code(q.dtype) == p.dtype, "q and the cache must share a dtype", TypeError)
-        p.num_tokens, p.num_q_heads = q.shape[:2]
-        p.q_stride[:] = q.stride()[:2]
-        p.scale = 1.0 / math.sqrt(p.head_dim) if scale is None else scale
-        p.causal = 1 if causal else 0
-        if sinks is not None:
-            _check(sinks.dtype == self.torch.float32 and sinks.device == self.device
-                   and sinks.numel() == q.shape[1] and sinks.is_contiguous(),
-                   "sinks must be a contiguous float32 CUDA tensor with Hq elements", TypeError)
-            p.sinks = sinks.data_ptr()
+def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
+    """Checks of what the paged calls share.  Returns the fields of
+    SdpaPagedParams that describe the cache: (kv heads, D, dtype code, pages,
+    page size), the batch's fields, and the strides of k and v."""
+    torch = _torch()
+    int32 = torch.int32
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if k_pages.dim() != 4 or k_pages.get_device() != dev or k_pages.stride(3) != 1:
+        raise ValueError("k_pages must be [pages, kv heads, page_size, D] on the same device "
+                         "with a contiguous last dimension")
+    shape = k_pages.shape
+    ks = vs = k_pages.stride()
+    if v_pages is not None:
+        vs = v_pages.stride()
+        if v_pages.shape != shape or v_pages.get_device() != dev or vs[3] != 1:
+            raise ValueError("v_pages must have k_pages' shape and device and a contiguous last "
+                             "dimension")
+        if v_pages.dtype is not k_pages.dtype:
+            raise TypeError("k_pages and v_pages must share a dtype")
+    B = seq_lens_kv.numel()
+    if (seq_lens_kv.dtype is not int32 or seq_lens_kv.get_device() != dev
+            or not seq_lens_kv.is_contiguous()):
+        raise TypeError("seq_lens_kv must be a contiguous int32 CUDA tensor")
+    if page_table.dtype is not int32 or page_table.get_device() != dev:
+        raise TypeError("page_table must be an int32 CUDA tensor")
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] != B or (ts[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [sequences, pages] with contiguous rows")
+    cu = 0
+    if cu_seqlens_q is not None:
+        if (cu_seqlens_q.dtype is not int32 or cu_seqlens_q.get_device() != dev
+                or cu_seqlens_q.numel() != B + 1 or not cu_seqlens_q.is_contiguous()):
+            raise TypeError("cu_seqlens_q must be a contiguous int32 CUDA tensor of sequences + "
+                            "1 elements")
+        cu = cu_seqlens_q.data_ptr()
+    pages, heads, page, D = shape
+    return (heads, D, dtype_code(k_pages.dtype), pages, page, B, ts[1], page_table.data_ptr(),
+            page_table.stride(0), cu, seq_lens_kv.data_ptr(), ks, vs)
 
-    def lse_ptr(self, lse):
-        _check(lse.dtype == self.torch.float32 and lse.device == self.device
-               and tuple(lse.shape) == (self.params.num_tokens, self.params.num_q_heads)
-               and lse.is_contiguous(), "lse must be a contiguous float32 [tokens, Hq] tensor")
-        return lse.data_ptr()
 
-    def scores(self, scores, what="scores"):
-        p = self.params
-        _check(scores.dtype == self.torch.float32 and scores.device == self.device
-               and scores.dim() == 3 and tuple(scores.shape[:2]) == (p.num_seqs, p.num_kv_heads)
-               and (scores.shape[2] <= 1 or scores.stride(2) == 1),
-               "%s must be a float32 CUDA tensor [sequences, kv heads, positions] with "
-               "contiguous rows" % what)
-        return (ctypes.c_int64 * 2)(*scores.stride()[:2])
+def _paged_pack(c, T, hq, scale, causal, sinks, qs, os):
+    heads, D, dt, pages, page, B, cols, table, tstride, cu, lens, ks, vs = c
+    return _PAGED.pack(B, T, hq, heads, D, dt, scale, causal, pages, page, cols, 0, table,
+                       tstride, cu, lens, sinks, qs[0], qs[1], os[0], os[1], ks[0], ks[1], ks[2],
+                       vs[0], vs[1], vs[2])
 
-    def run(self, make, call):
-        """make(): allocations, on the call's stream; call(lib, stream)."""
-        torch, dev = self.torch, self.device
-        if dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return self.run(make, call)
-        if self.stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
-            made = make()
-        else:  # a raw stream handle: what is allocated here belongs to that stream
-            stream = self.stream
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-                made = make()
-        st = call(load_library(), made, stream)
-        if st != 0:
-            raise SdpaError(st, sdpa_status_string(st))
-        return made
 
-    def workspace(self, workspace):
-        """A workspace of the call's own: calls on other streams, and graphs
-        captured from it, share none."""
-        if workspace is None:
-            n = load_library().sdpa_paged_workspace_size(ctypes.byref(self.params))
-            return self.torch.empty(n, dtype=self.torch.uint8, device=self.device)
-        _check(workspace.device == self.device and workspace.is_contiguous(),
-               "workspace must be a contiguous CUDA tensor on the same device")
-        return workspace
+def _paged_queries(q, c, dev):
+    if q.dim() != 3 or q.shape[2] != c[1] or q.stride(2) != 1:
+        raise ValueError("q must be [tokens, heads, D] with a contiguous last dimension")
+    if dtype_code(q.dtype) != c[2]:
+        raise TypeError("q and the cache must share a dtype")
+
+
+def _check_lse(lse, q, dev):
+    if (lse.dtype is not _torch().float32 or lse.get_device() != dev
+            or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [tokens, Hq] CUDA tensor")
+
+
+def _check_scores(scores, c, dev, what="scores"):
+    s = scores.shape
+    if (scores.dtype is not _torch().float32 or scores.get_device() != dev or len(s) != 3
+            or s[0] != c[5] or s[1] != c[0] or (s[2] > 1 and scores.stride(2) != 1)):
+        raise ValueError("%s must be a float32 CUDA tensor [sequences, kv heads, positions] with "
+                         "contiguous rows" % what)
+
+
+def _paged_workspace(workspace, dev, device, D, stream, own_stream):
+    """(address, bytes) of the given workspace, or of one that the binding
+    keeps for this thread and the current torch stream, whose calls follow one
+    another (those of two threads may interleave their kernels).  A call
+    under graph capture, or on a raw stream handle, gets one of its own: a
+    graph's belongs to the graph's pool, so that graphs share none."""
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    torch = _torch()
+    keep = own_stream and not torch._C._cuda_isCurrentStreamCapturing()
+    key = (dev, stream, D, threading.get_ident())
+    if keep:
+        kept = _paged_ws.get(key)
+        if kept is not None:
+            return kept
+    p = SdpaPagedParams()
+    p.num_seqs = p.num_tokens = p.num_q_heads = p.num_kv_heads = p.page_size = 1
+    p.head_dim, p.scale = D, 1.0
+    ws = torch.empty(max(sdpa_paged_workspace_size(p), 16), dtype=torch.uint8, device=device)
+    made = (ws, ws.data_ptr(), ws.numel())
+    if keep:
+        _paged_ws[key] = made
+    return made
+
+
+def _on(dev, stream, call):
+    """call(raw stream) with `dev` current, on the current stream or, where a
+    raw handle is given, with that stream current (what the call allocates
+    then belongs to it)."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _on(dev, stream, call)
+    if stream is None:
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        return call(stream)
+
+
+def _paged_status(st):
+    if st != 0:
+        raise SdpaError(st, sdpa_status_string(st))
 
 
 def sdpa_paged_workspace_size(params) -> int:
@@ -644,20 +682,19 @@ def sdpa_paged_write(k, v, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens
     int32 [B + 1], sequence b's tokens are rows cu[b] .. cu[b + 1]; None: one
     token a sequence.  Rows past the last sequence are not written.
     """
-    c = _PagedCall(k, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream)
-    p = c.params
-    for t in (k, v):
-        _check(t.dim() == 3 and tuple(t.shape[1:]) == (p.num_kv_heads, p.head_dim)
-               and t.stride(2) == 1 and t.device == c.device and t.shape[0] == k.shape[0],
-               "k and v must be [tokens, kv heads, D] on the same device with a contiguous last "
-               "dimension")
-        _check(t.dtype == k_pages.dtype, "k, v and the cache must share a dtype", TypeError)
-    p.num_tokens = k.shape[0]
-    st2 = ctypes.c_int64 * 2
-    ks, vs = st2(*k.stride()[:2]), st2(*v.stride()[:2])
-    c.run(lambda: None, lambda lib, _, stream: lib.sdpa_paged_write(
-        ctypes.byref(p), k.data_ptr(), v.data_ptr(), ks, vs, k_pages.data_ptr(),
-        v_pages.data_ptr(), stream))
+    dev = k.get_device()
+    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)
+    shape, kn, vn = k.shape, k.stride(), v.stride()
+    if (len(shape) != 3 or shape[1] != c[0] or shape[2] != c[1] or v.shape != shape
+            or kn[2] != 1 or vn[2] != 1 or v.get_device() != dev):
+        raise ValueError("k and v must be [tokens, kv heads, D] on the same device with a "
+                         "contiguous last dimension")
+    if k.dtype is not k_pages.dtype or v.dtype is not k_pages.dtype:
+        raise TypeError("k, v and the cache must share a dtype")
+    p = _paged_pack(c, shape[0], 0, 1.0, 1, 0, (0, 0), (0, 0))
+    _paged_status(_on(dev, stream, lambda s: _paged_call("sdpa_paged_write")(
+        p, k.data_ptr(), v.data_ptr(), _STRIDE2(kn[0], kn[1]), _STRIDE2(vn[0], vn[1]),
+        k_pages.data_ptr(), v_pages.data_ptr(), s)))
 
 
 def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q=None,
@@ -674,32 +711,34 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_
     sdpa_paged_workspace_size bytes (one is allocated otherwise).  float32,
     float16, bfloat16; D 64 or 128.  Returns (out, lse) or out.
     """
-    c = _PagedCall(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, stream)
-    c.queries(q, scale, causal, sinks)
-    p, torch = c.params, c.torch
-    if out is not None:
-        _check(out.shape == q.shape and out.dtype == q.dtype and out.device == c.device
-               and out.stride(2) == 1, "out must be like q with a contiguous last dimension")
+    torch = _torch()
+    dev = q.get_device()
+    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)
+    _paged_queries(q, c, dev)
+    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.get_device() != dev
+                              or sinks.numel() != q.shape[1] or not sinks.is_contiguous()):
+        raise TypeError("sinks must be a contiguous float32 CUDA tensor with Hq elements")
+    if out is not None and (out.shape != q.shape or out.dtype is not q.dtype
+                            or out.get_device() != dev or out.stride(2) != 1):
+        raise ValueError("out must be like q with a contiguous last dimension")
     if lse is not None:
-        c.lse_ptr(lse)
+        _check_lse(lse, q, dev)
 
-    def make():
+    def call(s):
         o = torch.empty_like(q) if out is None else out
         ls = lse
         if ls is None and return_lse:
-            ls = torch.empty(q.shape[:2], dtype=torch.float32, device=c.device)
-        return o, ls, c.workspace(workspace)
+            ls = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        ws, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s, stream is None)
+        p = _paged_pack(c, q.shape[0], q.shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
+                        1 if causal else 0, 0 if sinks is None else sinks.data_ptr(), q.stride(),
+                        o.stride())
+        _paged_status(_paged_call("sdpa_paged_forward")(
+            p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(),
+            None if ls is None else ls.data_ptr(), wp, wn, s))
+        return (o, ls) if return_lse else o
 
-    def call(lib, made, stream):
-        o, ls, ws = made
-        p.o_stride[:] = o.stride()[:2]
-        return lib.sdpa_paged_forward(ctypes.byref(p), q.data_ptr(), k_pages.data_ptr(),
-                                      v_pages.data_ptr(), o.data_ptr(),
-                                      None if ls is None else ls.data_ptr(), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), stream)
-
-    o, ls, _ = c.run(make, call)
-    return (o, ls) if return_lse else o
+    return _on(dev, stream, call)
 
 
 def sdpa_paged_scores(q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqlens_q=None,
@@ -712,13 +751,21 @@ def sdpa_paged_scores(q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqle
     q and the cache arguments as given to sdpa_paged_forward, lse its second
     result.
     """
-    c = _PagedCall(q, k_pages, None, page_table, seq_lens_kv, cu_seqlens_q, stream)
-    c.queries(q, scale, causal)
-    ss = c.scores(scores)
-    lp = c.lse_ptr(lse)
-    c.run(lambda: c.workspace(workspace), lambda lib, ws, stream: lib.sdpa_paged_scores(
-        ctypes.byref(c.params), q.data_ptr(), k_pages.data_ptr(), lp, scores.data_ptr(), ss,
-        scores.shape[2], ws.data_ptr(), ws.numel() * ws.element_size(), stream))
+    dev = q.get_device()
+    c = _paged_cache(dev, k_pages, None, page_table, seq_lens_kv, cu_seqlens_q)
+    _paged_queries(q, c, dev)
+    _check_scores(scores, c, dev)
+    _check_lse(lse, q, dev)
+    p = _paged_pack(c, q.shape[0], q.shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
+                    1 if causal else 0, 0, q.stride(), (0, 0))
+
+    def call(s):
+        ws, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s, stream is None)
+        return _paged_call("sdpa_paged_scores")(
+            p, q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(), scores.data_ptr(),
+            _STRIDE2(*scores.stride()[:2]), scores.shape[2], wp, wn, s)
+
+    _paged_status(_on(dev, stream, call))
     return scores
 
 
@@ -736,34 +783,36 @@ def sdpa_paged_evict(k_pages, v_pages, scores, page_table, seq_lens_kv, keep, re
     their new places (0 behind them).  scores_out and seq_lens_out may be
     `scores` and `seq_lens_kv` themselves.
     """
-    c = _PagedCall(k_pages, k_pages, v_pages, page_table, seq_lens_kv, None, stream)
-    p, torch = c.params, c.torch
-    ss = c.scores(scores)
-    keep = int(keep)
-    _check(keep >= 1 and recent >= 0, "keep must be at least 1 and recent at least 0")
+    torch = _torch()
+    dev = k_pages.get_device()
+    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, None)
+    _check_scores(scores, c, dev)
+    keep, recent, B = int(keep), int(recent), c[5]
+    if keep < 1 or recent < 0:
+        raise ValueError("keep must be at least 1 and recent at least 0")
     if scores_out is not None:
-        _check(scores_out.shape == scores.shape and scores_out.stride() == scores.stride(),
-               "scores_out must have the shape and strides of scores")
-        c.scores(scores_out, "scores_out")
-    for t, n, what in ((seq_lens_out, p.num_seqs, "seq_lens_out"),
-                       (kept, p.num_seqs * p.num_kv_heads * keep, "kept")):
-        _check(t is None or (t.dtype == torch.int32 and t.device == c.device
-                             and t.is_contiguous() and t.numel() == n),
-               "%s must be a contiguous int32 CUDA tensor of %d elements" % (what, n))
+        _check_scores(scores_out, c, dev, "scores_out")
+        if scores_out.shape != scores.shape or scores_out.stride() != scores.stride():
+            raise ValueError("scores_out must have the shape and strides of scores")
+    for t, n, what in ((seq_lens_out, B, "seq_lens_out"), (kept, B * c[0] * keep, "kept")):
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev
+                              or t.numel() != n or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous int32 CUDA tensor of %d elements" % (what, n))
+    p = _paged_pack(c, 0, 0, 1.0, 1, 0, (0, 0), (0, 0))
 
-    def make():
+    def call(s):
         kp = kept
         if kp is None:
-            kp = torch.empty((p.num_seqs, p.num_kv_heads, keep), dtype=torch.int32,
-                             device=c.device)
+            kp = torch.empty((B, c[0], keep), dtype=torch.int32, device=k_pages.device)
         sl = torch.empty_like(seq_lens_kv) if seq_lens_out is None else seq_lens_out
-        so = scores_out
-        if so is None:
+        so = torch.empty_like(scores) if scores_out is None else scores_out
+        if so.stride() != scores.stride():
             so = torch.empty_strided(scores.shape, scores.stride(), dtype=torch.float32,
-                                     device=c.device)
+                                     device=scores.device)
+        _paged_status(_paged_call("sdpa_paged_evict")(
+            p, keep, recent, k_pages.data_ptr(), v_pages.data_ptr(), scores.data_ptr(),
+            so.data_ptr(), _STRIDE2(*scores.stride()[:2]), scores.shape[2], kp.data_ptr(),
+            sl.data_ptr(), s))
         return kp, sl, so
 
-    return c.run(make, lambda lib, m, stream: lib.sdpa_paged_evict(
-        ctypes.byref(p), keep, int(recent), k_pages.data_ptr(), v_pages.data_ptr(),
-        scores.data_ptr(), m[2].data_ptr(), ss, scores.shape[2], m[0].data_ptr(),
-        m[1].data_ptr(), stream))
+    return _on(dev, stream, call)

@@ -59,6 +59,8 @@ sdpa_status_t launch_decode_tc128(const sdpa_params_t& p, const DecodePlan& plan
 // Device status word of the current device (nullptr if there is no device)
 // and the current bound on device-side waits; both owned by sdpa_api.cu.
 int* status_word_current_device();
+// The same with the SM count (false: no device).
+bool current_device(int** status, int* num_sms);
 uint64_t current_wait_limit_ns();
 // Current value of a test hook (sdpa_debug_set_option; sdpa_debug_option_t).
 int debug_option(int option);

@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 #include "sdpa.h"
 
 namespace gb300 {
@@ -321,6 +322,18 @@ __device__ __forceinline__ int pieces_of(const Unit& u, const Share& sh) {
   return static_cast<int>((u.pos + u.steps - 1) / sh.size - u.pos / sh.size) + 1;
 }
 
+#ifdef __CUDACC__
+// One copy of box_rows rows of a cache block (encode_row_blocks).
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                         int block) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(row >> 3), "r"(block)
+      : "memory");
+}
+#endif
+
 // Page of position p, or -1 (and the status word set) where the table names
 // none of the cache's.
 __device__ __forceinline__ int page_of(const Args& a, int b, int p) {
@@ -356,6 +369,32 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
                                  int* lens_out, cudaStream_t stream);
 
 namespace paged {
+// The tensor-core kernels see a cache as blocks of page_size rows, block (page,
+// head) at unit * (page * page_mul + head * head_mul) elements, the unit
+// being the greatest common divisor of the two strides.  `blocks` is one past
+// the last; a copy of that block reads zero (a bad page).
+struct CacheBlocks {
+  int page_mul, head_mul, blocks;
+};
+inline bool cache_blocks(const long long (&st)[3], int pages, int heads, CacheBlocks* c,
+                         long long* unit) {
+  long long x = pages > 1 ? st[0] : 0, y = heads > 1 ? st[1] : 0;
+  long long u = x, v = y;
+  while (v) {
+    const long long t = u % v;
+    u = v;
+    v = t;
+  }
+  if (u == 0) u = 64;  // one block
+  const long long last = (pages - 1) * (x / u) + (heads - 1) * (y / u);
+  if (x / u > 0x7fffffffLL || y / u > 0x7fffffffLL || last >= 0x7fffffffLL) return false;
+  c->page_mul = static_cast<int>(x / u);
+  c->head_mul = static_cast<int>(y / u);
+  c->blocks = static_cast<int>(last) + 1;
+  *unit = u;
+  return true;
+}
+
 // Heads per tile and tokens per tile of `rows` query rows.
 inline void fit_rows(Args& a, int rows) {
   a.nsub = (a.G + rows - 1) / rows;

@@ -77,9 +77,9 @@ bool cache_overlaps(const sdpa_paged_params_t& p) {
 }
 
 int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+  int* status = nullptr;
+  int sms = 0;
+  if (!current_device(&status, &sms)) {
     cudaGetLastError();  // no device: plan for a full GB300
     return 152;
   }
@@ -131,11 +131,9 @@ size_t workspace(const sdpa_paged_params_t& p, int sms) {
 }
 
 bool make_env(LaunchEnv* env, void* stream) {
-  env->status = status_word_current_device();
   env->wait_limit_ns = current_wait_limit_ns();
-  env->num_sms = device_sms();
   env->stream = static_cast<cudaStream_t>(stream);
-  return env->status != nullptr;
+  return current_device(&env->status, &env->num_sms);
 }
 
 // What sdpa_paged_forward and sdpa_paged_scores share before their launch.
@@ -166,10 +164,18 @@ bool tc_fits(const sdpa_paged_params_t& p, bool values) {
   const int64_t qn[2] = {p.num_tokens, p.num_q_heads};
   for (int i = 0; i < 3; ++i)
     for (const int64_t* s : {p.k_stride, p.v_stride})
-      if ((s == p.k_stride || values) && kv[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t(1) << 38)))
+      if ((s == p.k_stride || values) && kv[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t(1) << 35)))
         return false;
+  // the (page, head) blocks are numbered in 31 bits
+  paged::CacheBlocks c;
+  long long unit;
+  const long long ks[3] = {p.k_stride[0], p.k_stride[1], p.k_stride[2]};
+  const long long vs[3] = {p.v_stride[0], p.v_stride[1], p.v_stride[2]};
+  if (!paged::cache_blocks(ks, p.num_pages, p.num_kv_heads, &c, &unit) ||
+      (values && !paged::cache_blocks(vs, p.num_pages, p.num_kv_heads, &c, &unit)))
+    return false;
   for (int i = 0; i < 2; ++i)
-    if (qn[i] > 1 && (p.q_stride[i] <= 0 || p.q_stride[i] >= (int64_t(1) << 38))) return false;
+    if (qn[i] > 1 && (p.q_stride[i] <= 0 || p.q_stride[i] >= (int64_t(1) << 35))) return false;
   return true;
 }
 

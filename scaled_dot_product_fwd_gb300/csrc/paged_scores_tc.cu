@@ -96,7 +96,7 @@ template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     paged_scores_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK, const Args a,
-                           const int box_rows) {
+                           const int box_rows, const CacheBlocks kb) {
   using C = ScCfg<D, R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   if (warp == kLoad) {
     // ------------------------------------------------------------ producer
     const int nbox = 128 / box_rows;
-    const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * 128u;
+    const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * C::CB * 128u;
     bool ok = true;
     int ku = 0, g = 0;  // units, steps
     while (ok && next()) {
@@ -189,22 +189,19 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
       if (lane < 2 * nbox && key < u.s.nk) {
         page = page_of(a, u.b, key);
         row = key % a.page_size;
-        if (page < 0) page = a.num_pages;  // reads as zero
+        if (page < 0) page = -2;  // the table names none: reads as zero
       }
       const int boxes = min(2 * nbox, (u.s.nk - u.j * kUnitKeys + box_rows - 1) / box_rows);
       const int ks = ku % C::NK;
       if (lane == 0) {
         if (ku >= C::NK) ok = mbar_wait(&k_empty[ks], ((ku / C::NK) - 1) & 1, wc);
-        if (ok) mbar_arrive_expect_tx(&k_full[ks], C::CB * box_bytes * boxes);
+        if (ok) mbar_arrive_expect_tx(&k_full[ks], box_bytes * boxes);
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
-      if (page >= 0) {
-        uint8_t* dst = sK + (ks * 2 + lane / nbox) * C::TILE + (lane % nbox) * box_bytes;
-#pragma unroll
-        for (int cb = 0; cb < C::CB; ++cb)
-          tma_load_4d(dst + cb * 128 * 128, &tmK, &k_full[ks], cb * 64, row, u.h, page);
-      }
+      if (page != -1)
+        load_box(sK + ks * 2 * C::TILE + lane * box_bytes, &tmK, &k_full[ks], row,
+                 page < 0 ? kb.blocks : page * kb.page_mul + u.h * kb.head_mul);
       ++ku;
       k_fills = ku;
       if (lane == 0) {
@@ -226,12 +223,14 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   } else if (warp == kMma) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = idesc_f16(BF16, 128, R, false, false);
-    const uint64_t k_desc = sdesc(smem_addr(sK), 16, 1024, kSwizzle128B);
+    // K tiles: 8-key groups CB * 1024 bytes apart, 64-column blocks 1024
+    const uint64_t k_desc = sdesc(smem_addr(sK), 16, C::CB * 1024, kSwizzle128B);
     const uint64_t q_desc = sdesc(smem_addr(sQ), 16, 1024, kSwizzle128B);
-    const uint32_t hi = static_cast<uint32_t>(k_desc >> 32);
+    const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32);
+    const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32);
     const uint32_t k_lo = static_cast<uint32_t>(k_desc);
     const uint32_t q_lo = static_cast<uint32_t>(q_desc);
-    auto desc = [&](uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+    auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
     int ku = 0, g = 0;
     int uses[4] = {0, 0, 0, 0};  // of each (tile, buffer)
     while (next()) {
@@ -252,9 +251,9 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           const uint32_t qd = q_lo + static_cast<uint32_t>(((g % C::NQS) * C::QTILE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t ko = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+            const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
             const uint32_t qo = ((kk >> 2) * (R * 128) + (kk & 3) * 32) >> 4;
-            mma_f16_ss_elect(tmem + buf * 128, desc(kd + ko), desc(qd + qo), idS,
+            mma_f16_ss_elect(tmem + buf * 128, desc(k_hi, kd + ko), desc(q_hi, qd + qo), idS,
                              kk > 0 ? 1u : 0u, 1u);
           }
           mma_commit_elect(&s_full[buf], 1u);
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
 
 template <int D, bool BF16, int R>
 sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                        int box_rows, const LaunchEnv& env) {
+                        int box_rows, const CacheBlocks& kb, const LaunchEnv& env) {
   using C = ScCfg<D, R>;
   auto kern = paged_scores_tc_kernel<D, BF16, R>;
   static std::atomic<uint64_t> ready{0};  // devices on which the attribute is set
@@ -472,7 +471,7 @@ sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap&
   cfg.stream = env.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, a, box_rows) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, a, box_rows, kb) != cudaSuccess) return SDPA_ERR_CUDA;
   return launch_paged_scores_merge(a, kUnitKeys, env.stream);
 }
 
@@ -486,19 +485,23 @@ sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   int box_rows = 128;  // gcd(page_size, 128)
   while (a.page_size % box_rows) box_rows >>= 1;
+  CacheBlocks kb;
+  long long ku;
+  if (!cache_blocks(a.ks, a.num_pages, a.Hkv, &kb, &ku))
+    return SDPA_ERR_UNSUPPORTED;  // (the caller has checked)
   CUtensorMap tq, tk;
   // a stride of a dimension of one element is never followed: any valid one
   auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
   if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
                            static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
-      !encode_tiled_4d(&tk, dt, a.k, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
-                       st(a.ks[2], a.page_size), st(a.ks[1], a.Hkv), st(a.ks[0], a.num_pages)))
+      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, box_rows,
+                         st(a.ks[2], a.page_size), ku))
     return SDPA_ERR_CUDA;
   if (few)
-    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, box_rows, env)
-                : launch_sc<D, false, 16>(a, tq, tk, box_rows, env);
-  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, box_rows, env)
-              : launch_sc<D, false, 128>(a, tq, tk, box_rows, env);
+    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, box_rows, kb, env)
+                : launch_sc<D, false, 16>(a, tq, tk, box_rows, kb, env);
+  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, box_rows, kb, env)
+              : launch_sc<D, false, 128>(a, tq, tk, box_rows, kb, env);
 }
 
 }  // namespace

@@ -22,7 +22,10 @@
 //          HBM: few rows are live, and warps without one do no arithmetic.
 //
 // Key tiles are 128 keys in boxes of R = gcd(page_size, 128) rows, each
-// inside a page; one lane of the producer warp looks up and loads each box.
+// inside a page; one lane of the producer warp looks up and loads each box, in
+// one copy for both 64-column halves of its rows (a tile lies as [16 groups
+// of 8 keys][D / 64][8][64], which both operand descriptors take).  With a
+// copy per half, 16-row pages cost 40 % more: a copy has a price of its own.
 // Boxes past the sequence's length are not loaded.  What the last tile holds
 // behind it (a page's rows of no sequence yet: anything, NaN included) is kept
 // out of the results: such scores are replaced by -inf, the value product
@@ -49,10 +52,12 @@ template <int D, int NT>
 struct TcCfg {
   static constexpr int CB = D / 64;        // 128-byte column blocks of a row
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NS = NT == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 6 : 3);  // stages
-  static constexpr int STAGE = 2 * TILE;   // K_j, V_j
+  // Ring of K and V tiles (a slot each), in the order of their use: K_0 ..
+  // K_LA-1, then V_j, K_j+LA for every j: S runs LA key tiles ahead of P V.
+  static constexpr int NS = NT == 2 ? (D == 64 ? 8 : 4) : (D == 64 ? 12 : 6);
+  static constexpr int LA = NT == 2 ? 1 : 2;
   static constexpr int RING_OFF = NT * TILE;
-  static constexpr int BAR_OFF = RING_OFF + NS * STAGE;
+  static constexpr int BAR_OFF = RING_OFF + NS * TILE;
   // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain
   static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
@@ -81,6 +86,16 @@ struct TileGeo {
   int n[2];     // key tiles of each query tile, from s0
   int nmax;     // key tiles loaded
   int nk;
+  // ring positions of V_j and K_j, counted from the unit's first slot
+  template <int LA>
+  __device__ __forceinline__ int v_pos(int j) const {
+    const int ahead = min(LA, nmax);
+    return ahead + j + min(j, nmax - ahead);
+  }
+  template <int LA>
+  __device__ __forceinline__ int k_pos(int j) const {
+    return j < LA ? j : v_pos<LA>(j - LA) + 1;
+  }
 };
 template <int NT>
 __device__ __forceinline__ TileGeo tile_geo(const Args& a, const Unit& u) {
@@ -102,7 +117,8 @@ template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const Args a, const int box_rows) {
+                    const __grid_constant__ CUtensorMap tmV, const Args a, const int box_rows,
+                    const CacheBlocks kb, const CacheBlocks vb) {
   using C = TcCfg<D, NT>;
   using E = Elem<BF16>;
   using T = typename E::T;
@@ -178,34 +194,54 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
     if (lane == 0) more = walk->next(a, *sh, heads, unit);
     return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
   };
-  int last_use[C::NS];  // producer: last fill of each stage (-1: none)
-#pragma unroll
-  for (int s = 0; s < C::NS; ++s) last_use[s] = -1;
-  int last_q = -1;
+  int fills = 0;    // producer: ring slots filled
+  int last_q = -1;  // and last unit whose Q it loaded
 
   if (warp >= C::SOFT_WARPS) {
     if constexpr (NT == 2) setmaxnreg_dec<kControlRegs>();
     if (warp == kLoad) {
       // ---------------------------------------------------------- producer
       const int nbox = 128 / box_rows;
-      const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * 128u;
-      int g = 0;
+      const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * C::CB * 128u;
+      int g = 0;  // ring slots filled
       bool ok = true;
       for (int it = 0; ok && next(); ++it) {
         const Unit u = *unit;
         const TileGeo tg = tile_geo<NT>(a, u);
         const int kvh = u.h / a.nsub, sub = u.h % a.nsub;
-        // page of this lane's box of key tile t (num_pages, which reads as
-        // zero, where the table names none; -1: past the length)
-        auto lookup = [&](int t, int* row) {
-          const int key = t * 128 + lane * box_rows;
-          if (lane >= nbox || key >= u.s.nk) return -1;
-          const int page = page_of(a, u.b, key);
-          *row = key % a.page_size;
-          return page < 0 ? a.num_pages : page;
+        // Page and row of this lane's box of key tile t (page -2: the table
+        // names none; -1: past the length).  The lookups run LA + 1 tiles
+        // ahead of their use.
+        struct Box {
+          int page, row;
         };
-        int row = 0;
-        int page = lookup(tg.s0, &row);
+        auto lookup = [&](int j) {
+          Box x{-1, 0};
+          const int key = (tg.s0 + j) * 128 + lane * box_rows;
+          if (j < tg.nmax && lane < nbox && key < u.s.nk) {
+            x.page = page_of(a, u.b, key);
+            x.row = key % a.page_size;
+            if (x.page < 0) x.page = -2;
+          }
+          return x;
+        };
+        auto load = [&](const CUtensorMap* map, const CacheBlocks& c, int j, const Box& x) {
+          const int s = g % C::NS, use = g / C::NS;
+          const int boxes = min(nbox, (u.s.nk - (tg.s0 + j) * 128 + box_rows - 1) / box_rows);
+          if (lane == 0) {
+            if (ok && use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, wc);
+            if (ok) mbar_arrive_expect_tx(&full[s], box_bytes * boxes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) return;
+          if (x.page != -1)
+            load_box(sRing + s * C::TILE + lane * box_bytes, map, &full[s], x.row,
+                     x.page < 0 ? c.blocks : x.page * c.page_mul + kvh * c.head_mul);
+          fills = ++g;
+        };
+        Box bx[C::LA + 1];  // boxes of tiles j .. j + LA
+#pragma unroll
+        for (int i = 0; i < C::LA; ++i) bx[i] = lookup(i);
         if (lane == 0) {
           if (it > 0) ok = mbar_wait(q_empty, (it - 1) & 1, wc);
           if (ok) {
@@ -217,68 +253,65 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
                             kvh * a.G + sub * a.gu, u.s.q0 + (u.j * NT + t) * a.w, 0);
           }
         }
-        for (int j = 0; j < tg.nmax; ++j, ++g) {
-          const int s = g % C::NS, use = g / C::NS;
-          const int boxes = min(nbox, (u.s.nk - (tg.s0 + j) * 128 + box_rows - 1) / box_rows);
-          if (lane == 0) {
-            if (ok && use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, wc);
-            if (ok) mbar_arrive_expect_tx(&full[s], 2u * C::CB * box_bytes * boxes);
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          if (page >= 0) {
-            uint8_t* dst = sRing + s * C::STAGE + lane * box_bytes;
-#pragma unroll
-            for (int cb = 0; cb < C::CB; ++cb)
-              tma_load_4d(dst + cb * 128 * 128, &tmK, &full[s], cb * 64, row, kvh, page);
-#pragma unroll
-            for (int cb = 0; cb < C::CB; ++cb)
-              tma_load_4d(dst + C::TILE + cb * 128 * 128, &tmV, &full[s], cb * 64, row, kvh,
-                          page);
-          }
-          last_use[s] = use;
-          if (j + 1 < tg.nmax) page = lookup(tg.s0 + j + 1, &row);
-        }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+#pragma unroll
+        for (int i = 0; i < C::LA; ++i)
+          if (ok && i < tg.nmax) load(&tmK, kb, i, bx[i]);
+        bx[C::LA] = lookup(C::LA);
+        for (int j = 0; ok && j < tg.nmax; ++j) {
+          const Box nx = lookup(j + C::LA + 1);
+          load(&tmV, vb, j, bx[0]);
+          if (ok && j + C::LA < tg.nmax) load(&tmK, kb, j + C::LA, bx[C::LA]);
+#pragma unroll
+          for (int i = 0; i < C::LA; ++i) bx[i] = bx[i + 1];
+          bx[C::LA] = nx;
+        }
       }
     } else if (warp == kMma) {
       // -------------------------------------------------------- MMA issuer
       constexpr uint32_t idS = idesc_f16(BF16, 128, 128, false, false);
       constexpr uint32_t idO = idesc_f16(BF16, 128, D, false, true);
       const uint64_t q_desc = sdesc(smem_addr(sQ), 16, 1024, kSwizzle128B);
-      const uint64_t k_desc = sdesc(smem_addr(sRing), 16, 1024, kSwizzle128B);
-      const uint64_t v_desc = sdesc(smem_addr(sRing) + C::TILE, 128 * 128, 1024, kSwizzle128B);
-      const uint32_t qk_hi = static_cast<uint32_t>(q_desc >> 32);
+      // K and V tiles: 8-key groups CB * 1024 bytes apart, 64-column blocks
+      // 1024
+      const uint64_t k_desc = sdesc(smem_addr(sRing), 16, C::CB * 1024, kSwizzle128B);
+      const uint64_t v_desc = sdesc(smem_addr(sRing), 1024, C::CB * 1024, kSwizzle128B);
+      const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32);
+      const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32);
       const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
       const uint32_t q_lo = static_cast<uint32_t>(q_desc);
       const uint32_t k_lo = static_cast<uint32_t>(k_desc);
       const uint32_t v_lo = static_cast<uint32_t>(v_desc);
       auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
-      // S (columns of slot i) = Q_t K^T of the g-th loaded tile
-      auto issue_s = [&](int t, int i, int g) {
+      // S (columns of slot i) = Q_t K^T, K in ring slot s
+      auto issue_s = [&](int t, int i, int s) {
         const uint32_t qd = q_lo + static_cast<uint32_t>((t * C::TILE) >> 4);
-        const uint32_t kd = k_lo + static_cast<uint32_t>(((g % C::NS) * C::STAGE) >> 4);
+        const uint32_t kd = k_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-          mma_f16_ss_elect(tmem + C::s_col(i), desc(qk_hi, qd + off), desc(qk_hi, kd + off), idS,
+          const uint32_t qo = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+          const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+          mma_f16_ss_elect(tmem + C::s_col(i), desc(q_hi, qd + qo), desc(k_hi, kd + ko), idS,
                            kk > 0 ? 1u : 0u, 1u);
         }
       };
-      // O_t += P V of the g-th loaded tile, P in slot i, keys in groups of 16
-      auto issue_pv = [&](int t, int i, int g, bool first, int groups) {
-        const uint32_t vd = v_lo + static_cast<uint32_t>(((g % C::NS) * C::STAGE) >> 4);
+      // O_t += P V, P in slot i, V in ring slot s, keys in groups of 16
+      auto issue_pv = [&](int t, int i, int s, bool first, int groups) {
+        const uint32_t vd = v_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_f16_ts_elect(tmem + C::o_col(t), tmem + C::s_col(i) + kk * 8,
-                           desc(v_hi, vd + ((kk * 16 * 128) >> 4)), idO,
+                           desc(v_hi, vd + ((kk * 2 * C::CB * 1024) >> 4)), idO,
                            (!first || kk > 0) ? 1u : 0u, kk < groups ? 1u : 0u);
       };
-      int g0 = 0;
+      int p0 = 0;  // ring slots of earlier units
+      int g0 = 0;  // key tiles of earlier units
       while (next()) {
         const TileGeo tg = tile_geo<NT>(a, *unit);
         auto groups = [&](int j) { return min(8, (tg.nk - (tg.s0 + j) * 128 + 15) >> 4); };
-        named_bar_sync(kKBar, 64);  // Q and the first stage have landed
+        auto kslot = [&](int j) { return (p0 + tg.k_pos<C::LA>(j)) % C::NS; };
+        auto vslot = [&](int j) { return (p0 + tg.v_pos<C::LA>(j)) % C::NS; };
+        named_bar_sync(kKBar, 64);  // Q and K_0 have landed
         tc_fence_after();
         if constexpr (NT == 2) {
 #pragma unroll
@@ -287,65 +320,73 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
             if (tg.n[t] == 0) {
               mma_commit_elect(&o_done[t], 1u);
             } else {
-              issue_s(t, t, g0);
+              issue_s(t, t, kslot(0));
               mma_commit_elect(&s_full[t], 1u);
             }
           }
+          if (tg.nmax > 0) mma_commit_elect(&empty[kslot(0)], 1u);
           if (tg.nmax <= 1) mma_commit_elect(q_empty, 1u);
           for (int j = 0; j < tg.nmax; ++j) {
             bool waited = false;
+            const int ks = kslot(j + 1), vs = vslot(j);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (t >= tg.nt || j >= tg.n[t]) continue;
               named_bar_sync(kPBar + t, 32 * 5);
+              if (!waited) {  // V_j and K_j+1 have landed
+                named_bar_sync(kKBar, 64);
+                waited = true;
+              }
               tc_fence_after();
-              issue_pv(t, t, g0 + j, j == 0, groups(j));
+              issue_pv(t, t, vs, j == 0, groups(j));
               if (j + 1 < tg.n[t]) {
-                if (!waited) {
-                  named_bar_sync(kKBar, 64);
-                  waited = true;
-                }
-                issue_s(t, t, g0 + j + 1);
+                issue_s(t, t, ks);
                 mma_commit_elect(&s_full[t], 1u);
               } else {
                 mma_commit_elect(&o_done[t], 1u);
               }
             }
+            // K_j+1 and V_j are free once these land (S_1,j+1 is the last
+            // of them, or the P V products where the unit ends)
+            if (j + 1 < tg.nmax) mma_commit_elect(&empty[ks], 1u);
             if (j == tg.nmax - 2) mma_commit_elect(q_empty, 1u);
-            mma_commit_elect(&empty[(g0 + j) % C::NS], 1u);
+            mma_commit_elect(&empty[vs], 1u);
           }
         } else {
           if (tg.nmax == 0) {
             mma_commit_elect(&o_done[0], 1u);
             mma_commit_elect(q_empty, 1u);
           } else {
-            issue_s(0, g0 & 1, g0);
+            issue_s(0, g0 & 1, kslot(0));
             mma_commit_elect(&s_full[g0 & 1], 1u);
+            mma_commit_elect(&empty[kslot(0)], 1u);
             if (tg.nmax > 1) {
               named_bar_sync(kKBar, 64);
               tc_fence_after();
-              issue_s(0, (g0 + 1) & 1, g0 + 1);
+              issue_s(0, (g0 + 1) & 1, kslot(1));
               mma_commit_elect(&s_full[(g0 + 1) & 1], 1u);
+              mma_commit_elect(&empty[kslot(1)], 1u);
             }
             if (tg.nmax <= 2) mma_commit_elect(q_empty, 1u);
             for (int j = 0; j < tg.nmax; ++j) {
-              const int g = g0 + j;
+              const int i = (g0 + j) & 1;
               named_bar_sync(kPBar, 32 * 5);
+              named_bar_sync(kKBar, 64);  // V_j and K_j+2 have landed
               tc_fence_after();
-              issue_pv(0, g & 1, g, j == 0, groups(j));
+              issue_pv(0, i, vslot(j), j == 0, groups(j));
               mma_commit_elect(pv_done, 1u);
-              mma_commit_elect(&empty[g % C::NS], 1u);
+              mma_commit_elect(&empty[vslot(j)], 1u);
               if (j + 2 < tg.nmax) {
-                named_bar_sync(kKBar, 64);
-                tc_fence_after();
-                issue_s(0, g & 1, g + 2);
-                mma_commit_elect(&s_full[g & 1], 1u);
+                issue_s(0, i, kslot(j + 2));
+                mma_commit_elect(&s_full[i], 1u);
+                mma_commit_elect(&empty[kslot(j + 2)], 1u);
                 if (j + 3 == tg.nmax) mma_commit_elect(q_empty, 1u);
               }
             }
             mma_commit_elect(&o_done[0], 1u);
           }
         }
+        p0 += 2 * tg.nmax;
         g0 += tg.nmax;
       }
       // every MMA issued by this warp completes before TMEM is freed
@@ -354,35 +395,46 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
       __syncwarp();
     } else if (warp == kHelp) {
       // ------------------------------------------------------ stage helper
-      // Waits for each stage, zeroes the last tile's value rows between the
-      // length and the end of its group of 16 keys, and passes the stage on
-      // (same count of meetings on both sides, also after a failed wait).
+      // Waits for the tiles that the MMA warp's next products read, zeroes
+      // the last tile's value rows between the length and the end of its
+      // group of 16 keys, and meets the MMA warp (the same number of times,
+      // also after a failed wait).
       bool ok = true;
-      int g0 = 0;
+      int p0 = 0;
+      auto landed = [&](int p) {
+        const int s = p % C::NS;
+        ok = ok && mbar_wait(&full[s], static_cast<uint32_t>((p / C::NS) & 1), wc);
+        return s;
+      };
       for (int it = 0; next(); ++it) {
         const TileGeo tg = tile_geo<NT>(a, *unit);
-        // one meeting for Q and the first stage, then one for every further stage
-        for (int j = 0; j < max(tg.nmax, 1); ++j) {
-          if (j == 0) ok = ok && mbar_wait(q_full, static_cast<uint32_t>(it & 1), wc);
-          if (j < tg.nmax) {
-            const int g = g0 + j;
-            ok = ok && mbar_wait(&full[g % C::NS], static_cast<uint32_t>((g / C::NS) & 1), wc);
-            const int keys = tg.nk - (tg.s0 + j) * 128;
-            if (keys < 128 && (keys & 15)) {
-              uint8_t* v = sRing + (g % C::NS) * C::STAGE + C::TILE;
-              const int rows = 16 - (keys & 15);
-              for (int i = lane; i < rows * C::CB * 8; i += 32) {
-                const int cb = i / (rows * 8), x = i % (rows * 8);
-                reinterpret_cast<uint4*>(v + cb * 128 * 128 + keys * 128)[x] =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_shared();
-            }
-            __syncwarp();
-          }
+        ok = ok && mbar_wait(q_full, static_cast<uint32_t>(it & 1), wc);
+        if (tg.nmax > 0) landed(p0);
+        __syncwarp();
+        named_bar_sync(kKBar, 64);
+        if (NT == 1 && tg.nmax > 1) {
+          landed(p0 + 1);
+          __syncwarp();
           named_bar_sync(kKBar, 64);
         }
-        g0 += tg.nmax;
+        for (int j = 0; j < tg.nmax; ++j) {
+          const int s = landed(p0 + tg.v_pos<C::LA>(j));
+          const int keys = tg.nk - (tg.s0 + j) * 128;
+          if (keys < 128 && (keys & 15)) {
+            uint8_t* v = sRing + s * C::TILE;
+            const int rows = 16 - (keys & 15);
+            for (int i = lane; i < rows * C::CB * 8; i += 32) {
+              const int key = keys + i / (C::CB * 8), cb = (i >> 3) % C::CB;
+              *reinterpret_cast<uint4*>(v + ((key >> 3) * C::CB + cb) * 1024 + (key & 7) * 128 +
+                                        (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_shared();
+          }
+          if (j + C::LA < tg.nmax) landed(p0 + tg.k_pos<C::LA>(j + C::LA));
+          __syncwarp();
+          named_bar_sync(kKBar, 64);
+        }
+        p0 += 2 * tg.nmax;
       }
     }
   } else {
@@ -565,14 +617,15 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
   if (warp == kLoad && lane == 0 && *abort_flag) {
     // a role gave up: every copy the producer issued lands before the CTA exits
     if (last_q >= 0) drain_wait(q_full, static_cast<uint32_t>(last_q & 1), kDrainNs);
-    for (int s = 0; s < C::NS; ++s)
-      if (last_use[s] >= 0) drain_wait(&full[s], last_use[s] & 1, kDrainNs);
+    for (int i = max(0, fills - C::NS); i < fills; ++i)
+      drain_wait(&full[i % C::NS], static_cast<uint32_t>((i / C::NS) & 1), kDrainNs);
   }
 }
 
 template <int D, bool BF16, int NT>
 sdpa_status_t launch_tc_impl(Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                             const CUtensorMap& tv, int box_rows, const LaunchEnv& env) {
+                             const CUtensorMap& tv, int box_rows, const CacheBlocks& kb,
+                             const CacheBlocks& vb, const LaunchEnv& env) {
   using C = TcCfg<D, NT>;
   auto kern = paged_tc_kernel<D, BF16, NT>;
   // The setmaxnreg split must fit the registers the kernel is launched with
@@ -602,7 +655,7 @@ sdpa_status_t launch_tc_impl(Args& a, const CUtensorMap& tq, const CUtensorMap& 
   cfg.stream = env.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, box_rows) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, box_rows, kb, vb) != cudaSuccess)
     return SDPA_ERR_CUDA;
   return launch_paged_merge(a, D, BF16 ? SDPA_BF16 : SDPA_F16, 128, NT, env.stream);
 }
@@ -615,23 +668,28 @@ sdpa_status_t launch_tc(Args a, int dtype, const LaunchEnv& env) {
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   int box_rows = 128;  // gcd(page_size, 128)
   while (a.page_size % box_rows) box_rows >>= 1;
+  CacheBlocks kb, vb;
+  long long ku, vu;
+  if (!cache_blocks(a.ks, a.num_pages, a.Hkv, &kb, &ku) ||
+      !cache_blocks(a.vs, a.num_pages, a.Hkv, &vb, &vu))
+    return SDPA_ERR_UNSUPPORTED;  // (the caller has checked)
   CUtensorMap tq, tk, tv;
   // A stride of a dimension of one element is never followed: any valid one.
   auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
   if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
                            static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
-      !encode_tiled_4d(&tk, dt, a.k, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
-                       st(a.ks[2], a.page_size), st(a.ks[1], a.Hkv), st(a.ks[0], a.num_pages)) ||
-      !encode_tiled_4d(&tv, dt, a.v, D, a.page_size, a.Hkv, a.num_pages, 2, 64, box_rows,
-                       st(a.vs[2], a.page_size), st(a.vs[1], a.Hkv), st(a.vs[0], a.num_pages)))
+      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, box_rows,
+                         st(a.ks[2], a.page_size), ku) ||
+      !encode_row_blocks(&tv, dt, a.v, D / 64, a.page_size, vb.blocks, box_rows,
+                         st(a.vs[2], a.page_size), vu))
     return SDPA_ERR_CUDA;
   // more than 128 rows a sequence and head unit on average: two tiles a unit
   const bool two = static_cast<long long>(a.T) * a.gu > 128LL * a.B;
   if (bf16)
-    return two ? launch_tc_impl<D, true, 2>(a, tq, tk, tv, box_rows, env)
-               : launch_tc_impl<D, true, 1>(a, tq, tk, tv, box_rows, env);
-  return two ? launch_tc_impl<D, false, 2>(a, tq, tk, tv, box_rows, env)
-             : launch_tc_impl<D, false, 1>(a, tq, tk, tv, box_rows, env);
+    return two ? launch_tc_impl<D, true, 2>(a, tq, tk, tv, box_rows, kb, vb, env)
+               : launch_tc_impl<D, true, 1>(a, tq, tk, tv, box_rows, kb, vb, env);
+  return two ? launch_tc_impl<D, false, 2>(a, tq, tk, tv, box_rows, kb, vb, env)
+             : launch_tc_impl<D, false, 1>(a, tq, tk, tv, box_rows, kb, vb, env);
 }
 
 }  // namespace

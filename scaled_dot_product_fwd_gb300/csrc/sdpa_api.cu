@@ -174,6 +174,8 @@ int* status_word_current_device() {
   return device_state(nullptr, &status, nullptr) ? status : nullptr;
 }
 
+bool current_device(int** status, int* num_sms) { return device_state(nullptr, status, num_sms); }
+
 uint64_t current_wait_limit_ns() { return g_wait_ns.load(); }
 int debug_option(int option) {
   return (option >= 0 && option < kDebugOptions) ? g_debug[option].load() : 0;

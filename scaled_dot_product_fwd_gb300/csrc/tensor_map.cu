@@ -74,4 +74,19 @@ bool encode_tiled_4d_box(CUtensorMap* map, CUtensorMapDataType dtype, const void
   return r == CUDA_SUCCESS;
 }
 
+bool encode_row_blocks(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                       uint64_t chunks, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                       uint64_t row_stride, uint64_t block_stride) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[5] = {64, 8, chunks, rows / 8, blocks};
+  const cuuint64_t strides[4] = {row_stride * 2, 128, row_stride * 16, block_stride * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(chunks), box_rows / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, dtype, 5, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace gb300

@@ -35,4 +35,15 @@ bool encode_tiled_4d_box(CUtensorMap* map, CUtensorMapDataType dtype, const void
                          uint32_t box_heads, uint64_t row_stride, uint64_t head_stride,
                          uint64_t batch_stride);
 
+// 5-D tiled map of 2-byte elements over rows that lie in blocks (pages): row r
+// of block b starts at element b * block_stride + r * row_stride, a row holds
+// 64 * chunks elements, and a block `rows` rows (a multiple of 8).
+// Coordinates {0, 0, 0, r / 8, b}; the box (box_rows rows, a multiple of 8,
+// 128-byte swizzle) lands as [box_rows / 8][chunks][8 rows][64 elements], so
+// that a row's 64-element chunks come in one copy.  Blocks at or past
+// `blocks` read as zero.
+bool encode_row_blocks(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                       uint64_t chunks, uint64_t rows, uint64_t blocks, uint32_t box_rows,
+                       uint64_t row_stride, uint64_t block_stride);
+
 }  // namespace gb300
