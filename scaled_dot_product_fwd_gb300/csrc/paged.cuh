@@ -30,6 +30,38 @@ namespace paged {
 constexpr int kStatusPageTable = 7;  // SDPA_ERR_PAGE_TABLE
 constexpr int kUnitCost = 2;         // fixed cost of a unit, in steps
 
+// Division of n < 2^31 by a number known on the host: a high product, an add
+// and a shift (Granlund and Montgomery, "Division by Invariant Integers using
+// Multiplication", 1994).  The kernels' single-token paths are chains of
+// index arithmetic, in which the divide instruction sequence is several times
+// as long.
+struct FastDiv {
+  uint32_t d, m;
+  int l;
+  __host__ __device__ __forceinline__ int div(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n);
+#ifdef __CUDA_ARCH__
+    return static_cast<int>((__umulhi(m, u) + u) >> l);
+#else
+    return static_cast<int>(((static_cast<uint64_t>(m) * u >> 32) + u) >> l);
+#endif
+  }
+  __host__ __device__ __forceinline__ int mod(int n) const {
+    return n - div(n) * static_cast<int>(d);
+  }
+  __host__ __device__ __forceinline__ int ceil(int n) const {
+    return div(n + static_cast<int>(d) - 1);
+  }
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f;
+  f.d = static_cast<uint32_t>(d);
+  f.l = 0;
+  while ((1u << f.l) < f.d) ++f.l;
+  f.m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.l) - f.d)) / f.d + 1);
+  return f;
+}
+
 struct Args {
   int B, T, Hq, Hkv, G;
   int causal;
@@ -46,6 +78,8 @@ struct Args {
   // it fits a tile's rows), `nsub` times; a tile of `rows` rows holds w =
   // rows / gu tokens, row r = token r / gu, head r % gu.
   int gu, nsub, w;
+  FastDiv by_page, by_gu, by_nsub;
+  FastDiv by_w;  // tokens of a unit (attention: of all its tiles)
   const void* q;
   const void* k;
   const void* v;
@@ -110,12 +144,13 @@ __host__ __device__ inline long long floor_sum(long long n, long long m, long lo
 // `w` tokens and reads the key tiles of `tile` keys up to its last visible
 // key.
 struct AttendUnits {
-  int w, lg, causal;  // tiles of 2^lg keys
-  __host__ __device__ int count(int nq, int nk) const { return (nq + w - 1) / w; }
+  FastDiv by_w;
+  int lg, causal;  // tiles of 2^lg keys
+  __host__ __device__ int count(int nq, int nk) const { return by_w.ceil(nq); }
   __host__ __device__ int steps(int nq, int nk, int j) const {
     int lim = nk;
     if (causal) {
-      const long long last = static_cast<long long>(j + 1) * w;
+      const long long last = static_cast<long long>(j + 1) * by_w.d;
       lim = last < nq ? nk - nq + static_cast<int>(last) : nk;
     }
     return lim <= 0 ? 0 : (lim + (1 << lg) - 1) >> lg;
@@ -132,8 +167,8 @@ struct AttendUnits {
       r = steps(nq, nk, n - 1);
     }
     if (full > 0) {
-      const int off = nk - nq;
-      const int i0 = off + w > 0 ? 0 : -off / w;  // first block that sees a key
+      const int off = nk - nq, w = static_cast<int>(by_w.d);
+      const int i0 = off + w > 0 ? 0 : by_w.div(-off);  // first block that sees a key
       if (full > i0)
         r += floor_sum(full - i0, 1LL << lg, w,
                        off + static_cast<long long>(i0 + 1) * w + (1 << lg) - 1);
@@ -144,24 +179,26 @@ struct AttendUnits {
 // Score sums: unit j holds 2^lg keys and reads the chunks of `w` tokens
 // (times nsub head groups) from the first that sees one of its keys.
 struct ScoreUnits {
-  int w, lg, causal, nsub;
+  FastDiv by_w;
+  int lg, causal, nsub;
   __host__ __device__ int count(int nq, int nk) const {
     return nq > 0 ? (nk + (1 << lg) - 1) >> lg : 0;
   }
   __host__ __device__ int first(int nq, int nk, int j) const {
     const int d = (j << lg) - (nk - nq);
-    return causal && d > 0 ? d / w : 0;
+    return causal && d > 0 ? by_w.div(d) : 0;
   }
   __host__ __device__ int steps(int nq, int nk, int j) const {
-    return ((nq + w - 1) / w - first(nq, nk, j)) * nsub;
+    return (by_w.ceil(nq) - first(nq, nk, j)) * nsub;
   }
   __host__ __device__ long long before(int nq, int nk, int j) const {
     if (j <= 0) return 0;
-    long long r = static_cast<long long>(j) * ((nq + w - 1) / w);
+    long long r = static_cast<long long>(j) * by_w.ceil(nq);
     if (causal) {
       const int off = nk - nq;
       const int i0 = off > 0 ? (off + (1 << lg) - 1) >> lg : 0;  // first j with a cut
-      if (j > i0) r -= floor_sum(j - i0, w, 1LL << lg, (static_cast<long long>(i0) << lg) - off);
+      if (j > i0)
+        r -= floor_sum(j - i0, by_w.d, 1LL << lg, (static_cast<long long>(i0) << lg) - off);
     }
     return r * nsub;
   }
@@ -183,29 +220,21 @@ struct Share {
   long long begin, end, size;
   long long pos;  // start of the first unit
   int b, h, j;    // the first unit (b = B: none)
+  int n;          // units of its (sequence, head)
+  Seq s;
 };
 
 // Units whose cost reaches into the share, in order.
 template <typename Units>
 struct Walk {
-  Units u;
   long long pos;
   int b, h, j, n;
   Seq s;
-  __device__ Walk(const Args& a, const Units& units, const Share& sh) : u(units) {
-    b = sh.b;
-    h = sh.h;
-    j = sh.j;
-    pos = sh.pos;
-    n = 0;
-    s = Seq{0, 0, 0};
-    if (b < a.B) {
-      s = seq_of(a, b);
-      n = u.count(s.nq, s.nk);
-    }
-  }
+  __device__ __forceinline__ explicit Walk(const Share& sh)
+      : pos(sh.pos), b(sh.b), h(sh.h), j(sh.j), n(sh.n), s(sh.s) {}
   // heads: units of one sequence and block number (kv heads, times nsub)
-  __device__ bool next(const Args& a, const Share& sh, int heads, Unit* out) {
+  __device__ __forceinline__ bool next(const Args& a, const Units& u, const Share& sh, int heads,
+                                       Unit* out) {
     while (b < a.B && pos < sh.end) {
       if (j >= n) {
         j = 0;
@@ -237,22 +266,34 @@ struct Walk {
   }
 };
 
+// a / b for a >= 0, b > 0: 32-bit where the numbers allow it (the 64-bit
+// sequence is several times as long).
+__device__ __forceinline__ long long div_nonneg(long long a, long long b) {
+  if (((a | b) >> 31) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Divide the line among the grid's CTAs and find this CTA's share.  Every
 // thread of the CTA calls it (kThreads of them, whole warps); `scratch`
-// holds kThreads / 32 + 1 numbers.  Ends with a CTA barrier.
+// holds kThreads / 32 numbers.  Ends with a CTA barrier.
 template <int kThreads, typename Units>
-__device__ void plan_share(const Args& a, const Units& u, int heads, int min_share,
-                           long long* scratch, Share* sh) {
+__device__ __forceinline__ void plan_share(const Args& a, const Units& u, int heads,
+                                           int min_share, long long* scratch, Share* sh) {
   const int tid = threadIdx.x;
   const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  auto cost = [&](int b) {
-    const Seq s = seq_of(a, b);
-    const int n = u.count(s.nq, s.nk);
+  auto cost = [&](const Seq& s, int n) {
     return (u.before(s.nq, s.nk, n) + static_cast<long long>(n) * kUnitCost) * heads;
   };
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += cost(b);
+  Seq s{0, 0, 0};
+  int n = 0;
+  for (int b = b0; b < b1; ++b) {
+    s = seq_of(a, b);
+    n = u.count(s.nq, s.nk);
+    mine += cost(s, n);
+  }
   long long incl = mine;  // inclusive scan over the threads
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -261,23 +302,13 @@ __device__ void plan_share(const Args& a, const Units& u, int heads, int min_sha
   }
   if ((tid & 31) == 31) scratch[tid >> 5] = incl;
   __syncthreads();
-  if (tid == 0) {
-    long long run = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      const long long t = scratch[i];
-      scratch[i] = run;
-      run += t;
-    }
-    scratch[kThreads / 32] = run;
-    sh->b = a.B;
-    sh->h = 0;
-    sh->j = 0;
-    sh->pos = run;
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == (tid >> 5)) incl += total;
+    total += scratch[i];
   }
-  __syncthreads();
-  incl += scratch[tid >> 5];
-  const long long total = scratch[kThreads / 32];
-  long long size = (total + gridDim.x - 1) / gridDim.x;
+  long long size = div_nonneg(total + gridDim.x - 1, gridDim.x);
   if (size < min_share) size = min_share;
   const long long begin = size * blockIdx.x;
   const long long end = begin + size < total ? begin + size : total;
@@ -285,16 +316,24 @@ __device__ void plan_share(const Args& a, const Units& u, int heads, int min_sha
     sh->begin = begin;
     sh->end = end;
     sh->size = size;
+    if (begin >= total) {
+      sh->pos = total;
+      sh->b = a.B;
+      sh->h = sh->j = sh->n = 0;
+      sh->s = Seq{0, 0, 0};
+    }
   }
   long long pos = incl - mine;
   if (begin < total && begin >= pos && begin < incl) {
     for (int b = b0; b < b1; ++b) {
-      const long long c = cost(b);
+      if (b1 - b0 > 1) {
+        s = seq_of(a, b);
+        n = u.count(s.nq, s.nk);
+      }
+      const long long c = b1 - b0 > 1 ? cost(s, n) : mine;
       if (begin < pos + c) {
-        const Seq s = seq_of(a, b);
-        const int n = u.count(s.nq, s.nk);
-        const long long per_head = c / heads;
-        const int h = static_cast<int>((begin - pos) / per_head);
+        const long long per_head = div_nonneg(c, heads);
+        const int h = static_cast<int>(div_nonneg(begin - pos, per_head));
         pos += h * per_head;
         // last block that starts at or before `begin`
         int lo = 0, hi = n - 1;
@@ -307,6 +346,8 @@ __device__ void plan_share(const Args& a, const Units& u, int heads, int min_sha
         sh->b = b;
         sh->h = h;
         sh->j = lo;
+        sh->n = n;
+        sh->s = s;
         sh->pos = pos + u.before(s.nq, s.nk, lo) + static_cast<long long>(lo) * kUnitCost;
         break;
       }
@@ -319,10 +360,21 @@ __device__ void plan_share(const Args& a, const Units& u, int heads, int min_sha
 // Partial results that a unit has: the CTAs from the one that holds its
 // first step to the one that holds its last.
 __device__ __forceinline__ int pieces_of(const Unit& u, const Share& sh) {
-  return static_cast<int>((u.pos + u.steps - 1) / sh.size - u.pos / sh.size) + 1;
+  return static_cast<int>(div_nonneg(u.pos + u.steps - 1, sh.size) -
+                          div_nonneg(u.pos, sh.size)) + 1;
 }
 
-#ifdef __CUDACC__
+// Page of position p, or -1 (and the status word set) where the table names
+// none of the cache's.
+__device__ __forceinline__ int page_of(const Args& a, int b, int p) {
+  const int page = a.table[b * a.table_stride + a.by_page.div(p)];
+  if (page < 0 || page >= a.num_pages) {
+    atomicExch(a.status, kStatusPageTable);
+    return -1;
+  }
+  return page;
+}
+
 // One copy of box_rows rows of a cache block (encode_row_blocks).
 __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row,
                                          int block) {
@@ -332,18 +384,53 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(row >> 3), "r"(block)
       : "memory");
 }
-#endif
 
-// Page of position p, or -1 (and the status word set) where the table names
-// none of the cache's.
-__device__ __forceinline__ int page_of(const Args& a, int b, int p) {
-  const int page = a.table[b * a.table_stride + p / a.page_size];
-  if (page < 0 || page >= a.num_pages) {
-    atomicExch(a.status, kStatusPageTable);
-    return -1;
+// The page table as a producer warp reads it: the entries of 32 boxes of a
+// piece at a time, one a lane, fetched one batch before their use (a lookup a
+// tile, its load and its divisions, held a tile's copies back by more than a
+// microsecond).
+struct Boxes {
+  const Args& a;
+  const int* table;  // the sequence's row
+  int key0, nk;      // first key of the piece, keys of the sequence
+  int lg, nbox, lane;  // boxes of 2^lg rows, boxes of a tile
+  int cur_page, cur_row, nxt_page, nxt_row;
+  __device__ __forceinline__ Boxes(const Args& args, int b, int first_key, int keys, int lg_rows,
+                                   int lane_)
+      : a(args), table(args.table + b * args.table_stride), key0(first_key), nk(keys),
+        lg(lg_rows), nbox(128 >> lg_rows), lane(lane_), cur_page(-1), cur_row(0) {
+    fetch(0);
   }
-  return page;
-}
+  __device__ __forceinline__ void fetch(int batch) {
+    const int key = key0 + ((batch * 32 + lane) << lg);
+    nxt_page = -1;
+    nxt_row = 0;
+    if (key < nk) {
+      const int i = a.by_page.div(key);
+      nxt_row = key - i * a.page_size;
+      nxt_page = table[i];
+    }
+  }
+  // Box `lane` of the piece's key tile j (asked for in order): false where
+  // there is none; page -1 where the table names none of the cache's.
+  __device__ __forceinline__ bool tile(int j, int* page, int* row) {
+    const int q = j * nbox;
+    if ((q & 31) == 0) {
+      cur_page = nxt_page;
+      cur_row = nxt_row;
+      fetch((q >> 5) + 1);
+    }
+    const int src = (q & 31) + (lane & (nbox - 1));
+    *page = __shfl_sync(0xffffffffu, cur_page, src);
+    *row = __shfl_sync(0xffffffffu, cur_row, src);
+    if (lane >= nbox || key0 + ((q + lane) << lg) >= nk) return false;
+    if (*page < 0 || *page >= a.num_pages) {
+      atomicExch(a.status, kStatusPageTable);
+      *page = -1;
+    }
+    return true;
+  }
+};
 
 }  // namespace paged
 
@@ -354,6 +441,11 @@ sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
                                        const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d128(paged::Args a, int dtype, const LaunchEnv& env);
+// Rows of a tile of the few-row kernel for this call (8 or 16; 0: the calls
+// of more rows take paged_tc.cuh).
+int paged_decode_rows(const paged::Args& a);
+sdpa_status_t launch_paged_decode_tc(const paged::Args& a, int head_dim, int dtype, int rows,
+                                     const LaunchEnv& env);
 sdpa_status_t launch_paged_scores_tc(paged::Args a, int head_dim, int dtype,
                                      const LaunchEnv& env);
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
@@ -396,10 +488,19 @@ inline bool cache_blocks(const long long (&st)[3], int pages, int heads, CacheBl
 }
 
 // Heads per tile and tokens per tile of `rows` query rows.
-inline void fit_rows(Args& a, int rows) {
+inline void fit_rows(Args& a, int rows, int tiles = 1) {
   a.nsub = (a.G + rows - 1) / rows;
   a.gu = (a.G + a.nsub - 1) / a.nsub;
   a.w = rows / a.gu;
+  a.by_gu = fast_div(a.gu);
+  a.by_nsub = fast_div(a.nsub);
+  a.by_w = fast_div(a.w * tiles);
+}
+// Rows of a page box: log2 of gcd(page_size, 128).
+inline int box_log2(int page_size) {
+  int lg = 7;
+  while (page_size & ((1 << lg) - 1)) --lg;
+  return lg;
 }
 // Largest tile whose partial results a CTA may leave, in query rows (two
 // 128-row tiles) and in keys (score sums).

@@ -87,6 +87,7 @@ int device_sms() {
 }
 
 paged::Args make_args(const sdpa_paged_params_t& p) {
+  using paged::fast_div;
   paged::Args a = {};
   a.B = p.num_seqs;
   a.T = p.num_tokens;
@@ -113,6 +114,8 @@ paged::Args make_args(const sdpa_paged_params_t& p) {
   }
   a.sl2 = p.scale * 1.4426950408889634f;
   a.gu = a.w = a.nsub = 1;
+  a.by_page = fast_div(p.page_size);
+  a.by_gu = a.by_nsub = a.by_w = fast_div(1);
   return a;
 }
 
@@ -246,6 +249,8 @@ sdpa_status_t sdpa_paged_forward(const sdpa_paged_params_t* p, const void* q,
   a.lse = lse;
   if (!tc_fits(*p, true))
     st = launch_paged_simt(a, p->head_dim, p->dtype, env);
+  else if (const int rows = paged_decode_rows(a))
+    st = launch_paged_decode_tc(a, p->head_dim, p->dtype, rows, env);
   else
     st = p->head_dim == 64 ? launch_paged_tc_d64(a, p->dtype, env)
                            : launch_paged_tc_d128(a, p->dtype, env);

@@ -96,7 +96,7 @@ template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     paged_scores_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK, const Args a,
-                           const int box_rows, const CacheBlocks kb) {
+                           const int lg_box, const CacheBlocks kb) {
   using C = ScCfg<D, R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
-  const ScoreUnits units{a.w, kLgUnit, a.causal, a.nsub};
+  const ScoreUnits units{a.by_w, kLgUnit, a.causal, a.nsub};
   plan_share<C::THREADS>(a, units, a.Hkv, 2,
                          reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
   tc_fence_after();
@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   using W = Walk<ScoreUnits>;
   W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
   Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
-  if (lane == 0) *walk = W(a, units, *sh);
+  if (lane == 0) *walk = W(*sh);
   auto next = [&]() {
     __syncwarp();
     bool more = false;
-    if (lane == 0) more = walk->next(a, *sh, a.Hkv, unit);
+    if (lane == 0) more = walk->next(a, units, *sh, a.Hkv, unit);
     return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
   };
   // the two key tiles of unit j, or one where the length ends in the first
@@ -176,22 +176,22 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
 
   if (warp == kLoad) {
     // ------------------------------------------------------------ producer
-    const int nbox = 128 / box_rows;
-    const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * C::CB * 128u;
+    const int nbox = 128 >> lg_box;
+    const uint32_t box_bytes = (C::CB * 128u) << lg_box;
     bool ok = true;
     int ku = 0, g = 0;  // units, steps
     while (ok && next()) {
       const Unit u = *unit;
       const int first = units.first(u.s.nq, u.s.nk, u.j);
       // this lane's box: of tile lane / nbox
-      const int key = u.j * kUnitKeys + lane * box_rows;
+      const int key = u.j * kUnitKeys + (lane << lg_box);
       int page = -1, row = 0;
       if (lane < 2 * nbox && key < u.s.nk) {
         page = page_of(a, u.b, key);
-        row = key % a.page_size;
+        row = key - a.by_page.div(key) * a.page_size;
         if (page < 0) page = -2;  // the table names none: reads as zero
       }
-      const int boxes = min(2 * nbox, (u.s.nk - u.j * kUnitKeys + box_rows - 1) / box_rows);
+      const int boxes = min(2 * nbox, (u.s.nk - u.j * kUnitKeys + (1 << lg_box) - 1) >> lg_box);
       const int ks = ku % C::NK;
       if (lane == 0) {
         if (ku >= C::NK) ok = mbar_wait(&k_empty[ks], ((ku / C::NK) - 1) & 1, wc);
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           if (g >= C::NQS) ok = mbar_wait(&q_empty[qs], ((g / C::NQS) - 1) & 1, wc);
           if (!ok) break;
           mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(C::CB * a.gu * a.w * 128));
-          const int tok = u.s.q0 + (first + t / a.nsub) * a.w;
-          const int head = u.h * a.G + (t % a.nsub) * a.gu;
+          const int tok = u.s.q0 + (first + a.by_nsub.div(t)) * a.w;
+          const int head = u.h * a.G + (a.by_nsub.mod(t)) * a.gu;
           for (int cb = 0; cb < C::CB; ++cb)
             tma_load_4d(sQ + qs * C::QTILE + cb * R * 128, &tmQ, &q_full[qs], cb * 64, head,
                         tok, 0);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
       for (int t = u.s0; t < u.s1 && ok; ++t, ++g) {
         const int slot = g % kNL;
         float* dst = sLse + slot * 2 * R;
-        const int tok0 = (first + t / a.nsub) * a.w, sub = t % a.nsub;
+        const int tok0 = (first + a.by_nsub.div(t)) * a.w, sub = a.by_nsub.mod(t);
         float v[(R + 31) / 32];
         int lim[(R + 31) / 32];
         int mn = 0x7fffffff;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           v[i] = -INFINITY;
           lim[i] = 0;
           if (r < a.gu * a.w) {
-            const int tok = tok0 + r / a.gu, e = sub * a.gu + r % a.gu;
+            const int tok = tok0 + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
             if (tok < u.s.nq && e < a.G) {
               const float x =
                   a.lse[static_cast<size_t>(u.s.q0 + tok) * a.Hq + u.h * a.G + e] * kLog2e;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
 
 template <int D, bool BF16, int R>
 sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                        int box_rows, const CacheBlocks& kb, const LaunchEnv& env) {
+                        int lg_box, const CacheBlocks& kb, const LaunchEnv& env) {
   using C = ScCfg<D, R>;
   auto kern = paged_scores_tc_kernel<D, BF16, R>;
   static std::atomic<uint64_t> ready{0};  // devices on which the attribute is set
@@ -471,7 +471,7 @@ sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap&
   cfg.stream = env.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, a, box_rows, kb) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, a, lg_box, kb) != cudaSuccess) return SDPA_ERR_CUDA;
   return launch_paged_scores_merge(a, kUnitKeys, env.stream);
 }
 
@@ -483,8 +483,7 @@ sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType dt =
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  int box_rows = 128;  // gcd(page_size, 128)
-  while (a.page_size % box_rows) box_rows >>= 1;
+  const int lg_box = box_log2(a.page_size);
   CacheBlocks kb;
   long long ku;
   if (!cache_blocks(a.ks, a.num_pages, a.Hkv, &kb, &ku))
@@ -494,14 +493,14 @@ sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
   auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
   if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
                            static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
-      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, box_rows,
+      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, 1 << lg_box,
                          st(a.ks[2], a.page_size), ku))
     return SDPA_ERR_CUDA;
   if (few)
-    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, box_rows, kb, env)
-                : launch_sc<D, false, 16>(a, tq, tk, box_rows, kb, env);
-  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, box_rows, kb, env)
-              : launch_sc<D, false, 128>(a, tq, tk, box_rows, kb, env);
+    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, lg_box, kb, env)
+                : launch_sc<D, false, 16>(a, tq, tk, lg_box, kb, env);
+  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, lg_box, kb, env)
+              : launch_sc<D, false, 128>(a, tq, tk, lg_box, kb, env);
 }
 
 }  // namespace

@@ -66,7 +66,7 @@ __device__ __forceinline__ void row_offsets(const Args& a, int b, int kvh, int k
   if (r >= kKT) return;
   const int key = key0 + r;
   const int page = key < nk ? page_of(a, b, key) : -1;
-  const int row = key % a.page_size;
+  const int row = key - a.by_page.div(key) * a.page_size;
   off_k[r] = page < 0 ? -1 : page * a.ks[0] + kvh * a.ks[1] + row * a.ks[2];
   off_v[r] = page < 0 ? -1 : page * a.vs[0] + kvh * a.vs[1] + row * a.vs[2];
 }
@@ -93,7 +93,7 @@ __device__ void load_queries(const Args& a, const Seq& s, int tok0, int kvh, int
   constexpr int C = D / N;
   for (int i = threadIdx.x; i < RM * C; i += kT) {
     const int r = i / C, c = (i % C) * N;
-    const int tok = tok0 + r / a.gu, e = sub * a.gu + r % a.gu;
+    const int tok = tok0 + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
     const T* src = nullptr;
     if (r < a.w * a.gu && tok < s.nq && e < a.G)
       src = static_cast<const T*>(a.q) + (s.q0 + tok) * a.qs[0] +
@@ -150,14 +150,14 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(const Args a) {
   __shared__ Share sh;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   griddep_launch_dependents();
-  const AttendUnits units{a.w, kLgKT, a.causal};
+  const AttendUnits units{a.by_w, kLgKT, a.causal};
   const int heads = a.Hkv * a.nsub;
   plan_share<kT>(a, units, heads, 1, scratch, &sh);
   if (tid == 0) a.desc[blockIdx.x * kDesc] = 0;
-  Walk<AttendUnits> walk(a, units, sh);
+  Walk<AttendUnits> walk(sh);
   Unit u;
-  while (walk.next(a, sh, heads, &u)) {
-    const int kvh = u.h / a.nsub, sub = u.h % a.nsub;
+  while (walk.next(a, units, sh, heads, &u)) {
+    const int kvh = a.by_nsub.div(u.h), sub = a.by_nsub.mod(u.h);
     const int tok0 = u.j * a.w;
     __syncthreads();  // the previous unit's tiles are read
     load_queries<T, D, RM>(a, u.s, tok0, kvh, sub, sQ);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(const Args a) {
     float m[RPT], l[RPT], o[RPT][CG][4];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const int r = ty * RPT + i, tok = tok0 + r / a.gu;
+      const int r = ty * RPT + i, tok = tok0 + a.by_gu.div(r);
       limit[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
       m[i] = -INFINITY;
       l[i] = 0.f;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(const Args a) {
     float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + u.slot()) * kSlot;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const int r = ty * RPT + i, tok = tok0 + r / a.gu, e = sub * a.gu + r % a.gu;
+      const int r = ty * RPT + i, tok = tok0 + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
       if (r >= a.w * a.gu || tok >= u.s.nq || e >= a.G) continue;
       if (!whole) {
 #pragma unroll
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(256)
   const int n = d[0];
   if (n == 0) return;
   const int b_h = d[2], j = d[3], q0 = d[4], nq = d[5];
-  const int kvh = b_h / a.nsub, sub = b_h % a.nsub;
+  const int kvh = a.by_nsub.div(b_h), sub = a.by_nsub.mod(b_h);
   const int rows = tile_rows * tiles;
   const size_t slot_floats = static_cast<size_t>(rows) * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256)
   for (int r0 = wide ? blockIdx.y : blockIdx.y * 8; r0 < rows; r0 += step) {
     const int rr = wide ? r0 : r0 + warp;  // row of the unit
     const int t = rr / tile_rows, r = rr % tile_rows;
-    const int tok = (j * tiles + t) * a.w + r / a.gu, e = sub * a.gu + r % a.gu;
+    const int tok = (j * tiles + t) * a.w + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
     const bool live = rr < rows && r < a.w * a.gu && tok < nq && e < a.G;
     if (wide && !live) continue;  // the same for every warp
     float M = -INFINITY, L = 0.f, acc[E];
@@ -430,12 +430,12 @@ __global__ void __launch_bounds__(kT) paged_scores_simt_kernel(const Args a) {
   __shared__ Share sh;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   griddep_launch_dependents();
-  const ScoreUnits units{a.w, kLgKT, a.causal, a.nsub};
+  const ScoreUnits units{a.by_w, kLgKT, a.causal, a.nsub};
   plan_share<kT>(a, units, a.Hkv, 1, scratch, &sh);
   if (tid == 0) a.desc[blockIdx.x * kDesc] = 0;
-  Walk<ScoreUnits> walk(a, units, sh);
+  Walk<ScoreUnits> walk(sh);
   Unit u;
-  while (walk.next(a, sh, a.Hkv, &u)) {
+  while (walk.next(a, units, sh, a.Hkv, &u)) {
     const int key0 = u.j * kKT;
     const int first = units.first(u.s.nq, u.s.nk, u.j);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -444,11 +444,11 @@ __global__ void __launch_bounds__(kT) paged_scores_simt_kernel(const Args a) {
     __syncthreads();
     load_rows<T, D>(a.k, off_k, sK, D + 4);
     for (int t = u.s0; t < u.s1; ++t) {
-      const int tok0 = (first + t / a.nsub) * a.w, sub = t % a.nsub;
+      const int tok0 = (first + a.by_nsub.div(t)) * a.w, sub = a.by_nsub.mod(t);
       if (t > u.s0) __syncthreads();
       load_queries<T, D, RM>(a, u.s, tok0, u.h, sub, sQ);
       if (tid < RM) {
-        const int tok = tok0 + tid / a.gu, e = sub * a.gu + tid % a.gu;
+        const int tok = tok0 + a.by_gu.div(tid), e = sub * a.gu + a.by_gu.mod(tid);
         float ls = INFINITY;  // rows that do not exist add nothing
         int lim = 0;
         if (tid < a.w * a.gu && tok < u.s.nq && e < a.G) {
@@ -572,7 +572,7 @@ sdpa_status_t score(Args& a, const LaunchEnv& env) {
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
                                  int tiles, cudaStream_t stream) {
   using namespace paged;
-  const dim3 grid(a.nctas, tile_rows * tiles > 128 ? 32 : 16);
+  const dim3 grid(a.nctas, tile_rows <= 16 ? 8 : tile_rows * tiles > 128 ? 32 : 16);
   auto go = [&](auto kern) { return launch_after(kern, grid, 256, stream, a, tile_rows, tiles); };
   if (head_dim == 64) {
     if (dtype == SDPA_F32) return go(paged_merge_kernel<float, 64>);

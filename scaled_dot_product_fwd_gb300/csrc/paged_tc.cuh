@@ -117,7 +117,7 @@ template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const Args a, const int box_rows,
+                    const __grid_constant__ CUtensorMap tmV, const Args a, const int lg_box,
                     const CacheBlocks kb, const CacheBlocks vb) {
   using C = TcCfg<D, NT>;
   using E = Elem<BF16>;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
-  const AttendUnits units{a.w * NT, 7, a.causal};
+  const AttendUnits units{a.by_w, 7, a.causal};
   const int heads = a.Hkv * a.nsub;
   plan_share<C::THREADS>(a, units, heads, 2,
                          reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
   using W = Walk<AttendUnits>;
   W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
   Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
-  if (lane == 0) *walk = W(a, units, *sh);
+  if (lane == 0) *walk = W(*sh);
   auto next = [&]() {
     __syncwarp();
     bool more = false;
-    if (lane == 0) more = walk->next(a, *sh, heads, unit);
+    if (lane == 0) more = walk->next(a, units, *sh, heads, unit);
     return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
   };
   int fills = 0;    // producer: ring slots filled
@@ -201,39 +201,36 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
     if constexpr (NT == 2) setmaxnreg_dec<kControlRegs>();
     if (warp == kLoad) {
       // ---------------------------------------------------------- producer
-      const int nbox = 128 / box_rows;
-      const uint32_t box_bytes = static_cast<uint32_t>(box_rows) * C::CB * 128u;
+      const int nbox = 128 >> lg_box;
+      const uint32_t box_bytes = (C::CB * 128u) << lg_box;
       int g = 0;  // ring slots filled
       bool ok = true;
       for (int it = 0; ok && next(); ++it) {
         const Unit u = *unit;
         const TileGeo tg = tile_geo<NT>(a, u);
-        const int kvh = u.h / a.nsub, sub = u.h % a.nsub;
+        const int kvh = a.by_nsub.div(u.h), sub = a.by_nsub.mod(u.h);
         // Page and row of this lane's box of key tile t (page -2: the table
-        // names none; -1: past the length).  The lookups run LA + 1 tiles
-        // ahead of their use.
+        // names none; -1: past the length).
         struct Box {
           int page, row;
         };
+        Boxes boxes_of(a, u.b, tg.s0 * 128, u.s.nk, lg_box, lane);
         auto lookup = [&](int j) {
           Box x{-1, 0};
-          const int key = (tg.s0 + j) * 128 + lane * box_rows;
-          if (j < tg.nmax && lane < nbox && key < u.s.nk) {
-            x.page = page_of(a, u.b, key);
-            x.row = key % a.page_size;
+          if (j < tg.nmax && boxes_of.tile(j, &x.page, &x.row)) {
             if (x.page < 0) x.page = -2;
+          } else {
+            x.page = -1;
           }
           return x;
         };
         auto load = [&](const CUtensorMap* map, const CacheBlocks& c, int j, const Box& x) {
           const int s = g % C::NS, use = g / C::NS;
-          const int boxes = min(nbox, (u.s.nk - (tg.s0 + j) * 128 + box_rows - 1) / box_rows);
-          if (lane == 0) {
-            if (ok && use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, wc);
-            if (ok) mbar_arrive_expect_tx(&full[s], box_bytes * boxes);
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          const int boxes = min(nbox, (u.s.nk - (tg.s0 + j) * 128 + (1 << lg_box) - 1) >> lg_box);
+          ok = __all_sync(0xffffffffu, ok && (use == 0 || mbar_wait(&empty[s], (use - 1) & 1, wc)));
           if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], box_bytes * boxes);
+          __syncwarp();
           if (x.page != -1)
             load_box(sRing + s * C::TILE + lane * box_bytes, map, &full[s], x.row,
                      x.page < 0 ? c.blocks : x.page * c.page_mul + kvh * c.head_mul);
@@ -453,7 +450,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
       if (t >= tg.nt) continue;
       const int tok0 = (unit->j * NT + t) * a.w;  // first token of the tile
       const int nq = unit->s.nq;
-      const int tok = tok0 + r / a.gu;
+      const int tok = tok0 + a.by_gu.div(r);
       // rows of this warp that exist
       const bool live = (warp & 3) * 32 < min(a.w, nq - tok0) * a.gu;
       // visible keys of the row, counted from the piece's first key
@@ -544,8 +541,8 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
         began = true;
       }
       if (!ok || !live) continue;
-      const int sub = unit->h % a.nsub;
-      const int e = sub * a.gu + r % a.gu;
+      const int sub = a.by_nsub.mod(unit->h);
+      const int e = sub * a.gu + a.by_gu.mod(r);
       const bool row_ok = r < a.w * a.gu && tok < nq && e < a.G;
       tc_fence_after();
       __syncwarp();
@@ -569,7 +566,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
           slot[NT * 128 * (D + 1) + t * 128 + r] = l;
         }
       } else {
-        const int hq = (unit->h / a.nsub) * a.G + e;
+        const int hq = (a.by_nsub.div(unit->h)) * a.G + e;
         float f = 1.f;
         const float own = l;
         if (a.sinks && row_ok) {
@@ -624,7 +621,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
 
 template <int D, bool BF16, int NT>
 sdpa_status_t launch_tc_impl(Args& a, const CUtensorMap& tq, const CUtensorMap& tk,
-                             const CUtensorMap& tv, int box_rows, const CacheBlocks& kb,
+                             const CUtensorMap& tv, int lg_box, const CacheBlocks& kb,
                              const CacheBlocks& vb, const LaunchEnv& env) {
   using C = TcCfg<D, NT>;
   auto kern = paged_tc_kernel<D, BF16, NT>;
@@ -655,7 +652,7 @@ sdpa_status_t launch_tc_impl(Args& a, const CUtensorMap& tq, const CUtensorMap& 
   cfg.stream = env.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, box_rows, kb, vb) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a, lg_box, kb, vb) != cudaSuccess)
     return SDPA_ERR_CUDA;
   return launch_paged_merge(a, D, BF16 ? SDPA_BF16 : SDPA_F16, 128, NT, env.stream);
 }
@@ -666,8 +663,7 @@ sdpa_status_t launch_tc(Args a, int dtype, const LaunchEnv& env) {
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType dt =
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  int box_rows = 128;  // gcd(page_size, 128)
-  while (a.page_size % box_rows) box_rows >>= 1;
+  const int lg_box = box_log2(a.page_size);
   CacheBlocks kb, vb;
   long long ku, vu;
   if (!cache_blocks(a.ks, a.num_pages, a.Hkv, &kb, &ku) ||
@@ -678,18 +674,19 @@ sdpa_status_t launch_tc(Args a, int dtype, const LaunchEnv& env) {
   auto st = [](long long s, long long n) { return static_cast<uint64_t>(n > 1 ? s : D); };
   if (!encode_tiled_4d_box(&tq, dt, a.q, D, a.Hq, a.T, 1, 2, 64, static_cast<uint32_t>(a.gu),
                            static_cast<uint32_t>(a.w), st(a.qs[1], a.Hq), st(a.qs[0], a.T), D) ||
-      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, box_rows,
+      !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, 1 << lg_box,
                          st(a.ks[2], a.page_size), ku) ||
-      !encode_row_blocks(&tv, dt, a.v, D / 64, a.page_size, vb.blocks, box_rows,
+      !encode_row_blocks(&tv, dt, a.v, D / 64, a.page_size, vb.blocks, 1 << lg_box,
                          st(a.vs[2], a.page_size), vu))
     return SDPA_ERR_CUDA;
   // more than 128 rows a sequence and head unit on average: two tiles a unit
   const bool two = static_cast<long long>(a.T) * a.gu > 128LL * a.B;
+  if (two) fit_rows(a, 128, 2);
   if (bf16)
-    return two ? launch_tc_impl<D, true, 2>(a, tq, tk, tv, box_rows, kb, vb, env)
-               : launch_tc_impl<D, true, 1>(a, tq, tk, tv, box_rows, kb, vb, env);
-  return two ? launch_tc_impl<D, false, 2>(a, tq, tk, tv, box_rows, kb, vb, env)
-             : launch_tc_impl<D, false, 1>(a, tq, tk, tv, box_rows, kb, vb, env);
+    return two ? launch_tc_impl<D, true, 2>(a, tq, tk, tv, lg_box, kb, vb, env)
+               : launch_tc_impl<D, true, 1>(a, tq, tk, tv, lg_box, kb, vb, env);
+  return two ? launch_tc_impl<D, false, 2>(a, tq, tk, tv, lg_box, kb, vb, env)
+             : launch_tc_impl<D, false, 1>(a, tq, tk, tv, lg_box, kb, vb, env);
 }
 
 }  // namespace
