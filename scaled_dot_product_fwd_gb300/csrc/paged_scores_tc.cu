@@ -10,8 +10,8 @@
 // A unit is 256 keys (two TMEM tiles, one a warpgroup): each query chunk that
 // is brought in meets both, which halves the query traffic out of L2.  Its
 // steps are the chunks of w tokens x gu heads that see a key of it, and the
-// work is divided among the CTAs as paged.cuh describes.  The K tiles of two
-// units and three query chunks are in flight (head_dim 128); S^T is
+// work is divided among the CTAs as paged.cuh describes.  The K tiles of one
+// unit and four query chunks are in shared memory (head_dim 128); S^T is
 // double-buffered, so the products of a step run while the exponentials of
 // the one before do.  Chunks: bound by the exponentials (128 x 256 a step,
 // about 1100 clk at the measured 30 a clk and SM, against 1024 clk of
@@ -41,8 +41,8 @@ struct ScCfg {
   static constexpr int TILE = 128 * D * 2;  // a key tile
   static constexpr int QTILE = R * D * 2;   // a query chunk
   // units whose keys are in flight, and query chunks
-  static constexpr int NK = R == 16 ? (D == 64 ? 6 : 3) : 2;
-  static constexpr int NQS = R == 16 ? 4 : (D == 64 ? 6 : 2);
+  static constexpr int NK = R == 16 ? (D == 64 ? 6 : 3) : (D == 64 ? 2 : 1);
+  static constexpr int NQS = R == 16 ? 4 : (D == 64 ? 6 : 4);
   static constexpr int Q_OFF = NK * 2 * TILE;
   static constexpr int BAR_OFF = Q_OFF + NQS * QTILE;
   // k_full[NK], k_empty[NK], q_full[NQS], q_empty[NQS], s_full[2 tiles][2],
@@ -63,15 +63,14 @@ struct ScCfg {
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-template <int R>
-__device__ __forceinline__ void load_cols(uint32_t t0, uint32_t (&s)[R]) {
-  if constexpr (R == 128) {
-    tmem_ld4x32_sync(t0, t0 + 32, t0 + 64, t0 + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
-                     *reinterpret_cast<uint32_t(*)[32]>(&s[32]),
-                     *reinterpret_cast<uint32_t(*)[32]>(&s[64]),
-                     *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+// N columns (16 or 64) of this thread's row of S^T.
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t t0, uint32_t (&s)[N]) {
+  if constexpr (N == 64) {
+    tmem_ld2x32_sync(t0, t0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                     *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
   } else {
-    static_assert(R == 16, "columns of a chunk");
+    static_assert(N == 16, "columns of a chunk");
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15}, [%16];\n\t"
@@ -82,6 +81,43 @@ __device__ __forceinline__ void load_cols(uint32_t t0, uint32_t (&s)[R]) {
         : "r"(t0)
         : "memory");
   }
+}
+
+// Sum over N columns of 2^(s * sl2 + nl), with kMasked of those whose limit
+// is above `key`.
+template <int N, bool kMasked>
+__device__ __forceinline__ float weights(const uint32_t (&s)[N], float sl2, const float* nl,
+                                         const int* lim, int key) {
+  const uint64_t SL = f2_pack(sl2, sl2);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
+    const uint64_t x0 = f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), SL,
+                               f2_pack(l4.x, l4.y));
+    const uint64_t x1 = f2_fma(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), SL,
+                               f2_pack(l4.z, l4.w));
+    float e0, e1, e2, e3;
+    f2_unpack(x0, e0, e1);
+    f2_unpack(x1, e2, e3);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    e2 = ex2(e2);
+    e3 = ex2(e3);
+    if constexpr (kMasked) {
+      const int4 m4 = *reinterpret_cast<const int4*>(lim + i);
+      e0 = key < m4.x ? e0 : 0.f;
+      e1 = key < m4.y ? e1 : 0.f;
+      e2 = key < m4.z ? e2 : 0.f;
+      e3 = key < m4.w ? e3 : 0.f;
+    }
+    acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], f2_pack(e0, e1));
+    acc[((i >> 1) + 1) & 3] = f2_add(acc[((i >> 1) + 1) & 3], f2_pack(e2, e3));
+  }
+  const uint64_t x = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  return x0 + x1;
 }
 
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
@@ -286,39 +322,59 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     }
   } else if (warp == kLse) {
     // ------------------------------------- the rows' log-sum-exp and limits
+    // this lane's rows of a chunk: token and head (token past every
+    // sequence's for rows that no chunk has)
+    constexpr int N = (R + 31) / 32;
+    int row_t[N], row_e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = i * 32 + lane;
+      row_t[i] = a.by_gu.div(r);
+      row_e[i] = a.by_gu.mod(r);
+    }
     bool ok = true;
     int g = 0;
     while (ok && next()) {
       const Unit u = *unit;
       const int first = units.first(u.s.nq, u.s.nk, u.j);
+      // the next step's values are on their way while this one's are stored
+      float nxt[N];
+      auto fetch = [&](int t) {
+        const int tok0 = (first + a.by_nsub.div(t)) * a.w, e0 = a.by_nsub.mod(t) * a.gu;
+        const float* p =
+            a.lse + static_cast<size_t>(u.s.q0 + tok0) * a.Hq + u.h * a.G + e0;
+        const int nt = t < u.s1 ? min(a.w, u.s.nq - tok0) : 0, ne = a.G - e0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          nxt[i] = 0.f;
+          if (row_t[i] < nt && row_e[i] < ne) nxt[i] = p[row_t[i] * a.Hq + row_e[i]];
+        }
+      };
+      fetch(u.s0);
       for (int t = u.s0; t < u.s1 && ok; ++t, ++g) {
         const int slot = g % kNL;
         float* dst = sLse + slot * 2 * R;
-        const int tok0 = (first + a.by_nsub.div(t)) * a.w, sub = a.by_nsub.mod(t);
-        float v[(R + 31) / 32];
-        int lim[(R + 31) / 32];
+        const int tok0 = (first + a.by_nsub.div(t)) * a.w;
+        const int nt = min(a.w, u.s.nq - tok0), ne = a.G - a.by_nsub.mod(t) * a.gu;
+        const int lim0 = u.s.nk - u.s.nq + tok0 + 1;
+        float v[N];
+        int lim[N];
         int mn = 0x7fffffff;
 #pragma unroll
-        for (int i = 0; i < (R + 31) / 32; ++i) {
-          const int r = i * 32 + lane;
-          v[i] = -INFINITY;
-          lim[i] = 0;
-          if (r < a.gu * a.w) {
-            const int tok = tok0 + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
-            if (tok < u.s.nq && e < a.G) {
-              const float x =
-                  a.lse[static_cast<size_t>(u.s.q0 + tok) * a.Hq + u.h * a.G + e] * kLog2e;
-              v[i] = x == -INFINITY ? x : -x;  // a row that saw nothing adds nothing
-              lim[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
-            }
-            mn = min(mn, lim[i]);
-          }
+        for (int i = 0; i < N; ++i) {
+          const bool there = row_t[i] < nt && row_e[i] < ne;
+          const float x = nxt[i] * kLog2e;
+          // (a row that saw nothing adds nothing)
+          v[i] = there && x != -INFINITY ? -x : -INFINITY;
+          lim[i] = !there ? 0 : a.causal ? min(u.s.nk, lim0 + row_t[i]) : u.s.nk;
+          if (row_t[i] < a.w) mn = min(mn, lim[i]);
         }
+        fetch(t + 1);
         mn = __reduce_min_sync(0xffffffffu, mn);
         if (g >= kNL) ok = __all_sync(0xffffffffu, mbar_wait(&l_empty[slot], ((g / kNL) - 1) & 1, wc));
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < (R + 31) / 32; ++i) {
+        for (int i = 0; i < N; ++i) {
           const int r = i * 32 + lane;
           if (r < R) {
             dst[r] = v[i];
@@ -355,57 +411,29 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           const int buf = 2 * kt + (g & 1);
           const int p = (g & 1) ? ph[1]++ : ph[0]++;
           ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], static_cast<uint32_t>(p & 1), wc));
-          uint32_t s[R];
-          if (ok) {
-            tc_fence_after();
-            __syncwarp();
-            load_cols<R>(t0 + buf * 128, s);
-            tc_fence_before();
-          }
-          named_bar_arrive(kBarS + buf, 160);
-          if (ok) {
-            const float* nl = sLse + slot * 2 * R;
-            const int* lim = reinterpret_cast<const int*>(nl) + R;
-            const uint64_t SL = f2_pack(a.sl2, a.sl2);
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-            if (__all_sync(0xffffffffu, key < sMin[slot])) {
+          // a part of the columns at a time, so that registers are left to
+          // have the rows' constants on their way (with all 128 columns live
+          // the loop waited for each of its shared-memory reads)
+          constexpr int kPart = R == 128 ? 64 : R;
+          const float* nl = sLse + slot * 2 * R;
+          const int* lim = reinterpret_cast<const int*>(nl) + R;
+          const bool inside = __all_sync(0xffffffffu, key < sMin[slot]);
+          float part_sum = 0.f;
 #pragma unroll
-              for (int i = 0; i < R; i += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
-                const uint64_t x0 = f2_fma(
-                    f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), SL,
-                    f2_pack(l4.x, l4.y));
-                const uint64_t x1 = f2_fma(
-                    f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), SL,
-                    f2_pack(l4.z, l4.w));
-                float e0, e1, e2, e3;
-                f2_unpack(x0, e0, e1);
-                f2_unpack(x1, e2, e3);
-                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], f2_pack(ex2(e0), ex2(e1)));
-                acc[((i >> 1) + 1) & 3] =
-                    f2_add(acc[((i >> 1) + 1) & 3], f2_pack(ex2(e2), ex2(e3)));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < R; i += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
-                const int4 m4 = *reinterpret_cast<const int4*>(lim + i);
-                const float e0 = ex2(fmaf(__uint_as_float(s[i]), a.sl2, l4.x));
-                const float e1 = ex2(fmaf(__uint_as_float(s[i + 1]), a.sl2, l4.y));
-                const float e2 = ex2(fmaf(__uint_as_float(s[i + 2]), a.sl2, l4.z));
-                const float e3 = ex2(fmaf(__uint_as_float(s[i + 3]), a.sl2, l4.w));
-                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], f2_pack(key < m4.x ? e0 : 0.f,
-                                                                      key < m4.y ? e1 : 0.f));
-                acc[((i >> 1) + 1) & 3] =
-                    f2_add(acc[((i >> 1) + 1) & 3],
-                           f2_pack(key < m4.z ? e2 : 0.f, key < m4.w ? e3 : 0.f));
-              }
+          for (int part = 0; part < R / kPart; ++part) {
+            uint32_t s[kPart];
+            if (ok) {
+              tc_fence_after();
+              __syncwarp();
+              load_cols<kPart>(t0 + buf * 128 + part * kPart, s);
+              tc_fence_before();
             }
-            const uint64_t x = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
-            float x0, x1;
-            f2_unpack(x, x0, x1);
-            sum += x0 + x1;
+            if (part == R / kPart - 1) named_bar_arrive(kBarS + buf, 160);
+            if (ok) part_sum += inside ? weights<kPart, false>(s, a.sl2, nl + part * kPart, lim, key)
+                                       : weights<kPart, true>(s, a.sl2, nl + part * kPart,
+                                                              lim + part * kPart, key);
           }
+          sum += part_sum;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&l_empty[slot]);
