@@ -2,7 +2,9 @@
 // on the 5th-generation tensor cores (fp16/bf16, head_dim 64/128):
 //     scores[key] += sum over rows of 2^(S^T[key, row] * scale*log2e - lse2[row])
 // with S^T = K Q^T, 128 keys on the lanes of TMEM and a chunk of query rows
-// (tokens x heads of the kv head) on its columns.  A thread owns a key: it
+// (tokens x heads of the kv head) on its columns.  A thread owns a key (two
+// threads do, one for each half of a chunk's 128 columns: sixteen warps hide
+// the latencies of the loads that eight did not, 183 -> %s us): it
 // reads its row of S^T, subtracts the rows' log-sum-exp (shared memory, the
 // same address for a whole warp), and adds the exponentials up in registers
 // over all chunks, so no value crosses lanes and nothing is added atomically.
@@ -49,7 +51,11 @@ struct ScCfg {
   // l_full[kNL], l_empty[kNL], drain
   static constexpr int NBARS = 2 * NK + 2 * NQS + 4 + 2 * kNL + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int WARPS = 12;
+  // warps of the exponentials: four for each key tile, or four for each half
+  // of its columns
+  static constexpr int HALVES = R == 128 ? 2 : 1;
+  static constexpr int EW = 8 * HALVES;
+  static constexpr int WARPS = EW + 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
   static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
@@ -59,16 +65,16 @@ struct ScCfg {
   // per slot: -lse2[R], then the rows' limits [R]
   static constexpr int LSE_OFF =
       (UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 15) / 16 * 16;
-  static constexpr int SMEM = LSE_OFF + kNL * R * 8 + 1024;
+  static constexpr int SUM_OFF = LSE_OFF + kNL * R * 8;  // float[2][128]
+  static constexpr int SMEM = SUM_OFF + 2 * 128 * 4 + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// N columns (16 or 64) of this thread's row of S^T.
+// N columns (16 or 32) of this thread's row of S^T.
 template <int N>
 __device__ __forceinline__ void load_cols(uint32_t t0, uint32_t (&s)[N]) {
-  if constexpr (N == 64) {
-    tmem_ld2x32_sync(t0, t0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
-                     *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+  if constexpr (N == 32) {
+    tmem_ld32_sync(t0, s);
   } else {
     static_assert(N == 16, "columns of a chunk");
     asm volatile(
@@ -127,6 +133,7 @@ __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads)
 // that buffer of S^T; kBarQ: stage helper with the MMA warp
 constexpr uint32_t kBarS = 1;
 constexpr uint32_t kBarQ = 5;
+constexpr uint32_t kBarC = 6;  // + t: the two halves of key tile t
 
 template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   Share* sh = reinterpret_cast<Share*>(smem + C::SHARE_OFF);
   int* sMin = reinterpret_cast<int*>(smem + C::MIN_OFF);
   float* sLse = reinterpret_cast<float*>(smem + C::LSE_OFF);
-  constexpr int kLoad = 8, kMma = 9, kHelp = 10, kLse = 11;
+  constexpr int kLoad = C::EW, kMma = kLoad + 1, kHelp = kLoad + 2, kLse = kLoad + 3;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
     for (int i = 0; i < kNL; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], 8);
+      mbar_init(&l_empty[i], C::EW);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           const int buf = 2 * kt + (g & 1);
           // the buffer's previous scores have been read
           if ((g & 1) ? uses[2 * kt + 1]++ : uses[2 * kt]++) {
-            named_bar_sync(kBarS + buf, 160);
+            named_bar_sync(kBarS + buf, 32 + 128 * C::HALVES);
             tc_fence_after();
           }
           const uint32_t kd = k_lo + static_cast<uint32_t>((((ku % C::NK) * 2 + kt) * C::TILE) >> 4);
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     // meet the last readers of each buffer
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (uses[i] > 0) named_bar_sync(kBarS + i, 160);
+      if (uses[i] > 0) named_bar_sync(kBarS + i, 32 + 128 * C::HALVES);
     mma_commit_elect(drain, 1u);
     if (lane == 0) drain_wait(drain, 0, kDrainNs);
     __syncwarp();
@@ -387,9 +394,12 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     }
   } else {
     // -------------------------------------------------------- exponentials
-    const int kt = warp >> 2;
+    constexpr int kCols = R / C::HALVES;  // columns of a thread
+    const int kt = warp / (C::EW / 2);
+    const int half = (warp >> 2) % C::HALVES;
     const int r = (warp & 3) * 32 + lane;
-    const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* sSum = reinterpret_cast<float*>(smem + C::SUM_OFF) + kt * 128;
+    const uint32_t t0 = half * kCols + tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool ok = true;
     int g = 0;
     int ph[2] = {0, 0};  // phases of s_full consumed, per buffer
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
       float* dst = a.scores + unit->b * a.ss[0] + unit->h * a.ss[1] + key;
       const bool live = mine && key < unit->s.nk && key < a.score_len;
       float old = 0.f;
-      if (live && whole) old = *dst;  // on its way while the scores are computed
+      if (live && whole && half == 0) old = *dst;  // on its way while the scores are computed
       float sum = 0.f;
       for (int t = 0; t < n; ++t, ++g) {
         const int slot = g % kNL;
@@ -411,29 +421,25 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           const int buf = 2 * kt + (g & 1);
           const int p = (g & 1) ? ph[1]++ : ph[0]++;
           ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], static_cast<uint32_t>(p & 1), wc));
-          // a part of the columns at a time, so that registers are left to
-          // have the rows' constants on their way (with all 128 columns live
-          // the loop waited for each of its shared-memory reads)
-          constexpr int kPart = R == 128 ? 64 : R;
-          const float* nl = sLse + slot * 2 * R;
+          // 32 columns at a time, so that registers are left to have the
+          // rows' constants on their way
+          constexpr int kPart = kCols < 32 ? kCols : 32;
+          const float* nl = sLse + slot * 2 * R + half * kCols;
           const int* lim = reinterpret_cast<const int*>(nl) + R;
           const bool inside = __all_sync(0xffffffffu, key < sMin[slot]);
-          float part_sum = 0.f;
 #pragma unroll
-          for (int part = 0; part < R / kPart; ++part) {
+          for (int c = 0; c < kCols; c += kPart) {
             uint32_t s[kPart];
             if (ok) {
               tc_fence_after();
               __syncwarp();
-              load_cols<kPart>(t0 + buf * 128 + part * kPart, s);
+              load_cols<kPart>(t0 + buf * 128 + c, s);
               tc_fence_before();
             }
-            if (part == R / kPart - 1) named_bar_arrive(kBarS + buf, 160);
-            if (ok) part_sum += inside ? weights<kPart, false>(s, a.sl2, nl + part * kPart, lim, key)
-                                       : weights<kPart, true>(s, a.sl2, nl + part * kPart,
-                                                              lim + part * kPart, key);
+            if (c + kPart == kCols) named_bar_arrive(kBarS + buf, 32 + 128 * C::HALVES);
+            if (ok) sum += inside ? weights<kPart, false>(s, a.sl2, nl + c, lim + c, key)
+                                  : weights<kPart, true>(s, a.sl2, nl + c, lim + c, key);
           }
-          sum += part_sum;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&l_empty[slot]);
@@ -447,7 +453,16 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
         d[6] = unit->s.nk;
         began = true;
       }
-      if (ok && live) {
+      if constexpr (C::HALVES == 2) {
+        // the halves' sums meet (a unit's end; `mine` is the same for both)
+        if (mine) {
+          if (half == 1) sSum[r] = sum;
+          named_bar_sync(kBarC + kt, 256);
+          if (half == 0) sum += sSum[r];
+          named_bar_sync(kBarC + kt, 256);
+        }
+      }
+      if (ok && live && half == 0) {
         if (whole)
           *dst = old + sum;
         else
