@@ -3,8 +3,8 @@
 //     scores[key] += sum over rows of 2^(S^T[key, row] * scale*log2e - lse2[row])
 // with S^T = K Q^T, 128 keys on the lanes of TMEM and a chunk of query rows
 // (tokens x heads of the kv head) on its columns.  A thread owns a key (two
-// threads do, one for each half of a chunk's 128 columns: sixteen warps hide
-// the latencies of the loads that eight did not, 183 -> %s us): it
+// threads do, one for the even steps and one for the odd: their waits and
+// their arithmetic then alternate on an SM sub-partition): it
 // reads its row of S^T, subtracts the rows' log-sum-exp (shared memory, the
 // same address for a whole warp), and adds the exponentials up in registers
 // over all chunks, so no value crosses lanes and nothing is added atomically.
@@ -51,10 +51,10 @@ struct ScCfg {
   // l_full[kNL], l_empty[kNL], drain
   static constexpr int NBARS = 2 * NK + 2 * NQS + 4 + 2 * kNL + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
-  // warps of the exponentials: four for each key tile, or four for each half
-  // of its columns
-  static constexpr int HALVES = R == 128 ? 2 : 1;
-  static constexpr int EW = 8 * HALVES;
+  // warps of the exponentials: four for each key tile, or four for each tile
+  // and parity of the step
+  static constexpr int GROUPS = R == 128 ? 2 : 1;
+  static constexpr int EW = 8 * GROUPS;
   static constexpr int WARPS = EW + 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads)
 // that buffer of S^T; kBarQ: stage helper with the MMA warp
 constexpr uint32_t kBarS = 1;
 constexpr uint32_t kBarQ = 5;
-constexpr uint32_t kBarC = 6;  // + t: the two halves of key tile t
+constexpr uint32_t kBarC = 6;  // + t: the two groups of key tile t
 
 template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
     for (int i = 0; i < kNL; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], C::EW);
+      mbar_init(&l_empty[i], 8);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     while (next()) {
       const int nt = tiles_of(*unit), n = unit->s1 - unit->s0;
       for (int t = 0; t < n; ++t, ++g) {
-        named_bar_sync(kBarQ, 64);  // the chunk (and the unit's keys) have landed
+        named_bar_sync(kBarQ, 64);  // the chunk, its constants and the unit's keys have landed
         tc_fence_after();
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
           const int buf = 2 * kt + (g & 1);
           // the buffer's previous scores have been read
           if ((g & 1) ? uses[2 * kt + 1]++ : uses[2 * kt]++) {
-            named_bar_sync(kBarS + buf, 32 + 128 * C::HALVES);
+            named_bar_sync(kBarS + buf, 160);
             tc_fence_after();
           }
           const uint32_t kd = k_lo + static_cast<uint32_t>((((ku % C::NK) * 2 + kt) * C::TILE) >> 4);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     // meet the last readers of each buffer
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (uses[i] > 0) named_bar_sync(kBarS + i, 32 + 128 * C::HALVES);
+      if (uses[i] > 0) named_bar_sync(kBarS + i, 160);
     mma_commit_elect(drain, 1u);
     if (lane == 0) drain_wait(drain, 0, kDrainNs);
     __syncwarp();
@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
       const int n = unit->s1 - unit->s0;
       for (int t = 0; t < n; ++t, ++g) {
         ok = ok && mbar_wait(&q_full[g % C::NQS], static_cast<uint32_t>((g / C::NQS) & 1), wc);
+        ok = ok && mbar_wait(&l_full[g % kNL], static_cast<uint32_t>((g / kNL) & 1), wc);
         __syncwarp();
         named_bar_sync(kBarQ, 64);
       }
@@ -394,12 +395,11 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     }
   } else {
     // -------------------------------------------------------- exponentials
-    constexpr int kCols = R / C::HALVES;  // columns of a thread
     const int kt = warp / (C::EW / 2);
-    const int half = (warp >> 2) % C::HALVES;
+    const int grp = (warp >> 2) % C::GROUPS;  // takes the steps of its parity
     const int r = (warp & 3) * 32 + lane;
     float* sSum = reinterpret_cast<float*>(smem + C::SUM_OFF) + kt * 128;
-    const uint32_t t0 = half * kCols + tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool ok = true;
     int g = 0;
     int ph[2] = {0, 0};  // phases of s_full consumed, per buffer
@@ -412,23 +412,27 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
       float* dst = a.scores + unit->b * a.ss[0] + unit->h * a.ss[1] + key;
       const bool live = mine && key < unit->s.nk && key < a.score_len;
       float old = 0.f;
-      if (live && whole && half == 0) old = *dst;  // on its way while the scores are computed
+      if (live && whole && grp == 0) old = *dst;  // on its way while the scores are computed
       float sum = 0.f;
       for (int t = 0; t < n; ++t, ++g) {
+        if (C::GROUPS == 2 && (g & 1) != grp) continue;
         const int slot = g % kNL;
-        ok = ok && mbar_wait(&l_full[slot], static_cast<uint32_t>((g / kNL) & 1), wc);
+        // (a warp without a tile waits for the constants all the same: its
+        // arrival below counts for this use of the slot)
+        if (!mine)
+          ok = ok && mbar_wait(&l_full[slot], static_cast<uint32_t>((g / kNL) & 1), wc);
         if (mine) {
           const int buf = 2 * kt + (g & 1);
           const int p = (g & 1) ? ph[1]++ : ph[0]++;
           ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], static_cast<uint32_t>(p & 1), wc));
           // 32 columns at a time, so that registers are left to have the
-          // rows' constants on their way
-          constexpr int kPart = kCols < 32 ? kCols : 32;
-          const float* nl = sLse + slot * 2 * R + half * kCols;
+          // rows' constants (which landed before s_full) on their way
+          constexpr int kPart = R < 32 ? R : 32;
+          const float* nl = sLse + slot * 2 * R;
           const int* lim = reinterpret_cast<const int*>(nl) + R;
           const bool inside = __all_sync(0xffffffffu, key < sMin[slot]);
 #pragma unroll
-          for (int c = 0; c < kCols; c += kPart) {
+          for (int c = 0; c < R; c += kPart) {
             uint32_t s[kPart];
             if (ok) {
               tc_fence_after();
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
               load_cols<kPart>(t0 + buf * 128 + c, s);
               tc_fence_before();
             }
-            if (c + kPart == kCols) named_bar_arrive(kBarS + buf, 32 + 128 * C::HALVES);
+            if (c + kPart == R) named_bar_arrive(kBarS + buf, 160);
             if (ok) sum += inside ? weights<kPart, false>(s, a.sl2, nl + c, lim + c, key)
                                   : weights<kPart, true>(s, a.sl2, nl + c, lim + c, key);
           }
@@ -453,16 +457,16 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
         d[6] = unit->s.nk;
         began = true;
       }
-      if constexpr (C::HALVES == 2) {
-        // the halves' sums meet (a unit's end; `mine` is the same for both)
+      if constexpr (C::GROUPS == 2) {
+        // the groups' sums meet (a unit's end; `mine` is the same for both)
         if (mine) {
-          if (half == 1) sSum[r] = sum;
+          if (grp == 1) sSum[r] = sum;
           named_bar_sync(kBarC + kt, 256);
-          if (half == 0) sum += sSum[r];
+          if (grp == 0) sum += sSum[r];
           named_bar_sync(kBarC + kt, 256);
         }
       }
-      if (ok && live && half == 0) {
+      if (ok && live && grp == 0) {
         if (whole)
           *dst = old + sum;
         else
