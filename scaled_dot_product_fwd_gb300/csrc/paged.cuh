@@ -88,6 +88,7 @@ struct Args {
   float* ws;   // partial results (see the kernels)
   int* desc;   // [CTAs][kDesc]: the unit that a CTA began and did not finish
   int nctas;
+  int max_ctas;  // (a test hook may ask for fewer than the plan's)
   // score sums
   float* scores;
   long long ss[2];
@@ -506,6 +507,9 @@ inline int box_log2(int page_size) {
 // 128-row tiles) and in keys (score sums).
 constexpr int kMaxRows = 256;
 constexpr int kMaxKeys = 256;
+// CTAs an SM that share a call's work, at most (their slots' rows together
+// are at most kMaxRows an SM).
+constexpr int kMaxCtas = 4;
 }  // namespace paged
 
 }  // namespace gb300

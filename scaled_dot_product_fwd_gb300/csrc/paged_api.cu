@@ -119,14 +119,11 @@ paged::Args make_args(const sdpa_paged_params_t& p) {
   return a;
 }
 
-// CTAs that share a call's work (two an SM at most), and the workspace:
-// their descriptors, then two slots of partial results each.
-int plan_ctas(int sms) {
-  const int forced = debug_option(SDPA_DEBUG_PAGED_CTAS);  // test hook
-  return forced > 0 ? std::min(forced, sms) : sms;
-}
+// The workspace: descriptors of the CTAs that share a call's work (at most
+// kMaxCtas an SM), then two slots of partial results each: one CTA an SM with
+// slots of kMaxRows rows, or several with as many rows together.
 size_t desc_bytes(int sms) {
-  return align256(static_cast<size_t>(2 * sms) * paged::kDesc * sizeof(int));
+  return align256(static_cast<size_t>(paged::kMaxCtas * sms) * paged::kDesc * sizeof(int));
 }
 size_t workspace(const sdpa_paged_params_t& p, int sms) {
   const size_t slot = static_cast<size_t>(paged::kMaxRows) * (p.head_dim + 2) * sizeof(float);
@@ -149,7 +146,9 @@ sdpa_status_t enter(const sdpa_paged_params_t& p, void* ws, size_t ws_bytes, voi
   *a = make_args(p);
   a->desc = static_cast<int*>(ws);
   a->ws = reinterpret_cast<float*>(static_cast<char*>(ws) + desc_bytes(sms));
-  a->nctas = plan_ctas(sms);
+  const int forced = debug_option(SDPA_DEBUG_PAGED_CTAS);  // test hook
+  a->max_ctas = forced > 0 ? forced : paged::kMaxCtas * sms;
+  a->nctas = std::min(a->max_ctas, sms);
   a->status = env->status;
   a->wait_ns = env->wait_limit_ns;
   return SDPA_OK;

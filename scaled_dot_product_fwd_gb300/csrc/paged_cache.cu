@@ -7,12 +7,13 @@
 //
 // Eviction, two kernels:
 //  - select (a CTA per (sequence, kv head)): the threshold weight is the
-//    keep'-th largest of the candidates, found digit by digit (8 bits each)
-//    from histograms of the weights' order-preserving integer form; then one
+//    keep'-th largest of the candidates, found digit by digit (11, 11 and 10
+//    bits) from histograms of the weights' order-preserving integer form,
+//    which up to 48 Ki positions stay in shared memory; then one
 //    ordered pass over the positions writes the kept ones (above the
 //    threshold, the first of those equal to it, and the newest) in ascending
 //    order by a scan, and the weights' new places.
-//  - move (a CTA per (sequence, kv head), K or V, 128-byte slice of the
+//  - move (a CTA per (sequence, kv head), K or V, 64-byte slice of the
 //    rows): row kept[i] goes to row i.  kept[i] >= i, and the sources of a
 //    chunk lie behind the destinations of every earlier chunk, so a CTA that
 //    takes the chunks in order, loads the next one early and writes a chunk
@@ -118,7 +119,7 @@ struct EvictArgs {
   char* kp;
   char* vp;
   long long kb[3], vb[3];  // byte strides of the cache (page, head, row)
-  int slices;              // 128-byte slices of a row
+  int slices;              // kSlice-byte slices of a row
 };
 
 // Integer whose order is the weights' order: sign bit flipped for positive
@@ -131,11 +132,22 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 constexpr int kSelT = 1024;
+constexpr int kSelE = 4;  // positions of a thread in the ordered pass
+constexpr int kBins = 2048;
+// weights that the select kernel keeps in shared memory (more are read from
+// global memory again for each digit)
+constexpr int kSelCache = 48 * 1024;
 
-__global__ void __launch_bounds__(kSelT) paged_evict_select_kernel(const EvictArgs e) {
+__global__ void __launch_bounds__(kSelT)
+    paged_evict_select_kernel(const EvictArgs e, const int cache) {
   const Args& a = e.a;
   const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ uint32_t s_key[];  // [cache]
+  __shared__ int hist[kBins];
+  __shared__ int warp_sum[32];
+  __shared__ uint32_t s_digit;
+  __shared__ int s_want;
   griddep_launch_dependents();
   const int nk = min(max(a.lens[b], 0), a.cap);
   int* kept = e.kept + static_cast<size_t>(blockIdx.x) * e.keep;
@@ -151,63 +163,70 @@ __global__ void __launch_bounds__(kSelT) paged_evict_select_kernel(const EvictAr
     return;
   }
   const int rec = min(e.recent, e.keep);
-  const int cand = nk - rec;    // positions below it compete
-  int want = e.keep - rec;      // for these places
+  const int cand = nk - rec;  // positions below it compete
+  int want = e.keep - rec;    // for these places
   auto weight = [&](int i) { return i < e.score_len ? sc[i] : 0.f; };
+  const bool cached = cand <= cache;
+  if (cached) {
+#pragma unroll 8
+    for (int i = tid; i < cand; i += kSelT) s_key[i] = order_key(weight(i));
+  }
+  auto key_of = [&](int i) { return cached ? s_key[i] : order_key(weight(i)); };
 
-  // the want-th largest key, from its top digit down
-  __shared__ int hist[256];
-  __shared__ int warp_sum[32];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_want;
+  // the want-th largest key, from its top digit down (11, 11 and 10 bits)
   uint32_t prefix = 0, mask = 0;
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      const uint32_t dmask = d == 2 ? 1023u : 2047u;
+      hist[tid] = 0;
+      hist[tid + kSelT] = 0;
+      __syncthreads();  // (and the keys are in shared memory)
+#pragma unroll 4
       for (int i0 = 0; i0 < cand; i0 += kSelT) {
         const int i = i0 + tid;
-        uint32_t key = 0;
-        bool in = i < cand;
-        if (in) {
-          key = order_key(weight(i));
-          in = (key & mask) == prefix;
+        const uint32_t key = i < cand ? key_of(i) : 0u;
+        const bool in = i < cand && (key & mask) == prefix;
+        const uint32_t digit = (key >> shift) & dmask;
+        // one add for a warp of one digit (equal weights)
+        int same;
+        __match_all_sync(0xffffffffu, in ? digit : 0x80000000u + lane, &same);
+        if (same) {
+          if (lane == 0) atomicAdd(&hist[digit], 32);
+        } else if (in) {
+          atomicAdd(&hist[digit], 1);
         }
-        // lanes of one digit add up before the shared-memory atomic: weights
-        // share their top digits
-        const uint32_t digit = (key >> shift) & 255u;
-        const uint32_t same = __match_any_sync(0xffffffffu, in ? digit : 256u);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
       }
       __syncthreads();
-      if (warp == 0) {  // suffix sums: lane holds digits 255 - 8 lane .. 248 - 8 lane
-        int c[8], sum = 0;
+      // how many keys have a larger digit: thread t holds digits 2047 - 2t
+      // and 2046 - 2t
+      const int c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
+      int incl = c0 + c1;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          c[k] = hist[255 - 8 * lane - k];
-          sum += c[k];
-        }
-        int incl = sum;
+      for (int k = 1; k < 32; k <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, k);
+        if (lane >= k) incl += t;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      int w = warp_sum[lane];
+      int wi = w;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int t = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += t;
-        }
-        int before = incl - sum;
-        if (before < want && want <= incl) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (before < want && want <= before + c[k]) {
-              s_digit = static_cast<uint32_t>(255 - 8 * lane - k);
-              s_want = want - before;
-            }
-            before += c[k];
-          }
-        }
+      for (int k = 1; k < 32; k <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, wi, k);
+        if (lane >= k) wi += t;
+      }
+      const int before = incl - c0 - c1 + __shfl_sync(0xffffffffu, wi - w, warp);
+      if (before < want && want <= before + c0) {
+        s_digit = static_cast<uint32_t>(kBins - 1 - 2 * tid);
+        s_want = want - before;
+      } else if (before + c0 < want && want <= before + c0 + c1) {
+        s_digit = static_cast<uint32_t>(kBins - 2 - 2 * tid);
+        s_want = want - before - c0;
       }
       __syncthreads();
       prefix |= s_digit << shift;
-      mask |= 255u << shift;
+      mask |= dmask << shift;
       want = s_want;
     }
   }
@@ -216,39 +235,53 @@ __global__ void __launch_bounds__(kSelT) paged_evict_select_kernel(const EvictAr
   // recent, and of the equal ones at most `want`).
   const bool none = e.keep == rec;  // only the newest stay
   int run_gt = 0, run_eq = 0;
-  for (int i0 = 0; i0 < nk; i0 += kSelT) {
-    const int i = i0 + tid;
-    bool gt = false, eq = false;
-    float x = 0.f;
-    if (i < nk) {
-      x = weight(i);
-      if (i >= cand) {
-        gt = true;
-      } else if (!none) {
-        const uint32_t key = order_key(x);
-        gt = key > prefix;
-        eq = key == prefix;
+  for (int i0 = 0; i0 < nk; i0 += kSelT * kSelE) {
+    uint32_t gt = 0, eq = 0;  // a bit for each of the thread's positions
+    float x[kSelE];
+#pragma unroll
+    for (int k = 0; k < kSelE; ++k) {
+      const int i = i0 + tid * kSelE + k;
+      x[k] = 0.f;
+      if (i < nk) {
+        if (out || !cached || i >= cand) x[k] = weight(i);
+        if (i >= cand) {
+          gt |= 1u << k;
+        } else if (!none) {
+          const uint32_t key = cached ? s_key[i] : order_key(x[k]);
+          if (key > prefix) gt |= 1u << k;
+          if (key == prefix) eq |= 1u << k;
+        }
       }
     }
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    const uint32_t lt = (1u << lane) - 1u;
-    int before = __popc(bg & lt) | (__popc(be & lt) << 16);
-    if (lane == 0) warp_sum[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();  // (every weight of this chunk is read: `out` may be `sc`)
-    int w = warp_sum[lane];
-    int incl = w;
+    const int mine = __popc(gt) | (__popc(eq) << 16);
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += t;
     }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    before += __shfl_sync(0xffffffffu, incl - w, warp);
-    const int ng = run_gt + (before & 0xffff), ne = run_eq + (before >> 16);
-    if (gt || (eq && ne < want)) {
-      const int place = ng + min(ne, want);
-      kept[place] = i;
-      if (out && place < e.score_len) out[place] = x;
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();  // (every weight of this chunk is read: `out` may be `sc`)
+    int w = warp_sum[lane];
+    int wi = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, wi, d);
+      if (lane >= d) wi += t;
+    }
+    const int total = __shfl_sync(0xffffffffu, wi, 31);
+    const int before = incl - mine + __shfl_sync(0xffffffffu, wi - w, warp);
+    int ng = run_gt + (before & 0xffff), ne = run_eq + (before >> 16);
+#pragma unroll
+    for (int k = 0; k < kSelE; ++k) {
+      const bool g = (gt >> k) & 1u, q = (eq >> k) & 1u;
+      if (g || (q && ne < want)) {
+        const int place = ng + min(ne, want);
+        kept[place] = i0 + tid * kSelE + k;
+        if (out && place < e.score_len) out[place] = x[k];
+      }
+      ng += g;
+      ne += q;
     }
     run_gt += total & 0xffff;
     run_eq += total >> 16;
@@ -259,10 +292,13 @@ __global__ void __launch_bounds__(kSelT) paged_evict_select_kernel(const EvictAr
 }
 
 constexpr int kMoveT = 256;
-constexpr int kMoveRows = 4;                        // rows of a thread in a chunk
-constexpr int kMoveChunk = kMoveRows * kMoveT / 8;  // rows of a chunk (8 threads a slice)
+constexpr int kSlice = 64;                              // bytes of a row that a CTA moves
+constexpr int kLanes = kSlice / 16;                     // threads of a row
+constexpr int kMoveRows = 8;                            // rows of a thread in a chunk
+constexpr int kMoveStep = kMoveT / kLanes;              // rows of the CTA at a time
+constexpr int kMoveChunk = kMoveRows * kMoveStep;
 
-__global__ void __launch_bounds__(kMoveT) paged_evict_move_kernel(const EvictArgs e) {
+__global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const EvictArgs e) {
   const Args& a = e.a;
   griddep_wait();
   int x = blockIdx.x;
@@ -275,31 +311,42 @@ __global__ void __launch_bounds__(kMoveT) paged_evict_move_kernel(const EvictArg
   if (h == 0 && slice == 0 && !is_v && threadIdx.x == 0 && e.lens_out)
     e.lens_out[b] = min(min(max(a.lens[b], 0), a.cap), e.keep);
   const long long* st = is_v ? e.vb : e.kb;
-  char* base = (is_v ? e.vp : e.kp) + h * st[1] + slice * 128 + (threadIdx.x & 7) * 16;
-  const int r0 = threadIdx.x >> 3;
+  char* base = (is_v ? e.vp : e.kp) + h * st[1] + slice * kSlice + (threadIdx.x % kLanes) * 16;
+  const int* table = a.table + b * a.table_stride;
+  const int r0 = threadIdx.x / kLanes;
   struct Chunk {
     uint4 data[kMoveRows];
-    char* dst[kMoveRows];  // nullptr: nothing to move
+    long long dst[kMoveRows];  // -1: nothing to move
   };
-  // rows [i0, i0 + kMoveChunk): issue the loads
+  // rows [i0, i0 + kMoveChunk): positions, then pages, then the loads
   auto load = [&](int i0, Chunk& c) {
-    int src[kMoveRows];
+    int src[kMoveRows], ps[kMoveRows], pd[kMoveRows];
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
-      const int i = i0 + r0 + k * (kMoveT / 8);
+      const int i = i0 + r0 + k * kMoveStep;
       src[k] = i < e.keep ? kept[i] : -1;
     }
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
-      const int i = i0 + r0 + k * (kMoveT / 8);
-      c.dst[k] = nullptr;
-      c.data[k] = make_uint4(0, 0, 0, 0);
+      const int i = i0 + r0 + k * kMoveStep;
+      ps[k] = pd[k] = -1;
       if (src[k] > i) {  // (a row that stays needs no move)
-        const int ps = page_of(a, b, src[k]), pd = page_of(a, b, i);
-        if (ps >= 0 && pd >= 0) {
-          c.data[k] = *reinterpret_cast<const uint4*>(base + ps * st[0] +
-                                                      (src[k] % a.page_size) * st[2]);
-          c.dst[k] = base + pd * st[0] + (i % a.page_size) * st[2];
+        ps[k] = table[a.by_page.div(src[k])];
+        pd[k] = table[a.by_page.div(i)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int i = i0 + r0 + k * kMoveStep;
+      c.dst[k] = -1;
+      c.data[k] = make_uint4(0, 0, 0, 0);
+      if (src[k] > i) {
+        if (ps[k] < 0 || ps[k] >= a.num_pages || pd[k] < 0 || pd[k] >= a.num_pages) {
+          atomicExch(a.status, kStatusPageTable);
+        } else {
+          c.data[k] = *reinterpret_cast<const uint4*>(base + ps[k] * st[0] +
+                                                      a.by_page.mod(src[k]) * st[2]);
+          c.dst[k] = pd[k] * st[0] + a.by_page.mod(i) * st[2];
         }
       }
     }
@@ -313,7 +360,7 @@ __global__ void __launch_bounds__(kMoveT) paged_evict_move_kernel(const EvictArg
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k)
-      if (c.dst[k]) *reinterpret_cast<uint4*>(c.dst[k]) = c.data[k];
+      if (c.dst[k] >= 0) *reinterpret_cast<uint4*>(base + c.dst[k]) = c.data[k];
   };
   Chunk c0, c1;
   load(0, c0);
@@ -379,9 +426,13 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
     e.kb[i] = a.ks[i] * elem;
     e.vb[i] = a.vs[i] * elem;
   }
-  e.slices = row_bytes / 128;
+  e.slices = row_bytes / kSlice;
   const unsigned bh = static_cast<unsigned>(a.B) * a.Hkv;
-  paged_evict_select_kernel<<<bh, kSelT, 0, stream>>>(e);
+  const int cache = a.cap < kSelCache ? a.cap : kSelCache;
+  if (cudaFuncSetAttribute(paged_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSelCache * 4) != cudaSuccess)
+    return SDPA_ERR_CUDA;
+  paged_evict_select_kernel<<<bh, kSelT, cache * 4, stream>>>(e, cache);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -135,8 +136,19 @@ constexpr int attend_smem() {
   return (RM * D + kKT * (D + 4) + kKT * D + RM * (kKT + 4)) * 4;
 }
 
+// CTAs an SM: what the shared memory and the registers of a tile allow (one of
+// 8 warps alone leaves the FMA pipes waiting for shared memory).
+template <int D, int RM>
+constexpr int attend_ctas() {
+  return RM == 16 ? (D == 64 ? 4 : 2) : (D == 64 ? 2 : 1);
+}
+template <int D>
+constexpr int scores_ctas() {
+  return D == 64 ? 3 : 2;
+}
+
 template <typename T, int D, int RM>
-__global__ void __launch_bounds__(kT) paged_simt_kernel(const Args a) {
+__global__ void __launch_bounds__(kT, attend_ctas<D, RM>()) paged_simt_kernel(const Args a) {
   constexpr int RPT = RM / 16;
   constexpr int CG = D / 64;  // float4 column groups of a thread
   constexpr int kSlot = RM * (D + 2);
@@ -417,7 +429,7 @@ constexpr int scores_smem() {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kT) paged_scores_simt_kernel(const Args a) {
+__global__ void __launch_bounds__(kT, scores_ctas<D>()) paged_scores_simt_kernel(const Args a) {
   constexpr int RM = 64;
   extern __shared__ float smem[];
   float* sQ = smem;
@@ -534,7 +546,8 @@ sdpa_status_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStrea
 }
 
 template <typename K>
-sdpa_status_t start(K kern, const Args& a, int smem, cudaStream_t stream) {
+sdpa_status_t start(K kern, Args& a, int smem, int ctas, cudaStream_t stream) {
+  a.nctas = std::min(a.max_ctas, ctas);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return SDPA_ERR_CUDA;
@@ -549,8 +562,10 @@ sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   fit_rows(a, few && a.G <= 16 ? 16 : 64);
   const int rows = few && a.G <= 16 ? 16 : 64;
   const sdpa_status_t st =
-      rows == 16 ? start(paged_simt_kernel<T, D, 16>, a, attend_smem<D, 16>(), env.stream)
-                 : start(paged_simt_kernel<T, D, 64>, a, attend_smem<D, 64>(), env.stream);
+      rows == 16 ? start(paged_simt_kernel<T, D, 16>, a, attend_smem<D, 16>(),
+                         attend_ctas<D, 16>() * env.num_sms, env.stream)
+                 : start(paged_simt_kernel<T, D, 64>, a, attend_smem<D, 64>(),
+                         attend_ctas<D, 64>() * env.num_sms, env.stream);
   return st != SDPA_OK ? st
                        : launch_paged_merge(a, D, sizeof(T) == 4                          ? SDPA_F32
                                                   : std::is_same<T, __half>::value ? SDPA_F16
@@ -562,7 +577,7 @@ template <typename T, int D>
 sdpa_status_t score(Args& a, const LaunchEnv& env) {
   fit_rows(a, 64);
   const sdpa_status_t st =
-      start(paged_scores_simt_kernel<T, D>, a, scores_smem<D>(), env.stream);
+      start(paged_scores_simt_kernel<T, D>, a, scores_smem<D>(), scores_ctas<D>() * env.num_sms, env.stream);
   return st != SDPA_OK ? st : launch_paged_scores_merge(a, kKT, env.stream);
 }
 
