@@ -315,7 +315,7 @@ sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* p, int32_t keep, int32
   const int es = elem_size(*p);
   st = launch_paged_evict(a, p->head_dim * es, es, keep, recent, k_pages, v_pages, scores,
                           scores_out, score_stride, score_len, kept, seq_lens_out, env.stream);
-  if (st == SDPA_OK) set_last_launches(2);
+  if (st == SDPA_OK) set_last_launches(3);
   return st;
 }
 

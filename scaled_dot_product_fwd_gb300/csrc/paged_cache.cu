@@ -5,7 +5,7 @@
 // Write: one warp a token; its lanes bring the token's K and V rows (all kv
 // heads) with 16-byte loads, issued before the warp looks its sequence up.
 //
-// Eviction, two kernels:
+// Eviction, three kernels:
 //  - select (a CTA per (sequence, kv head)): the threshold weight is the
 //    keep'-th largest of the candidates, found digit by digit (11, 11 and 10
 //    bits) from histograms of the weights' order-preserving integer form,
@@ -14,11 +14,14 @@
 //    threshold, the first of those equal to it, and the newest) in ascending
 //    order by a scan, and the weights' new places.
 //  - move (a CTA per (sequence, kv head), K or V, 64-byte slice of the
-//    rows): row kept[i] goes to row i.  kept[i] >= i, and the sources of a
-//    chunk lie behind the destinations of every earlier chunk, so a CTA that
-//    takes the chunks in order, loads the next one early and writes a chunk
-//    only when every thread has its rows in registers, moves in place
-//    without losing a row.
+//    rows): row kept[i] goes to row i, for the kept[i] below `keep`, whose
+//    rows other moves overwrite.  kept[i] >= i, and the sources of a chunk lie
+//    behind the destinations of every earlier chunk, so a CTA that takes the
+//    chunks in order, loads the next one early and writes a chunk only when
+//    every thread has its rows in registers, moves in place without losing a
+//    row.
+//  - far: the rows from positions at or past `keep`, which no move writes, in
+//    any order over the whole GPU.
 #include <cuda_runtime.h>
 
 #include "paged.cuh"
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kSelT)
   const Args& a = e.a;
   const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  extern __shared__ uint32_t s_key[];  // [cache]
+  extern __shared__ float s_weight[];  // [cache]
   __shared__ int hist[kBins];
   __shared__ int warp_sum[32];
   __shared__ uint32_t s_digit;
@@ -165,13 +168,16 @@ __global__ void __launch_bounds__(kSelT)
   const int rec = min(e.recent, e.keep);
   const int cand = nk - rec;  // positions below it compete
   int want = e.keep - rec;    // for these places
-  auto weight = [&](int i) { return i < e.score_len ? sc[i] : 0.f; };
-  const bool cached = cand <= cache;
+  const bool cached = nk <= cache;
   if (cached) {
 #pragma unroll 8
-    for (int i = tid; i < cand; i += kSelT) s_key[i] = order_key(weight(i));
+    for (int i = tid; i < nk; i += kSelT) s_weight[i] = i < e.score_len ? sc[i] : 0.f;
+    __syncthreads();
   }
-  auto key_of = [&](int i) { return cached ? s_key[i] : order_key(weight(i)); };
+  auto weight = [&](int i) {
+    return cached ? s_weight[i] : i < e.score_len ? sc[i] : 0.f;
+  };
+  auto key_of = [&](int i) { return order_key(weight(i)); };
 
   // the want-th largest key, from its top digit down (11, 11 and 10 bits)
   uint32_t prefix = 0, mask = 0;
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kSelT)
       const uint32_t dmask = d == 2 ? 1023u : 2047u;
       hist[tid] = 0;
       hist[tid + kSelT] = 0;
-      __syncthreads();  // (and the keys are in shared memory)
+      __syncthreads();
 #pragma unroll 4
       for (int i0 = 0; i0 < cand; i0 += kSelT) {
         const int i = i0 + tid;
@@ -243,11 +249,11 @@ __global__ void __launch_bounds__(kSelT)
       const int i = i0 + tid * kSelE + k;
       x[k] = 0.f;
       if (i < nk) {
-        if (out || !cached || i >= cand) x[k] = weight(i);
+        x[k] = weight(i);
         if (i >= cand) {
           gt |= 1u << k;
         } else if (!none) {
-          const uint32_t key = cached ? s_key[i] : order_key(x[k]);
+          const uint32_t key = order_key(x[k]);
           if (key > prefix) gt |= 1u << k;
           if (key == prefix) eq |= 1u << k;
         }
@@ -300,76 +306,143 @@ constexpr int kMoveChunk = kMoveRows * kMoveStep;
 
 __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const EvictArgs e) {
   const Args& a = e.a;
+  // Where a chunk's rows come from (-1: no move) and go to, looked up two
+  // chunks ahead by one thread a row; four chunks' worth, so that the writes
+  // for chunk n + 2 never meet the last reads for chunk n - 1.
+  __shared__ long long s_from[4][kMoveChunk], s_to[4][kMoveChunk];
+  __shared__ int s_more[4];
   griddep_wait();
+  griddep_launch_dependents();
   int x = blockIdx.x;
   const int slice = x % e.slices;
   x /= e.slices;
   const bool is_v = x & 1;
   const int bh = x >> 1;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int tid = threadIdx.x;
   const int* kept = e.kept + static_cast<size_t>(bh) * e.keep;
-  if (h == 0 && slice == 0 && !is_v && threadIdx.x == 0 && e.lens_out)
+  if (h == 0 && slice == 0 && !is_v && tid == 0 && e.lens_out)
     e.lens_out[b] = min(min(max(a.lens[b], 0), a.cap), e.keep);
   const long long* st = is_v ? e.vb : e.kb;
-  char* base = (is_v ? e.vp : e.kp) + h * st[1] + slice * kSlice + (threadIdx.x % kLanes) * 16;
+  char* base = (is_v ? e.vp : e.kp) + h * st[1] + slice * kSlice + (tid % kLanes) * 16;
   const int* table = a.table + b * a.table_stride;
-  const int r0 = threadIdx.x / kLanes;
-  struct Chunk {
-    uint4 data[kMoveRows];
-    long long dst[kMoveRows];  // -1: nothing to move
-  };
-  // rows [i0, i0 + kMoveChunk): positions, then pages, then the loads
-  auto load = [&](int i0, Chunk& c) {
-    int src[kMoveRows], ps[kMoveRows], pd[kMoveRows];
+  const int r0 = tid / kLanes;
+  auto lookup = [&](int n) {
+    constexpr int N = kMoveChunk / kMoveT;
+    int src[N];
 #pragma unroll
-    for (int k = 0; k < kMoveRows; ++k) {
-      const int i = i0 + r0 + k * kMoveStep;
+    for (int k = 0; k < N; ++k) {
+      const long long i = static_cast<long long>(n) * kMoveChunk + k * kMoveT + tid;
       src[k] = i < e.keep ? kept[i] : -1;
     }
+    // (the positions ascend: the first at or past `keep`, the second kernel's,
+    // or the end of a short sequence ends this kernel's part)
+    if (tid == 0) s_more[n & 3] = src[0] >= 0 && src[0] < e.keep;
 #pragma unroll
-    for (int k = 0; k < kMoveRows; ++k) {
-      const int i = i0 + r0 + k * kMoveStep;
-      ps[k] = pd[k] = -1;
-      if (src[k] > i) {  // (a row that stays needs no move)
-        ps[k] = table[a.by_page.div(src[k])];
-        pd[k] = table[a.by_page.div(i)];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kMoveRows; ++k) {
-      const int i = i0 + r0 + k * kMoveStep;
-      c.dst[k] = -1;
-      c.data[k] = make_uint4(0, 0, 0, 0);
-      if (src[k] > i) {
-        if (ps[k] < 0 || ps[k] >= a.num_pages || pd[k] < 0 || pd[k] >= a.num_pages) {
+    for (int k = 0; k < N; ++k) {
+      const int r = k * kMoveT + tid, i = n * kMoveChunk + r;
+      long long from = -1, to = 0;
+      if (src[k] > i && src[k] < e.keep) {  // (a row that stays needs no move)
+        const int ps = table[a.by_page.div(src[k])], pd = table[a.by_page.div(i)];
+        if (ps < 0 || ps >= a.num_pages || pd < 0 || pd >= a.num_pages) {
           atomicExch(a.status, kStatusPageTable);
         } else {
-          c.data[k] = *reinterpret_cast<const uint4*>(base + ps[k] * st[0] +
-                                                      a.by_page.mod(src[k]) * st[2]);
-          c.dst[k] = pd[k] * st[0] + a.by_page.mod(i) * st[2];
+          from = ps * st[0] + a.by_page.mod(src[k]) * st[2];
+          to = pd * st[0] + a.by_page.mod(i) * st[2];
         }
       }
+      s_from[n & 3][r] = from;
+      s_to[n & 3][r] = to;
     }
   };
-  auto store = [&](Chunk& c) {
+  auto load = [&](int n, uint4 (&data)[kMoveRows]) {
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      const long long from = s_from[n & 3][r0 + k * kMoveStep];
+      data[k] = make_uint4(0, 0, 0, 0);
+      if (from >= 0) data[k] = *reinterpret_cast<const uint4*>(base + from);
+    }
+  };
+  auto store = [&](int n, uint4 (&data)[kMoveRows]) {
     // every row of the chunk is in registers before any thread writes
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k)
-      asm volatile("" : "+r"(c.data[k].x), "+r"(c.data[k].y), "+r"(c.data[k].z),
-                        "+r"(c.data[k].w) : : "memory");
+      asm volatile("" : "+r"(data[k].x), "+r"(data[k].y), "+r"(data[k].z), "+r"(data[k].w)
+                   : : "memory");
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMoveRows; ++k)
-      if (c.dst[k] >= 0) *reinterpret_cast<uint4*>(base + c.dst[k]) = c.data[k];
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int r = r0 + k * kMoveStep;
+      if (s_from[n & 3][r] >= 0) *reinterpret_cast<uint4*>(base + s_to[n & 3][r]) = data[k];
+    }
   };
-  Chunk c0, c1;
-  load(0, c0);
-  for (int i0 = 0; i0 < e.keep; i0 += 2 * kMoveChunk) {
-    load(i0 + kMoveChunk, c1);
-    store(c0);
-    if (i0 + kMoveChunk >= e.keep) break;
-    load(i0 + 2 * kMoveChunk, c0);
-    store(c1);
+  lookup(0);
+  lookup(1);
+  __syncthreads();
+  uint4 d0[kMoveRows], d1[kMoveRows];
+  load(0, d0);
+  for (int n = 0; s_more[n & 3]; n += 2) {
+    load(n + 1, d1);
+    lookup(n + 2);
+    store(n, d0);
+    if (!s_more[(n + 1) & 3]) break;
+    load(n + 2, d0);
+    lookup(n + 3);
+    store(n + 1, d1);
+  }
+}
+
+// Rows from positions at or past `keep`: no move writes there, so they go in
+// any order once the rows above have been read.  A warp takes 32 rows: a lane
+// looks one row's pages up, and the warp copies the rows two to eight at a
+// time.
+constexpr int kFarT = 256;
+constexpr int kFarPer = 32 * kFarT / 32;  // rows of a CTA
+
+__global__ void __launch_bounds__(kFarT) paged_evict_far_kernel(const EvictArgs e, int lg_lanes) {
+  const Args& a = e.a;
+  griddep_wait();
+  const int chunks = (e.keep + kFarPer - 1) / kFarPer;
+  const int chunk = blockIdx.x % chunks;
+  const int x = blockIdx.x / chunks;
+  const bool is_v = x & 1;
+  const int bh = x >> 1;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int lane = threadIdx.x & 31;
+  const long long* st = is_v ? e.vb : e.kb;
+  char* base = (is_v ? e.vp : e.kp) + h * st[1] + (lane & ((1 << lg_lanes) - 1)) * 16;
+  const int* table = a.table + b * a.table_stride;
+  const int i = chunk * kFarPer + (threadIdx.x & ~31) + lane;
+  const int src = i < e.keep ? e.kept[static_cast<size_t>(bh) * e.keep + i] : -1;
+  long long from = -1, to = 0;
+  if (src >= e.keep) {
+    const int ps = table[a.by_page.div(src)], pd = table[a.by_page.div(i)];
+    if (ps < 0 || ps >= a.num_pages || pd < 0 || pd >= a.num_pages) {
+      atomicExch(a.status, kStatusPageTable);
+    } else {
+      from = ps * st[0] + a.by_page.mod(src) * st[2];
+      to = pd * st[0] + a.by_page.mod(i) * st[2];
+    }
+  }
+  if (__all_sync(0xffffffffu, from < 0)) return;
+  const int rows = 32 >> lg_lanes;  // rows at a time (2 lanes << lg_lanes = 32)
+  constexpr int U = 8;
+  for (int r0 = 0; r0 < 32; r0 += U * rows) {
+    uint4 data[U];
+    long long dst[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int r = r0 + k * rows + (lane >> lg_lanes);
+      const long long f = __shfl_sync(0xffffffffu, from, r & 31);
+      dst[k] = __shfl_sync(0xffffffffu, to, r & 31);
+      if (r >= 32 || f < 0)
+        dst[k] = -1;
+      else
+        data[k] = *reinterpret_cast<const uint4*>(base + f);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (dst[k] >= 0) *reinterpret_cast<uint4*>(base + dst[k]) = data[k];
   }
 }
 
@@ -432,6 +505,9 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
   if (cudaFuncSetAttribute(paged_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSelCache * 4) != cudaSuccess)
     return SDPA_ERR_CUDA;
+  // (checked before the first launch, so that a refused call moves nothing)
+  if (static_cast<long long>(bh) * 2 * ((keep - 1) / kFarPer + 1) > 0x7fffffffLL)
+    return SDPA_ERR_UNSUPPORTED;
   paged_evict_select_kernel<<<bh, kSelT, cache * 4, stream>>>(e, cache);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
@@ -443,8 +519,13 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_evict_move_kernel, e) == cudaSuccess ? SDPA_OK
-                                                                             : SDPA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_evict_move_kernel, e) != cudaSuccess) return SDPA_ERR_CUDA;
+  int lg = 0;  // lanes of a row
+  while ((16 << lg) < row_bytes) ++lg;
+  cfg.gridDim = dim3(bh * 2 * static_cast<unsigned>((keep - 1) / kFarPer + 1));
+  cfg.blockDim = dim3(kFarT);
+  return cudaLaunchKernelEx(&cfg, paged_evict_far_kernel, e, lg) == cudaSuccess ? SDPA_OK
+                                                                                : SDPA_ERR_CUDA;
 }
 
 }  // namespace gb300
