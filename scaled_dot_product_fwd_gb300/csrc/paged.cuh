@@ -459,7 +459,7 @@ sdpa_status_t launch_paged_write(const paged::Args& a, int row_bytes, const void
 sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, int keep,
                                  int recent, void* k_pages, void* v_pages, const float* scores,
                                  float* scores_out, const int64_t* ss, int score_len, int* kept,
-                                 int* lens_out, cudaStream_t stream);
+                                 int* lens_out, cudaStream_t stream, int* launches);
 
 namespace paged {
 // The tensor-core kernels see a cache as blocks of page_size rows, block (page,

@@ -313,9 +313,11 @@ sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* p, int32_t keep, int32
   paged::Args a = make_args(*p);
   a.status = env.status;
   const int es = elem_size(*p);
+  int launches = 0;
   st = launch_paged_evict(a, p->head_dim * es, es, keep, recent, k_pages, v_pages, scores,
-                          scores_out, score_stride, score_len, kept, seq_lens_out, env.stream);
-  if (st == SDPA_OK) set_last_launches(3);
+                          scores_out, score_stride, score_len, kept, seq_lens_out, env.stream,
+                          &launches);
+  if (st == SDPA_OK) set_last_launches(launches);
   return st;
 }
 
