@@ -308,13 +308,31 @@ __global__ void __launch_bounds__(kT, attend_ctas<D, RM>()) paged_simt_kernel(co
 
 // Joins the partial results of the units that CTAs of the attention kernels
 // began and did not finish: M = max of the m's, weights 2^(m - M), in the
-// order of the pieces.  Block (c, y) takes rows y, y + gridDim.y, ... of the
-// unit that CTA c began (by groups of 8 rows, one a warp; of a unit in more
-// than kWide pieces one row at a time, its pieces spread over the warps).
+// order of the pieces.  Block (c, y) takes a part of the rows of the unit that
+// CTA c began.  Bound by the latency of its few loads, so a warp takes two rows
+// and has their (m, l), a piece a lane, and up to kAhead pieces of their
+// outputs on their way at once.  A unit of more than kWide pieces (a few rows
+// of a long sequence spread over the whole GPU): a row at a time, its pieces
+// spread over the block's warps.
 constexpr int kWide = 12;
+constexpr int kAhead = 3;
+constexpr int kMergeRows = 2;
+
+template <int D>
+struct MergeVec;
+template <>
+struct MergeVec<128> {
+  using V = float4;
+};
+template <>
+struct MergeVec<64> {
+  using V = float2;
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     paged_merge_kernel(const Args a, int tile_rows, int tiles) {
+  using V = typename MergeVec<D>::V;
   constexpr int E = D / 32;  // columns of a lane
   griddep_wait();
   const int c = blockIdx.x;
@@ -326,73 +344,20 @@ __global__ void __launch_bounds__(256)
   const int rows = tile_rows * tiles;
   const size_t slot_floats = static_cast<size_t>(rows) * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool wide = n > kWide;
-  __shared__ float sM[8], sL[8], sO[8][D];
   auto piece = [&](int p) {
     return a.ws + (p == 0 ? static_cast<size_t>(c * 2 + 1) : static_cast<size_t>((c + p) * 2)) *
                       slot_floats;
   };
-  const int step = wide ? gridDim.y : gridDim.y * 8;
-  for (int r0 = wide ? blockIdx.y : blockIdx.y * 8; r0 < rows; r0 += step) {
-    const int rr = wide ? r0 : r0 + warp;  // row of the unit
-    const int t = rr / tile_rows, r = rr % tile_rows;
-    const int tok = (j * tiles + t) * a.w + a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
-    const bool live = rr < rows && r < a.w * a.gu && tok < nq && e < a.G;
-    if (wide && !live) continue;  // the same for every warp
-    float M = -INFINITY, L = 0.f, acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.f;
-    if (live) {
-#pragma unroll 4
-      for (int p = wide ? warp : 0; p < n; p += wide ? 8 : 1) {
-        const float* s = piece(p);
-        const float m = s[static_cast<size_t>(rows) * D + rr];
-        const float l = s[static_cast<size_t>(rows) * (D + 1) + rr];
-        float v[E];
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(s + static_cast<size_t>(rr) * D +
-                                                            (i / 2) * 64 + lane * 2);
-          v[i] = x.x;
-          v[i + 1] = x.y;
-        }
-        if (l != 0.f) {  // a piece whose keys the row does not see holds nothing
-          const float mn = fmaxf(M, m);
-          const float f = ex2(M - mn), g = ex2(m - mn);
-          L = L * f + l * g;
-#pragma unroll
-          for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + v[i] * g;
-          M = mn;
-        }
-      }
-    }
-    if (wide) {
-      __syncthreads();
-      if (lane == 0) {
-        sM[warp] = M;
-        sL[warp] = L;
-      }
-#pragma unroll
-      for (int i = 0; i < E; i += 2)
-        *reinterpret_cast<float2*>(&sO[warp][(i / 2) * 64 + lane * 2]) =
-            make_float2(acc[i], acc[i + 1]);
-      __syncthreads();
-      if (warp != 0) continue;
-      for (int w = 1; w < 8; ++w) {
-        const float m = sM[w], l = sL[w];
-        if (l != 0.f) {
-          const float mn = fmaxf(M, m);
-          const float f = ex2(M - mn), g = ex2(m - mn);
-          L = L * f + l * g;
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            acc[i] = acc[i] * f + sO[w][(i / 2) * 64 + lane * 2 + (i & 1)] * g;
-          M = mn;
-        }
-      }
-    }
-    if (!live) continue;
-    const int hq = kvh * a.G + e;
+  // token and head of row rr (false: no such row)
+  auto locate = [&](int rr, int* tok, int* head) {
+    const int t = rr >= tile_rows ? rr / tile_rows : 0, r = rr - t * tile_rows;
+    const int g = a.by_gu.div(r), e = sub * a.gu + r - g * a.gu;
+    *tok = (j * tiles + t) * a.w + g;
+    *head = kvh * a.G + e;
+    return rr < rows && g < a.w && *tok < nq && e < a.G;
+  };
+  // O, LSE of a row from its joined accumulator
+  auto finish = [&](int tok, int hq, float M, float L, const float (&acc)[E]) {
     const bool any = L != 0.f;
     float f = 1.f;
     if (a.sinks) {
@@ -403,19 +368,119 @@ __global__ void __launch_bounds__(256)
       M = mn;
     }
     const float inv = any ? f / L : 0.f;
-    T* orow = static_cast<T*>(a.o) + (q0 + tok) * a.os[0] + hq * a.os[1];
+    T* orow = static_cast<T*>(a.o) + static_cast<long long>(q0 + tok) * a.os[0] + hq * a.os[1];
+    T x[E];
 #pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      T x[2] = {narrow<T>(acc[i] * inv), narrow<T>(acc[i + 1] * inv)};
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<uint2*>(orow + (i / 2) * 64 + lane * 2) = *reinterpret_cast<uint2*>(x);
-      else
-        *reinterpret_cast<uint32_t*>(orow + (i / 2) * 64 + lane * 2) =
-            *reinterpret_cast<uint32_t*>(x);
-    }
+    for (int i = 0; i < E; ++i) x[i] = narrow<T>(acc[i] * inv);
+    if constexpr (E * sizeof(T) == 16)
+      *reinterpret_cast<uint4*>(orow + lane * E) = *reinterpret_cast<uint4*>(x);
+    else if constexpr (E * sizeof(T) == 8)
+      *reinterpret_cast<uint2*>(orow + lane * E) = *reinterpret_cast<uint2*>(x);
+    else
+      *reinterpret_cast<uint32_t*>(orow + lane * E) = *reinterpret_cast<uint32_t*>(x);
     if (a.lse && lane == 0)
       a.lse[static_cast<size_t>(q0 + tok) * a.Hq + hq] =
           L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  };
+  if (n <= kWide) {
+    for (int r0 = (blockIdx.y * 8 + warp) * kMergeRows; r0 < rows;
+         r0 += gridDim.y * 8 * kMergeRows) {
+      int tok[kMergeRows], head[kMergeRows];
+      bool live[kMergeRows];
+      float m[kMergeRows], l[kMergeRows], acc[kMergeRows][E];
+      V v[kAhead][kMergeRows];
+      auto fetch = [&](int p, V (&x)[kMergeRows]) {
+        const float* s = piece(p) + static_cast<size_t>(r0) * D + lane * E;
+#pragma unroll
+        for (int k = 0; k < kMergeRows; ++k)
+          if (p < n && live[k]) x[k] = *reinterpret_cast<const V*>(s + k * D);
+      };
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k) {
+        live[k] = locate(r0 + k, &tok[k], &head[k]);
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        if (live[k] && lane < n) {
+          const float* s = piece(lane);
+          m[k] = s[static_cast<size_t>(rows) * D + r0 + k];
+          l[k] = s[static_cast<size_t>(rows) * (D + 1) + r0 + k];
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[k][i] = 0.f;
+      }
+#pragma unroll
+      for (int p = 0; p < kAhead; ++p) fetch(p, v[p]);
+      float wgt[kMergeRows], L[kMergeRows], M[kMergeRows];
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k) {
+        // (a piece whose keys the row does not see holds nothing)
+        M[k] = l[k] != 0.f ? m[k] : -INFINITY;
+#pragma unroll
+        for (int i = 16; i >= 1; i >>= 1)
+          M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], i));
+        wgt[k] = l[k] != 0.f ? ex2(m[k] - M[k]) : 0.f;
+        L[k] = 0.f;
+      }
+      for (int p0 = 0; p0 < n; p0 += kAhead) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+          const int p = p0 + x;
+          if (p < n) {
+#pragma unroll
+            for (int k = 0; k < kMergeRows; ++k) {
+              const float w = __shfl_sync(0xffffffffu, wgt[k], p);
+              const float lp = __shfl_sync(0xffffffffu, l[k], p);
+              if (live[k] && lp != 0.f) {
+                L[k] += lp * w;
+                const float* e = reinterpret_cast<const float*>(&v[x][k]);
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[k][i] = fmaf(e[i], w, acc[k][i]);
+              }
+            }
+            fetch(p + kAhead, v[x]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k)
+        if (live[k]) finish(tok[k], head[k], M[k], L[k], acc[k]);
+    }
+    return;
+  }
+  __shared__ float sM[8], sL[8], sO[8][D];
+  for (int rr = blockIdx.y; rr < rows; rr += gridDim.y) {
+    int tok, head;
+    if (!locate(rr, &tok, &head)) continue;  // the same for every warp
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    auto join = [&](float m, float l, const float* v) {
+      if (l != 0.f) {
+        const float mn = fmaxf(M, m);
+        const float f = ex2(M - mn), g = ex2(m - mn);
+        L = L * f + l * g;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + v[i] * g;
+        M = mn;
+      }
+    };
+#pragma unroll 4
+    for (int p = warp; p < n; p += 8) {
+      const float* s = piece(p);
+      const V v = *reinterpret_cast<const V*>(s + static_cast<size_t>(rr) * D + lane * E);
+      join(s[static_cast<size_t>(rows) * D + rr], s[static_cast<size_t>(rows) * (D + 1) + rr],
+           reinterpret_cast<const float*>(&v));
+    }
+    __syncthreads();
+    if (lane == 0) {
+      sM[warp] = M;
+      sL[warp] = L;
+    }
+    *reinterpret_cast<V*>(&sO[warp][lane * E]) = *reinterpret_cast<V*>(acc);
+    __syncthreads();
+    if (warp != 0) continue;
+    for (int w = 1; w < 8; ++w) join(sM[w], sL[w], &sO[w][lane * E]);
+    finish(tok, head, M, L, acc);
   }
 }
 
@@ -587,7 +652,7 @@ sdpa_status_t score(Args& a, const LaunchEnv& env) {
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
                                  int tiles, cudaStream_t stream) {
   using namespace paged;
-  const dim3 grid(a.nctas, tile_rows <= 16 ? 8 : tile_rows * tiles > 128 ? 32 : 16);
+  const dim3 grid(a.nctas, tile_rows * tiles > 16 ? 16 : 8);
   auto go = [&](auto kern) { return launch_after(kern, grid, 256, stream, a, tile_rows, tiles); };
   if (head_dim == 64) {
     if (dtype == SDPA_F32) return go(paged_merge_kernel<float, 64>);
