@@ -5,8 +5,8 @@
 // a block of query rows for attention, a run of keys for the score sums.  A
 // unit takes a number of equal steps (key tiles, or query chunks) that
 // follows from the lengths and the causal rule, and the lengths are known on
-// the device only.  So every CTA computes the whole call's cost (kUnitCost +
-// steps per unit, summed per sequence in closed form), takes its equal share
+// the device only.  So every CTA computes the whole call's cost (a fixed
+// cost and the steps of every unit, summed per sequence in closed form), takes its equal share
 // of the line of all units, finds where it begins, and walks on from there.
 // A unit that crosses the end of a share is finished by the next CTAs: each
 // leaves a partial result in the workspace (slot 1 of the CTA that began the
@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "sdpa.h"
@@ -28,7 +30,6 @@ namespace gb300 {
 namespace paged {
 
 constexpr int kStatusPageTable = 7;  // SDPA_ERR_PAGE_TABLE
-constexpr int kUnitCost = 2;         // fixed cost of a unit, in steps
 
 // Division of n < 2^31 by a number known on the host: a high product, an add
 // and a shift (Granlund and Montgomery, "Division by Invariant Integers using
@@ -147,6 +148,7 @@ __host__ __device__ inline long long floor_sum(long long n, long long m, long lo
 struct AttendUnits {
   FastDiv by_w;
   int lg, causal;  // tiles of 2^lg keys
+  int cost;        // fixed cost of a unit, in steps
   __host__ __device__ int count(int nq, int nk) const { return by_w.ceil(nq); }
   __host__ __device__ int steps(int nq, int nk, int j) const {
     int lim = nk;
@@ -181,7 +183,7 @@ struct AttendUnits {
 // (times nsub head groups) from the first that sees one of its keys.
 struct ScoreUnits {
   FastDiv by_w;
-  int lg, causal, nsub;
+  int lg, causal, nsub, cost;
   __host__ __device__ int count(int nq, int nk) const {
     return nq > 0 ? (nk + (1 << lg) - 1) >> lg : 0;
   }
@@ -252,7 +254,7 @@ struct Walk {
       out->j = j;
       out->s = s;
       const int steps = u.steps(s.nq, s.nk, j);
-      const long long p0 = pos + kUnitCost;
+      const long long p0 = pos + u.cost;
       const long long lo = sh.begin - p0, hi = sh.end - p0;
       out->steps = steps;
       out->s0 = lo <= 0 ? 0 : lo >= steps ? steps : static_cast<int>(lo);
@@ -285,7 +287,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
   const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   auto cost = [&](const Seq& s, int n) {
-    return (u.before(s.nq, s.nk, n) + static_cast<long long>(n) * kUnitCost) * heads;
+    return (u.before(s.nq, s.nk, n) + static_cast<long long>(n) * u.cost) * heads;
   };
   long long mine = 0;
   Seq s{0, 0, 0};
@@ -341,7 +343,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
           const long long at =
-              pos + u.before(s.nq, s.nk, mid) + static_cast<long long>(mid) * kUnitCost;
+              pos + u.before(s.nq, s.nk, mid) + static_cast<long long>(mid) * u.cost;
           if (at <= begin) lo = mid; else hi = mid - 1;
         }
         sh->b = b;
@@ -349,7 +351,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
         sh->j = lo;
         sh->n = n;
         sh->s = s;
-        sh->pos = pos + u.before(s.nq, s.nk, lo) + static_cast<long long>(lo) * kUnitCost;
+        sh->pos = pos + u.before(s.nq, s.nk, lo) + static_cast<long long>(lo) * u.cost;
         break;
       }
       pos += c;
@@ -497,6 +499,22 @@ inline void fit_rows(Args& a, int rows, int tiles = 1) {
   a.by_nsub = fast_div(a.nsub);
   a.by_w = fast_div(a.w * tiles);
 }
+// Lets a kernel have `bytes` of dynamic shared memory on the current device;
+// done once a device.
+template <auto kKernel>
+bool allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load() & bit) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit);
+  return true;
+}
+
 // Rows of a page box: log2 of gcd(page_size, 128).
 inline int box_log2(int page_size) {
   int lg = 7;

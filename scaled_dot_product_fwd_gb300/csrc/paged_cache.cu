@@ -507,9 +507,7 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
   e.near = keep <= 2 * kMoveChunk ? 0x7fffffff : keep;
   const unsigned bh = static_cast<unsigned>(a.B) * a.Hkv;
   const int cache = a.cap < kSelCache ? a.cap : kSelCache;
-  if (cudaFuncSetAttribute(paged_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSelCache * 4) != cudaSuccess)
-    return SDPA_ERR_CUDA;
+  if (!allow_smem<paged_evict_select_kernel>(kSelCache * 4)) return SDPA_ERR_CUDA;
   // (checked before the first launch, so that a refused call moves nothing)
   if (static_cast<long long>(bh) * 2 * ((keep - 1) / kFarPer + 1) > 0x7fffffffLL)
     return SDPA_ERR_UNSUPPORTED;

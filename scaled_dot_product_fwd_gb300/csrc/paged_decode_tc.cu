@@ -21,8 +21,6 @@
 //
 // Bound by HBM: six 32 KB K/V slots in flight (twelve of 16 KB at head_dim
 // 64), S three tiles ahead of P V; TMEM holds eight S^T tiles and O^T.
-#include <atomic>
-
 #include "paged.cuh"
 #include "prefill_tc.cuh"
 
@@ -209,7 +207,7 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
-  const AttendUnits units{a.by_w, 7, a.causal};
+  const AttendUnits units{a.by_w, 7, a.causal, 2};
   const int heads = a.Hkv * a.nsub;
   plan_share<C::THREADS>(a, units, heads, 2,
                          reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
@@ -574,16 +572,7 @@ sdpa_status_t launch_dec(const Args& a, const CUtensorMap& tq, const CUtensorMap
                          const CacheBlocks& vb, const LaunchEnv& env) {
   using C = DecCfg<D>;
   auto kern = paged_decode_tc_kernel<D, BF16, NR>;
-  static std::atomic<uint64_t> ready{0};  // devices on which the attribute is set
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(ready.load() & bit)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
-        cudaSuccess)
-      return SDPA_ERR_CUDA;
-    ready.fetch_or(bit);
-  }
+  if (!allow_smem<paged_decode_tc_kernel<D, BF16, NR>>(C::SMEM)) return SDPA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

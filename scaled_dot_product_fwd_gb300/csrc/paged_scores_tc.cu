@@ -24,8 +24,6 @@
 // part: their limit is 0, and a chunk that holds one, or a key that some row
 // does not see, takes the path with a comparison for every column.  Keys past
 // the length produce sums that are never written.
-#include <atomic>
-
 #include "paged.cuh"
 #include "prefill_tc.cuh"
 
@@ -197,7 +195,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
-  const ScoreUnits units{a.by_w, kLgUnit, a.causal, a.nsub};
+  const ScoreUnits units{a.by_w, kLgUnit, a.causal, a.nsub, 4};
   plan_share<C::THREADS>(a, units, a.Hkv, 2,
                          reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
   tc_fence_after();
@@ -498,16 +496,7 @@ sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap&
                         int lg_box, const CacheBlocks& kb, const LaunchEnv& env) {
   using C = ScCfg<D, R>;
   auto kern = paged_scores_tc_kernel<D, BF16, R>;
-  static std::atomic<uint64_t> ready{0};  // devices on which the attribute is set
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(ready.load() & bit)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
-        cudaSuccess)
-      return SDPA_ERR_CUDA;
-    ready.fetch_or(bit);
-  }
+  if (!allow_smem<paged_scores_tc_kernel<D, BF16, R>>(C::SMEM)) return SDPA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kT, attend_ctas<D, RM>()) paged_simt_kernel(co
   __shared__ Share sh;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   griddep_launch_dependents();
-  const AttendUnits units{a.by_w, kLgKT, a.causal};
+  const AttendUnits units{a.by_w, kLgKT, a.causal, 1};
   const int heads = a.Hkv * a.nsub;
   plan_share<kT>(a, units, heads, 1, scratch, &sh);
   if (tid == 0) a.desc[blockIdx.x * kDesc] = 0;
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kT, scores_ctas<D>()) paged_scores_simt_kernel
   __shared__ Share sh;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   griddep_launch_dependents();
-  const ScoreUnits units{a.by_w, kLgKT, a.causal, a.nsub};
+  const ScoreUnits units{a.by_w, kLgKT, a.causal, a.nsub, 1};
   plan_share<kT>(a, units, a.Hkv, 1, scratch, &sh);
   if (tid == 0) a.desc[blockIdx.x * kDesc] = 0;
   Walk<ScoreUnits> walk(sh);
@@ -610,13 +610,11 @@ sdpa_status_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
-template <typename K>
-sdpa_status_t start(K kern, Args& a, int smem, int ctas, cudaStream_t stream) {
+template <auto kKernel>
+sdpa_status_t start(Args& a, int smem, int ctas, cudaStream_t stream) {
   a.nctas = std::min(a.max_ctas, ctas);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return SDPA_ERR_CUDA;
-  kern<<<a.nctas, kT, smem, stream>>>(a);
+  if (!allow_smem<kKernel>(smem)) return SDPA_ERR_CUDA;
+  kKernel<<<a.nctas, kT, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
@@ -627,10 +625,10 @@ sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   fit_rows(a, few && a.G <= 16 ? 16 : 64);
   const int rows = few && a.G <= 16 ? 16 : 64;
   const sdpa_status_t st =
-      rows == 16 ? start(paged_simt_kernel<T, D, 16>, a, attend_smem<D, 16>(),
-                         attend_ctas<D, 16>() * env.num_sms, env.stream)
-                 : start(paged_simt_kernel<T, D, 64>, a, attend_smem<D, 64>(),
-                         attend_ctas<D, 64>() * env.num_sms, env.stream);
+      rows == 16 ? start<paged_simt_kernel<T, D, 16>>(a, attend_smem<D, 16>(), attend_ctas<D, 16>() * env.num_sms,
+                                               env.stream)
+                 : start<paged_simt_kernel<T, D, 64>>(a, attend_smem<D, 64>(), attend_ctas<D, 64>() * env.num_sms,
+                                               env.stream);
   return st != SDPA_OK ? st
                        : launch_paged_merge(a, D, sizeof(T) == 4                          ? SDPA_F32
                                                   : std::is_same<T, __half>::value ? SDPA_F16
@@ -642,7 +640,8 @@ template <typename T, int D>
 sdpa_status_t score(Args& a, const LaunchEnv& env) {
   fit_rows(a, 64);
   const sdpa_status_t st =
-      start(paged_scores_simt_kernel<T, D>, a, scores_smem<D>(), scores_ctas<D>() * env.num_sms, env.stream);
+      start<paged_scores_simt_kernel<T, D>>(a, scores_smem<D>(),
+                                            scores_ctas<D>() * env.num_sms, env.stream);
   return st != SDPA_OK ? st : launch_paged_scores_merge(a, kKT, env.stream);
 }
 
