@@ -85,6 +85,23 @@ __device__ void load_rows(const void* base, const long long* off, float* dst, in
   }
 }
 
+// The same for fp32 caches as asynchronous copies straight into shared memory
+// (nothing to widen), zeros where there is no row.
+template <int D>
+__device__ void copy_rows(const void* base, const long long* off, float* dst, int pitch) {
+  constexpr int C = D / 4;  // 16-byte pieces of a row
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kKT * C; i += kT) {
+    const int r = i / C, c = (i % C) * 4;
+    const long long o = off[r];
+    const float* src = static_cast<const float*>(base) + (o >= 0 ? o + c : 0);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_addr(dst + r * pitch + c)),
+                 "l"(src), "r"(o >= 0 ? 16 : 0)
+                 : "memory");
+  }
+}
+
 // Query rows of tile (first token tok0) of head unit (kvh, sub) as fp32 rows
 // of D floats; rows that do not exist are zero.
 template <typename T, int D, int RM>
@@ -131,15 +148,18 @@ __device__ __forceinline__ void scores_tile(const float* sQ, const float* sK, in
   }
 }
 
-template <int D, int RM>
+// fp32 tiles are double-buffered (copies of the next beside the arithmetic on
+// this one)
+template <typename T, int D, int RM>
 constexpr int attend_smem() {
-  return (RM * D + kKT * (D + 4) + kKT * D + RM * (kKT + 4)) * 4;
+  return (RM * D + (sizeof(T) == 4 ? 2 : 1) * kKT * (2 * D + 4) + RM * (kKT + 4)) * 4;
 }
 
 // CTAs an SM: what the shared memory and the registers of a tile allow (one of
 // 8 warps alone leaves the FMA pipes waiting for shared memory).
-template <int D, int RM>
+template <typename T, int D, int RM>
 constexpr int attend_ctas() {
+  if (sizeof(T) == 4) return D == 64 ? 2 : 1;
   return RM == 16 ? (D == 64 ? 4 : 2) : (D == 64 ? 2 : 1);
 }
 template <int D>
@@ -148,15 +168,16 @@ constexpr int scores_ctas() {
 }
 
 template <typename T, int D, int RM>
-__global__ void __launch_bounds__(kT, attend_ctas<D, RM>()) paged_simt_kernel(const Args a) {
+__global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel(const Args a) {
   constexpr int RPT = RM / 16;
   constexpr int CG = D / 64;  // float4 column groups of a thread
   constexpr int kSlot = RM * (D + 2);
   extern __shared__ float smem[];
   float* sQ = smem;
   float* sK = sQ + RM * D;
-  float* sV = sK + kKT * (D + 4);
-  float* sP = sV + kKT * D;
+  constexpr bool kAsync = sizeof(T) == 4;
+  constexpr int kTile = kKT * (2 * D + 4);  // a K and a V tile
+  float* sP = sK + (kAsync ? 2 : 1) * kTile;
   __shared__ long long off_k[2][kKT], off_v[2][kKT];
   __shared__ long long scratch[kT / 32 + 1];
   __shared__ Share sh;
@@ -188,17 +209,40 @@ __global__ void __launch_bounds__(kT, attend_ctas<D, RM>()) paged_simt_kernel(co
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
     }
+    auto copy_tile = [&](int par) {
+      float* k = sK + par * kTile;
+      copy_rows<D>(a.k, off_k[par], k, D + 4);
+      copy_rows<D>(a.v, off_v[par], k + kKT * (D + 4), D);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (kAsync && u.s0 < u.s1) {
+      copy_tile(0);
+      if (u.s0 + 1 < u.s1)
+        row_offsets(a, u.b, kvh, (u.s0 + 1) * kKT, u.s.nk, off_k[1], off_v[1]);
+    }
     for (int t = u.s0; t < u.s1; ++t) {
       const int key0 = t * kKT;
-      if (t > u.s0) __syncthreads();
       const int par = (t - u.s0) & 1;
-      load_rows<T, D>(a.k, off_k[par], sK, D + 4);
-      load_rows<T, D>(a.v, off_v[par], sV, D);
-      __syncthreads();
-      if (t + 1 < u.s1)
-        row_offsets(a, u.b, kvh, key0 + kKT, u.s.nk, off_k[par ^ 1], off_v[par ^ 1]);
+      float* sKt = sK;
+      if constexpr (kAsync) {
+        // this tile's copies have landed, and the last tile's buffers are read
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        sKt = sK + par * kTile;
+        if (t + 1 < u.s1) copy_tile(par ^ 1);
+        if (t + 2 < u.s1)
+          row_offsets(a, u.b, kvh, key0 + 2 * kKT, u.s.nk, off_k[par], off_v[par]);
+      } else {
+        if (t > u.s0) __syncthreads();
+        load_rows<T, D>(a.k, off_k[par], sK, D + 4);
+        load_rows<T, D>(a.v, off_v[par], sK + kKT * (D + 4), D);
+        __syncthreads();
+        if (t + 1 < u.s1)
+          row_offsets(a, u.b, kvh, key0 + kKT, u.s.nk, off_k[par ^ 1], off_v[par ^ 1]);
+      }
+      const float* sV = sKt + kKT * (D + 4);
       float s[RPT][4];
-      scores_tile<D, RPT>(sQ, sK, ty, tx, s);
+      scores_tile<D, RPT>(sQ, sKt, ty, tx, s);
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
         float mx = -INFINITY;
@@ -625,15 +669,13 @@ sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   fit_rows(a, few && a.G <= 16 ? 16 : 64);
   const int rows = few && a.G <= 16 ? 16 : 64;
   const sdpa_status_t st =
-      rows == 16 ? start<paged_simt_kernel<T, D, 16>>(a, attend_smem<D, 16>(), attend_ctas<D, 16>() * env.num_sms,
-                                               env.stream)
-                 : start<paged_simt_kernel<T, D, 64>>(a, attend_smem<D, 64>(), attend_ctas<D, 64>() * env.num_sms,
-                                               env.stream);
-  return st != SDPA_OK ? st
-                       : launch_paged_merge(a, D, sizeof(T) == 4                          ? SDPA_F32
-                                                  : std::is_same<T, __half>::value ? SDPA_F16
-                                                                                   : SDPA_BF16,
-                                            rows, 1, env.stream);
+      rows == 16 ? start<paged_simt_kernel<T, D, 16>>(
+                       a, attend_smem<T, D, 16>(), attend_ctas<T, D, 16>() * env.num_sms, env.stream)
+                 : start<paged_simt_kernel<T, D, 64>>(
+                       a, attend_smem<T, D, 64>(), attend_ctas<T, D, 64>() * env.num_sms, env.stream);
+  if (st != SDPA_OK) return st;
+  const int dtype = sizeof(T) == 4 ? SDPA_F32 : std::is_same<T, __half>::value ? SDPA_F16 : SDPA_BF16;
+  return launch_paged_merge(a, D, dtype, rows, 1, env.stream);
 }
 
 template <typename T, int D>
