@@ -162,9 +162,9 @@ constexpr int attend_ctas() {
   if (sizeof(T) == 4) return D == 64 ? 2 : 1;
   return RM == 16 ? (D == 64 ? 4 : 2) : (D == 64 ? 2 : 1);
 }
-template <int D>
+template <int D, int RM>
 constexpr int scores_ctas() {
-  return D == 64 ? 3 : 2;
+  return RM == 16 ? 4 : D == 64 ? 3 : 2;
 }
 
 template <typename T, int D, int RM>
@@ -528,18 +528,19 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
-// Score sums: a unit is 64 keys, its steps the chunks of 64 query rows that
-// see them; a thread's 4 keys x 4 rows of each score tile become
+// Score sums: a unit is 64 keys, its steps the chunks of RM query rows that
+// see them; a thread's 4 keys x RM / 16 rows of each score tile become
 // probabilities against the rows' log-sum-exp and are added up in registers,
 // and the 16 row groups meet in shared memory at the end of the unit.
-template <int D>
+template <int D, int RM>
 constexpr int scores_smem() {
-  return (64 * D + kKT * (D + 4) + 16 * kKT) * 4;
+  return (RM * D + kKT * (D + 4) + 16 * kKT) * 4;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kT, scores_ctas<D>()) paged_scores_simt_kernel(const Args a) {
-  constexpr int RM = 64;
+template <typename T, int D, int RM>
+__global__ void __launch_bounds__(kT, scores_ctas<D, RM>())
+    paged_scores_simt_kernel(const Args a) {
+  constexpr int RPT = RM / 16;
   extern __shared__ float smem[];
   float* sQ = smem;
   float* sK = sQ + RM * D;
@@ -581,14 +582,14 @@ __global__ void __launch_bounds__(kT, scores_ctas<D>()) paged_scores_simt_kernel
         sLim[tid] = lim;
       }
       __syncthreads();
-      float s[4][4];
-      scores_tile<D, 4>(sQ, sK, ty, tx, s);
+      float s[RPT][4];
+      scores_tile<D, RPT>(sQ, sK, ty, tx, s);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
         float add = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = ty * 4 + i;
+        for (int i = 0; i < RPT; ++i) {
+          const int r = ty * RPT + i;
           const bool vis = key0 + tx + 16 * jj < sLim[r];
           add += vis ? ex2(fmaf(s[i][jj], a.sl2, -sLse[r])) : 0.f;
         }
@@ -680,10 +681,13 @@ sdpa_status_t attend(Args& a, const LaunchEnv& env) {
 
 template <typename T, int D>
 sdpa_status_t score(Args& a, const LaunchEnv& env) {
-  fit_rows(a, 64);
+  const bool few = a.G <= 16 && static_cast<long long>(a.T) * a.G <= 16LL * a.B;
+  fit_rows(a, few ? 16 : 64);
   const sdpa_status_t st =
-      start<paged_scores_simt_kernel<T, D>>(a, scores_smem<D>(),
-                                            scores_ctas<D>() * env.num_sms, env.stream);
+      few ? start<paged_scores_simt_kernel<T, D, 16>>(
+                a, scores_smem<D, 16>(), scores_ctas<D, 16>() * env.num_sms, env.stream)
+          : start<paged_scores_simt_kernel<T, D, 64>>(
+                a, scores_smem<D, 64>(), scores_ctas<D, 64>() * env.num_sms, env.stream);
   return st != SDPA_OK ? st : launch_paged_scores_merge(a, kKT, env.stream);
 }
 
