@@ -13,8 +13,7 @@
 //    ordered pass over the positions writes the kept ones (above the
 //    threshold, the first of those equal to it, and the newest) in ascending
 //    order by a scan, and the weights' new places.
-//  - move (a CTA per (sequence, kv head), K or V, 64-byte slice of the
-//    rows): row kept[i] goes to row i, for the kept[i] below `keep`, whose
+//  - move (a CTA per (sequence, kv head), K or V, slice of the rows): row kept[i] goes to row i, for the kept[i] below `keep`, whose
 //    rows other moves overwrite.  kept[i] >= i, and the sources of a chunk lie
 //    behind the destinations of every earlier chunk, so a CTA that takes the
 //    chunks in order, loads the next one early and writes a chunk only when
@@ -123,7 +122,7 @@ struct EvictArgs {
   char* kp;
   char* vp;
   long long kb[3], vb[3];  // byte strides of the cache (page, head, row)
-  int slices;              // kSlice-byte slices of a row
+  int slices;  // parts of a row, a CTA each (ordered kernel)
 };
 
 // Integer whose order is the weights' order: sign bit flipped for positive
@@ -135,13 +134,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelT = 1024;
 constexpr int kSelE = 4;  // positions of a thread in the ordered pass
 constexpr int kBins = 2048;
 // weights that the select kernel keeps in shared memory (more are read from
 // global memory again for each digit)
 constexpr int kSelCache = 48 * 1024;
 
+template <int kSelT>
 __global__ void __launch_bounds__(kSelT)
     paged_evict_select_kernel(const EvictArgs e, const int cache) {
   const Args& a = e.a;
@@ -180,14 +179,34 @@ __global__ void __launch_bounds__(kSelT)
   };
   auto key_of = [&](int i) { return order_key(weight(i)); };
 
+  // exclusive sum of v over the CTA's threads, and its total
+  auto scan = [&](int v, int* total) {
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    const int w = lane < kSelT / 32 ? warp_sum[lane] : 0;
+    int wi = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, wi, d);
+      if (lane >= d) wi += t;
+    }
+    if (total) *total = __shfl_sync(0xffffffffu, wi, 31);
+    return incl - v + __shfl_sync(0xffffffffu, wi - w, warp);
+  };
+
   // the want-th largest key, from its top digit down (11, 11 and 10 bits)
   uint32_t prefix = 0, mask = 0;
   if (want > 0) {
     for (int d = 0; d < 3; ++d) {
       const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
       const uint32_t dmask = d == 2 ? 1023u : 2047u;
-      hist[tid] = 0;
-      hist[tid + kSelT] = 0;
+      for (int i = tid; i < kBins; i += kSelT) hist[i] = 0;
       __syncthreads();
 #pragma unroll 4
       for (int i0 = 0; i0 < cand; i0 += kSelT) {
@@ -205,31 +224,23 @@ __global__ void __launch_bounds__(kSelT)
         }
       }
       __syncthreads();
-      // how many keys have a larger digit: thread t holds digits 2047 - 2t
-      // and 2046 - 2t
-      const int c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
-      int incl = c0 + c1;
+      // how many keys have a larger digit: thread t holds the kBT digits
+      // from 2047 - kBT t down
+      constexpr int kBT = kBins / kSelT;
+      int c[kBT], sum = 0;
 #pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, k);
-        if (lane >= k) incl += t;
+      for (int k = 0; k < kBT; ++k) {
+        c[k] = hist[kBins - 1 - kBT * tid - k];
+        sum += c[k];
       }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int w = warp_sum[lane];
-      int wi = w;
+      int before = scan(sum, nullptr);
 #pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, wi, k);
-        if (lane >= k) wi += t;
-      }
-      const int before = incl - c0 - c1 + __shfl_sync(0xffffffffu, wi - w, warp);
-      if (before < want && want <= before + c0) {
-        s_digit = static_cast<uint32_t>(kBins - 1 - 2 * tid);
-        s_want = want - before;
-      } else if (before + c0 < want && want <= before + c0 + c1) {
-        s_digit = static_cast<uint32_t>(kBins - 2 - 2 * tid);
-        s_want = want - before - c0;
+      for (int k = 0; k < kBT; ++k) {
+        if (before < want && want <= before + c[k]) {
+          s_digit = static_cast<uint32_t>(kBins - 1 - kBT * tid - k);
+          s_want = want - before;
+        }
+        before += c[k];
       }
       __syncthreads();
       prefix |= s_digit << shift;
@@ -261,23 +272,9 @@ __global__ void __launch_bounds__(kSelT)
       }
     }
     const int mine = __popc(gt) | (__popc(eq) << 16);
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += t;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();  // (every weight of this chunk is read: `out` may be `sc`)
-    int w = warp_sum[lane];
-    int wi = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, wi, d);
-      if (lane >= d) wi += t;
-    }
-    const int total = __shfl_sync(0xffffffffu, wi, 31);
-    const int before = incl - mine + __shfl_sync(0xffffffffu, wi - w, warp);
+    // (its barrier: every weight of this chunk is read; `out` may be `sc`)
+    int total;
+    const int before = scan(mine, &total);
     int ng = run_gt + (before & 0xffff), ne = run_eq + (before >> 16);
 #pragma unroll
     for (int k = 0; k < kSelE; ++k) {
@@ -299,18 +296,21 @@ __global__ void __launch_bounds__(kSelT)
 }
 
 constexpr int kMoveT = 256;
-constexpr int kSlice = 64;                              // bytes of a row that a CTA moves
-constexpr int kLanes = kSlice / 16;                     // threads of a row
-constexpr int kMoveRows = 8;                            // rows of a thread in a chunk
-constexpr int kMoveStep = kMoveT / kLanes;              // rows of the CTA at a time
-constexpr int kMoveChunk = kMoveRows * kMoveStep;
+constexpr int kMoveRows = 8;  // rows of a thread in a chunk
+// rows of a chunk where a CTA takes 16 * lanes bytes of a row
+constexpr int move_chunk(int lanes) { return kMoveRows * kMoveT / lanes; }
 
+template <int kLanes>
 __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const EvictArgs e) {
+  constexpr int kSlice = 16 * kLanes;         // bytes of a row that the CTA moves
+  constexpr int kMoveStep = kMoveT / kLanes;  // rows at a time
+  constexpr int kMoveChunk = move_chunk(kLanes);
+  constexpr int kRows = kMoveChunk < kMoveT ? kMoveT : kMoveChunk;
   const Args& a = e.a;
   // Where a chunk's rows come from (-1: no move) and go to, looked up two
   // chunks ahead by one thread a row; four chunks' worth, so that the writes
   // for chunk n + 2 never meet the last reads for chunk n - 1.
-  __shared__ long long s_from[4][kMoveChunk], s_to[4][kMoveChunk];
+  __shared__ long long s_from[4][kRows], s_to[4][kRows];
   __shared__ int s_more[4];
   griddep_wait();
   griddep_launch_dependents();
@@ -329,12 +329,13 @@ __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const Evict
   const int* table = a.table + b * a.table_stride;
   const int r0 = tid / kLanes;
   auto lookup = [&](int n) {
-    constexpr int N = kMoveChunk / kMoveT;
+    constexpr int N = kRows / kMoveT;
     int src[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const long long i = static_cast<long long>(n) * kMoveChunk + k * kMoveT + tid;
-      src[k] = i < e.keep ? kept[i] : -1;
+      const int r = k * kMoveT + tid;
+      const long long i = static_cast<long long>(n) * kMoveChunk + r;
+      src[k] = r < kMoveChunk && i < e.keep ? kept[i] : -1;
     }
     // (the positions ascend: the first at or past `keep`, the second kernel's,
     // or the end of a short sequence ends this kernel's part)
@@ -500,18 +501,28 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
     e.kb[i] = a.ks[i] * elem;
     e.vb[i] = a.vs[i] * elem;
   }
-  e.slices = row_bytes / kSlice;
+  // Lanes of a row in the ordered kernel: a whole row where the budget is one
+  // chunk then (fewer CTAs), else 64 bytes (more bytes on their way; 8 x 16384
+  // keys in 128-byte slices: 85 us against 89).
+  const int row_lanes = row_bytes / 16;
+  const int lanes = keep <= move_chunk(row_lanes) ? row_lanes : 4;
+  e.slices = row_lanes / lanes;
   // A budget of up to two chunks moves in the ordered kernel alone: a launch
   // less (measured at 2 x 1500 keys, budget 1024: 12.4 us against 16.7), while
   // at 8 x 16384 keys and a budget of 4096 the two take 71 us against 89.
-  e.near = keep <= 2 * kMoveChunk ? 0x7fffffff : keep;
+  e.near = keep <= 2 * move_chunk(lanes) ? 0x7fffffff : keep;
   const unsigned bh = static_cast<unsigned>(a.B) * a.Hkv;
   const int cache = a.cap < kSelCache ? a.cap : kSelCache;
-  if (!allow_smem<paged_evict_select_kernel>(kSelCache * 4)) return SDPA_ERR_CUDA;
+  if (!allow_smem<paged_evict_select_kernel<1024>>(kSelCache * 4)) return SDPA_ERR_CUDA;
   // (checked before the first launch, so that a refused call moves nothing)
   if (static_cast<long long>(bh) * 2 * ((keep - 1) / kFarPer + 1) > 0x7fffffffLL)
     return SDPA_ERR_UNSUPPORTED;
-  paged_evict_select_kernel<<<bh, kSelT, cache * 4, stream>>>(e, cache);
+  // many short sequences: small CTAs, several an SM (1406 rows of 7 keys 84 ->
+  // 32 us; 16 rows of 1500 take 12.0 us with 1024 threads and 13.4 with 256)
+  if (a.cap <= 4096 && bh > 256)
+    paged_evict_select_kernel<256><<<bh, 256, cache * 4, stream>>>(e, cache);
+  else
+    paged_evict_select_kernel<1024><<<bh, 1024, cache * 4, stream>>>(e, cache);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -522,7 +533,11 @@ sdpa_status_t launch_paged_evict(const paged::Args& a, int row_bytes, int elem, 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_evict_move_kernel, e) != cudaSuccess) return SDPA_ERR_CUDA;
+  auto move = lanes == 4    ? paged_evict_move_kernel<4>
+              : lanes == 8  ? paged_evict_move_kernel<8>
+              : lanes == 16 ? paged_evict_move_kernel<16>
+                            : paged_evict_move_kernel<32>;
+  if (cudaLaunchKernelEx(&cfg, move, e) != cudaSuccess) return SDPA_ERR_CUDA;
   *launches = 2;
   if (e.near != keep) return SDPA_OK;
   *launches = 3;
