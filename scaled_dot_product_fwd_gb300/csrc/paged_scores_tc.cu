@@ -17,8 +17,8 @@
 // double-buffered, so the products of a step run while the exponentials of
 // the one before do.  Chunks: bound by the exponentials (128 x 256 a step,
 // about 1100 clk at the measured 30 a clk and SM, against 1024 clk of
-// products at head_dim 128).  Single tokens: the chunk has R = 16 columns
-// and K streams once, bound by HBM.
+// products at head_dim 128).  Few rows a sequence (single tokens): the
+// chunk has R = 16, 32 or 64 columns and K streams once, bound by HBM.
 //
 // Rows that do not exist (past the sequence's tokens, another head's) take no
 // part: their limit is 0, and a chunk that holds one, or a key that some row
@@ -41,8 +41,8 @@ struct ScCfg {
   static constexpr int TILE = 128 * D * 2;  // a key tile
   static constexpr int QTILE = R * D * 2;   // a query chunk
   // units whose keys are in flight, and query chunks
-  static constexpr int NK = R == 16 ? (D == 64 ? 6 : 3) : (D == 64 ? 2 : 1);
-  static constexpr int NQS = R == 16 ? 4 : (D == 64 ? 6 : 4);
+  static constexpr int NK = (R <= 32 ? 3 : R == 64 ? 2 : 1) * (D == 64 ? 2 : 1);
+  static constexpr int NQS = R == 128 && D == 64 ? 6 : R == 32 ? 2 : 4;
   static constexpr int Q_OFF = NK * 2 * TILE;
   static constexpr int BAR_OFF = Q_OFF + NQS * QTILE;
   // k_full[NK], k_empty[NK], q_full[NQS], q_empty[NQS], s_full[2 tiles][2],
@@ -51,7 +51,7 @@ struct ScCfg {
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   // warps of the exponentials: four for each key tile, or four for each tile
   // and parity of the step
-  static constexpr int GROUPS = R == 128 ? 2 : 1;
+  static constexpr int GROUPS = R >= 64 ? 2 : 1;
   static constexpr int EW = 8 * GROUPS;
   static constexpr int WARPS = EW + 4;
   static constexpr int THREADS = 32 * WARPS;
@@ -513,9 +513,14 @@ sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap&
 
 template <int D>
 sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
-  // single tokens: 16 columns hold a sequence's rows
-  const bool few = a.G <= 16 && static_cast<long long>(a.T) * a.G <= 16LL * a.B;
-  fit_rows(a, few ? 16 : 128);
+  // Columns of a chunk: the fewest that hold a sequence's rows on average (a
+  // column costs an exponential whether its row exists or not: 10 x 34 tokens
+  // over up to 24727 keys, one head a kv head, took 106 us with 128 columns
+  // and 67 with 64).
+  const long long rows = static_cast<long long>(a.T) * a.G;
+  int cols = 16;
+  while (cols < 128 && (a.G > cols || rows > static_cast<long long>(cols) * a.B)) cols *= 2;
+  fit_rows(a, cols);
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType dt =
       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -532,11 +537,16 @@ sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
       !encode_row_blocks(&tk, dt, a.k, D / 64, a.page_size, kb.blocks, 1 << lg_box,
                          st(a.ks[2], a.page_size), ku))
     return SDPA_ERR_CUDA;
-  if (few)
-    return bf16 ? launch_sc<D, true, 16>(a, tq, tk, lg_box, kb, env)
-                : launch_sc<D, false, 16>(a, tq, tk, lg_box, kb, env);
-  return bf16 ? launch_sc<D, true, 128>(a, tq, tk, lg_box, kb, env)
-              : launch_sc<D, false, 128>(a, tq, tk, lg_box, kb, env);
+#define GB300_SCORES(R)                                                 \
+  (bf16 ? launch_sc<D, true, R>(a, tq, tk, lg_box, kb, env)             \
+        : launch_sc<D, false, R>(a, tq, tk, lg_box, kb, env))
+  switch (cols) {
+    case 16: return GB300_SCORES(16);
+    case 32: return GB300_SCORES(32);
+    case 64: return GB300_SCORES(64);
+    default: return GB300_SCORES(128);
+  }
+#undef GB300_SCORES
 }
 
 }  // namespace
