@@ -422,6 +422,10 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
  *  - causal nonzero (the usual case): a token sees the keys at and before
  *    its own position; zero: every key of its sequence.  A token that sees
  *    no key (nq > nk) gives o = 0 and lse = -inf, or the sink.
+ *  - The cache's rows below a sequence's length hold finite values (a row
+ *    meets the weight 0 of tokens that do not see it); rows at or past it may
+ *    hold anything, NaN included.  The lengths, offsets and page tables do not
+ *    change while a call runs.
  *  - head_dim 64 or 128; fp32, fp16, bf16; any Hq that Hkv divides; page_size
  *    >= 1.  fp16/bf16 with page_size a multiple of 8 run on the tensor cores,
  *    everything else on fp32 CUDA-core kernels.

@@ -367,6 +367,19 @@ __device__ __forceinline__ int pieces_of(const Unit& u, const Share& sh) {
                           div_nonneg(u.pos, sh.size)) + 1;
 }
 
+// The sink logit joins a row's denominator (its value row is zero): m, l
+// become those of the row with it, and the factor of what was summed before
+// is returned.  A sink of -inf adds nothing, also to a row that saw no key.
+__device__ __forceinline__ float add_sink(float sink, float& m, float& l) {
+  const float sk = sink * 1.4426950408889634f;
+  const float mn = fmaxf(m, sk);
+  if (mn == -INFINITY) return 1.f;
+  const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+  l = l * f + ex2(sk - mn);
+  m = mn;
+  return f;
+}
+
 // Page of position p, or -1 (and the status word set) where the table names
 // none of the cache's.
 __device__ __forceinline__ int page_of(const Args& a, int b, int p) {

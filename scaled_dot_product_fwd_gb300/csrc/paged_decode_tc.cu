@@ -502,13 +502,7 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
           }
         } else if (row_ok) {
           const int hq = kvh * a.G + e;
-          if (a.sinks) {
-            const float sk = a.sinks[hq] * kLog2e;
-            const float mn = fmaxf(M, sk);
-            f *= ex2(M - mn);
-            L = L * ex2(M - mn) + ex2(sk - mn);
-            M = mn;
-          }
+          if (a.sinks) f *= add_sink(a.sinks[hq], M, L);
           f = L != 0.f ? f / L : 0.f;
           if (a.lse)
             a.lse[static_cast<long long>(s.q0 + tok0 + t) * a.Hq + hq] =

@@ -315,13 +315,7 @@ __global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel
       }
       const int hq = kvh * a.G + e;
       float mm = m[i], ll = l[i], f = 1.f;
-      if (a.sinks) {
-        const float sk = a.sinks[hq] * kLog2e;
-        const float mn = fmaxf(mm, sk);
-        f = mm == -INFINITY ? 0.f : ex2(mm - mn);
-        ll = ll * f + ex2(sk - mn);
-        mm = mn;
-      }
+      if (a.sinks) f = add_sink(a.sinks[hq], mm, ll);
       const float inv = l[i] != 0.f ? f / ll : 0.f;  // (a NaN sum stays one)
       T* orow = static_cast<T*>(a.o) + (u.s.q0 + tok) * a.os[0] + hq * a.os[1];
 #pragma unroll
@@ -404,13 +398,7 @@ __global__ void __launch_bounds__(256, 4)
   auto finish = [&](int tok, int hq, float M, float L, const float (&acc)[E]) {
     const bool any = L != 0.f;
     float f = 1.f;
-    if (a.sinks) {
-      const float sk = a.sinks[hq] * kLog2e;
-      const float mn = fmaxf(M, sk);
-      f = any ? ex2(M - mn) : 0.f;
-      L = L * f + ex2(sk - mn);
-      M = mn;
-    }
+    if (a.sinks) f = add_sink(a.sinks[hq], M, L);
     const float inv = any ? f / L : 0.f;
     T* orow = static_cast<T*>(a.o) + static_cast<long long>(q0 + tok) * a.os[0] + hq * a.os[1];
     T x[E];

@@ -572,13 +572,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
         const int hq = (a.by_nsub.div(unit->h)) * a.G + e;
         float f = 1.f;
         const float own = l;
-        if (a.sinks && row_ok) {
-          const float sk = a.sinks[hq] * kLog2e;
-          const float mn = fmaxf(m, sk);
-          f = ex2(m - mn);
-          l = l * f + ex2(sk - mn);
-          m = mn;
-        }
+        if (a.sinks && row_ok) f = add_sink(a.sinks[hq], m, l);
         const float inv = own != 0.f ? f / l : 0.f;
         const long long q = unit->s.q0 + tok;
         T* orow = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1];

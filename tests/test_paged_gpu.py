@@ -228,6 +228,60 @@ def test_forward_empty_rows(cuda, S, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[4], SHAPES[7]], ids=str)
+def test_sink_of_minus_infinity_is_none(cuda, S, shape, dtype):
+    t = Batch(cuda, *shape[:5], dtype, shape[5])
+    t.lens[-1] = 0  # and a sequence whose tokens see nothing
+    o, lse = forward(S, t)
+    o2, lse2 = forward(S, t, sinks=cuda.full((t.hq,), -math.inf, device="cuda"))
+    assert cuda.equal(o, o2) and cuda.equal(lse, lse2)
+    assert (lse[t.rows(len(t.qs) - 1)] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_tokens_between_and_before_the_sequences(cuda, S, dtype):
+    """Offsets that start behind row 0 and end before the last row."""
+    t = Batch(cuda, [4, 50, 1], [60, 444, 9], 8, 2, 64, dtype, 16)
+    ref, ref_lse = forward(S, t)
+    q = cuda.cat([cuda.full_like(t.q[:5], float("nan")), t.q, cuda.full_like(t.q[:7], float("nan"))])
+    o = cuda.full_like(q, 3.0)
+    lse = cuda.full(q.shape[:2], 3.0, device="cuda")
+    S.sdpa_paged_forward(q, t.k_pages, t.v_pages, t.table, t.lens, cu_seqlens_q=t.cu + 5, out=o,
+                         lse=lse)
+    assert cuda.equal(o[5:-7], ref) and cuda.equal(lse[5:-7], ref_lse)
+    for x in (o, lse):
+        assert (x[:5] == 3).all() and (x[-7:] == 3).all()
+    k, v = (cuda.cat([x[:5], x, x[:7]]) for x in (t.k, t.v))
+    before = t.k_pages.clone()
+    S.sdpa_paged_write(k, v, t.k_pages, t.v_pages, t.table, t.lens, cu_seqlens_q=t.cu + 5)
+    pos = 444 - 50 + 7
+    assert cuda.equal(t.k_pages[int(t.table[1, pos // 16]), :, pos % 16], t.k[4 + 7])
+    assert (before.nan_to_num() != t.k_pages.nan_to_num()).any(-1).sum() <= 55 * 2
+
+
+def test_threads_on_one_stream(cuda, S):
+    """Calls of several host threads on one stream: their kernels interleave,
+    their workspaces are their own."""
+    import threading
+    ts = [Batch(cuda, [1, 9, 300], [3000, 900, 1500], 8, 2, 64, "bf16", 16, seed=i)
+          for i in range(4)]
+    refs = [forward(S, t) for t in ts]
+    cuda.cuda.synchronize()
+    bad = []
+
+    def work(t, ref):
+        for _ in range(30):
+            o, lse = forward(S, t)
+            if not (cuda.equal(o, ref[0]) and cuda.equal(lse, ref[1])):
+                bad.append(1)
+
+    th = [threading.Thread(target=work, args=x) for x in zip(ts, refs)]
+    [x.start() for x in th]
+    [x.join() for x in th]
+    assert not bad
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_forward_one_token_each_without_offsets(cuda, S, dtype):
     t = Batch(cuda, [1] * 5, [3, 99, 1, 500, 64], 8, 4, 128, dtype, 16, pad=2)
     o, lse = forward(S, t)
@@ -469,7 +523,8 @@ EVICT = [  # ks, hkv, D, page, keep, recent
     ([5, 1, 9], 2, 64, 16, 4, 1), ([1], 1, 128, 16, 1, 0), ([2, 3, 0], 3, 64, 8, 1, 5),
     ([1000, 300, 4000], 2, 128, 16, 300, 50), ([2500, 2049], 8, 64, 64, 2048, 0),
     ([700, 123], 4, 128, 7, 128, 128), ([9000], 1, 64, 48, 4500, 1000),
-    ([5000, 5000], 38, 64, 256, 129, 300),
+    ([5000, 5000], 38, 64, 256, 129, 300), ([7, 3, 20] * 40, 4, 64, 8, 5, 2),
+    ([4000, 2600], 3, 128, 32, 1500, 0), ([130], 2, 64, 16, 129, 4),
 ]
 
 
