@@ -552,21 +552,20 @@ def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
     """Checks of what the paged calls share.  Returns the fields of
     SdpaPagedParams that describe the cache: (kv heads, D, dtype code, pages,
     page size), the batch's fields, and the strides of k and v."""
-    torch = _torch()
-    int32 = torch.int32
+    int32 = _torch().int32
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if k_pages.dim() != 4 or k_pages.get_device() != dev or k_pages.stride(3) != 1:
+    shape, ks, dtype = k_pages.shape, k_pages.stride(), k_pages.dtype
+    if len(shape) != 4 or ks[3] != 1 or k_pages.get_device() != dev:
         raise ValueError("k_pages must be [pages, kv heads, page_size, D] on the same device "
                          "with a contiguous last dimension")
-    shape = k_pages.shape
-    ks = vs = k_pages.stride()
+    vs = ks
     if v_pages is not None:
         vs = v_pages.stride()
-        if v_pages.shape != shape or v_pages.get_device() != dev or vs[3] != 1:
+        if v_pages.shape != shape or vs[3] != 1 or v_pages.get_device() != dev:
             raise ValueError("v_pages must have k_pages' shape and device and a contiguous last "
                              "dimension")
-        if v_pages.dtype is not k_pages.dtype:
+        if v_pages.dtype is not dtype:
             raise TypeError("k_pages and v_pages must share a dtype")
     B = seq_lens_kv.numel()
     if (seq_lens_kv.dtype is not int32 or seq_lens_kv.get_device() != dev
@@ -574,8 +573,8 @@ def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
         raise TypeError("seq_lens_kv must be a contiguous int32 CUDA tensor")
     if page_table.dtype is not int32 or page_table.get_device() != dev:
         raise TypeError("page_table must be an int32 CUDA tensor")
-    ts = page_table.shape
-    if len(ts) != 2 or ts[0] != B or (ts[1] > 1 and page_table.stride(1) != 1):
+    ts, tst = page_table.shape, page_table.stride()
+    if len(ts) != 2 or ts[0] != B or (tst[1] != 1 and ts[1] > 1):
         raise ValueError("page_table must be [sequences, pages] with contiguous rows")
     cu = 0
     if cu_seqlens_q is not None:
@@ -585,8 +584,8 @@ def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
                             "1 elements")
         cu = cu_seqlens_q.data_ptr()
     pages, heads, page, D = shape
-    return (heads, D, dtype_code(k_pages.dtype), pages, page, B, ts[1], page_table.data_ptr(),
-            page_table.stride(0), cu, seq_lens_kv.data_ptr(), ks, vs)
+    return (heads, D, dtype_code(dtype), pages, page, B, ts[1], page_table.data_ptr(), tst[0], cu,
+            seq_lens_kv.data_ptr(), ks, vs)
 
 
 def _paged_pack(c, T, hq, scale, causal, sinks, qs, os):
@@ -596,66 +595,78 @@ def _paged_pack(c, T, hq, scale, causal, sinks, qs, os):
                        vs[0], vs[1], vs[2])
 
 
-def _paged_queries(q, c, dev):
-    if q.dim() != 3 or q.shape[2] != c[1] or q.stride(2) != 1:
+def _paged_queries(q, c):
+    """q's shape and strides, checked against the cache's."""
+    shape, st = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != c[1] or st[2] != 1:
         raise ValueError("q must be [tokens, heads, D] with a contiguous last dimension")
     if dtype_code(q.dtype) != c[2]:
         raise TypeError("q and the cache must share a dtype")
+    return shape, st
 
 
-def _check_lse(lse, q, dev):
+def _check_lse(lse, shape, dev):
     if (lse.dtype is not _torch().float32 or lse.get_device() != dev
-            or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+            or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] CUDA tensor")
 
 
 def _check_scores(scores, c, dev, what="scores"):
-    s = scores.shape
-    if (scores.dtype is not _torch().float32 or scores.get_device() != dev or len(s) != 3
-            or s[0] != c[5] or s[1] != c[0] or (s[2] > 1 and scores.stride(2) != 1)):
+    """The strides of a scores tensor."""
+    s, st = scores.shape, scores.stride()
+    if (len(s) != 3 or s[0] != c[5] or s[1] != c[0] or (st[2] != 1 and s[2] > 1)
+            or scores.dtype is not _torch().float32 or scores.get_device() != dev):
         raise ValueError("%s must be a float32 CUDA tensor [sequences, kv heads, positions] with "
                          "contiguous rows" % what)
+    return st
 
 
-def _paged_workspace(workspace, dev, device, D, stream, own_stream):
-    """(address, bytes) of the given workspace, or of one that the binding
-    keeps for this thread and the current torch stream, whose calls follow one
-    another (those of two threads may interleave their kernels).  A call
-    under graph capture, or on a raw stream handle, gets one of its own: a
-    graph's belongs to the graph's pool, so that graphs share none."""
+def _check_int32(t, n, dev, what):
+    if (t.dtype is not _torch().int32 or t.get_device() != dev or t.numel() != n
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous int32 CUDA tensor of %d elements" % (what, n))
+
+
+def _new_workspace(device, D):
+    p = SdpaPagedParams()
+    p.num_seqs = p.num_tokens = p.num_q_heads = p.num_kv_heads = p.page_size = 1
+    p.head_dim, p.scale = D, 1.0
+    torch = _torch()
+    return torch.empty(max(sdpa_paged_workspace_size(p), 16), dtype=torch.uint8, device=device)
+
+
+def _paged_workspace(workspace, dev, device, D, stream):
+    """(tensor, address, bytes) of the given workspace, or of one that the
+    binding keeps for this thread and the current torch stream, whose calls
+    follow one another (those of two threads may interleave their kernels).  A
+    call under graph capture gets one of its own, which belongs to the graph's
+    pool, so that graphs share none."""
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    torch = _torch()
-    keep = own_stream and not torch._C._cuda_isCurrentStreamCapturing()
+    keep = not _torch()._C._cuda_isCurrentStreamCapturing()
     key = (dev, stream, D, threading.get_ident())
     if keep:
         kept = _paged_ws.get(key)
         if kept is not None:
             return kept
-    p = SdpaPagedParams()
-    p.num_seqs = p.num_tokens = p.num_q_heads = p.num_kv_heads = p.page_size = 1
-    p.head_dim, p.scale = D, 1.0
-    ws = torch.empty(max(sdpa_paged_workspace_size(p), 16), dtype=torch.uint8, device=device)
+    ws = _new_workspace(device, D)
     made = (ws, ws.data_ptr(), ws.numel())
     if keep:
         _paged_ws[key] = made
     return made
 
 
-def _on(dev, stream, call):
-    """call(raw stream) with `dev` current, on the current stream or, where a
-    raw handle is given, with that stream current (what the call allocates
-    then belongs to it)."""
+def _elsewhere(dev, stream, call):
+    """call() with `dev` current and, where a raw stream handle is given, that
+    stream current: what the call allocates then belongs to it."""
     torch = _torch()
-    if torch._C._cuda_getDevice() != dev:
-        with torch.cuda.device(dev):
-            return _on(dev, stream, call)
-    if stream is None:
-        return call(torch._C._cuda_getCurrentRawStream(dev))
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
-        return call(stream)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call()
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+            return call()
 
 
 def _paged_status(st):
@@ -684,17 +695,21 @@ def sdpa_paged_write(k, v, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens
     """
     dev = k.get_device()
     c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)
-    shape, kn, vn = k.shape, k.stride(), v.stride()
+    cuda = _torch()._C
+    if stream is not None or cuda._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_write(
+            k, v, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q))
+    shape, kn, vn, dtype = k.shape, k.stride(), v.stride(), k_pages.dtype
     if (len(shape) != 3 or shape[1] != c[0] or shape[2] != c[1] or v.shape != shape
             or kn[2] != 1 or vn[2] != 1 or v.get_device() != dev):
         raise ValueError("k and v must be [tokens, kv heads, D] on the same device with a "
                          "contiguous last dimension")
-    if k.dtype is not k_pages.dtype or v.dtype is not k_pages.dtype:
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise TypeError("k, v and the cache must share a dtype")
     p = _paged_pack(c, shape[0], 0, 1.0, 1, 0, (0, 0), (0, 0))
-    _paged_status(_on(dev, stream, lambda s: _paged_call("sdpa_paged_write")(
+    _paged_status(_paged_call("sdpa_paged_write")(
         p, k.data_ptr(), v.data_ptr(), _STRIDE2(kn[0], kn[1]), _STRIDE2(vn[0], vn[1]),
-        k_pages.data_ptr(), v_pages.data_ptr(), s)))
+        k_pages.data_ptr(), v_pages.data_ptr(), cuda._cuda_getCurrentRawStream(dev)))
 
 
 def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q=None,
@@ -714,31 +729,34 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_
     torch = _torch()
     dev = q.get_device()
     c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)
-    _paged_queries(q, c, dev)
+    shape, qs = _paged_queries(q, c)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_forward(
+            q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, scale, causal, sinks, out,
+            lse, return_lse, _new_workspace(q.device, c[1]) if workspace is None else workspace))
     if sinks is not None and (sinks.dtype is not torch.float32 or sinks.get_device() != dev
-                              or sinks.numel() != q.shape[1] or not sinks.is_contiguous()):
+                              or sinks.numel() != shape[1] or not sinks.is_contiguous()):
         raise TypeError("sinks must be a contiguous float32 CUDA tensor with Hq elements")
-    if out is not None and (out.shape != q.shape or out.dtype is not q.dtype
-                            or out.get_device() != dev or out.stride(2) != 1):
-        raise ValueError("out must be like q with a contiguous last dimension")
+    if out is None:
+        out = torch.empty_like(q)
+        os = out.stride()
+    else:
+        os = out.stride()
+        if (out.shape != shape or os[2] != 1 or out.dtype is not q.dtype
+                or out.get_device() != dev):
+            raise ValueError("out must be like q with a contiguous last dimension")
     if lse is not None:
-        _check_lse(lse, q, dev)
-
-    def call(s):
-        o = torch.empty_like(q) if out is None else out
-        ls = lse
-        if ls is None and return_lse:
-            ls = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        ws, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s, stream is None)
-        p = _paged_pack(c, q.shape[0], q.shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
-                        1 if causal else 0, 0 if sinks is None else sinks.data_ptr(), q.stride(),
-                        o.stride())
-        _paged_status(_paged_call("sdpa_paged_forward")(
-            p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(),
-            None if ls is None else ls.data_ptr(), wp, wn, s))
-        return (o, ls) if return_lse else o
-
-    return _on(dev, stream, call)
+        _check_lse(lse, shape, dev)
+    elif return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    s = torch._C._cuda_getCurrentRawStream(dev)
+    _, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s)
+    p = _paged_pack(c, shape[0], shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
+                    1 if causal else 0, 0 if sinks is None else sinks.data_ptr(), qs, os)
+    _paged_status(_paged_call("sdpa_paged_forward")(
+        p, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), wp, wn, s))
+    return (out, lse) if return_lse else out
 
 
 def sdpa_paged_scores(q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqlens_q=None,
@@ -751,21 +769,23 @@ def sdpa_paged_scores(q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqle
     q and the cache arguments as given to sdpa_paged_forward, lse its second
     result.
     """
+    cuda = _torch()._C
     dev = q.get_device()
     c = _paged_cache(dev, k_pages, None, page_table, seq_lens_kv, cu_seqlens_q)
-    _paged_queries(q, c, dev)
-    _check_scores(scores, c, dev)
-    _check_lse(lse, q, dev)
-    p = _paged_pack(c, q.shape[0], q.shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
-                    1 if causal else 0, 0, q.stride(), (0, 0))
-
-    def call(s):
-        ws, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s, stream is None)
-        return _paged_call("sdpa_paged_scores")(
-            p, q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(), scores.data_ptr(),
-            _STRIDE2(*scores.stride()[:2]), scores.shape[2], wp, wn, s)
-
-    _paged_status(_on(dev, stream, call))
+    shape, qs = _paged_queries(q, c)
+    if stream is not None or cuda._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_scores(
+            q, k_pages, lse, scores, page_table, seq_lens_kv, cu_seqlens_q, scale, causal,
+            _new_workspace(q.device, c[1]) if workspace is None else workspace))
+    ss = _check_scores(scores, c, dev)
+    _check_lse(lse, shape, dev)
+    s = cuda._cuda_getCurrentRawStream(dev)
+    _, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s)
+    p = _paged_pack(c, shape[0], shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
+                    1 if causal else 0, 0, qs, (0, 0))
+    _paged_status(_paged_call("sdpa_paged_scores")(
+        p, q.data_ptr(), k_pages.data_ptr(), lse.data_ptr(), scores.data_ptr(),
+        _STRIDE2(ss[0], ss[1]), scores.shape[2], wp, wn, s))
     return scores
 
 
@@ -786,33 +806,31 @@ def sdpa_paged_evict(k_pages, v_pages, scores, page_table, seq_lens_kv, keep, re
     torch = _torch()
     dev = k_pages.get_device()
     c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, None)
-    _check_scores(scores, c, dev)
-    keep, recent, B = int(keep), int(recent), c[5]
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_evict(
+            k_pages, v_pages, scores, page_table, seq_lens_kv, keep, recent, scores_out,
+            seq_lens_out, kept))
+    ss = _check_scores(scores, c, dev)
+    keep, recent, B, heads = int(keep), int(recent), c[5], c[0]
     if keep < 1 or recent < 0:
         raise ValueError("keep must be at least 1 and recent at least 0")
-    if scores_out is not None:
-        _check_scores(scores_out, c, dev, "scores_out")
-        if scores_out.shape != scores.shape or scores_out.stride() != scores.stride():
-            raise ValueError("scores_out must have the shape and strides of scores")
-    for t, n, what in ((seq_lens_out, B, "seq_lens_out"), (kept, B * c[0] * keep, "kept")):
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != dev
-                              or t.numel() != n or not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous int32 CUDA tensor of %d elements" % (what, n))
+    device = scores.device
+    if scores_out is None:
+        scores_out = (torch.empty_like(scores) if scores.is_contiguous() else
+                      torch.empty_strided(scores.shape, ss, dtype=torch.float32, device=device))
+    elif scores_out.shape != scores.shape or _check_scores(scores_out, c, dev, "scores_out") != ss:
+        raise ValueError("scores_out must have the shape and strides of scores")
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens_kv)
+    else:
+        _check_int32(seq_lens_out, B, dev, "seq_lens_out")
+    if kept is None:
+        kept = torch.empty((B, heads, keep), dtype=torch.int32, device=device)
+    else:
+        _check_int32(kept, B * heads * keep, dev, "kept")
     p = _paged_pack(c, 0, 0, 1.0, 1, 0, (0, 0), (0, 0))
-
-    def call(s):
-        kp = kept
-        if kp is None:
-            kp = torch.empty((B, c[0], keep), dtype=torch.int32, device=k_pages.device)
-        sl = torch.empty_like(seq_lens_kv) if seq_lens_out is None else seq_lens_out
-        so = torch.empty_like(scores) if scores_out is None else scores_out
-        if so.stride() != scores.stride():
-            so = torch.empty_strided(scores.shape, scores.stride(), dtype=torch.float32,
-                                     device=scores.device)
-        _paged_status(_paged_call("sdpa_paged_evict")(
-            p, keep, recent, k_pages.data_ptr(), v_pages.data_ptr(), scores.data_ptr(),
-            so.data_ptr(), _STRIDE2(*scores.stride()[:2]), scores.shape[2], kp.data_ptr(),
-            sl.data_ptr(), s))
-        return kp, sl, so
-
-    return _on(dev, stream, call)
+    _paged_status(_paged_call("sdpa_paged_evict")(
+        p, keep, recent, k_pages.data_ptr(), v_pages.data_ptr(), scores.data_ptr(),
+        scores_out.data_ptr(), _STRIDE2(ss[0], ss[1]), scores.shape[2], kept.data_ptr(),
+        seq_lens_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
+    return kept, seq_lens_out, scores_out
