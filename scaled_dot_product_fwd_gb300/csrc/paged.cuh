@@ -453,6 +453,9 @@ struct Boxes {
 // Launchers (host side).  `a` holds the problem and the workspace; the
 // attention and score launchers fill in the tile's rows (gu, nsub, w).
 sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
+int paged_vector_rows(const paged::Args& a);
+sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
+                                      const LaunchEnv& env);
 sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
                                        const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);

@@ -246,8 +246,11 @@ sdpa_status_t sdpa_paged_forward(const sdpa_paged_params_t* p, const void* q,
   a.v = v_pages;
   a.o = o;
   a.lse = lse;
-  if (!tc_fits(*p, true))
-    st = launch_paged_simt(a, p->head_dim, p->dtype, env);
+  if (!tc_fits(*p, true)) {
+    const int rows = p->dtype == SDPA_F32 ? paged_vector_rows(a) : 0;
+    st = rows ? launch_paged_vector_f32(a, p->head_dim, rows, env)
+              : launch_paged_simt(a, p->head_dim, p->dtype, env);
+  }
   else if (const int rows = paged_decode_rows(a))
     st = launch_paged_decode_tc(a, p->head_dim, p->dtype, rows, env);
   else
