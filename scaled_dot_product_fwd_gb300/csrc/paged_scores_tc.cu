@@ -15,10 +15,12 @@
 // work is divided among the CTAs as paged.cuh describes.  The K tiles of one
 // unit and four query chunks are in shared memory (head_dim 128); S^T is
 // double-buffered, so the products of a step run while the exponentials of
-// the one before do.  Chunks: bound by the exponentials (128 x 256 a step,
-// about 1100 clk at the measured 30 a clk and SM, against 1024 clk of
-// products at head_dim 128).  Few rows a sequence (single tokens): the
-// chunk has R = 16, 32 or 64 columns and K streams once, bound by HBM.
+// the one before do.  Chunks (8192 tokens over themselves, 32 heads over 8,
+// head_dim 128: 213 us, 1290 TFLOP/s): bound by the issue and latency of the
+// exponentials' loop; its floors are 1024 clk of products a step and about
+// 1100 of exponentials, and it takes about 1800.  Few rows a sequence (single
+// tokens): the chunk has R = 16, 32 or 64 columns and K streams once, bound by
+// HBM (8 x 32768 keys: 102 us, 5.4 TB/s).
 //
 // Rows that do not exist (past the sequence's tokens, another head's) take no
 // part: their limit is 0, and a chunk that holds one, or a key that some row

@@ -6,26 +6,33 @@
 // The rows of a 128-row query tile are (token, query head) pairs of one kv
 // head: w = 128 / gu tokens times gu heads, row = token * gu + head, which a
 // TMA box of w tokens x gu heads lays down in that order.  So the tokens and
-// heads that read the same keys share every K and V tile, a single token
-// included, and one kernel serves prompt chunks and decode steps.  The work is
-// divided as paged.cuh describes (equal shares of all key tiles of all units,
-// cut units merged after).
+// heads that read the same keys share every K and V tile.  The work is divided
+// as paged.cuh describes (equal shares of all key tiles of all units, cut
+// units merged after); calls of up to 16 rows a sequence and kv head take
+// paged_decode_tc.cu.
 //
 // Two forms:
 //  NT = 2  (sequences of more than 128 rows on average): a unit is two query
 //          tiles that share each K/V tile; S_0 | S_1 | O_0 | O_1 in TMEM, and
 //          the softmax of one tile overlaps the products of the other.  Bound
-//          by the softmax warps and the tensor pipe.
-//  NT = 1  (decode and short chunks): one query tile; S is double-buffered
-//          over the key tiles (S_j+1 is computed while the softmax works on
-//          S_j), three 64 KB K/V stages in flight at head_dim 128.  Bound by
-//          HBM: few rows are live, and warps without one do no arithmetic.
+//          by the tensor pipe and the softmax warps (4096 tokens over 32768
+//          keys, 32 heads over 8, head_dim 128, bf16: 1190 us, 1730 TFLOP/s,
+//          the pipe 71 % active).
+//  NT = 1  (short chunks, 17 to 128 rows): one query tile; S is
+//          double-buffered over the key tiles (S_j+1 is computed while the
+//          softmax works on S_j), six 32 KB K/V slots in flight at head_dim
+//          128.  Bound by the softmax chain of a key tile where HBM is not
+//          (8 x 16 tokens over 4096 keys: 37 us, 3.6 TB/s); warps without a
+//          row do no arithmetic.
+// K and V have ring slots of their own, each released when its products are
+// done: loads then run a step further ahead than with a slot for both (the
+// 4096-token chunk above 1715 -> 1210 us).
 //
 // Key tiles are 128 keys in boxes of R = gcd(page_size, 128) rows, each
 // inside a page; one lane of the producer warp looks up and loads each box, in
 // one copy for both 64-column halves of its rows (a tile lies as [16 groups
 // of 8 keys][D / 64][8][64], which both operand descriptors take).  With a
-// copy per half, 16-row pages cost 40 % more: a copy has a price of its own.
+// copy per half, 16-row pages cost 30 % more: a copy has a price of its own.
 // Boxes past the sequence's length are not loaded.  What the last tile holds
 // behind it (a page's rows of no sequence yet: anything, NaN included) is kept
 // out of the results: such scores are replaced by -inf, the value product
