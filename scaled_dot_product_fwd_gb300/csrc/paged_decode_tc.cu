@@ -9,7 +9,7 @@
 //     O^T += V^T P^T   M = 128 head dims,  N = 16 rows, K = 128 keys
 // so each of 128 threads has one key of a tile and NR exponentials, instead
 // of one warp having 128 for each of a few rows (64 x 4096 keys, 16 heads over
-// 2, head_dim 64: 33.7 us; with rows on the lanes 41).
+// 2, head_dim 64: 32.8 us; with rows on the lanes 36.8).
 //
 // A CTA walks its share of the line of key tiles (paged.cuh), so the running
 // form of the softmax is needed: every thread holds the rows' reference
@@ -19,8 +19,9 @@
 // TMEM) is rescaled; after a row's first tile that is rare.  The sums stay
 // per thread until the unit ends.
 //
-// Bound by HBM (8 x 32768 keys, head_dim 128, bf16: 164 us, 6.5 TB/s): six 32 KB K/V slots in flight (twelve of 16 KB at head_dim
-// 64), S three tiles ahead of P V; TMEM holds eight S^T tiles and O^T.
+// Bound by HBM (8 x 32768 keys, head_dim 128, bf16: 164-170 us, 6.3-6.5
+// TB/s): six 32 KB K/V slots in flight (twelve of 16 KB at head_dim 64), S
+// three tiles ahead of P V; TMEM holds eight S^T tiles and O^T.
 #include "paged.cuh"
 #include "prefill_tc.cuh"
 
@@ -615,7 +616,11 @@ sdpa_status_t launch_decode_of(Args a, int dtype, int rows, const LaunchEnv& env
 }  // namespace paged
 
 int paged_decode_rows(const paged::Args& a) {
-  // rows of a sequence and kv head, on average over the batch
+  // Rows of a sequence and kv head, on average over the batch.  Against the
+  // 128-row form of paged_tc.cuh (us): 4 sequences of up to 1000 keys, 4 rows,
+  // 10.9 and 13.7; 16 x 4096 keys, 16 rows, 52.5 and 56.6.  Eight rows a tile
+  // against sixteen: 10.9 and 12.1, and 32.8 and 35.1 at 64 x 4096 keys, 8
+  // rows, head_dim 64.
   const long long rows = static_cast<long long>(a.T) * a.G;
   if (a.G <= 8 && rows <= 8LL * a.B) return 8;
   return a.G <= 16 && rows <= 16LL * a.B ? 16 : 0;
