@@ -531,6 +531,18 @@ bool allow_smem(int bytes) {
   return true;
 }
 
+// Query rows (tokens times heads of a kv head) of a sequence on average, by
+// which a kernel is chosen: the offsets are on the device.  A chunk among
+// single tokens is read in passes of few rows then, but it can be at most a
+// few tokens a sequence of the batch long where the average is small, so that
+// its passes weigh no more than the single tokens' (255 single tokens and a
+// chunk of 257 over 4096 keys, 32 heads over 8, head_dim 128: 675 us with
+// 8-row tiles, 651 with one 128-row tile a unit, 812 with two; the chunk's
+// length alone as the rule slowed its score sums from 515 to 892).
+inline long long call_rows(const Args& a) {
+  return a.cu ? (static_cast<long long>(a.T) * a.G + a.B - 1) / a.B : a.G;
+}
+
 // Rows of a page box: log2 of gcd(page_size, 128).
 inline int box_log2(int page_size) {
   int lg = 7;

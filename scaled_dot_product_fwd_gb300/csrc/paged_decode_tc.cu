@@ -616,14 +616,12 @@ sdpa_status_t launch_decode_of(Args a, int dtype, int rows, const LaunchEnv& env
 }  // namespace paged
 
 int paged_decode_rows(const paged::Args& a) {
-  // Rows of a sequence and kv head, on average over the batch.  Against the
-  // 128-row form of paged_tc.cuh (us): 4 sequences of up to 1000 keys, 4 rows,
+  // Against the 128-row form of paged_tc.cuh (us): 4 sequences of up to 1000 keys, 4 rows,
   // 10.9 and 13.7; 16 x 4096 keys, 16 rows, 52.5 and 56.6.  Eight rows a tile
   // against sixteen: 10.9 and 12.1, and 32.8 and 35.1 at 64 x 4096 keys, 8
   // rows, head_dim 64.
-  const long long rows = static_cast<long long>(a.T) * a.G;
-  if (a.G <= 8 && rows <= 8LL * a.B) return 8;
-  return a.G <= 16 && rows <= 16LL * a.B ? 16 : 0;
+  const long long rows = paged::call_rows(a);
+  return a.G > 16 ? 0 : a.G <= 8 && rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
 }
 
 sdpa_status_t launch_paged_decode_tc(const paged::Args& a, int head_dim, int dtype, int rows,

@@ -515,13 +515,12 @@ sdpa_status_t launch_sc(const Args& a, const CUtensorMap& tq, const CUtensorMap&
 
 template <int D>
 sdpa_status_t launch_scores(Args& a, int dtype, const LaunchEnv& env) {
-  // Columns of a chunk: the fewest that hold a sequence's rows on average (a
+  // Columns of a chunk: the fewest that hold a sequence's rows (a
   // column costs an exponential whether its row exists or not: 10 x 34 tokens
   // over up to 24727 keys, one head a kv head, took 106 us with 128 columns
   // and 67 with 64).
-  const long long rows = static_cast<long long>(a.T) * a.G;
   int cols = 16;
-  while (cols < 128 && (a.G > cols || rows > static_cast<long long>(cols) * a.B)) cols *= 2;
+  while (cols < 128 && (a.G > cols || call_rows(a) > cols)) cols *= 2;
   fit_rows(a, cols);
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType dt =

@@ -656,9 +656,8 @@ sdpa_status_t start(Args& a, int smem, int ctas, cudaStream_t stream) {
 template <typename T, int D>
 sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   // few rows a sequence (decode): the 16-row tile, see the top of the file
-  const bool few = static_cast<long long>(a.T) * a.G <= 16LL * a.B;
-  fit_rows(a, few && a.G <= 16 ? 16 : 64);
-  const int rows = few && a.G <= 16 ? 16 : 64;
+  const int rows = a.G <= 16 && call_rows(a) <= 16 ? 16 : 64;
+  fit_rows(a, rows);
   const sdpa_status_t st =
       rows == 16 ? start<paged_simt_kernel<T, D, 16>>(
                        a, attend_smem<T, D, 16>(), attend_ctas<T, D, 16>() * env.num_sms, env.stream)
@@ -671,7 +670,7 @@ sdpa_status_t attend(Args& a, const LaunchEnv& env) {
 
 template <typename T, int D>
 sdpa_status_t score(Args& a, const LaunchEnv& env) {
-  const bool few = a.G <= 16 && static_cast<long long>(a.T) * a.G <= 16LL * a.B;
+  const bool few = a.G <= 16 && call_rows(a) <= 16;
   fit_rows(a, few ? 16 : 64);
   const sdpa_status_t st =
       few ? start<paged_scores_simt_kernel<T, D, 16>>(

@@ -12,7 +12,7 @@
 // paged_decode_tc.cu.
 //
 // Two forms:
-//  NT = 2  (sequences of more than 128 rows on average): a unit is two query
+//  NT = 2  (sequences of more than 128 rows): a unit is two query
 //          tiles that share each K/V tile; S_0 | S_1 | O_0 | O_1 in TMEM, and
 //          the softmax of one tile overlaps the products of the other.  Bound
 //          by the tensor pipe and the softmax warps (4096 tokens over 32768

@@ -307,9 +307,8 @@ sdpa_status_t launch_vector(Args& a, const LaunchEnv& env) {
 
 // Rows of a tile of this kernel for a call (4 or 8; 0: the tile kernel's).
 int paged_vector_rows(const paged::Args& a) {
-  const long long rows = static_cast<long long>(a.T) * a.G;
-  if (a.G <= 4 && rows <= 4LL * a.B) return 4;
-  return a.G <= 8 && rows <= 8LL * a.B ? 8 : 0;
+  const long long rows = paged::call_rows(a);
+  return a.G <= 4 && rows <= 4 ? 4 : a.G <= 8 && rows <= 8 ? 8 : 0;
 }
 
 sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
