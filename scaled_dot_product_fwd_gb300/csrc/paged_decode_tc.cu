@@ -356,7 +356,9 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
         mma_commit_elect(&empty[s], 1u);
         if (j + rp.ahead < n) scores(j + rp.ahead);
       }
-      mma_commit_elect(o_done, 1u);
+      // (a unit without keys hands over nothing: the softmax warps, who did not
+      // hold this warp up there, could miss a phase)
+      if (n > 0) mma_commit_elect(o_done, 1u);
       p0 += 2 * n;
       g0 += n;
     }
@@ -511,8 +513,11 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
         }
         red[128 + i] = f;
       }
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(o_done, static_cast<uint32_t>(units_done & 1), wc));
-      ++units_done;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu,
+                        ok && mbar_wait(o_done, static_cast<uint32_t>(units_done & 1), wc));
+        ++units_done;
+      }
       tc_fence_after();
       __syncwarp();
       uint32_t ov[NR];

@@ -324,9 +324,9 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t >= tg.nt) continue;
-            if (tg.n[t] == 0) {
-              mma_commit_elect(&o_done[t], 1u);
-            } else {
+            // (a tile without keys hands over nothing: its softmax warps, who
+            // would not hold this warp up, could miss a phase of o_done)
+            if (tg.n[t] > 0) {
               issue_s(t, t, kslot(0));
               mma_commit_elect(&s_full[t], 1u);
             }
@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
           }
         } else {
           if (tg.nmax == 0) {
-            mma_commit_elect(&o_done[0], 1u);
             mma_commit_elect(q_empty, 1u);
           } else {
             issue_s(0, g0 & 1, kslot(0));
@@ -534,10 +533,12 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
         // hand P_j to the MMA warp; met every step, also after a failed wait
         named_bar_sync(kPBar + (NT == 2 ? t : 0), 32 * 5);
       }
-      ok = ok && mbar_wait(&o_done[t], static_cast<uint32_t>(oph & 1), wc);
-      ok = __all_sync(0xffffffffu, ok);
+      if (n > 0) {
+        ok = ok && mbar_wait(&o_done[t], static_cast<uint32_t>(oph & 1), wc);
+        ok = __all_sync(0xffffffffu, ok);
+        ++oph;
+      }
       g0 += n;
-      ++oph;
       // ------------------------------------------------------------ epilogue
       const bool whole = unit->whole();
       if (!whole && unit->s0 == 0 && threadIdx.x == 0) {

@@ -227,6 +227,23 @@ def test_forward_empty_rows(cuda, S, dtype):
     assert (o == 0).all() and (lse == -math.inf).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,nq", [(4, 1), (12, 1), (20, 3), (20, 40)])
+@pytest.mark.parametrize("ctas", [1, 2, 0])
+def test_sequences_without_keys_among_others(cuda, S, hook, ctas, hq, nq, D, dtype):
+    """Units without a key, alone and several in a row, before and behind
+    units with some in one CTA's share."""
+    hook("paged_ctas", ctas)
+    ks = [0, 300, 0, 5, 0, 0, 140, 128, 0, 0, 0, 17, 2, 0]
+    t = Batch(cuda, [nq] * len(ks), ks, hq, 1, D, dtype, 16)
+    for causal in (True, False):
+        o, lse = forward(S, t, causal=causal)
+        check_forward(t, o, lse, 1 / math.sqrt(D), causal)
+    cuda.cuda.synchronize()
+    assert S.sdpa_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[4], SHAPES[7]], ids=str)
 def test_sink_of_minus_infinity_is_none(cuda, S, shape, dtype):
@@ -423,6 +440,26 @@ def test_scores_options(cuda, S, dtype):
         check_scores(t, got, base, lse, kw.get("scale", 1 / 8), kw.get("causal", True), sinks)
         wide[:, ::2, 3:253] = 0
         assert (wide == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,D,page", [(2, 128, 16), (4, 64, 5), (14, 64, 8)])
+@pytest.mark.parametrize("ctas", [0, 3])
+def test_single_tokens_with_a_chunk(cuda, S, hook, ctas, hq, D, page, causal, dtype):
+    """Few rows a sequence on average, one sequence with many: its keys'
+    sums take several blocks of rows."""
+    hook("paged_ctas", ctas)
+    qs = [1, 1, 70 if hq == 4 else 9, 0, 2, 1, 1] + [1] * (120 if hq == 4 else 10)
+    ks = [130, 64, 300, 77, 2, 0, 200] + [1 + 7 * i % 190 for i in range(len(qs) - 7)]
+    t = Batch(cuda, qs, ks, hq, 2, D, dtype, page, pad=1)
+    o, lse = forward(S, t, causal=causal)
+    check_forward(t, o, lse, 1 / math.sqrt(D), causal)
+    base = cuda.rand(len(ks), 2, 310, device="cuda")
+    got = base.clone()
+    S.sdpa_paged_scores(t.q, t.k_pages, lse, got, t.table, t.lens, cu_seqlens_q=t.cu,
+                        causal=causal)
+    check_scores(t, got, base, lse, 1 / math.sqrt(D), causal)
 
 
 # --------------------------------------------------------------------- write
