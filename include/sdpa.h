@@ -330,8 +330,8 @@ SDPA_API uint64_t sdpa_debug_set_wait_limit_ns(uint64_t ns);
  *  SDPA_DEBUG_DECODE_VECTOR   1: head_dim-64/128 fp16/bf16 decode on the
  *                             vector path instead of the tensor-core pass
  *                             (default 0)
- *  SDPA_DEBUG_PAGED_SIMT      1: fp16/bf16 sdpa_paged_forward and
- *                             sdpa_paged_scores on the CUDA-core kernels
+ *  SDPA_DEBUG_PAGED_SIMT      1: sdpa_paged_forward and sdpa_paged_scores of
+ *                             every type on the CUDA-core tile kernels
  *                             (default 0)
  *  SDPA_DEBUG_PAGED_CTAS      CTAs that share the work of sdpa_paged_forward
  *                             and sdpa_paged_scores (0: the plan's; at most

@@ -456,6 +456,8 @@ sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const La
 int paged_vector_rows(const paged::Args& a);
 sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
                                       const LaunchEnv& env);
+sdpa_status_t launch_paged_scores_vector_f32(paged::Args a, int head_dim, int rows,
+                                             const LaunchEnv& env);
 sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
                                        const LaunchEnv& env);
 sdpa_status_t launch_paged_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);

@@ -286,9 +286,20 @@ sdpa_status_t sdpa_paged_scores(const sdpa_paged_params_t* p, const void* q,
   a.ss[0] = score_stride[0];
   a.ss[1] = score_stride[1];
   a.score_len = score_len;
-  st = tc_fits(*p, false) ? launch_paged_scores_tc(a, p->head_dim, p->dtype, env)
-                          : launch_paged_scores_simt(a, p->head_dim, p->dtype, env);
-  if (st == SDPA_OK) set_last_launches(2);
+  int launches = 2;
+  // (the few-row kernel counts a sequence's steps, key tiles times blocks of
+  // rows, in 32 bits)
+  const int rows = p->dtype == SDPA_F32 && (a.cap / 64 + 1LL) * a.T <= INT32_MAX
+                       ? paged_vector_rows(a) : 0;
+  if (tc_fits(*p, false)) {
+    st = launch_paged_scores_tc(a, p->head_dim, p->dtype, env);
+  } else if (rows) {
+    launches = 1;
+    st = launch_paged_scores_vector_f32(a, p->head_dim, rows, env);
+  } else {
+    st = launch_paged_scores_simt(a, p->head_dim, p->dtype, env);
+  }
+  if (st == SDPA_OK) set_last_launches(launches);
   return st;
 }
 
