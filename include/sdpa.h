@@ -430,7 +430,9 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
  *    >= 1.  fp16/bf16 with page_size a multiple of 8 run on the tensor cores,
  *    everything else on fp32 CUDA-core kernels.
  *  - Base pointers 16-byte aligned, row strides multiples of 16 bytes; o must
- *    not overlap the inputs.  flags and reserved fields must be 0.
+ *    not overlap the inputs.  sdpa_paged_write and sdpa_paged_evict want k_pages
+ *    and v_pages without a common row (interleaved is fine; one cache for both
+ *    is refused, unless the rows written are the same too).  flags and reserved fields must be 0.
  *  - Asynchronous on `stream`, nothing allocated, results independent of
  *    timing (fixed summation order).  Host-side errors as for sdpa_forward.
  *    Two calls that overlap on the GPU must not share a workspace.
@@ -517,7 +519,8 @@ SDPA_API sdpa_status_t sdpa_paged_scores(const sdpa_paged_params_t* params, cons
  * others those of largest score (ties to the lower position; NaN counts as
  * -inf, 0 and -0 tie).  The kept rows of K and V move, in order, to positions
  * 0, 1, ... of the sequence's own pages; the heads choose independently.
- * Sequences of at most `keep` keys stay as they are.
+ * Sequences of at most `keep` keys stay as they are.  keep and score_len are
+ * at most 2^30.
  *  scores: float32 [num_seqs, Hkv, score_len] as for sdpa_paged_scores; keys
  *      at or past score_len count as score 0.
  *  scores_out: NULL or the kept keys' scores in their new places, 0 behind

@@ -213,6 +213,7 @@ sdpa_status_t sdpa_paged_write(const sdpa_paged_params_t* p, const void* k, cons
   if ((st = check_arrays(*p)) != SDPA_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
     return SDPA_ERR_MISALIGNED;
+  if (p->num_pages > 0 && k_pages == v_pages && k != v) return SDPA_ERR_INVALID_ARGUMENT;
   LaunchEnv env;
   if (!make_env(&env, stream)) return SDPA_ERR_CUDA;
   paged::Args a = make_args(*p);
@@ -312,6 +313,8 @@ sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* p, int32_t keep, int32
   sdpa_status_t st = validate(p, kUsesV);
   if (st != SDPA_OK) return st;
   if (keep < 1 || recent < 0 || score_len < 0) return SDPA_ERR_INVALID_ARGUMENT;
+  // (as for the positions: loops over either step past them in 32 bits)
+  if (keep > (1 << 30) || score_len > (1 << 30)) return SDPA_ERR_UNSUPPORTED;
   if (p->num_seqs == 0) return SDPA_OK;
   if (!scores || !score_stride || score_stride[0] < 0 || score_stride[1] < 0 || !kept ||
       (p->num_pages > 0 && (!k_pages || !v_pages)) || cache_overlaps(*p) ||
@@ -322,6 +325,8 @@ sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* p, int32_t keep, int32
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(scores, 4) ||
       !aligned(scores_out, 4) || !aligned(kept, 4) || !aligned(seq_lens_out, 4))
     return SDPA_ERR_MISALIGNED;
+  // (K and V move side by side: rows of one cache would move twice)
+  if (p->num_pages > 0 && k_pages == v_pages) return SDPA_ERR_INVALID_ARGUMENT;
   LaunchEnv env;
   if (!make_env(&env, stream)) return SDPA_ERR_CUDA;
   paged::Args a = make_args(*p);

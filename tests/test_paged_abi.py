@@ -147,6 +147,22 @@ def test_evict_rejects(sdpa_lib):
     assert call(P(k_stride=(0, 128, 256))) == 1
 
 
+def test_evict_rejects_counts_past_the_positions(sdpa_lib):
+    """Loops over keep and score_len step past them: near 2^31 they would wrap."""
+    f = sdpa_lib.sdpa_paged_evict
+    p, st, big = P(), i64(128, 64), (1 << 30) + 1
+    for keep, n in ((big, 64), ((1 << 31) - 1, 64), (8, big), (8, (1 << 31) - 1)):
+        assert f(ctypes.byref(p), keep, 2, 256, 512, 256, None, st, n, 256, None, None) == 2
+
+
+def test_one_cache_for_keys_and_values_is_not_written(sdpa_lib):
+    p, st = P(), i64(128, 64)
+    assert sdpa_lib.sdpa_paged_evict(ctypes.byref(p), 8, 2, 256, 256, 256, None, st, 64, 256,
+                                     None, None) == 1
+    kn = i64(256, 128)
+    assert sdpa_lib.sdpa_paged_write(ctypes.byref(p), 256, 512, kn, kn, 1024, 1024, None) == 1
+
+
 def test_binding_rejects_cpu_tensors(sdpa_lib):
     torch = pytest.importorskip("torch")
     q = torch.zeros(1, 2, 64)
