@@ -432,7 +432,8 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
  *  - Base pointers 16-byte aligned, row strides multiples of 16 bytes; o must
  *    not overlap the inputs.  sdpa_paged_write and sdpa_paged_evict want k_pages
  *    and v_pages without a common row (interleaved is fine; one cache for both
- *    is refused, unless the rows written are the same too).  flags and reserved fields must be 0.
+ *    is refused, unless the rows written are the same too).  flags and reserved
+ *    fields must be 0.
  *  - Asynchronous on `stream`, nothing allocated, results independent of
  *    timing (fixed summation order).  Host-side errors as for sdpa_forward.
  *    Two calls that overlap on the GPU must not share a workspace.

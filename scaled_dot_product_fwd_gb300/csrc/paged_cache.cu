@@ -15,10 +15,10 @@
 //    order by a scan, and the weights' new places.
 //  - move (a CTA per (sequence, kv head), K or V, slice of the rows): row
 //    kept[i] goes to row i, for the kept[i] below `keep`, whose rows other
-//    moves overwrite.  kept[i] >= i, and the sources of a chunk lie behind the destinations of every earlier chunk, so a CTA that takes the
-//    chunks in order, loads the next one early and writes a chunk only when
-//    every thread has its rows in registers, moves in place without losing a
-//    row.
+//    moves overwrite.  kept[i] >= i, and the sources of a chunk lie behind the
+//    destinations of every earlier chunk, so a CTA that takes the chunks in
+//    order, loads the next one early and writes a chunk only when every thread
+//    has its rows in registers, moves in place without losing a row.
 //  - far: the rows from positions at or past `keep`, which no move writes, in
 //    any order over the whole GPU.
 #include <cuda_runtime.h>
