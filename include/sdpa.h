@@ -411,14 +411,19 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
  *    reads as zero keys and values (written rows are dropped) and sets the
  *    device status word to SDPA_ERR_PAGE_TABLE.
  *  - seq_lens_kv: device int32 [num_seqs], the keys of each sequence with its
- *    new tokens included (clamped to [0, max_pages * page_size]).
+ *    new tokens included (negative: 0).  Positions at or past max_pages *
+ *    page_size have no place in the cache: nothing is written there, no token
+ *    sees them, and sdpa_paged_evict counts the keys before them only.  The new
+ *    tokens of such a length keep their positions; those past the end see every
+ *    key that has a place.
  *  - New tokens are packed: q is [num_tokens, Hq, D] with element strides
  *    q_stride = {token, head}; the tokens of sequence b are rows
  *    [cu_seqlens_q[b], cu_seqlens_q[b + 1]) (device int32 [num_seqs + 1],
  *    non-decreasing, clamped to [0, num_tokens]).  cu_seqlens_q NULL: one
  *    token a sequence, row b.  They are the sequence's last positions: token
- *    i of nq sits at position nk - nq + i.  Rows past the last sequence's end
- *    belong to none: their rows of o and lse are left as they were.
+ *    i of nq sits at position nk - nq + i, nk the length.  Rows past the last
+ *    sequence's end belong to none: their rows of o and lse are left as they
+ *    were.
  *  - causal nonzero (the usual case): a token sees the keys at and before
  *    its own position; zero: every key of its sequence.  A token that sees
  *    no key (nq > nk) gives o = 0 and lse = -inf, or the sink.

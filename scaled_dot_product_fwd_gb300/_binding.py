@@ -691,7 +691,8 @@ def sdpa_paged_write(k, v, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens
     page_table[b, p // page_size].  seq_lens_kv: int32 [B], keys of each
     sequence with its new tokens, which are its last ones.  cu_seqlens_q:
     int32 [B + 1], sequence b's tokens are rows cu[b] .. cu[b + 1]; None: one
-    token a sequence.  Rows past the last sequence are not written.
+    token a sequence.  Rows past the last sequence are not written, nor are
+    tokens whose position is negative or past the table's columns.
     """
     dev = k.get_device()
     c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)

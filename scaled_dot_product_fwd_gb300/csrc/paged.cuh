@@ -103,9 +103,12 @@ struct Args {
 // token row, query tokens, keys.
 constexpr int kDesc = 8;
 
-// First packed row, new tokens and keys of a sequence.
+// First packed row, new tokens and keys of a sequence, and the position of its
+// first token (negative where the tokens are more than its length).  A length
+// past the table's end leaves the tokens their positions: only the keys end
+// there (`off` stops at the end too, from where every key is seen).
 struct Seq {
-  int q0, nq, nk;
+  int q0, nq, nk, off;
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
@@ -116,7 +119,9 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
     s.q0 = min(b, a.T);
     s.nq = b < a.T ? 1 : 0;
   }
-  s.nk = min(max(a.lens[b], 0), a.cap);
+  const int len = max(a.lens[b], 0);
+  s.nk = min(len, a.cap);
+  s.off = min(len - s.nq, a.cap);
   return s;
 }
 
@@ -149,33 +154,29 @@ struct AttendUnits {
   FastDiv by_w;
   int lg, causal;  // tiles of 2^lg keys
   int cost;        // fixed cost of a unit, in steps
-  __host__ __device__ int count(int nq, int nk) const { return by_w.ceil(nq); }
-  __host__ __device__ int steps(int nq, int nk, int j) const {
-    int lim = nk;
+  __host__ __device__ int count(const Seq& s) const { return by_w.ceil(s.nq); }
+  __host__ __device__ int steps(const Seq& s, int j) const {
+    int lim = s.nk;
     if (causal) {
       const long long last = static_cast<long long>(j + 1) * by_w.d;
-      lim = last < nq ? nk - nq + static_cast<int>(last) : nk;
+      lim = last < s.nk - s.off ? s.off + static_cast<int>(last) : s.nk;
     }
     return lim <= 0 ? 0 : (lim + (1 << lg) - 1) >> lg;
   }
   // steps of the blocks before j
-  __host__ __device__ long long before(int nq, int nk, int j) const {
+  __host__ __device__ long long before(const Seq& s, int j) const {
     if (j <= 0) return 0;
-    if (!causal) return static_cast<long long>(j) * steps(nq, nk, 0);
-    const int n = count(nq, nk);
-    long long r = 0;
-    int full = j;  // blocks that hold w tokens
-    if (j >= n) {
-      full = n - 1;
-      r = steps(nq, nk, n - 1);
-    }
-    if (full > 0) {
-      const int off = nk - nq, w = static_cast<int>(by_w.d);
-      const int i0 = off + w > 0 ? 0 : by_w.div(-off);  // first block that sees a key
-      if (full > i0)
-        r += floor_sum(full - i0, 1LL << lg, w,
-                       off + static_cast<long long>(i0 + 1) * w + (1 << lg) - 1);
-    }
+    const long long all = (s.nk + (1 << lg) - 1) >> lg;
+    if (!causal) return j * all;
+    // blocks whose last token does not see every key: (i + 1) w < nk - off
+    const int cut = s.nk > s.off ? by_w.div(s.nk - s.off - 1) : 0;
+    const int part = j < cut ? j : cut;
+    long long r = (j - part) * all;
+    const int off = s.off, w = static_cast<int>(by_w.d);
+    const int i0 = off + w > 0 ? 0 : by_w.div(-off);  // first block that sees a key
+    if (part > i0)
+      r += floor_sum(part - i0, 1LL << lg, w,
+                     off + static_cast<long long>(i0 + 1) * w + (1 << lg) - 1);
     return r;
   }
 };
@@ -184,21 +185,21 @@ struct AttendUnits {
 struct ScoreUnits {
   FastDiv by_w;
   int lg, causal, nsub, cost;
-  __host__ __device__ int count(int nq, int nk) const {
-    return nq > 0 ? (nk + (1 << lg) - 1) >> lg : 0;
+  __host__ __device__ int count(const Seq& s) const {
+    return s.nq > 0 ? (s.nk + (1 << lg) - 1) >> lg : 0;
   }
-  __host__ __device__ int first(int nq, int nk, int j) const {
-    const int d = (j << lg) - (nk - nq);
+  __host__ __device__ int first(const Seq& s, int j) const {
+    const int d = (j << lg) - s.off;
     return causal && d > 0 ? by_w.div(d) : 0;
   }
-  __host__ __device__ int steps(int nq, int nk, int j) const {
-    return (by_w.ceil(nq) - first(nq, nk, j)) * nsub;
+  __host__ __device__ int steps(const Seq& s, int j) const {
+    return (by_w.ceil(s.nq) - first(s, j)) * nsub;
   }
-  __host__ __device__ long long before(int nq, int nk, int j) const {
+  __host__ __device__ long long before(const Seq& s, int j) const {
     if (j <= 0) return 0;
-    long long r = static_cast<long long>(j) * by_w.ceil(nq);
+    long long r = static_cast<long long>(j) * by_w.ceil(s.nq);
     if (causal) {
-      const int off = nk - nq;
+      const int off = s.off;
       const int i0 = off > 0 ? (off + (1 << lg) - 1) >> lg : 0;  // first j with a cut
       if (j > i0)
         r -= floor_sum(j - i0, by_w.d, 1LL << lg, (static_cast<long long>(i0) << lg) - off);
@@ -245,7 +246,7 @@ struct Walk {
           h = 0;
           if (++b >= a.B) return false;
           s = seq_of(a, b);
-          n = u.count(s.nq, s.nk);
+          n = u.count(s);
         }
         continue;
       }
@@ -253,7 +254,7 @@ struct Walk {
       out->h = h;
       out->j = j;
       out->s = s;
-      const int steps = u.steps(s.nq, s.nk, j);
+      const int steps = u.steps(s, j);
       const long long p0 = pos + u.cost;
       const long long lo = sh.begin - p0, hi = sh.end - p0;
       out->steps = steps;
@@ -287,14 +288,14 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
   const int per = (a.B + kThreads - 1) / kThreads;  // sequences of a thread
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   auto cost = [&](const Seq& s, int n) {
-    return (u.before(s.nq, s.nk, n) + static_cast<long long>(n) * u.cost) * heads;
+    return (u.before(s, n) + static_cast<long long>(n) * u.cost) * heads;
   };
   long long mine = 0;
-  Seq s{0, 0, 0};
+  Seq s{0, 0, 0, 0};
   int n = 0;
   for (int b = b0; b < b1; ++b) {
     s = seq_of(a, b);
-    n = u.count(s.nq, s.nk);
+    n = u.count(s);
     mine += cost(s, n);
   }
   long long incl = mine;  // inclusive scan over the threads
@@ -323,7 +324,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
       sh->pos = total;
       sh->b = a.B;
       sh->h = sh->j = sh->n = 0;
-      sh->s = Seq{0, 0, 0};
+      sh->s = Seq{0, 0, 0, 0};
     }
   }
   long long pos = incl - mine;
@@ -331,7 +332,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
     for (int b = b0; b < b1; ++b) {
       if (b1 - b0 > 1) {
         s = seq_of(a, b);
-        n = u.count(s.nq, s.nk);
+        n = u.count(s);
       }
       const long long c = b1 - b0 > 1 ? cost(s, n) : mine;
       if (begin < pos + c) {
@@ -342,8 +343,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
         int lo = 0, hi = n - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          const long long at =
-              pos + u.before(s.nq, s.nk, mid) + static_cast<long long>(mid) * u.cost;
+          const long long at = pos + u.before(s, mid) + static_cast<long long>(mid) * u.cost;
           if (at <= begin) lo = mid; else hi = mid - 1;
         }
         sh->b = b;
@@ -351,7 +351,7 @@ __device__ __forceinline__ void plan_share(const Args& a, const Units& u, int he
         sh->j = lo;
         sh->n = n;
         sh->s = s;
-        sh->pos = pos + u.before(s.nq, s.nk, lo) + static_cast<long long>(lo) * u.cost;
+        sh->pos = pos + u.before(s, lo) + static_cast<long long>(lo) * u.cost;
         break;
       }
       pos += c;

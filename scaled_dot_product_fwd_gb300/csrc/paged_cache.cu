@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const Wri
   const int b = find_seq(a, t, lane);
   if (b < 0) return;
   const Seq s = seq_of(a, b);
-  const int pos = s.nk - s.nq + (t - s.q0);
-  if (pos < 0 || pos >= s.nk) return;
+  const int pos = s.off + (t - s.q0);
+  if (pos < 0 || pos >= s.nk) return;  // (at or past the table's end: no place)
   const int page = page_of(a, b, pos);
   if (page < 0) return;
   const int row = pos % a.page_size;

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(DecCfg<D>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < NR; ++c) {
         const int tok = tok0 + a.by_gu.div(c);
-        const int l = a.causal ? min(s.nk, s.nk - s.nq + tok + 1) : s.nk;
+        const int l = a.causal ? min(s.nk, s.off + tok + 1) : s.nk;
         lim[c] = l - u.s0 * 128;
       }
       float m[NR], l[NR];

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     int ku = 0, g = 0;  // units, steps
     while (ok && next()) {
       const Unit u = *unit;
-      const int first = units.first(u.s.nq, u.s.nk, u.j);
+      const int first = units.first(u.s, u.j);
       // this lane's box: of tile lane / nbox
       const int key = u.j * kUnitKeys + (lane << lg_box);
       int page = -1, row = 0;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
     int g = 0;
     while (ok && next()) {
       const Unit u = *unit;
-      const int first = units.first(u.s.nq, u.s.nk, u.j);
+      const int first = units.first(u.s, u.j);
       // the next step's values are on their way while this one's are stored
       float nxt[N];
       auto fetch = [&](int t) {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(ScCfg<D, R>::THREADS, 1)
         float* dst = sLse + slot * 2 * R;
         const int tok0 = (first + a.by_nsub.div(t)) * a.w;
         const int nt = min(a.w, u.s.nq - tok0), ne = a.G - a.by_nsub.mod(t) * a.gu;
-        const int lim0 = u.s.nk - u.s.nq + tok0 + 1;
+        const int lim0 = u.s.off + tok0 + 1;
         float v[N];
         int lim[N];
         int mn = 0x7fffffff;

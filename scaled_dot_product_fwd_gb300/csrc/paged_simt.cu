@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = ty * RPT + i, tok = tok0 + a.by_gu.div(r);
-      limit[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
+      limit[i] = a.causal ? min(u.s.nk, u.s.off + tok + 1) : u.s.nk;
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kT, scores_ctas<D, RM>())
   Unit u;
   while (walk.next(a, units, sh, a.Hkv, &u)) {
     const int key0 = u.j * kKT;
-    const int first = units.first(u.s.nq, u.s.nk, u.j);
+    const int first = units.first(u.s, u.j);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     __syncthreads();
     row_offsets(a, u.b, u.h, key0, u.s.nk, off_k, off_v);
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kT, scores_ctas<D, RM>())
         if (tid < a.w * a.gu && tok < u.s.nq && e < a.G) {
           ls = a.lse[static_cast<size_t>(u.s.q0 + tok) * a.Hq + u.h * a.G + e] * kLog2e;
           if (ls == -INFINITY) ls = INFINITY;
-          lim = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
+          lim = a.causal ? min(u.s.nk, u.s.off + tok + 1) : u.s.nk;
         }
         sLse[tid] = ls;
         sLim[tid] = lim;

@@ -117,7 +117,7 @@ __device__ __forceinline__ TileGeo tile_geo(const Args& a, const Unit& u) {
   g.nt = NT == 2 && tok0 + a.w < u.s.nq ? 2 : 1;
   g.n[0] = g.n[1] = g.nmax;
   if (NT == 2 && a.causal && g.nt == 2) {  // the first tile may see fewer keys
-    const int lim = max(0, u.s.nk - u.s.nq + tok0 + a.w);
+    const int lim = min(u.s.nk, max(0, u.s.off + tok0 + a.w));
     g.n[0] = max(0, min(u.s1, (lim + 127) >> 7) - u.s0);
   }
   return g;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(TcCfg<D, NT>::THREADS, 1)
       const bool live = (warp & 3) * 32 < min(a.w, nq - tok0) * a.gu;
       // visible keys of the row, counted from the piece's first key
       const int limit =
-          (a.causal ? min(tg.nk, tg.nk - nq + tok + 1) : tg.nk) - tg.s0 * 128;
+          (a.causal ? min(tg.nk, unit->s.off + tok + 1) : tg.nk) - tg.s0 * 128;
       float m = -INFINITY, l = 0.f;
       const int n = tg.n[t];
       for (int j = 0; j < n; ++j) {

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kVT, 1) paged_vector_f32_kernel(const Args a) 
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int tok = tok0 + a.by_gu.div(PL * (lane & 3) + i);
-      lim[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
+      lim[i] = a.causal ? min(u.s.nk, u.s.off + tok + 1) : u.s.nk;
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
@@ -305,12 +305,12 @@ __global__ void __launch_bounds__(kVT, 1) paged_vector_f32_kernel(const Args a) 
 struct KeyTileUnits {
   FastDiv by_w;
   int cost;
-  __host__ __device__ int count(int nq, int) const { return nq > 0; }
-  __host__ __device__ int steps(int nq, int nk, int) const {
-    return ((nk + (1 << kVLg) - 1) >> kVLg) * by_w.ceil(nq);
+  __host__ __device__ int count(const Seq& s) const { return s.nq > 0; }
+  __host__ __device__ int steps(const Seq& s, int) const {
+    return ((s.nk + (1 << kVLg) - 1) >> kVLg) * by_w.ceil(s.nq);
   }
-  __host__ __device__ long long before(int nq, int nk, int j) const {
-    return j <= 0 ? 0 : steps(nq, nk, 0);
+  __host__ __device__ long long before(const Seq& s, int j) const {
+    return j <= 0 ? 0 : steps(s, 0);
   }
 };
 template <int D>
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kVT, 1) paged_scores_vector_f32_kernel(const A
           const float x = a.lse[static_cast<size_t>(u.s.q0 + tok) * a.Hq + u.h * a.G +
                                 a.by_gu.mod(c)] * 1.4426950408889634f;
           nl[i] = x == -INFINITY ? x : -x;  // nor does one that saw nothing
-          lim[i] = a.causal ? min(u.s.nk, u.s.nk - u.s.nq + tok + 1) : u.s.nk;
+          lim[i] = a.causal ? min(u.s.nk, u.s.off + tok + 1) : u.s.nk;
         }
       }
     };
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kVT, 1) paged_scores_vector_f32_kernel(const A
       const bool mine = (lane & 3) == 0 && key < u.s.nk && key < a.score_len;
       const float old = mine ? out[key] : 0.f;
       float sum = 0.f;
-      const int behind = (t << kVLg) - (u.s.nk - u.s.nq);  // first token that sees the tile
+      const int behind = (t << kVLg) - u.s.off;  // first token that sees the tile
       const int blk0 = a.causal && behind > 0 ? a.by_w.div(behind) : 0;
 #pragma unroll 1
       for (int blk = blk0; blk < blocks; ++blk) {
