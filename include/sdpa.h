@@ -535,6 +535,8 @@ SDPA_API sdpa_status_t sdpa_paged_scores(const sdpa_paged_params_t* params, cons
  *      behind the last.
  *  seq_lens_out: NULL or int32 [num_seqs], min(length, keep); may be
  *      params->seq_lens_kv itself.
+ * A kept row of a page outside the cache arrives as zeros, and one that would
+ * move to such a page is dropped (SDPA_ERR_PAGE_TABLE in the status word).
  * The pages that a sequence longer than `keep` uses below position `keep`
  * are rewritten, so no other sequence may share them, and no page may appear
  * twice among a sequence's own.  num_tokens, num_q_heads, scale, causal,

@@ -295,6 +295,21 @@ __global__ void __launch_bounds__(kSelT)
     for (int i = e.keep + tid; i < e.score_len; i += kSelT) out[i] = 0.f;
 }
 
+// Where row `src` of a sequence comes from and row `dst` goes to, as byte
+// offsets into the cache of one head.  A page that the table does not name
+// sets the status word: one to be read gives zeros (`from` kZeros), one to be
+// written drops the row (`from` kNoMove).
+constexpr long long kNoMove = -1, kZeros = -2;
+__device__ __forceinline__ void locate_move(const Args& a, const int* table, const long long* st,
+                                            int src, int dst, long long* from, long long* to) {
+  const int ps = table[a.by_page.div(src)], pd = table[a.by_page.div(dst)];
+  const bool ok_s = ps >= 0 && ps < a.num_pages, ok_d = pd >= 0 && pd < a.num_pages;
+  if (!ok_s || !ok_d) atomicExch(a.status, kStatusPageTable);
+  if (!ok_d) return;
+  *from = ok_s ? ps * st[0] + a.by_page.mod(src) * st[2] : kZeros;
+  *to = pd * st[0] + a.by_page.mod(dst) * st[2];
+}
+
 constexpr int kMoveT = 256;
 constexpr int kMoveRows = 8;  // rows of a thread in a chunk
 // rows of a chunk where a CTA takes 16 * lanes bytes of a row
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const Evict
   constexpr int kMoveChunk = move_chunk(kLanes);
   constexpr int kRows = kMoveChunk < kMoveT ? kMoveT : kMoveChunk;
   const Args& a = e.a;
-  // Where a chunk's rows come from (-1: no move) and go to, looked up two
+  // Where a chunk's rows come from and go to (locate_move), looked up two
   // chunks ahead by one thread a row; four chunks' worth, so that the writes
   // for chunk n + 2 never meet the last reads for chunk n - 1.
   __shared__ long long s_from[4][kRows], s_to[4][kRows];
@@ -343,16 +358,9 @@ __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const Evict
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int r = k * kMoveT + tid, i = n * kMoveChunk + r;
-      long long from = -1, to = 0;
-      if (src[k] > i && src[k] < e.near) {  // (a row that stays needs no move)
-        const int ps = table[a.by_page.div(src[k])], pd = table[a.by_page.div(i)];
-        if (ps < 0 || ps >= a.num_pages || pd < 0 || pd >= a.num_pages) {
-          atomicExch(a.status, kStatusPageTable);
-        } else {
-          from = ps * st[0] + a.by_page.mod(src[k]) * st[2];
-          to = pd * st[0] + a.by_page.mod(i) * st[2];
-        }
-      }
+      long long from = kNoMove, to = 0;
+      if (src[k] > i && src[k] < e.near)  // (a row that stays needs no move)
+        locate_move(a, table, st, src[k], i, &from, &to);
       s_from[n & 3][r] = from;
       s_to[n & 3][r] = to;
     }
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kMoveT, 2) paged_evict_move_kernel(const Evict
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
       const int r = r0 + k * kMoveStep;
-      if (s_from[n & 3][r] >= 0) *reinterpret_cast<uint4*>(base + s_to[n & 3][r]) = data[k];
+      if (s_from[n & 3][r] != kNoMove) *reinterpret_cast<uint4*>(base + s_to[n & 3][r]) = data[k];
     }
   };
   lookup(0);
@@ -416,17 +424,9 @@ __global__ void __launch_bounds__(kFarT) paged_evict_far_kernel(const EvictArgs 
   const int* table = a.table + b * a.table_stride;
   const int i = chunk * kFarPer + (threadIdx.x & ~31) + lane;
   const int src = i < e.keep ? e.kept[static_cast<size_t>(bh) * e.keep + i] : -1;
-  long long from = -1, to = 0;
-  if (src >= e.keep) {
-    const int ps = table[a.by_page.div(src)], pd = table[a.by_page.div(i)];
-    if (ps < 0 || ps >= a.num_pages || pd < 0 || pd >= a.num_pages) {
-      atomicExch(a.status, kStatusPageTable);
-    } else {
-      from = ps * st[0] + a.by_page.mod(src) * st[2];
-      to = pd * st[0] + a.by_page.mod(i) * st[2];
-    }
-  }
-  if (__all_sync(0xffffffffu, from < 0)) return;
+  long long from = kNoMove, to = 0;
+  if (src >= e.keep) locate_move(a, table, st, src, i, &from, &to);
+  if (__all_sync(0xffffffffu, from == kNoMove)) return;
   const int rows = 32 >> lg_lanes;  // rows at a time (2 lanes << lg_lanes = 32)
   constexpr int U = 8;
   for (int r0 = 0; r0 < 32; r0 += U * rows) {
@@ -437,9 +437,10 @@ __global__ void __launch_bounds__(kFarT) paged_evict_far_kernel(const EvictArgs 
       const int r = r0 + k * rows + (lane >> lg_lanes);
       const long long f = __shfl_sync(0xffffffffu, from, r & 31);
       dst[k] = __shfl_sync(0xffffffffu, to, r & 31);
-      if (r >= 32 || f < 0)
+      data[k] = make_uint4(0, 0, 0, 0);
+      if (r >= 32 || f == kNoMove)
         dst[k] = -1;
-      else
+      else if (f >= 0)
         data[k] = *reinterpret_cast<const uint4*>(base + f);
     }
 #pragma unroll
