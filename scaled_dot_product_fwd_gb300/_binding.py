@@ -532,7 +532,18 @@ def sdpa_forward_host(q, k, v, scale=None, causal=False, mask=None, sinks=None, 
 _PAGED = struct.Struct("<6ifi3iIQqQQQ10q")
 _STRIDE2 = ctypes.c_int64 * 2
 _paged_fn = {}
-_paged_ws = {}
+_PAGED_KEPT = 4  # workspaces (some 20 or 40 MB each) that a thread keeps at most
+
+
+class _PagedLocal(threading.local):
+    """A thread's workspaces by (device, stream, D), oldest first; they go with
+    the thread."""
+
+    def __init__(self):
+        self.ws = {}
+
+
+_paged_local = _PagedLocal()
 
 
 def _paged_call(name):
@@ -638,23 +649,27 @@ def _new_workspace(device, D):
 def _paged_workspace(workspace, dev, device, D, stream):
     """(tensor, address, bytes) of the given workspace, or of one that the
     binding keeps for this thread and the current torch stream, whose calls
-    follow one another (those of two threads may interleave their kernels).  A
-    call under graph capture gets one of its own, which belongs to the graph's
-    pool, so that graphs share none."""
+    follow one another (those of two threads may interleave their kernels).  It
+    comes from that stream's memory, so that one that is dropped (the thread's
+    end, or its oldest where it uses more than _PAGED_KEPT) serves nothing else
+    before the calls in flight are done.  A call under graph capture gets one of
+    its own, which belongs to the graph's pool, so that graphs share none."""
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the same device")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     keep = not _torch()._C._cuda_isCurrentStreamCapturing()
-    key = (dev, stream, D, threading.get_ident())
     if keep:
-        kept = _paged_ws.get(key)
+        mine, key = _paged_local.ws, (dev, stream, D)
+        kept = mine.get(key)
         if kept is not None:
             return kept
     ws = _new_workspace(device, D)
     made = (ws, ws.data_ptr(), ws.numel())
     if keep:
-        _paged_ws[key] = made
+        if len(mine) >= _PAGED_KEPT:
+            del mine[next(iter(mine))]
+        mine[key] = made
     return made
 
 
