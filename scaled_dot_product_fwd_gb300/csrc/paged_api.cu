@@ -76,6 +76,15 @@ bool cache_overlaps(const sdpa_paged_params_t& p) {
   return false;
 }
 
+// Whether two tensors of one base address are the same one: strides of
+// dimensions of one element do not count.
+template <int N>
+bool same_layout(const int64_t* x, const int64_t* y, const int64_t (&n)[N]) {
+  for (int i = 0; i < N; ++i)
+    if (n[i] > 1 && x[i] != y[i]) return false;
+  return true;
+}
+
 int device_sms() {
   int* status = nullptr;
   int sms = 0;
@@ -213,7 +222,14 @@ sdpa_status_t sdpa_paged_write(const sdpa_paged_params_t* p, const void* k, cons
   if ((st = check_arrays(*p)) != SDPA_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
     return SDPA_ERR_MISALIGNED;
-  if (p->num_pages > 0 && k_pages == v_pages && k != v) return SDPA_ERR_INVALID_ARGUMENT;
+  // One cache for both: every row is written twice, with the same values only
+  // where both come from the same place and go to the same one.
+  const int64_t rows[2] = {p->num_tokens, p->num_kv_heads};
+  const int64_t places[3] = {p->num_pages, p->num_kv_heads, p->page_size};
+  if (p->num_pages > 0 && k_pages == v_pages &&
+      (k != v || !same_layout(k_new_stride, v_new_stride, rows) ||
+       !same_layout(p->k_stride, p->v_stride, places)))
+    return SDPA_ERR_INVALID_ARGUMENT;
   LaunchEnv env;
   if (!make_env(&env, stream)) return SDPA_ERR_CUDA;
   paged::Args a = make_args(*p);
