@@ -432,8 +432,12 @@ SDPA_API sdpa_status_t sdpa_forward_decode_noalloc(const sdpa_params_t* params,
  *    hold anything, NaN included.  The lengths, offsets and page tables do not
  *    change while a call runs.
  *  - head_dim 64 or 128; fp32, fp16, bf16; any Hq that Hkv divides; page_size
- *    >= 1.  fp16/bf16 with page_size a multiple of 8 run on the tensor cores,
- *    everything else on fp32 CUDA-core kernels.
+ *    >= 1.  fp16/bf16 with page_size a multiple of 8 and a positive scale run
+ *    on the tensor cores, everything else on fp32 CUDA-core kernels.  Scores,
+ *    sums and outputs are held in fp32 and o is rounded once.  On the tensor
+ *    cores sdpa_paged_forward also rounds each softmax weight to the cache's
+ *    type before it meets its value row (2^-8 relative in bf16, 2^-11 in fp16;
+ *    lse and the accumulated weights are not affected).
  *  - Base pointers 16-byte aligned, row strides multiples of 16 bytes; o must
  *    not overlap the inputs.  sdpa_paged_write and sdpa_paged_evict want k_pages
  *    and v_pages without a common row (interleaved is fine; one cache for both

@@ -535,12 +535,18 @@ bool allow_smem(int bytes) {
 
 // Query rows (tokens times heads of a kv head) of a sequence on average, by
 // which a kernel is chosen: the offsets are on the device.  A chunk among
-// single tokens is read in passes of few rows then, but it can be at most a
-// few tokens a sequence of the batch long where the average is small, so that
-// its passes weigh no more than the single tokens' (255 single tokens and a
-// chunk of 257 over 4096 keys, 32 heads over 8, head_dim 128: 675 us with
-// 8-row tiles, 651 with one 128-row tile a unit, 812 with two; the chunk's
-// length alone as the rule slowed its score sums from 515 to 892).
+// single tokens is read in passes of few rows then.  Where the chunk's keys are
+// about as many as theirs, its passes weigh about what the single tokens do;
+// where they are many more, the passes are the call's whole time, and the
+// kernels of many rows would be several times as fast.  Attention / score sums
+// (us) with the kernels chosen here and with those of many rows, 32 heads over
+// 8, head_dim 128, bf16, and 16 heads over 4 in fp32:
+//   255 single tokens and a chunk of 257, all over 4096 keys:
+//       bf16 687 / 521 and 671 / 912; fp32 1066 / 2540 and 3573 / 3176
+//   128 single tokens over 512 keys and a chunk of 384 over 32768:
+//       bf16 1398 / 337 and 272 / 147; fp32 7083 / 3210 and 2753 / 1604
+//   255 single tokens over 64 keys and a chunk of 257 over 32768:
+//       bf16 1789 / 245 and 249 / 132; fp32 3340 / 4586 and 1904 / 1042
 inline long long call_rows(const Args& a) {
   return a.cu ? (static_cast<long long>(a.T) * a.G + a.B - 1) / a.B : a.G;
 }
@@ -551,10 +557,9 @@ inline int box_log2(int page_size) {
   while (page_size & ((1 << lg) - 1)) --lg;
   return lg;
 }
-// Largest tile whose partial results a CTA may leave, in query rows (two
-// 128-row tiles) and in keys (score sums).
+// Largest tile whose partial results a CTA may leave, in query rows: two
+// 128-row tiles.  (Score sums leave one number a key, at most 256.)
 constexpr int kMaxRows = 256;
-constexpr int kMaxKeys = 256;
 // CTAs an SM that share a call's work, at most (their slots' rows together
 // are at most kMaxRows an SM).
 constexpr int kMaxCtas = 4;

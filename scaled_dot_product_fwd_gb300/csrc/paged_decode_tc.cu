@@ -19,6 +19,9 @@
 // TMEM) is rescaled; after a row's first tile that is rare.  The sums stay
 // per thread until the unit ends.
 //
+// P enters the value product rounded to the cache's type, for the reason and
+// at the cost that paged_tc.cuh gives; the sums take it unrounded.
+//
 // Bound by HBM (8 x 32768 keys, head_dim 128, bf16: 164-170 us, 6.3-6.5
 // TB/s): six 32 KB K/V slots in flight (twelve of 16 KB at head_dim 64), S
 // three tiles ahead of P V; TMEM holds eight S^T tiles and O^T.

@@ -15,9 +15,10 @@
 //  NT = 2  (sequences of more than 128 rows): a unit is two query
 //          tiles that share each K/V tile; S_0 | S_1 | O_0 | O_1 in TMEM, and
 //          the softmax of one tile overlaps the products of the other.  Bound
-//          by the tensor pipe and the softmax warps (4096 tokens over 32768
-//          keys, 32 heads over 8, head_dim 128, bf16: 1190 us, 1730 TFLOP/s,
-//          the pipe 71 % active).
+//          by the tensor pipe, 71 % active, the softmax warps and the clock
+//          under that load (4096 tokens over 32768 keys, 32 heads over 8,
+//          head_dim 128, bf16: 1190 to 1374 us from one GPU to the next, 1730
+//          to 1500 TFLOP/s).
 //  NT = 1  (short chunks, 17 to 128 rows): one query tile; S is
 //          double-buffered over the key tiles (S_j+1 is computed while the
 //          softmax works on S_j), six 32 KB K/V slots in flight at head_dim
@@ -44,6 +45,13 @@
 // (prefill_tc.cuh), whose softmax arithmetic this one uses: p = 2^(s * scale *
 // log2e - m) against a reference max m that moves only when a row sum passes
 // 2^15, so P stays in the exact range of fp16 and bf16.
+//
+// Rounding: P goes into the value product in the cache's type, since the
+// product takes one type for both operands (half a step of it, 2^-8 relative
+// in bf16 and 2^-11 in fp16, on each weight; a second product for the rest of P
+// would add half of the tensor pipe's work).  The sums take P before that
+// rounding.  Relative error of O against 64 bits: 2.3e-3 in bf16 and 2.9e-4 in
+// fp16, where rounding the exact O once gives 1.7e-3 and 2.1e-4.
 #pragma once
 
 #include <atomic>

@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(kVT, 1) paged_vector_f32_kernel(const Args a) 
 // 8 x 16384 keys, 16 heads over 4, D = 128: 66 us, 4.1 TB/s (195 us with the
 // 16-row tiles); 32 heads over 8, D = 64: 108 us (210), where the products and
 // their reduction bound it.  A chunk of 9 tokens among 16 single ones, 4096
-// keys: 146 us (228); of 257 among 255: 4547 us (3348), for a block's queries
-// come from L2 every time.
+// keys: 146 us (228); of 257 among 255, 32 heads over 8, D = 128: 4578 us
+// (3391), for a block's queries come from L2 every time.
 struct KeyTileUnits {
   FastDiv by_w;
   int cost;
