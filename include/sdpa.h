@@ -71,8 +71,10 @@ typedef enum {
   SDPA_ERR_WORKSPACE_TOO_SMALL = 4,
   SDPA_ERR_CUDA = 5,             /* a CUDA runtime call or launch failed */
   SDPA_ERR_TIMEOUT = 6,          /* a device-side wait gave up (status word) */
-  SDPA_ERR_PAGE_TABLE = 7        /* a page number outside the cache was met
+  SDPA_ERR_PAGE_TABLE = 7,       /* a page number outside the cache was met
                                     (status word; paged entry points) */
+  SDPA_ERR_POSITION = 8          /* a position outside the rotation table was
+                                    met (status word; rotary entry points) */
 } sdpa_status_t;
 
 /* Kernel paths.  The launcher picks one from the shape alone: one query row
@@ -299,9 +301,10 @@ SDPA_API const char* sdpa_status_string(sdpa_status_t status);
 
 /*
  * sdpa_device_status — synchronise `stream`, then read and clear the device
- * status word that kernels set when one of their bounded waits gives up or a
- * page table names a page outside the cache.  Returns SDPA_OK,
- * SDPA_ERR_TIMEOUT, SDPA_ERR_PAGE_TABLE, or SDPA_ERR_CUDA if the
+ * status word that kernels set when one of their bounded waits gives up, a
+ * page table names a page outside the cache or a token's position lies outside
+ * the rotation table.  Returns SDPA_OK, SDPA_ERR_TIMEOUT, SDPA_ERR_PAGE_TABLE,
+ * SDPA_ERR_POSITION (the last one met), or SDPA_ERR_CUDA if the
  * synchronisation itself failed.  The status word is per device and shared by all streams.
  */
 SDPA_API sdpa_status_t sdpa_device_status(void* stream);
@@ -551,6 +554,147 @@ SDPA_API sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* params, int32
                                         const float* scores, float* scores_out,
                                         const int64_t* score_stride, int32_t score_len,
                                         int32_t* kept, int32_t* seq_lens_out, void* stream);
+
+/* ------------------------------------------------------ rotary positions ---
+ * Pair i of a head, i < R / 2, turns by the angle of its token's position:
+ *     (x, y) -> (x cos - y sin, y cos + x sin)
+ * with the pairs (i, i + R / 2), or (2 i, 2 i + 1) where `interleaved`; the
+ * elements from R on pass unchanged.  The rotation is computed in fp32 and
+ * rounded once.
+ */
+typedef struct {
+  const float* table;       /* [table_len, rotary_dim / 2, 2]: cosine and sine
+                               of every position and pair, 16-byte aligned */
+  int64_t table_len;
+  int32_t rotary_dim;       /* R: a multiple of 16, at most head_dim */
+  int32_t interleaved;
+  const int32_t* positions; /* device int32, or NULL: see the calls */
+} sdpa_rotation_t;
+
+/*
+ * sdpa_rope_table — fill a rotation table: entry (p, i) is (gain * cos, gain *
+ * sin) of p * inv_freq[i], the angle and its functions in 64 bits, rounded
+ * once.  table: device float32 [length, rotary_dim / 2, 2], 16-byte aligned.
+ * inv_freq: HOST array of rotary_dim / 2 numbers (rotary_dim a multiple of 16,
+ * at most 512), read before the call returns.
+ */
+SDPA_API sdpa_status_t sdpa_rope_table(float* table, int64_t length, int32_t rotary_dim,
+                                       const double* inv_freq, double gain, void* stream);
+
+/*
+ * sdpa_rope — rotate q and k.  q: [B, Hq, L, D], k: [B, Hkv, L, D], D 64, 128
+ * or 512, element strides {batch, head, row} (D contiguous; times the element
+ * size multiples of 16 bytes); q_out and k_out likewise, either the input
+ * itself (same pointer and strides) or without a common element with the
+ * inputs.  num_kv_heads 0 (k and k_out unused) rotates q alone.
+ * rotation.positions: int32, token (b, l) at b * position_stride + l (a stride
+ * of 0 shares them among the batches); NULL: l itself.  A position outside
+ * [0, table_len) leaves its row as it is and sets the device status word to
+ * SDPA_ERR_POSITION.
+ * transpose nonzero: the transposed rotation, which takes the gradients of
+ * q_out and k_out to those of q and k (with a table of gain 1 the inverse).
+ */
+typedef struct {
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t seq_len;
+  int32_t head_dim;
+  int32_t dtype;      /* sdpa_dtype_t of all four tensors */
+  int32_t transpose;
+  uint32_t flags;     /* 0 */
+  sdpa_rotation_t rotation;
+  int64_t position_stride;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t q_out_stride[3];
+  int64_t k_out_stride[3];
+} sdpa_rope_params_t;
+SDPA_API sdpa_status_t sdpa_rope(const sdpa_rope_params_t* params, const void* q, const void* k,
+                                 void* q_out, void* k_out, void* stream);
+
+/*
+ * sdpa_paged_append — rotate a step's new tokens and write them to the paged
+ * cache: sdpa_rope and sdpa_paged_write in one pass.
+ *  q, q_out: [num_tokens, Hq, D], strides params->q_stride and o_stride; q_out
+ *      is q itself (same strides) or has no common element with the inputs.
+ *      num_q_heads 0: no queries (q and q_out unused).
+ *  k, v, k_new_stride, v_new_stride, k_pages, v_pages: as for
+ *      sdpa_paged_write; k is rotated, rounded to its type and written, v
+ *      written as it is.
+ *  rotation->positions: int32 [num_tokens], or NULL: token i of the nq of
+ *      sequence b is at position seq_lens_kv[b] - nq + i.  A token whose
+ *      position the table does not hold keeps its q and k unrotated and sets
+ *      the status word to SDPA_ERR_POSITION (but not one before the sequence's
+ *      start, which has no place in the cache either).
+ * Rows of q_out of tokens that belong to no sequence are left as they were.
+ * scale, causal and sinks are not used.
+ */
+SDPA_API sdpa_status_t sdpa_paged_append(const sdpa_paged_params_t* params,
+                                         const sdpa_rotation_t* rotation, const void* q,
+                                         const void* k, const void* v, void* q_out,
+                                         const int64_t* k_new_stride,
+                                         const int64_t* v_new_stride, void* k_pages,
+                                         void* v_pages, void* stream);
+
+/* --------------------------------------------------- 4-bit paged KV cache ---
+ * The paged cache at 4.5 bits an element.  A row of D elements is D / 2 bytes of
+ * codes, two 4-bit floats each (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6), the even element in the low half, and D / 16 scales, an
+ * 8-bit float (4 exponent bits, 3 mantissa bits; e4m3) for 16 consecutive
+ * elements.  An element stands for code * scale * g, g its kv head's gain.
+ * A row x in its own type is written as follows: y = x / g in fp32; the scale
+ * is max |y| over the 16 elements, divided by 6 and rounded to e4m3, at least
+ * 2^-9 and at most 448; the code is y / scale rounded to the nearest code, ties
+ * to even, at most 6 in magnitude.  Rows hold finite values (an infinity is
+ * stored as the largest value, a NaN as some finite one).
+ *
+ * Codes and scales are two tensors of bytes for K and two for V, [num_pages,
+ * Hkv, page_size, D / 2] and [num_pages, Hkv, page_size, D / 16] by shape; the
+ * codes' byte strides {page, head, row} are k_stride and v_stride of
+ * sdpa_paged_params_t (multiples of 16), the scales' are here (multiples of
+ * D / 16).  Codes 16-byte aligned, scales D / 16 bytes.  Everything else is as
+ * for the paged cache above: page tables, lengths, packed tokens, status word.
+ */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  int64_t k_scale_stride[3];
+  int64_t v_scale_stride[3];
+  const float* k_gain; /* NULL (1), or device float32 [Hkv], finite, not 0 */
+  const float* v_gain;
+} sdpa_fp4_cache_t;
+
+/*
+ * sdpa_paged_append_fp4 — sdpa_paged_append into a 4-bit cache.
+ *  rotation: NULL leaves q and k unrotated (num_q_heads 0 then, or q is
+ *      copied).
+ *  k_out, v_out: NULL, or [num_tokens, Hkv, D] in params->dtype with strides
+ *      out_stride = {token, head}: what the written rows stand for, rounded to
+ *      the type (the same for a token without a place in the cache; rows of
+ *      tokens of no sequence are left as they were).  They overlap no other
+ *      tensor of the call.
+ */
+SDPA_API sdpa_status_t sdpa_paged_append_fp4(const sdpa_paged_params_t* params,
+                                             const sdpa_rotation_t* rotation,
+                                             const sdpa_fp4_cache_t* cache, const void* q,
+                                             const void* k, const void* v, void* q_out,
+                                             const int64_t* k_new_stride,
+                                             const int64_t* v_new_stride, void* k_out,
+                                             void* v_out, const int64_t* out_stride,
+                                             void* stream);
+
+/*
+ * sdpa_paged_forward_fp4 — sdpa_paged_forward over a 4-bit cache.  q, o and
+ * lse as there, in params->dtype; workspace of sdpa_paged_workspace_size bytes.
+ * A scale byte of NaN below a sequence's length gives NaN.
+ */
+SDPA_API sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* params,
+                                              const sdpa_fp4_cache_t* cache, const void* q,
+                                              void* o, float* lse, void* workspace,
+                                              size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -23,7 +23,7 @@ SDPA_FLAG_BOOL_MASK = 0x2
 SDPA_FLAG_STRIDES = 0x4
 STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARGUMENT", 2: "SDPA_ERR_UNSUPPORTED",
           3: "SDPA_ERR_MISALIGNED", 4: "SDPA_ERR_WORKSPACE_TOO_SMALL", 5: "SDPA_ERR_CUDA",
-          6: "SDPA_ERR_TIMEOUT", 7: "SDPA_ERR_PAGE_TABLE"}
+          6: "SDPA_ERR_TIMEOUT", 7: "SDPA_ERR_PAGE_TABLE", 8: "SDPA_ERR_POSITION"}
 KERNELS = {0: "none", 1: "prefill_tc", 2: "prefill_f32", 3: "decode_splitkv", 4: "no_keys",
            5: "prefill_tc_f32"}
 
@@ -34,7 +34,8 @@ EXPORTS = ("sdpa_workspace_size", "sdpa_select_kernel", "sdpa_forward", "sdpa_st
            "sdpa_backward_workspace_size", "sdpa_backward", "sdpa_debug_set_option",
            "sdpa_host_staging_size", "sdpa_forward_host", "sdpa_paged_write",
            "sdpa_paged_workspace_size", "sdpa_paged_forward", "sdpa_paged_scores",
-           "sdpa_paged_evict")
+           "sdpa_paged_evict", "sdpa_rope_table", "sdpa_rope", "sdpa_paged_append",
+           "sdpa_paged_append_fp4", "sdpa_paged_forward_fp4")
 
 # sdpa_debug_option_t
 DEBUG_OPTIONS = {"decode_splits": 0, "decode_cluster": 1, "decode_drop_last": 2,
@@ -69,6 +70,32 @@ class SdpaPagedParams(ctypes.Structure):
                 ("sinks", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
                 ("o_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 3),
                 ("v_stride", ctypes.c_int64 * 3)]
+
+
+class SdpaRotation(ctypes.Structure):
+    """Mirror of sdpa_rotation_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_len", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p)]
+
+
+class SdpaRopeParams(ctypes.Structure):
+    """Mirror of sdpa_rope_params_t."""
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("seq_len", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("transpose", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("rotation", SdpaRotation), ("position_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("q_out_stride", ctypes.c_int64 * 3), ("k_out_stride", ctypes.c_int64 * 3)]
+
+
+class SdpaFp4Cache(ctypes.Structure):
+    """Mirror of sdpa_fp4_cache_t."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("k_scale_stride", ctypes.c_int64 * 3), ("v_scale_stride", ctypes.c_int64 * 3),
+                ("k_gain", ctypes.c_void_p), ("v_gain", ctypes.c_void_p)]
 
 
 class SdpaError(RuntimeError):
@@ -133,6 +160,18 @@ def load_library(path: str = LIB_PATH):
             lib.sdpa_paged_evict.argtypes = [PP, ctypes.c_int32, ctypes.c_int32] + [vp] * 5 + [
                 ctypes.c_int32] + [vp] * 3
             lib.sdpa_paged_evict.restype = ctypes.c_int
+            lib.sdpa_rope_table.argtypes = [vp, ctypes.c_int64, ctypes.c_int32, vp,
+                                            ctypes.c_double, vp]
+            lib.sdpa_rope_table.restype = ctypes.c_int
+            lib.sdpa_rope.argtypes = [ctypes.POINTER(SdpaRopeParams)] + [vp] * 5
+            lib.sdpa_rope.restype = ctypes.c_int
+            lib.sdpa_paged_append.argtypes = [PP, ctypes.POINTER(SdpaRotation)] + [vp] * 9
+            lib.sdpa_paged_append.restype = ctypes.c_int
+            FP = ctypes.POINTER(SdpaFp4Cache)
+            lib.sdpa_paged_append_fp4.argtypes = [PP, ctypes.POINTER(SdpaRotation), FP] + [vp] * 10
+            lib.sdpa_paged_append_fp4.restype = ctypes.c_int
+            lib.sdpa_paged_forward_fp4.argtypes = [PP, FP] + [vp] * 4 + [ctypes.c_size_t, vp]
+            lib.sdpa_paged_forward_fp4.restype = ctypes.c_int
             _lib = lib
     return _lib
 
@@ -546,21 +585,23 @@ class _PagedLocal(threading.local):
 _paged_local = _PagedLocal()
 
 
-def _paged_call(name):
-    """The C entry point taking the packed parameters as bytes."""
+def _paged_call(name, structs=1):
+    """The C entry point taking its parameter structs (the first arguments) as
+    bytes."""
     fn = _paged_fn.get(name)
     if fn is None:
         lib = load_library()
         typed = getattr(lib, name)
         fn = type(typed)((name, lib))
-        fn.argtypes = [ctypes.c_char_p] + typed.argtypes[1:]
+        fn.argtypes = [ctypes.c_char_p] * structs + typed.argtypes[structs:]
         fn.restype = typed.restype
         _paged_fn[name] = fn
     return fn
 
 
-def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
-    """Checks of what the paged calls share.  Returns the fields of
+def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, code=None):
+    """Checks of what the paged calls share (code: the dtype code of q and o
+    where it is not the cache's).  Returns the fields of
     SdpaPagedParams that describe the cache: (kv heads, D, dtype code, pages,
     page size), the batch's fields, and the strides of k and v."""
     int32 = _torch().int32
@@ -595,7 +636,7 @@ def _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q):
                             "1 elements")
         cu = cu_seqlens_q.data_ptr()
     pages, heads, page, D = shape
-    return (heads, D, dtype_code(dtype), pages, page, B, ts[1], page_table.data_ptr(), tst[0], cu,
+    return (heads, D, dtype_code(dtype) if code is None else code, pages, page, B, ts[1], page_table.data_ptr(), tst[0], cu,
             seq_lens_kv.data_ptr(), ks, vs)
 
 
@@ -620,6 +661,29 @@ def _check_lse(lse, shape, dev):
     if (lse.dtype is not _torch().float32 or lse.get_device() != dev
             or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, Hq] CUDA tensor")
+
+
+def _paged_results(q, sinks, out, lse, return_lse, dev):
+    """The attention calls' sinks checked, and out, its strides and lse, made
+    where they are not given."""
+    torch = _torch()
+    shape = q.shape
+    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.get_device() != dev
+                              or sinks.numel() != shape[1] or not sinks.is_contiguous()):
+        raise TypeError("sinks must be a contiguous float32 CUDA tensor with Hq elements")
+    if out is None:
+        out = torch.empty_like(q)
+        os = out.stride()
+    else:
+        os = out.stride()
+        if (out.shape != shape or os[2] != 1 or out.dtype is not q.dtype
+                or out.get_device() != dev):
+            raise ValueError("out must be like q with a contiguous last dimension")
+    if lse is not None:
+        _check_lse(lse, shape, dev)
+    elif return_lse:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    return out, os, lse
 
 
 def _check_scores(scores, c, dev, what="scores"):
@@ -750,21 +814,7 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_
         return _elsewhere(dev, stream, lambda: sdpa_paged_forward(
             q, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, scale, causal, sinks, out,
             lse, return_lse, _new_workspace(q.device, c[1]) if workspace is None else workspace))
-    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.get_device() != dev
-                              or sinks.numel() != shape[1] or not sinks.is_contiguous()):
-        raise TypeError("sinks must be a contiguous float32 CUDA tensor with Hq elements")
-    if out is None:
-        out = torch.empty_like(q)
-        os = out.stride()
-    else:
-        os = out.stride()
-        if (out.shape != shape or os[2] != 1 or out.dtype is not q.dtype
-                or out.get_device() != dev):
-            raise ValueError("out must be like q with a contiguous last dimension")
-    if lse is not None:
-        _check_lse(lse, shape, dev)
-    elif return_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    out, os, lse = _paged_results(q, sinks, out, lse, return_lse, dev)
     s = torch._C._cuda_getCurrentRawStream(dev)
     _, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s)
     p = _paged_pack(c, shape[0], shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
@@ -850,3 +900,369 @@ def sdpa_paged_evict(k_pages, v_pages, scores, page_table, seq_lens_kv, keep, re
         scores_out.data_ptr(), _STRIDE2(ss[0], ss[1]), scores.shape[2], kept.data_ptr(),
         seq_lens_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
     return kept, seq_lens_out, scores_out
+
+
+# ------------------------------------------------------------ rotary positions
+# SdpaRotation, SdpaRopeParams and SdpaFp4Cache as pack calls
+_ROTATION = struct.Struct("<QqiiQ")
+_ROPE = struct.Struct("<7iIQqiiQq12q")
+_FP4 = struct.Struct("<4Q6qQQ")
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_length=None,
+                     beta_fast=32.0, beta_slow=1.0):
+    """Angles per position of a head's rotary_dim / 2 pairs, and the gain of the
+    rotation: (list of floats, float).
+
+    Pair i turns by base^(-2 i / rotary_dim) a position.  For contexts longer
+    than those a model was trained on, `factor` times as long:
+      scaling="linear"  positions count 1 / factor (Chen et al., 2023);
+      scaling="ntk"     the base grows by factor^(R / (R - 2)), so that the
+                        slowest pair counts 1 / factor and the fastest stays;
+      scaling="yarn"    pairs that turn more than beta_fast times within
+                        original_length positions stay, those that turn less
+                        than beta_slow times count 1 / factor, those between
+                        are blended, and the gain is 0.1 ln(factor) + 1 (Peng
+                        et al., 2023).
+    """
+    R = int(rotary_dim)
+    if R < 2 or R % 2 or not base > 0.0 or not factor > 0.0:
+        raise ValueError("rotary_dim must be even and positive, base and factor positive")
+    half = R // 2
+    if scaling == "ntk":
+        if R == 2:
+            raise ValueError("scaling='ntk' needs more than one pair")
+        base = base * factor ** (R / (R - 2))
+    freq = [base ** (-2.0 * i / R) for i in range(half)]
+    if scaling is None or scaling == "ntk":
+        return freq, 1.0
+    if scaling == "linear":
+        return [f / factor for f in freq], 1.0
+    if scaling != "yarn":
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    if original_length is None or original_length < 1 or not beta_fast > beta_slow > 0.0 \
+            or base == 1.0:
+        raise ValueError("scaling='yarn' needs original_length >= 1, beta_fast > beta_slow > 0 "
+                         "and a base other than 1")
+
+    def pair_of(turns):  # the (fractional) pair that turns so often in original_length
+        return R * math.log(original_length / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+
+    lo = max(math.floor(pair_of(beta_fast)), 0)
+    hi = min(math.ceil(pair_of(beta_slow)), R - 1)
+    span = max(hi - lo, 0.001)
+    ramp = [min(max((i - lo) / span, 0.0), 1.0) for i in range(half)]
+    return ([f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)],
+            0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0)
+
+
+def sdpa_rope_table(length, rotary_dim, base=10000.0, scaling=None, factor=1.0,
+                    original_length=None, beta_fast=32.0, beta_slow=1.0, inv_freq=None, gain=None,
+                    device=None, stream=None):
+    """The rotation table float32 [length, rotary_dim / 2, 2] on the GPU: cosine
+    and sine of position * frequency, from angles in 64 bits, times the gain.
+
+    Frequencies and gain are those of rope_frequencies(rotary_dim, base,
+    scaling, factor, ...), unless inv_freq (rotary_dim / 2 numbers) or gain are
+    given.  rotary_dim: a multiple of 16 (the rotary calls' rule).
+    """
+    torch = _torch()
+    length, R = int(length), int(rotary_dim)
+    freq, own = rope_frequencies(R, base, scaling, factor, original_length, beta_fast, beta_slow)
+    if inv_freq is not None:
+        freq = [float(f) for f in inv_freq]
+        if len(freq) != R // 2:
+            raise ValueError("inv_freq must have rotary_dim / 2 numbers")
+    if length < 0:
+        raise ValueError("length must not be negative")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else \
+        torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    dev = torch.cuda.current_device() if device.index is None else device.index
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_rope_table(
+            length, R, inv_freq=freq, gain=own if gain is None else gain))
+    table = torch.empty((length, R // 2, 2), dtype=torch.float32, device=device)
+    _paged_status(load_library().sdpa_rope_table(
+        table.data_ptr(), length, R, (ctypes.c_double * len(freq))(*freq),
+        float(own if gain is None else gain), torch._C._cuda_getCurrentRawStream(dev)))
+    return table
+
+
+def _check_table(table, dev):
+    """Positions and rotated elements of a rotation table."""
+    s = table.shape
+    if (len(s) != 3 or s[2] != 2 or table.dtype is not _torch().float32
+            or table.get_device() != dev or not table.is_contiguous()):
+        raise ValueError("the rotation table must be a contiguous float32 CUDA tensor [positions, "
+                         "rotary_dim / 2, 2] on the same device")
+    return s[0], 2 * s[1]
+
+
+def _rope(q, k, table, positions, interleaved, q_out, k_out, stream, transpose):
+    torch = _torch()
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    shape, dtype = q.shape, q.dtype
+    qs = q.stride()
+    if len(shape) != 4 or qs[3] != 1:
+        raise ValueError("q must be [batch, heads, length, D] with a contiguous last dimension")
+    B, H, L, D = shape
+    if k is not None and (k.dim() != 4 or k.get_device() != dev or k.stride(3) != 1
+                          or k.shape[0] != B or k.shape[2:] != shape[2:]):
+        raise ValueError("k must be [batch, kv heads, length, D] like q")
+    if k is not None and k.dtype is not dtype:
+        raise TypeError("q and k must share a dtype")
+    P, R = _check_table(table, dev)
+    pos, pstride = 0, 0
+    if positions is not None:
+        if positions.dtype is not torch.int32 or positions.get_device() != dev:
+            raise TypeError("positions must be an int32 CUDA tensor on the same device")
+        ps, pst = positions.shape, positions.stride()
+        if ps[-1:] != (L,) or len(ps) > 2 or (len(ps) == 2 and ps[0] not in (1, B)) \
+                or (L > 1 and pst[-1] != 1):
+            raise ValueError("positions must be [length] or [batch, length] with contiguous rows")
+        pos = positions.data_ptr()
+        pstride = pst[0] if len(ps) == 2 and ps[0] > 1 else 0
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: _rope(q, k, table, positions, interleaved, q_out,
+                                                     k_out, None, transpose))
+    outs = []
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            if out is not None:
+                raise ValueError("%s without its input" % name)
+        elif out is None:
+            out = torch.empty_like(x)
+        elif (out.shape != x.shape or out.dtype is not dtype or out.get_device() != dev
+              or out.stride(3) != 1):
+            raise ValueError("%s must be like its input with a contiguous last dimension" % name)
+        outs.append(out)
+    q_out, k_out = outs
+    zero = (0, 0, 0)
+    qo = q_out.stride()
+    ks, ko = (zero, zero) if k is None else (k.stride(), k_out.stride())
+    p = _ROPE.pack(B, H, 0 if k is None else k.shape[1], L, D, dtype_code(dtype), transpose, 0,
+                   table.data_ptr(), P, R, 1 if interleaved else 0, pos, pstride, qs[0], qs[1],
+                   qs[2], ks[0], ks[1], ks[2], qo[0], qo[1], qo[2], ko[0], ko[1], ko[2])
+    _paged_status(_paged_call("sdpa_rope")(
+        p, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+        None if k is None else k_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
+    return q_out, k_out
+
+
+def sdpa_rope(q, k, table, positions=None, interleaved=False, q_out=None, k_out=None,
+              stream=None):
+    """Rotary positions of q [B, Hq, L, D] and k [B, Hkv, L, D] (k may be None).
+
+    table: float32 [positions, R / 2, 2] as sdpa_rope_table makes it, R <= D a
+    multiple of 16: the first R elements of a head turn in pairs (i, i + R / 2),
+    or (2 i, 2 i + 1) where interleaved; the others pass.  positions: int32
+    [L] or [B, L]; None: 0 .. L - 1.  Any strides with a contiguous last
+    dimension (multiples of 16 bytes); D 64, 128 or 512; float32, float16,
+    bfloat16.  q_out and k_out may be q and k themselves.  A position outside
+    the table leaves its row unrotated and sets the device status word.
+    Returns (q_out, k_out).
+    """
+    return _rope(q, k, table, positions, interleaved, q_out, k_out, stream, 0)
+
+
+def sdpa_rope_backward(dq_out, dk_out, table, positions=None, interleaved=False, dq=None,
+                       dk=None, stream=None):
+    """Gradients of q and k from those of sdpa_rope's results (the transposed
+    rotation): arguments as for sdpa_rope, which may be given dq_out and dk_out
+    themselves as dq and dk.  Returns (dq, dk)."""
+    return _rope(dq_out, dk_out, table, positions, interleaved, dq, dk, stream, 1)
+
+
+def _rotation(table, positions, interleaved, T, dev):
+    """SdpaRotation of a step's packed tokens, packed (None: no table)."""
+    if table is None:
+        if positions is not None:
+            raise ValueError("positions without a rotation table")
+        return None
+    P, R = _check_table(table, dev)
+    pos = 0
+    if positions is not None:
+        _check_int32(positions, T, dev, "positions")
+        pos = positions.data_ptr()
+    return _ROTATION.pack(table.data_ptr(), P, R, 1 if interleaved else 0, pos)
+
+
+def _new_tokens(q, k, v, q_out, c, dev):
+    """Checks of an append's tokens.  Returns (tokens, heads of q, strides of q,
+    q_out and its strides)."""
+    shape, dtype = k.shape, k.dtype
+    if (len(shape) != 3 or shape[1] != c[0] or shape[2] != c[1] or v.shape != shape
+            or k.stride(2) != 1 or v.stride(2) != 1 or v.get_device() != dev):
+        raise ValueError("k and v must be [tokens, kv heads, D] on the same device with a "
+                         "contiguous last dimension")
+    if v.dtype is not dtype:
+        raise TypeError("k and v must share a dtype")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return shape[0], 0, (0, 0), None, (0, 0)
+    qsh, qs = q.shape, q.stride()
+    if (len(qsh) != 3 or qsh[0] != shape[0] or qsh[2] != shape[2] or qs[2] != 1
+            or q.get_device() != dev):
+        raise ValueError("q must be [tokens, heads, D] on the same device with a contiguous last "
+                         "dimension")
+    if q.dtype is not dtype:
+        raise TypeError("q, k and v must share a dtype")
+    if q_out is None:
+        q_out = _torch().empty_like(q)
+    elif (q_out.shape != qsh or q_out.dtype is not dtype or q_out.get_device() != dev
+          or q_out.stride(2) != 1):
+        raise ValueError("q_out must be like q with a contiguous last dimension")
+    return shape[0], qsh[1], qs, q_out, q_out.stride()
+
+
+def sdpa_paged_append(q, k, v, k_pages, v_pages, page_table, seq_lens_kv, rope_table,
+                      cu_seqlens_q=None, positions=None, interleaved=False, q_out=None,
+                      stream=None):
+    """Rotate a step's new tokens and write them to the paged cache: q rotated to
+    q_out, k rotated to its page row, v to its page row (sdpa_rope and
+    sdpa_paged_write in one pass).
+
+    q: [T, Hq, D] or None, k and v: [T, Hkv, D] packed new tokens; the cache
+    arguments as for sdpa_paged_write; rope_table and interleaved as for
+    sdpa_rope.  positions: int32 [T]; None: a token's place in its sequence
+    (give them where keys were evicted).  q_out may be q; rows past the last
+    sequence are left as they are.  Returns q_out (None without q).
+    """
+    dev = k.get_device()
+    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q)
+    cuda = _torch()._C
+    if rope_table is None:
+        raise ValueError("rope_table is needed (sdpa_paged_write writes rows as they are)")
+    if stream is not None or cuda._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_append(
+            q, k, v, k_pages, v_pages, page_table, seq_lens_kv, rope_table, cu_seqlens_q,
+            positions, interleaved, q_out))
+    T, hq, qs, q_out, os = _new_tokens(q, k, v, q_out, c, dev)
+    if k.dtype is not k_pages.dtype:
+        raise TypeError("k, v and the cache must share a dtype")
+    kn, vn = k.stride(), v.stride()
+    p = _paged_pack(c, T, hq, 1.0, 1, 0, qs, os)
+    _paged_status(_paged_call("sdpa_paged_append", 2)(
+        p, _rotation(rope_table, positions, interleaved, T, dev),
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if q is None else q_out.data_ptr(), _STRIDE2(kn[0], kn[1]), _STRIDE2(vn[0], vn[1]),
+        k_pages.data_ptr(), v_pages.data_ptr(), cuda._cuda_getCurrentRawStream(dev)))
+    return q_out
+
+
+# ---------------------------------------------------------- 4-bit paged KV cache
+def _fp4_cache(dev, dtype, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv,
+               cu_seqlens_q, k_gain, v_gain):
+    """Checks of a 4-bit cache: the fields of _paged_cache for rows of `dtype`,
+    and SdpaFp4Cache packed."""
+    torch = _torch()
+    if k_pages.dtype is not torch.uint8:
+        raise TypeError("k_pages and v_pages must be uint8 (two codes a byte)")
+    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q,
+                     dtype_code(dtype))
+    shape = k_pages.shape
+    D = 2 * shape[3]
+    want = (shape[0], shape[1], shape[2], D // 16)
+    for t in (k_scales, v_scales):
+        if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
+            raise TypeError("k_scales and v_scales must be uint8 or float8_e4m3fn")
+        if t.shape != want or t.get_device() != dev or (t.stride(3) != 1 and want[3] > 1):
+            raise ValueError("k_scales and v_scales must be [pages, kv heads, page_size, D / 16] "
+                             "on the same device with a contiguous last dimension")
+    gains = []
+    for g in (k_gain, v_gain):
+        if g is None:
+            gains.append(0)
+            continue
+        if (g.dtype is not torch.float32 or g.get_device() != dev or g.numel() != shape[1]
+                or not g.is_contiguous()):
+            raise ValueError("k_gain and v_gain must be contiguous float32 CUDA tensors of one "
+                             "number a kv head")
+        gains.append(g.data_ptr())
+    ks, vs = k_scales.stride(), v_scales.stride()
+    return (c[0], D) + c[2:], _FP4.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ks[0],
+        ks[1], ks[2], vs[0], vs[1], vs[2], gains[0], gains[1])
+
+
+def sdpa_paged_append_fp4(q, k, v, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv,
+                          rope_table=None, cu_seqlens_q=None, positions=None, interleaved=False,
+                          k_gain=None, v_gain=None, q_out=None, k_out=None, v_out=None,
+                          stream=None):
+    """sdpa_paged_append into a 4-bit cache: the rows of k (rotated, rounded to
+    their type) and v as 4-bit floats with an 8-bit scale for 16 elements.
+
+    k_pages, v_pages: uint8 [pages, Hkv, page_size, D / 2] (two codes a byte, the
+    even element's in the low half); k_scales, v_scales: uint8 or float8_e4m3fn
+    [pages, Hkv, page_size, D / 16]; any strides with a contiguous last
+    dimension (the pages' multiples of 16 bytes, the scales' of D / 16).
+    k_gain, v_gain: float32 [Hkv] or None (1): an element stands for code *
+    scale * gain, so that a head's magnitudes fit 2^-10 .. 2688.  rope_table
+    None: no rotation (q is copied).  k_out, v_out: None, or [T, Hkv, D] tensors
+    of one layout that receive what the written rows stand for, in k's dtype.
+    Everything else as for sdpa_paged_append.  Returns q_out (None without q).
+    """
+    torch = _torch()
+    dev = k.get_device()
+    c, cache = _fp4_cache(dev, k.dtype, k_pages, v_pages, k_scales, v_scales, page_table,
+                          seq_lens_kv, cu_seqlens_q, k_gain, v_gain)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_append_fp4(
+            q, k, v, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv, rope_table,
+            cu_seqlens_q, positions, interleaved, k_gain, v_gain, q_out, k_out, v_out))
+    T, hq, qs, q_out, os = _new_tokens(q, k, v, q_out, c, dev)
+    ostr = None
+    for out in (k_out, v_out):
+        if out is not None:
+            st = out.stride()
+            if (out.shape != k.shape or out.dtype is not k.dtype or out.get_device() != dev
+                    or st[2] != 1 or (ostr is not None and st != ostr)):
+                raise ValueError("k_out and v_out must be like k, of one layout, with a contiguous "
+                                 "last dimension")
+            ostr = st
+    kn, vn = k.stride(), v.stride()
+    p = _paged_pack(c, T, hq, 1.0, 1, 0, qs, os)
+    _paged_status(_paged_call("sdpa_paged_append_fp4", 3)(
+        p, _rotation(rope_table, positions, interleaved, T, dev), cache,
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if q is None else q_out.data_ptr(), _STRIDE2(kn[0], kn[1]), _STRIDE2(vn[0], vn[1]),
+        None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+        None if ostr is None else _STRIDE2(ostr[0], ostr[1]),
+        torch._C._cuda_getCurrentRawStream(dev)))
+    return q_out
+
+
+def sdpa_paged_forward_fp4(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv,
+                           cu_seqlens_q=None, scale=None, causal=True, sinks=None, k_gain=None,
+                           v_gain=None, out=None, lse=None, return_lse=True, workspace=None,
+                           stream=None):
+    """O (and LSE) of the new tokens' attention over a 4-bit paged cache.
+
+    The cache as for sdpa_paged_append_fp4; everything else as for
+    sdpa_paged_forward (q and out float32, float16 or bfloat16; D 64 or 128).
+    Returns (out, lse) or out.
+    """
+    torch = _torch()
+    dev = q.get_device()
+    c, cache = _fp4_cache(dev, q.dtype, k_pages, v_pages, k_scales, v_scales, page_table,
+                          seq_lens_kv, cu_seqlens_q, k_gain, v_gain)
+    shape, qs = _paged_queries(q, c)
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        return _elsewhere(dev, stream, lambda: sdpa_paged_forward_fp4(
+            q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv, cu_seqlens_q, scale,
+            causal, sinks, k_gain, v_gain, out, lse, return_lse,
+            _new_workspace(q.device, c[1]) if workspace is None else workspace))
+    out, os, lse = _paged_results(q, sinks, out, lse, return_lse, dev)
+    s = torch._C._cuda_getCurrentRawStream(dev)
+    _, wp, wn = _paged_workspace(workspace, dev, q.device, c[1], s)
+    p = _paged_pack(c, shape[0], shape[1], 1.0 / math.sqrt(c[1]) if scale is None else scale,
+                    1 if causal else 0, 0 if sinks is None else sinks.data_ptr(), qs, os)
+    _paged_status(_paged_call("sdpa_paged_forward_fp4", 2)(
+        p, cache, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn,
+        s))
+    return (out, lse) if return_lse else out

@@ -96,6 +96,13 @@ struct Args {
   int score_len;
   int* status;
   unsigned long long wait_ns;
+  // 4-bit cache: k, v, ks and vs are the codes' (bytes); scales, their byte
+  // strides, and the kv heads' gains (or null)
+  const char* k_scales;
+  const char* v_scales;
+  long long kss[3], vss[3];
+  const float* k_gain;
+  const float* v_gain;
 };
 
 // Descriptor of a cut unit, written by the CTA that began it: partial
@@ -123,6 +130,22 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   s.nk = min(len, a.cap);
   s.off = min(len - s.nq, a.cap);
   return s;
+}
+
+// Sequence of packed row t: the last b with cu[b] <= t, found by the warp 32
+// ways at a time; -1 where t belongs to none.
+__device__ __forceinline__ int find_seq(const Args& a, int t, int lane) {
+  if (!a.cu) return t < a.B ? t : -1;
+  int lo = 0, n = a.B;  // candidates lo .. lo + n - 1, cu[lo] <= t wanted
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const bool le = i < n && (i == 0 || a.cu[lo + i] <= t);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return a.cu[lo] <= t && t < a.cu[lo + 1] ? lo : -1;
 }
 
 // sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0 and m >= 1:
@@ -453,6 +476,7 @@ struct Boxes {
 // Launchers (host side).  `a` holds the problem and the workspace; the
 // attention and score launchers fill in the tile's rows (gu, nsub, w).
 sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
+sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
 int paged_vector_rows(const paged::Args& a);
 sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
                                       const LaunchEnv& env);

@@ -7,6 +7,8 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_append.cuh"
+#include "rotate.cuh"
 #include "sdpa.h"
 
 namespace gb300 {
@@ -190,6 +192,88 @@ bool tc_fits(const sdpa_paged_params_t& p, bool values) {
   return true;
 }
 
+// The 4-bit cache of a problem whose k_stride and v_stride are the codes' byte
+// strides (`writes`: every row has a place of its own).
+sdpa_status_t check_fp4(const sdpa_paged_params_t& p, const sdpa_fp4_cache_t* c, bool writes) {
+  if (!c) return SDPA_ERR_INVALID_ARGUMENT;
+  const int n = p.head_dim / 16;  // bytes of a row's scales
+  sdpa_status_t st = check_strides(p.k_stride, 3, 1);
+  if (st == SDPA_OK) st = check_strides(p.v_stride, 3, 1);
+  if (st != SDPA_OK) return st;
+  const int64_t places[3] = {p.num_pages, p.num_kv_heads, p.page_size};
+  for (const int64_t* s : {c->k_scale_stride, c->v_scale_stride})
+    for (int i = 0; i < 3; ++i) {
+      if (s[i] < 0 || s[i] > (int64_t(1) << 40)) return SDPA_ERR_INVALID_ARGUMENT;
+      if (s[i] % n != 0) return SDPA_ERR_MISALIGNED;
+      if (writes && overlaps(s[i], places[i])) return SDPA_ERR_INVALID_ARGUMENT;
+    }
+  if (writes && cache_overlaps(p)) return SDPA_ERR_INVALID_ARGUMENT;
+  if (p.num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales))
+    return SDPA_ERR_INVALID_ARGUMENT;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, n) ||
+      !aligned(c->v_scales, n) || !aligned(c->k_gain, 4) || !aligned(c->v_gain, 4))
+    return SDPA_ERR_MISALIGNED;
+  return SDPA_OK;
+}
+
+// The checks of validate() for a 4-bit cache (its strides are check_fp4's).
+sdpa_status_t validate_fp4(const sdpa_paged_params_t* p, unsigned uses) {
+  if (!p) return SDPA_ERR_INVALID_ARGUMENT;
+  sdpa_paged_params_t x = *p;
+  for (int i = 0; i < 3; ++i) x.k_stride[i] = x.v_stride[i] = 0;
+  return validate(&x, uses);
+}
+
+// sdpa_paged_append and sdpa_paged_append_fp4 after validate().
+sdpa_status_t append(const sdpa_paged_params_t& p, const paged::AppendIo& io, const void* q,
+                     void* stream) {
+  if (p.num_q_heads < 0 || p.num_q_heads % p.num_kv_heads != 0) return SDPA_ERR_INVALID_ARGUMENT;
+  const int es = elem_size(p);
+  sdpa_status_t st = io.rotation ? check_rotation(*io.rotation, p.head_dim) : SDPA_OK;
+  if (st != SDPA_OK) return st;
+  if (p.num_seqs == 0 || p.num_tokens == 0) return SDPA_OK;
+  const int64_t rows[2] = {p.num_tokens, p.num_q_heads};
+  if (p.num_q_heads > 0) {
+    if ((st = check_strides(p.q_stride, 2, es)) != SDPA_OK) return st;
+    if ((st = check_strides(p.o_stride, 2, es)) != SDPA_OK) return st;
+    if (!q || !io.q_out || overlaps(p.o_stride[0], rows[0]) || overlaps(p.o_stride[1], rows[1]) ||
+        (q == io.q_out && !same_layout(p.q_stride, p.o_stride, rows)))
+      return SDPA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(io.q_out, 16)) return SDPA_ERR_MISALIGNED;
+  }
+  if (!io.k || !io.v || !io.k_new_stride || !io.v_new_stride) return SDPA_ERR_INVALID_ARGUMENT;
+  if ((st = check_strides(io.k_new_stride, 2, es)) != SDPA_OK) return st;
+  if ((st = check_strides(io.v_new_stride, 2, es)) != SDPA_OK) return st;
+  if ((st = check_arrays(p)) != SDPA_OK) return st;
+  if (!aligned(io.k, 16) || !aligned(io.v, 16)) return SDPA_ERR_MISALIGNED;
+  if (io.fp4) {
+    // (K and V are written side by side: one place for both would keep either)
+    if (p.num_pages > 0 && (io.fp4->k_codes == io.fp4->v_codes ||
+                            io.fp4->k_scales == io.fp4->v_scales))
+      return SDPA_ERR_INVALID_ARGUMENT;
+    if (io.k_out || io.v_out) {
+      if (!io.out_stride || overlaps(io.out_stride[0], p.num_tokens) ||
+          overlaps(io.out_stride[1], p.num_kv_heads) || io.k_out == io.v_out)
+        return SDPA_ERR_INVALID_ARGUMENT;
+      if ((st = check_strides(io.out_stride, 2, es)) != SDPA_OK) return st;
+      if (!aligned(io.k_out, 16) || !aligned(io.v_out, 16)) return SDPA_ERR_MISALIGNED;
+    }
+  } else {
+    if ((p.num_pages > 0 && (!io.k_pages || !io.v_pages || io.k_pages == io.v_pages)) ||
+        cache_overlaps(p))
+      return SDPA_ERR_INVALID_ARGUMENT;
+    if (!aligned(io.k_pages, 16) || !aligned(io.v_pages, 16)) return SDPA_ERR_MISALIGNED;
+  }
+  LaunchEnv env;
+  if (!make_env(&env, stream)) return SDPA_ERR_CUDA;
+  paged::Args a = make_args(p);
+  a.status = env.status;
+  a.q = q;
+  st = launch_paged_append(a, p.head_dim, p.dtype, io, env);
+  if (st == SDPA_OK) set_last_launches(1);
+  return st;
+}
+
 bool no_rows(const sdpa_paged_params_t& p) {
   return p.num_seqs == 0 || p.num_tokens == 0 || p.num_q_heads == 0;
 }
@@ -353,6 +437,83 @@ sdpa_status_t sdpa_paged_evict(const sdpa_paged_params_t* p, int32_t keep, int32
                           scores_out, score_stride, score_len, kept, seq_lens_out, env.stream,
                           &launches);
   if (st == SDPA_OK) set_last_launches(launches);
+  return st;
+}
+
+sdpa_status_t sdpa_paged_append(const sdpa_paged_params_t* p, const sdpa_rotation_t* rotation,
+                                const void* q, const void* k, const void* v, void* q_out,
+                                const int64_t* k_new_stride, const int64_t* v_new_stride,
+                                void* k_pages, void* v_pages, void* stream) {
+  set_last_launches(0);
+  const sdpa_status_t st = validate(p, kUsesV);
+  if (st != SDPA_OK) return st;
+  if (!rotation) return SDPA_ERR_INVALID_ARGUMENT;
+  paged::AppendIo io = {};
+  io.rotation = rotation;
+  io.k = k;
+  io.v = v;
+  io.q_out = q_out;
+  io.k_new_stride = k_new_stride;
+  io.v_new_stride = v_new_stride;
+  io.k_pages = k_pages;
+  io.v_pages = v_pages;
+  return append(*p, io, q, stream);
+}
+
+sdpa_status_t sdpa_paged_append_fp4(const sdpa_paged_params_t* p, const sdpa_rotation_t* rotation,
+                                    const sdpa_fp4_cache_t* cache, const void* q, const void* k,
+                                    const void* v, void* q_out, const int64_t* k_new_stride,
+                                    const int64_t* v_new_stride, void* k_out, void* v_out,
+                                    const int64_t* out_stride, void* stream) {
+  set_last_launches(0);
+  sdpa_status_t st = validate_fp4(p, 0);
+  if (st == SDPA_OK) st = check_fp4(*p, cache, true);
+  if (st != SDPA_OK) return st;
+  paged::AppendIo io = {};
+  io.rotation = rotation;
+  io.fp4 = cache;
+  io.k = k;
+  io.v = v;
+  io.q_out = q_out;
+  io.k_new_stride = k_new_stride;
+  io.v_new_stride = v_new_stride;
+  io.k_out = k_out;
+  io.v_out = v_out;
+  io.out_stride = out_stride;
+  return append(*p, io, q, stream);
+}
+
+sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* p, const sdpa_fp4_cache_t* cache,
+                                     const void* q, void* o, float* lse, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  set_last_launches(0);
+  sdpa_status_t st = validate_fp4(p, kUsesQ | kUsesO);
+  if (st == SDPA_OK) st = check_fp4(*p, cache, false);
+  if (st != SDPA_OK) return st;
+  if (no_rows(*p)) return SDPA_OK;
+  if (overlaps(p->o_stride[0], p->num_tokens) || overlaps(p->o_stride[1], p->num_q_heads) || !q ||
+      !o)
+    return SDPA_ERR_INVALID_ARGUMENT;
+  if ((st = check_arrays(*p)) != SDPA_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return SDPA_ERR_MISALIGNED;
+  paged::Args a;
+  LaunchEnv env;
+  if ((st = enter(*p, ws, ws_bytes, stream, &a, &env)) != SDPA_OK) return st;
+  a.q = q;
+  a.k = cache->k_codes;
+  a.v = cache->v_codes;
+  a.o = o;
+  a.lse = lse;
+  a.k_scales = static_cast<const char*>(cache->k_scales);
+  a.v_scales = static_cast<const char*>(cache->v_scales);
+  for (int i = 0; i < 3; ++i) {
+    a.kss[i] = cache->k_scale_stride[i];
+    a.vss[i] = cache->v_scale_stride[i];
+  }
+  a.k_gain = cache->k_gain;
+  a.v_gain = cache->v_gain;
+  st = launch_paged_simt_fp4(a, p->head_dim, p->dtype, env);
+  if (st == SDPA_OK) set_last_launches(2);
   return st;
 }
 

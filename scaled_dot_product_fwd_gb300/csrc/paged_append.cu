@@ -1,0 +1,267 @@
+// paged_append.cu — a step's new tokens on their way to the paged cache: q
+// rotated, k rotated and written to its page row, v written; and the same into
+// the 4-bit cache, where the rows of k and v become codes and scales.
+//
+// Bound by HBM where there are many tokens (each row in and out once), by the
+// chain of dependent loads (sequence, length, page; position, table) where
+// there are few.  A warp takes rows of one token, D / 16 lanes a row
+// (rotate.cuh), so the lookups are made once a warp, beside the rows' loads.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fp4.cuh"
+#include "paged.cuh"
+#include "paged_append.cuh"
+#include "rotate.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace {
+
+using namespace rotary;
+
+constexpr int kWarps = 8;
+
+struct AppendArgs {
+  Args a;
+  Rotation rot;
+  int lg_u;    // log2 of the pieces of a row
+  int times;   // groups of 32 * 16 / D rows that a warp takes
+  int rows;    // rows of a token: q heads, k heads, v heads
+  const char* k;
+  const char* v;
+  char* q_out;
+  // byte strides: q, q_out, new k and v (token, head); pages (page, head, row)
+  long long qi[2], qo[2], kn[2], vn[2], kb[3], vb[3];
+  char* pages[2];
+  // 4-bit cache
+  char* scales[2];
+  long long sb[2][3];
+  const float* gain[2];
+  char* value[2];  // k_out and v_out, or null
+  long long vo[2];
+};
+
+template <typename T, int D, bool kFp4>
+__global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendArgs w) {
+  constexpr int U = D / 16;    // pieces of a row
+  constexpr int RW = 32 / U;   // rows of a warp at a time
+  const Args& a = w.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = lane % U;
+  // a warp's rows in fp32 where 16 consecutive elements of a rotated row come
+  // from two lanes
+  __shared__ float s_rows[kFp4 ? kWarps * 512 : 1];
+  const long long tt = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  if (tt >= a.T) return;
+  const int t = static_cast<int>(tt);
+  const int row0 = blockIdx.y * w.times * RW + lane / U;
+  const Piece pc = piece_of(w.rot, u);
+  const Piece straight{16 * u, 16 * u + 8, false};
+  // what row r is: 0 a query, 1 a key, 2 a value
+  auto kind = [&](int r) { return r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2; };
+  Raw<T> lo, hi;
+  auto load = [&](int r) {
+    if (r >= w.rows) return;
+    const int kd = kind(r);
+    const char* x = kd == 0   ? static_cast<const char*>(a.q) + t * w.qi[0] + r * w.qi[1]
+                    : kd == 1 ? w.k + t * w.kn[0] + (r - a.Hq) * w.kn[1]
+                              : w.v + t * w.vn[0] + (r - a.Hq - a.Hkv) * w.vn[1];
+    const Piece p = kd == 2 ? straight : pc;
+    lo = load8(reinterpret_cast<const T*>(x) + p.lo);
+    hi = load8(reinterpret_cast<const T*>(x) + p.hi);
+  };
+  load(row0);
+  const int b = find_seq(a, t, lane);
+  if (b < 0) return;
+  const Seq s = seq_of(a, b);
+  // the token's position (seq_of ends the keys at the table's end, not this)
+  const long long own = static_cast<long long>(max(a.lens[b], 0)) - s.nq + (t - s.q0);
+  const long long pos = w.rot.positions ? w.rot.positions[t] : own;
+  Angles ang = {};
+  bool turned = pc.turned && pos >= 0 && pos < w.rot.len;
+  if (turned) ang = load_angles(w.rot, pos, u);
+  if (pc.turned && !turned && u == 0 && (w.rot.positions || pos >= 0))
+    atomicExch(a.status, kStatusPosition);
+  int page = -1, prow = 0;
+  if (own >= 0 && own < a.cap) {
+    page = page_of(a, b, static_cast<int>(own));
+    prow = a.by_page.mod(static_cast<int>(own));
+  }
+  for (int i = 0; i < w.times; ++i) {
+    const int r = row0 + i * RW;
+    if (i > 0) load(r);
+    const bool live = r < w.rows;
+    if (!kFp4 && !live) break;
+    const int kd = kind(r);
+    const int h = r - (kd == 0 ? 0 : kd == 1 ? a.Hq : a.Hq + a.Hkv);
+    const Piece p = kd == 2 ? straight : pc;
+    Values x;
+    const bool tn = turned && kd != 2;
+    if (live && (tn || (kFp4 && kd != 0))) {
+      widen8(lo, x.lo);
+      widen8(hi, x.hi);
+      if (tn) {
+        turn_piece<kFp4>(x, ang, w.rot.interleaved, 1.f);
+        lo = narrow8<T>(x.lo);
+        hi = narrow8<T>(x.hi);
+      }
+    }
+    if (live && (kd == 0 || !kFp4)) {
+      char* dst = nullptr;
+      if (kd == 0)
+        dst = w.q_out + t * w.qo[0] + h * w.qo[1];
+      else if (page >= 0)
+        dst = w.pages[kd - 1] + page * (kd == 1 ? w.kb : w.vb)[0] +
+              h * (kd == 1 ? w.kb : w.vb)[1] + prow * (kd == 1 ? w.kb : w.vb)[2];
+      if (dst) {
+        store8(reinterpret_cast<T*>(dst) + p.lo, lo);
+        store8(reinterpret_cast<T*>(dst) + p.hi, hi);
+      }
+    }
+    if constexpr (kFp4) {
+      const bool mine = live && kd != 0;
+      if (mine && tn) {  // the row as its type holds it
+        widen8(lo, x.lo);
+        widen8(hi, x.hi);
+      }
+      if (__any_sync(0xffffffffu, mine && p.hi != 16 * u + 8)) {
+        float* row = s_rows + warp * 512 + (lane / U) * D;
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            row[p.lo + k] = x.lo[k];
+            row[p.hi + k] = x.hi[k];
+          }
+        }
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x.lo[k] = row[16 * u + k];
+            x.hi[k] = row[16 * u + 8 + k];
+          }
+        }
+      }
+      if (mine) {
+        const int c = kd - 1;
+        const float g = w.gain[c] ? w.gain[c][h] : 1.f;
+        float top = 0.f;
+        if (w.gain[c]) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x.lo[k] = __fdiv_rn(x.lo[k], g);
+            x.hi[k] = __fdiv_rn(x.hi[k], g);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaxf(fabsf(x.lo[k]), fabsf(x.hi[k])));
+        float sc;
+        const uint32_t sbyte = fp4::scale_of(top, &sc);
+        // (true quotients: a tie between two codes is found exactly)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x.lo[k] = __fdiv_rn(x.lo[k], sc);
+          x.hi[k] = __fdiv_rn(x.hi[k], sc);
+        }
+        const uint32_t c0 = fp4::codes_of(x.lo), c1 = fp4::codes_of(x.hi);
+        if (page >= 0) {
+          const long long* st = c == 0 ? w.kb : w.vb;
+          char* dst = w.pages[c] + page * st[0] + h * st[1] + prow * st[2] + 8 * u;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(c0, c1);
+          w.scales[c][page * w.sb[c][0] + h * w.sb[c][1] + prow * w.sb[c][2] + u] =
+              static_cast<char>(sbyte);
+        }
+        if (w.value[c]) {
+          uint32_t f[8];
+          fp4::codes_f16(c0, reinterpret_cast<uint32_t(&)[4]>(f[0]));
+          fp4::codes_f16(c1, reinterpret_cast<uint32_t(&)[4]>(f[4]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 y0 = __half22float2(fp4::as_half2(f[k]));
+            const float2 y1 = __half22float2(fp4::as_half2(f[4 + k]));
+            x.lo[2 * k] = y0.x * sc * g;
+            x.lo[2 * k + 1] = y0.y * sc * g;
+            x.hi[2 * k] = y1.x * sc * g;
+            x.hi[2 * k + 1] = y1.y * sc * g;
+          }
+          T* dst = reinterpret_cast<T*>(w.value[c] + t * w.vo[0] + h * w.vo[1]) + 16 * u;
+          store8(dst, narrow8<T>(x.lo));
+          store8(dst + 8, narrow8<T>(x.hi));
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int D, bool kFp4>
+sdpa_status_t launch(AppendArgs& w, const LaunchEnv& env) {
+  constexpr int RW = 512 / D;
+  const long long blocks = (static_cast<long long>(w.a.T) + kWarps - 1) / kWarps;
+  const int groups = (w.rows + RW - 1) / RW;
+  // Groups of rows of a warp: one where the call is small (the shortest
+  // chain), up to four where that still fills the GPU.
+  int times = 4;
+  while (times > 1 && blocks * ((groups + times - 1) / times) < 8LL * env.num_sms) times >>= 1;
+  times = std::max(times, (groups + 65534) / 65535);
+  w.times = times;
+  const dim3 grid(static_cast<unsigned>(blocks),
+                  static_cast<unsigned>((groups + times - 1) / times));
+  paged_append_kernel<T, D, kFp4><<<grid, kWarps * 32, 0, env.stream>>>(w);
+  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+template <typename T>
+sdpa_status_t by_dim(AppendArgs& w, int head_dim, bool fp4, const LaunchEnv& env) {
+  if (head_dim == 64) return fp4 ? launch<T, 64, true>(w, env) : launch<T, 64, false>(w, env);
+  return fp4 ? launch<T, 128, true>(w, env) : launch<T, 128, false>(w, env);
+}
+
+}  // namespace
+}  // namespace paged
+
+sdpa_status_t launch_paged_append(const paged::Args& a, int head_dim, int dtype,
+                                  const paged::AppendIo& io, const LaunchEnv& env) {
+  using namespace paged;
+  const int es = dtype == SDPA_F32 ? 4 : 2;
+  const int cs = io.fp4 ? 1 : es;  // bytes of the pages' stride unit
+  AppendArgs w = {};
+  w.a = a;
+  w.rot = make_rotation(io.rotation);
+  w.rows = a.Hq + 2 * a.Hkv;
+  w.k = static_cast<const char*>(io.k);
+  w.v = static_cast<const char*>(io.v);
+  w.q_out = static_cast<char*>(io.q_out);
+  for (int i = 0; i < 2; ++i) {
+    w.qi[i] = a.qs[i] * es;
+    w.qo[i] = a.os[i] * es;
+    w.kn[i] = io.k_new_stride[i] * es;
+    w.vn[i] = io.v_new_stride[i] * es;
+  }
+  for (int i = 0; i < 3; ++i) {
+    w.kb[i] = a.ks[i] * cs;
+    w.vb[i] = a.vs[i] * cs;
+  }
+  w.pages[0] = static_cast<char*>(io.fp4 ? io.fp4->k_codes : io.k_pages);
+  w.pages[1] = static_cast<char*>(io.fp4 ? io.fp4->v_codes : io.v_pages);
+  if (io.fp4) {
+    w.scales[0] = static_cast<char*>(io.fp4->k_scales);
+    w.scales[1] = static_cast<char*>(io.fp4->v_scales);
+    for (int i = 0; i < 3; ++i) {
+      w.sb[0][i] = io.fp4->k_scale_stride[i];
+      w.sb[1][i] = io.fp4->v_scale_stride[i];
+    }
+    w.gain[0] = io.fp4->k_gain;
+    w.gain[1] = io.fp4->v_gain;
+    w.value[0] = static_cast<char*>(io.k_out);
+    w.value[1] = static_cast<char*>(io.v_out);
+    for (int i = 0; i < 2; ++i) w.vo[i] = io.out_stride ? io.out_stride[i] * es : 0;
+  }
+  if (dtype == SDPA_F32) return by_dim<float>(w, head_dim, io.fp4 != nullptr, env);
+  return dtype == SDPA_F16 ? by_dim<__half>(w, head_dim, io.fp4 != nullptr, env)
+                           : by_dim<__nv_bfloat16>(w, head_dim, io.fp4 != nullptr, env);
+}
+
+}  // namespace gb300

@@ -45,22 +45,6 @@ struct WriteArgs {
   int lg;                  // its log2
 };
 
-// Sequence of packed row t: the last b with cu[b] <= t, found by the warp 32
-// ways at a time; -1 where t belongs to none.
-__device__ __forceinline__ int find_seq(const Args& a, int t, int lane) {
-  if (!a.cu) return t < a.B ? t : -1;
-  int lo = 0, n = a.B;  // candidates lo .. lo + n - 1, cu[lo] <= t wanted
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int i = lane * step;
-    const bool le = i < n && (i == 0 || a.cu[lo + i] <= t);
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return a.cu[lo] <= t && t < a.cu[lo + 1] ? lo : -1;
-}
-
 __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const WriteArgs w) {
   const Args& a = w.a;
   const int lane = threadIdx.x & 31;

@@ -27,12 +27,15 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
 namespace gb300 {
 namespace paged {
 namespace {
+
+struct Fp4 {};  // the element of a 4-bit cache
 
 constexpr int kT = 256;   // threads of a CTA
 constexpr int kKT = 64;   // keys of a tile
@@ -91,6 +94,38 @@ __device__ void load_rows(const void* base, const long long* off, float* dst, in
     const int r = i / C, c = (i % C) * N;
     const long long o = off[r];
     widen16<T>(dst + r * pitch + c, o >= 0 ? static_cast<const T*>(base) + o + c : nullptr);
+  }
+}
+
+// The rows of a 4-bit cache tile as fp32: a thread takes the 16 codes of a
+// scale.  `codes`, `scales`: the kv head's; off: page and row (-1: none).
+template <int D>
+__device__ void load_rows_fp4(const char* codes, const char* scales, const long long* st,
+                              const long long* ss, const int2* off, float gain, float* dst,
+                              int pitch) {
+  constexpr int C = D / 16;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < kKT * C; i += kT) {
+    const int r = i / C, c = i % C;
+    const int2 at = off[r];
+    float* x = dst + r * pitch + 16 * c;
+    uint2 w = make_uint2(0, 0);
+    uint32_t sb = 0;
+    if (at.x >= 0) {
+      w = *reinterpret_cast<const uint2*>(codes + at.x * st[0] + at.y * st[2] + 8 * c);
+      sb = static_cast<uint8_t>(scales[at.x * ss[0] + at.y * ss[2] + c]);
+    }
+    const float g = __low2float(fp4::as_half2(fp4::scales_f16(sb)));
+    uint32_t f[8];
+    fp4::codes_f16(w.x, reinterpret_cast<uint32_t(&)[4]>(f[0]));
+    fp4::codes_f16(w.y, reinterpret_cast<uint32_t(&)[4]>(f[4]));
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float2 a = __half22float2(fp4::as_half2(f[k]));
+      const float2 b = __half22float2(fp4::as_half2(f[k + 1]));
+      *reinterpret_cast<float4*>(x + 2 * k) =
+          make_float4(a.x * g * gain, a.y * g * gain, b.x * g * gain, b.y * g * gain);
+    }
   }
 }
 
@@ -160,8 +195,9 @@ __device__ __forceinline__ void scores_tile(const float* sQ, const float* sK, in
 // fp32 tiles are double-buffered (copies of the next beside the arithmetic on
 // this one)
 template <typename T, int D, int RM>
-constexpr int attend_smem() {
-  return (RM * D + (sizeof(T) == 4 ? 2 : 1) * kKT * (2 * D + 4) + RM * (kKT + 4)) * 4;
+constexpr int attend_smem() {  // T: the cache's
+  return (RM * D + (std::is_same<T, float>::value ? 2 : 1) * kKT * (2 * D + 4) + RM * (kKT + 4)) *
+         4;
 }
 
 // CTAs an SM: what the shared memory and the registers of a tile allow (one of
@@ -176,15 +212,17 @@ constexpr int scores_ctas() {
   return RM == 16 ? 4 : D == 64 ? 3 : 2;
 }
 
-template <typename T, int D, int RM>
-__global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel(const Args a) {
+// T: the type of q and o, CT: the cache's.
+template <typename T, int D, int RM, typename CT = T>
+__global__ void __launch_bounds__(kT, attend_ctas<CT, D, RM>()) paged_simt_kernel(const Args a) {
   constexpr int RPT = RM / 16;
   constexpr int CG = D / 64;  // float4 column groups of a thread
   constexpr int kSlot = RM * (D + 2);
   extern __shared__ float smem[];
   float* sQ = smem;
   float* sK = sQ + RM * D;
-  constexpr bool kAsync = sizeof(T) == 4;
+  constexpr bool kAsync = std::is_same<CT, float>::value;
+  constexpr bool kFp4 = std::is_same<CT, Fp4>::value;
   constexpr int kTile = kKT * (2 * D + 4);  // a K and a V tile
   float* sP = sK + (kAsync ? 2 : 1) * kTile;
   __shared__ long long off_k[2][kKT], off_v[2][kKT];
@@ -203,7 +241,14 @@ __global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel
     const int tok0 = u.j * a.w;
     __syncthreads();  // the previous unit's tiles are read
     load_queries<T, D, RM>(a, u.s, tok0, kvh, sub, sQ);
-    row_offsets(a, u.b, kvh, u.s0 * kKT, u.s.nk, off_k[0], off_v[0]);
+    int2* at = reinterpret_cast<int2*>(off_k);  // (4-bit cache) pages and rows of a tile
+    auto places = [&](int key0) {
+      if (tid < kKT) {
+        const int key = key0 + tid;
+        at[tid] = make_int2(key < u.s.nk ? page_of(a, u.b, key) : -1, a.by_page.mod(key));
+      }
+    };
+    if constexpr (!kFp4) row_offsets(a, u.b, kvh, u.s0 * kKT, u.s.nk, off_k[0], off_v[0]);
     __syncthreads();
     int limit[RPT];  // keys below it are visible to the row
     float m[RPT], l[RPT], o[RPT][CG][4];
@@ -241,6 +286,17 @@ __global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel
         if (t + 1 < u.s1) copy_tile(par ^ 1);
         if (t + 2 < u.s1)
           row_offsets(a, u.b, kvh, key0 + 2 * kKT, u.s.nk, off_k[par], off_v[par]);
+      } else if constexpr (kFp4) {
+        if (t > u.s0) __syncthreads();
+        places(key0);
+        __syncthreads();
+        load_rows_fp4<D>(static_cast<const char*>(a.k) + kvh * a.ks[1],
+                         a.k_scales + kvh * a.kss[1], a.ks, a.kss, at,
+                         a.k_gain ? a.k_gain[kvh] : 1.f, sK, D + 4);
+        load_rows_fp4<D>(static_cast<const char*>(a.v) + kvh * a.vs[1],
+                         a.v_scales + kvh * a.vss[1], a.vs, a.vss, at,
+                         a.v_gain ? a.v_gain[kvh] : 1.f, sK + kKT * (D + 4), D);
+        __syncthreads();
       } else {
         if (t > u.s0) __syncthreads();
         load_rows<T, D>(a.k, off_k[par], sK, D + 4);
@@ -660,16 +716,19 @@ sdpa_status_t start(Args& a, int smem, int ctas, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
-template <typename T, int D>
+template <typename T, int D, typename CT = T>
 sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   // few rows a sequence (decode): the 16-row tile, see the top of the file
   const int rows = a.G <= 16 && call_rows(a) <= 16 ? 16 : 64;
   fit_rows(a, rows);
   const sdpa_status_t st =
-      rows == 16 ? start<paged_simt_kernel<T, D, 16>>(
-                       a, attend_smem<T, D, 16>(), attend_ctas<T, D, 16>() * env.num_sms, env.stream)
-                 : start<paged_simt_kernel<T, D, 64>>(
-                       a, attend_smem<T, D, 64>(), attend_ctas<T, D, 64>() * env.num_sms, env.stream);
+      rows == 16
+          ? start<paged_simt_kernel<T, D, 16, CT>>(a, attend_smem<CT, D, 16>(),
+                                                   attend_ctas<CT, D, 16>() * env.num_sms,
+                                                   env.stream)
+          : start<paged_simt_kernel<T, D, 64, CT>>(a, attend_smem<CT, D, 64>(),
+                                                   attend_ctas<CT, D, 64>() * env.num_sms,
+                                                   env.stream);
   if (st != SDPA_OK) return st;
   const int dtype = sizeof(T) == 4 ? SDPA_F32 : std::is_same<T, __half>::value ? SDPA_F16 : SDPA_BF16;
   return launch_paged_merge(a, D, dtype, rows, 1, env.stream);
@@ -719,6 +778,19 @@ sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const La
   }
   if (dtype == SDPA_F32) return attend<float, 128>(a, env);
   return dtype == SDPA_F16 ? attend<__half, 128>(a, env) : attend<__nv_bfloat16, 128>(a, env);
+}
+
+sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype,
+                                    const LaunchEnv& env) {
+  using namespace paged;
+  if (head_dim == 64) {
+    if (dtype == SDPA_F32) return attend<float, 64, Fp4>(a, env);
+    return dtype == SDPA_F16 ? attend<__half, 64, Fp4>(a, env)
+                             : attend<__nv_bfloat16, 64, Fp4>(a, env);
+  }
+  if (dtype == SDPA_F32) return attend<float, 128, Fp4>(a, env);
+  return dtype == SDPA_F16 ? attend<__half, 128, Fp4>(a, env)
+                           : attend<__nv_bfloat16, 128, Fp4>(a, env);
 }
 
 sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,

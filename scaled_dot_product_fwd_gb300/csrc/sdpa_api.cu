@@ -201,6 +201,7 @@ const char* sdpa_status_string(sdpa_status_t s) {
     case SDPA_ERR_CUDA: return "CUDA error";
     case SDPA_ERR_TIMEOUT: return "device wait timed out";
     case SDPA_ERR_PAGE_TABLE: return "page table names a page outside the cache";
+    case SDPA_ERR_POSITION: return "position outside the rotation table";
     default: return "unknown status";
   }
 }
