@@ -477,6 +477,11 @@ struct Boxes {
 // attention and score launchers fill in the tile's rows (gu, nsub, w).
 sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
 sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
+// Rows of a tile of the 4-bit cache's few-row kernel for this call (8 or 16; 0:
+// the calls of more rows).
+int paged_fp4_decode_rows(const paged::Args& a);
+sdpa_status_t launch_paged_fp4_decode(paged::Args a, int head_dim, int dtype, int rows,
+                                      const LaunchEnv& env);
 int paged_vector_rows(const paged::Args& a);
 sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
                                       const LaunchEnv& env);

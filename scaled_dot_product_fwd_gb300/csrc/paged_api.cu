@@ -512,7 +512,10 @@ sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* p, const sdpa_fp
   }
   a.k_gain = cache->k_gain;
   a.v_gain = cache->v_gain;
-  st = launch_paged_simt_fp4(a, p->head_dim, p->dtype, env);
+  if (const int rows = paged_fp4_decode_rows(a))
+    st = launch_paged_fp4_decode(a, p->head_dim, p->dtype, rows, env);
+  else
+    st = launch_paged_simt_fp4(a, p->head_dim, p->dtype, env);
   if (st == SDPA_OK) set_last_launches(2);
   return st;
 }
