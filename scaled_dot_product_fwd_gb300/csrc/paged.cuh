@@ -482,6 +482,8 @@ sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype, cons
 int paged_fp4_decode_rows(const paged::Args& a);
 sdpa_status_t launch_paged_fp4_decode(paged::Args a, int head_dim, int dtype, int rows,
                                       const LaunchEnv& env);
+sdpa_status_t launch_paged_fp4_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);
+sdpa_status_t launch_paged_fp4_tc_d128(paged::Args a, int dtype, const LaunchEnv& env);
 int paged_vector_rows(const paged::Args& a);
 sdpa_status_t launch_paged_vector_f32(paged::Args a, int head_dim, int rows,
                                       const LaunchEnv& env);
@@ -499,7 +501,7 @@ sdpa_status_t launch_paged_decode_tc(const paged::Args& a, int head_dim, int dty
 sdpa_status_t launch_paged_scores_tc(paged::Args a, int head_dim, int dtype,
                                      const LaunchEnv& env);
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
-                                 int tiles, cudaStream_t stream);
+                                 int tiles, cudaStream_t stream, bool by_head = false);
 sdpa_status_t launch_paged_scores_merge(const paged::Args& a, int tile_keys,
                                         cudaStream_t stream);
 sdpa_status_t launch_paged_write(const paged::Args& a, int row_bytes, const void* k,

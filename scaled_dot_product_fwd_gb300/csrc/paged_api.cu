@@ -515,7 +515,8 @@ sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* p, const sdpa_fp
   if (const int rows = paged_fp4_decode_rows(a))
     st = launch_paged_fp4_decode(a, p->head_dim, p->dtype, rows, env);
   else
-    st = launch_paged_simt_fp4(a, p->head_dim, p->dtype, env);
+    st = p->head_dim == 64 ? launch_paged_fp4_tc_d64(a, p->dtype, env)
+                           : launch_paged_fp4_tc_d128(a, p->dtype, env);
   if (st == SDPA_OK) set_last_launches(2);
   return st;
 }

@@ -38,6 +38,7 @@
 #include "fp4.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace gb300 {
 namespace paged {
@@ -45,34 +46,65 @@ namespace {
 
 constexpr int kT = 256;
 constexpr int kWarps = kT / 32;
-constexpr int kLgTile = 8;  // keys of a CTA's step (32 a warp)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kHead = 7.f;    // weights are 2^kHead at the reference maximum
 constexpr float kLimit = 15.f;  // and at most 2^kLimit
 
 template <int D>
 struct Cfg {
-  static constexpr int ROW = D / 2;                 // bytes of a row's codes
-  static constexpr int SC = D / 16;                 // of its scales
-  static constexpr int STAGE = 32 * 2 * (ROW + SC);  // a warp's 32 keys: K, V, scales
-  static constexpr int NS = D == 128 ? 3 : 5;
-  static constexpr int V_OFF = 32 * ROW;
+  static constexpr int ROW = D / 2;   // bytes of a row's codes
+  static constexpr int SC = D / 16;   // of its scales
+  static constexpr int V_OFF = 32 * ROW;  // a warp's 32 keys: K, V, scales of K and V
   static constexpr int KS_OFF = 2 * V_OFF;
   static constexpr int VS_OFF = KS_OFF + 32 * SC;
-  static constexpr int SMEM = kWarps * NS * STAGE;
+  static constexpr int CELL = VS_OFF + 32 * SC;
+  static constexpr int NS = D == 128 ? 3 : 5;
+  static constexpr int RING = kWarps * NS * CELL;
+  static constexpr int SMEM = RING + 512;
+  static_assert(CELL % 128 == 0 && (D == 64 || CELL % 512 == 0), "swizzle atoms aligned");
 };
+
+// How the codes of a page reach shared memory: a tensor copy of `box` = 2^lg rows
+// of one head (rows x heads x pages; a dimension whose rows lie on one another
+// has its coordinate times 0), or, where no 8 rows are sure to share a page
+// (lg < 0), 16-byte copies.
+struct CodeMaps {
+  int lg;
+  int page_mul, head_mul;  // K; V's in the next two
+  int v_page_mul, v_head_mul;
+  int no_page, v_no_page;  // coordinates that read zeros
+};
+
+// Row of a 16-key group in which slot s (row of an operand fragment) keeps its
+// key.  A lane of the value product reads slots 2 t, 2 t + 1, 2 t + 8, 2 t + 9, of
+// the score product slots g and g + 8, and neither may meet a bank twice:
+// D = 128: 64-byte rows under the 64-byte swizzle (16-byte piece c of row r at
+// c ^ (r / 2 % 4)); D = 64: 32-byte rows as they are.
+template <int D>
+__device__ __forceinline__ int even_row(int t) {  // slot 2 t
+  return D == 128 ? (t & 1) + 2 * (t & 2) : t;    // 0 1 4 5; 0 1 2 3
+}
+template <int D>
+__device__ __forceinline__ int odd_row(int t) {  // slot 2 t + 1
+  return even_row<D>(t) ^ (D == 128 ? 3 : 6);    // 3 2 7 6; 6 7 4 5
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) break;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t x, __half2 s) {
@@ -99,10 +131,13 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(x);
 }
 
-// NT: row tiles of 8.
+// NT: row tiles of 8.  hw: 2^lg_hw kv heads are a unit, a warp's keys and head
+// are number warp >> lg_hw and warp & (hw - 1).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
-    paged_fp4_decode_kernel(const Args a) {
+    paged_fp4_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                            const __grid_constant__ CUtensorMap tmV, const Args a,
+                            const CodeMaps cm, const int lg_hw) {
   using C = Cfg<D>;
   constexpr int NR = 8 * NT;
   constexpr bool kSplit = sizeof(T) == 4;
@@ -110,49 +145,61 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   constexpr int KW = D / 32;          // words of a lane's part of a K row
   constexpr int VW = D / 64;          // and of its part of a V row
   constexpr int MT = D / 16;          // 16-row tiles of O^T
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ long long scratch[kWarps];
   __shared__ Share sh;
   __shared__ float s_m[kWarps][NR], s_l[kWarps][NR];
+  __shared__ uint64_t s_full[kWarps][C::NS];
+  __shared__ int s_abort;
+  uint8_t* smem = smem_raw + ((512u - (smem_addr(smem_raw) & 511u)) & 511u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem_raw + warp * C::NS * C::STAGE;
+  const int hw = 1 << lg_hw, lg_tile = 8 - lg_hw;
+  uint8_t* ring = smem + warp * (C::NS * C::CELL);
+  uint64_t* full = s_full[warp];
+  if (lane == 0) {
+    for (int i = 0; i < C::NS; ++i) mbar_init(&full[i], 1);
+    if (warp == 0) s_abort = 0;
+    fence_mbar_init();
+  }
+  const WaitCtl wc{a.wait_ns, &s_abort, a.status};
   griddep_launch_dependents();
-  const AttendUnits units{a.by_w, kLgTile, a.causal, 1};
-  const int heads = a.Hkv * a.nsub;
-  plan_share<kT>(a, units, heads, 1, scratch, &sh);
+  const AttendUnits units{a.by_w, lg_tile, a.causal, 1};
+  const int heads = ((a.Hkv + hw - 1) >> lg_hw) * a.nsub;
+  plan_share<kT>(a, units, heads, 1, scratch, &sh);  // (ends with a CTA barrier)
   if (tid == 0) a.desc[blockIdx.x * kDesc] = 0;
   Walk<AttendUnits> walk(sh);
   Unit u;
+  // ring slots filled and read (their stage and the parity of its barrier)
+  int fill = 0, read = 0;
+  uint32_t read_par = 0;
+  bool ok_wait = true;
   while (walk.next(a, units, sh, heads, &u)) {
-    const int kvh = a.by_nsub.div(u.h), e0 = a.by_nsub.mod(u.h) * a.gu;
+    const int h0 = a.by_nsub.div(u.h) << lg_hw, e0 = a.by_nsub.mod(u.h) * a.gu;
+    const int kvh = h0 + (warp & (hw - 1));  // this warp's head (it may be past the last)
+    const bool head_ok = kvh < a.Hkv;
     const int tok0 = u.j * a.w;
-    auto row_ok = [&](int c) {
+    auto row_ok = [&](int h, int c) {
       const int tk = a.by_gu.div(c);
-      return c < a.gu * a.w && tok0 + tk < u.s.nq && e0 + a.by_gu.mod(c) < a.G;
+      return h < a.Hkv && c < a.gu * a.w && tok0 + tk < u.s.nq && e0 + a.by_gu.mod(c) < a.G;
     };
     // ------------------------------------------------------------- copies
-    // A lane looks up one key of its warp's 32, a step before its copies.
-    const char* kc = static_cast<const char*>(a.k) + kvh * a.ks[1];
-    const char* vc = static_cast<const char*>(a.v) + kvh * a.vs[1];
-    const char* ksc = a.k_scales + kvh * a.kss[1];
-    const char* vsc = a.v_scales + kvh * a.vss[1];
+    // Lane i looks up key i of its warp's 32 a step before their copies, copies
+    // its scales, and brings the box of codes that begins there.
+    const int sub = warp >> lg_hw;
     int nx_page = -1, nx_row = 0;
     auto lookup = [&](int step) {
-      const int key = (step << kLgTile) + warp * 32 + lane;
+      const int key = (step << lg_tile) + sub * 32 + lane;
       nx_page = -1;
-      if (step < u.s1 && key < u.s.nk) {
+      if (head_ok && step < u.s1 && key < u.s.nk) {
         const int i = a.by_page.div(key);
         nx_row = key - i * a.page_size;
         nx_page = a.table[u.b * a.table_stride + i];
         if (nx_page < 0 || nx_page >= a.num_pages) nx_page = -2;
       }
     };
-    auto copy16 = [&](uint8_t* dst, const char* src, bool ok) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
-                   "r"(ok ? 16 : 0)
-                   : "memory");
-    };
+    const char* ksc = a.k_scales + kvh * a.kss[1];
+    const char* vsc = a.v_scales + kvh * a.vss[1];
     auto copy_scales = [&](uint8_t* dst, const char* src, bool ok) {
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src),
                    "n"(C::SC), "r"(ok ? C::SC : 0)
@@ -162,27 +209,46 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       if (step < u.s1) {
         if (nx_page == -2) atomicExch(a.status, kStatusPageTable);
         const bool own = nx_page >= 0;
-        const long long ko = own ? nx_page * a.ks[0] + nx_row * a.ks[2] : -1;
-        const long long vo = own ? nx_page * a.vs[0] + nx_row * a.vs[2] : 0;
-        uint8_t* st = ring + ((step - u.s0) % C::NS) * C::STAGE;
-        constexpr int P = C::ROW / 16;  // 16-byte pieces of a row
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int x = i * 32 + lane, r = x / P, c = x % P;
-          const long long k = __shfl_sync(0xffffffffu, ko, r), v = __shfl_sync(0xffffffffu, vo, r);
-          copy16(st + r * C::ROW + c * 16, kc + (k >= 0 ? k + c * 16 : 0), k >= 0);
-          // V rows: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of 16 lie in rows t, t + 4,
-          // t + 8, t + 12, and the halves of 64-byte rows 2 and 3 of four are
-          // swapped, so that a warp's reads of four keys meet no bank twice
-          const int pr = (r & 16) | ((r & 1) << 2) | (r & 8) | ((r >> 1) & 3);
-          const int pc = P == 4 ? c ^ (pr & 2) : c;
-          copy16(st + C::V_OFF + pr * C::ROW + pc * 16, vc + (k >= 0 ? v + c * 16 : 0), k >= 0);
+        uint8_t* cell = ring + fill * C::CELL;
+        copy_scales(cell + C::KS_OFF + lane * C::SC,
+                    own ? ksc + nx_page * a.kss[0] + nx_row * a.kss[2] : a.k_scales, own);
+        copy_scales(cell + C::VS_OFF + lane * C::SC,
+                    own ? vsc + nx_page * a.vss[0] + nx_row * a.vss[2] : a.v_scales, own);
+        if (cm.lg >= 0) {
+          const int keys = head_ok ? u.s.nk - ((step << lg_tile) + sub * 32) : 0;
+          const int boxes = keys <= 0 ? 0 : min(32 >> cm.lg, (keys + (1 << cm.lg) - 1) >> cm.lg);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&full[fill], static_cast<uint32_t>(boxes * 2 * C::ROW) << cm.lg);
+          __syncwarp();
+          if ((lane & ((1 << cm.lg) - 1)) == 0 && (lane >> cm.lg) < boxes) {
+            tma_load_4d(cell + lane * C::ROW, &tmK, &full[fill], 0, nx_row, kvh * cm.head_mul,
+                        own ? nx_page * cm.page_mul : cm.no_page);
+            tma_load_4d(cell + C::V_OFF + lane * C::ROW, &tmV, &full[fill], 0, nx_row,
+                        kvh * cm.v_head_mul, own ? nx_page * cm.v_page_mul : cm.v_no_page);
+          }
+        } else {
+          constexpr int P = C::ROW / 16;  // 16-byte pieces of a row
+          const long long ko = own ? nx_page * a.ks[0] + kvh * a.ks[1] + nx_row * a.ks[2] : -1;
+          const long long vo = nx_page * a.vs[0] + kvh * a.vs[1] + nx_row * a.vs[2];
+#pragma unroll 1
+          for (int i = 0; i < P; ++i) {
+            const int x = i * 32 + lane, r = x / P, c = x % P, pc = P == 4 ? c ^ ((r >> 1) & 3) : c;
+            const long long k = __shfl_sync(0xffffffffu, ko, r);
+            const long long v = __shfl_sync(0xffffffffu, vo, r);
+            const char* src = static_cast<const char*>(a.k);
+            uint8_t* dst = cell + r * C::ROW + pc * 16;
+#pragma unroll 1
+            for (int y = 0; y < 2; ++y) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+                           "l"(k >= 0 ? src + (y ? v : k) + c * 16 : src), "r"(k >= 0 ? 16 : 0)
+                           : "memory");
+              src = static_cast<const char*>(a.v);
+              dst += C::V_OFF;
+            }
+          }
+          if (lane == 0) mbar_arrive(&full[fill]);
         }
-        const int pr = (lane & 16) | ((lane & 1) << 2) | (lane & 8) | ((lane >> 1) & 3);
-        copy_scales(st + C::KS_OFF + lane * C::SC,
-                    ksc + (own ? nx_page * a.kss[0] + nx_row * a.kss[2] : 0), own);
-        copy_scales(st + C::VS_OFF + pr * C::SC,
-                    vsc + (own ? nx_page * a.vss[0] + nx_row * a.vss[2] : 0), own);
+        fill = fill + 1 == C::NS ? 0 : fill + 1;
         lookup(step + 1);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -196,11 +262,11 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     float f[NT][2];  // score factors of this lane's columns 2 t, 2 t + 1 of S
     int lim[NT][2];  // and their visible keys
     int lim_min = u.s.nk;
-    const float gain = a.k_gain ? a.k_gain[kvh] : 1.f;
+    const float gain = a.k_gain && head_ok ? a.k_gain[kvh] : 1.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int c = n * 8 + g;
-      const bool ok = row_ok(c);
+      const bool ok = row_ok(kvh, c);
       const int tok = tok0 + a.by_gu.div(c);
       float x[D / 4];
 #pragma unroll
@@ -268,65 +334,95 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
     }
-    const int v_off = C::V_OFF + t * C::ROW +
-                      (D == 128 ? (((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8) : g * 4);
-    const int vs_off = C::VS_OFF + t * C::SC + (D == 128 ? g : g >> 1);
+    // addresses in a cell: this lane's piece of K slots g (and g + 8, 8 rows on),
+    // of V slots 2 t and 2 t + 1, and of their scales
+    const int k_row = (g & 1) ? odd_row<D>(g >> 1) : even_row<D>(g >> 1);
+    const int v_even = even_row<D>(t), v_odd = odd_row<D>(t);
+    auto v_at = [&](int row) {
+      return C::V_OFF + row * C::ROW +
+             (D == 128 ? (((g >> 1) ^ ((row >> 1) & 3)) * 16 + (g & 1) * 8) : g * 4);
+    };
+    const int k_off = k_row * C::ROW + (D == 128 ? (t ^ ((k_row >> 1) & 3)) * 16 : t * 8);
+    const int v_off[2] = {v_at(v_even), v_at(v_odd)};
+    const int ks_off = C::KS_OFF + k_row * C::SC + (D == 128 ? 2 * t : t);
+    const int vs_off[2] = {C::VS_OFF + v_even * C::SC + (D == 128 ? g : g >> 1),
+                           C::VS_OFF + v_odd * C::SC + (D == 128 ? g : g >> 1)};
     // ------------------------------------------------------------- steps
 #pragma unroll 1
     for (int step = u.s0; step < u.s1; ++step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::NS - 2) : "memory");
+      ok_wait = __all_sync(0xffffffffu, ok_wait && mbar_wait(&full[read], read_par, wc));
       __syncwarp();  // every lane's copies of this step have landed, and the last step is read
       copy(step + C::NS - 1);
-      const int key0 = (step << kLgTile) + warp * 32;
-      if (key0 >= u.s.nk) continue;
-      const uint8_t* st = ring + ((step - u.s0) % C::NS) * C::STAGE;
+      const int key0 = (step << lg_tile) + sub * 32;
+      const uint8_t* st = ring + read * C::CELL;
+      if (++read == C::NS) {
+        read = 0;
+        read_par ^= 1;
+      }
+      if (key0 >= u.s.nk || !head_ok) continue;
       float s[2][NT][4];
+      {
+        uint32_t w[2][2][KW];
+        __half2 sc[2][2][2];
 #pragma unroll
-      for (int kg = 0; kg < 2; ++kg) {
+        for (int kg = 0; kg < 2; ++kg)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[kg][n][k] = 0.f;
-        uint32_t w[2][KW];
-        __half2 sc[2][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = kg * 16 + r * 8 + g;
-          const uint8_t* p = st + row * C::ROW + t * (C::ROW / 4);
-          if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
-            w[r][0] = x.x;
-            w[r][1] = x.y;
-            w[r][2] = x.z;
-            w[r][3] = x.w;
-            const __half2 h = fp4::as_half2(
-                fp4::scales_f16(*reinterpret_cast<const uint16_t*>(st + C::KS_OFF + row * 8 + 2 * t)));
-            sc[r][0] = __low2half2(h);
-            sc[r][1] = __high2half2(h);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            w[r][0] = x.x;
-            w[r][1] = x.y;
-            sc[r][0] = sc[r][1] =
-                __low2half2(fp4::as_half2(fp4::scales_f16(st[C::KS_OFF + row * 4 + t])));
+          for (int r = 0; r < 2; ++r) {
+            const int row = kg * 16 + r * 8;
+            const uint8_t* p = st + k_off + row * C::ROW;
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(p);
+              w[kg][r][0] = x.x;
+              w[kg][r][1] = x.y;
+              w[kg][r][2] = x.z;
+              w[kg][r][3] = x.w;
+              const __half2 h = fp4::as_half2(fp4::scales_f16(
+                  *reinterpret_cast<const uint16_t*>(st + ks_off + row * C::SC)));
+              sc[kg][r][0] = __low2half2(h);
+              sc[kg][r][1] = __high2half2(h);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(p);
+              w[kg][r][0] = x.x;
+              w[kg][r][1] = x.y;
+              sc[kg][r][0] = sc[kg][r][1] =
+                  __low2half2(fp4::as_half2(fp4::scales_f16(st[ks_off + row * C::SC])));
+            }
           }
-        }
+        // two sums each, so that products wait less for one another
+        float z[2][2][NT][4];
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-          uint32_t x[4], y[4];
-          widen4(w[0][i], sc[0][i >> 1], x);
-          widen4(w[1][i], sc[1][i >> 1], y);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int kg = 0; kg < 2; ++kg)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) z[x][kg][n][k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i)
+#pragma unroll
+          for (int kg = 0; kg < 2; ++kg) {
+            uint32_t x[4], y[4];
+            widen4(w[kg][0][i], sc[kg][0][i >> 1], x);
+            widen4(w[kg][1][i], sc[kg][1][i >> 1], y);
+#pragma unroll
+            for (int p = 0; p < QN; ++p)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816(z[0][kg][n], x[0], y[0], x[1], y[1], q[p][n][2 * i][0], q[p][n][2 * i][1]);
+                mma16816(z[1][kg][n], x[2], y[2], x[3], y[3], q[p][n][2 * i + 1][0],
+                         q[p][n][2 * i + 1][1]);
+              }
+          }
+#pragma unroll
+        for (int kg = 0; kg < 2; ++kg)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int p = 0; p < QN; ++p) {
-              mma16816(s[kg][n], x[0], y[0], x[1], y[1], q[p][n][2 * i][0], q[p][n][2 * i][1]);
-              mma16816(s[kg][n], x[2], y[2], x[3], y[3], q[p][n][2 * i + 1][0],
-                       q[p][n][2 * i + 1][1]);
-            }
-        }
+            for (int k = 0; k < 4; ++k) s[kg][n][k] = z[0][kg][n][k] + z[1][kg][n][k];
       }
-      // exponents of the weights, x - mb; element k of a fragment: key g + 8 (k / 2), column k & 1
+      // exponents of the weights, x - mb; element k of a fragment: slot g + 8 (k / 2), column k & 1
       bool over = false;
 #pragma unroll
       for (int kg = 0; kg < 2; ++kg)
@@ -334,8 +430,7 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float x = fmaf(s[kg][n][k], f[n][k & 1], -mb[n][k & 1]);
-            s[kg][n][k] = x;
+            s[kg][n][k] = fmaf(s[kg][n][k], f[n][k & 1], -mb[n][k & 1]);
           }
       if (key0 + 32 > lim_min) {
 #pragma unroll
@@ -344,7 +439,7 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (key0 + kg * 16 + (k >> 1) * 8 + g >= lim[n][k & 1]) s[kg][n][k] = -INFINITY;
+              if (key0 + kg * 16 + (k >> 1) * 8 + k_row >= lim[n][k & 1]) s[kg][n][k] = -INFINITY;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -403,8 +498,9 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         uint32_t w[4][VW];
         uint32_t sb[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // rows t + 4 k: keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-          const uint8_t* x = st + v_off + (kg * 16 + 4 * k) * C::ROW;
+        for (int k = 0; k < 4; ++k) {  // slots 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          const int row = kg * 16 + (k >> 1) * 8;
+          const uint8_t* x = st + v_off[k & 1] + row * C::ROW;
           if constexpr (D == 128) {
             const uint2 y = *reinterpret_cast<const uint2*>(x);
             w[k][0] = y.x;
@@ -412,10 +508,10 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           } else {
             w[k][0] = *reinterpret_cast<const uint32_t*>(x);
           }
-          sb[k] = st[vs_off + (kg * 16 + 4 * k) * C::SC];
+          sb[k] = st[vs_off[k & 1] + row * C::SC];
         }
-        const __half2 s0 = fp4::as_half2(fp4::scales_f16(sb[0] | (sb[1] << 8)));
-        const __half2 s1 = fp4::as_half2(fp4::scales_f16(sb[2] | (sb[3] << 8)));
+        const __half2 s0 = fp4::as_half2(fp4::scales_f16(__byte_perm(sb[0], sb[1], 0x0040)));
+        const __half2 s1 = fp4::as_half2(fp4::scales_f16(__byte_perm(sb[2], sb[3], 0x0040)));
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
           // the codes of two keys side by side: even elements, odd elements
@@ -450,7 +546,7 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         }
       }
     __syncthreads();  // every warp has left its loop: the rings are free
-    float* red = reinterpret_cast<float*>(smem_raw);
+    float* red = reinterpret_cast<float*>(smem);
     // lane (g, t): elements D / 8 * g .. of columns 2 t and 2 t + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -464,18 +560,17 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       }
     __syncthreads();
     const bool whole = u.whole();
-    const float v_gain = a.v_gain ? a.v_gain[kvh] : 1.f;
-    float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + u.slot()) * (NR * (D + 2));
-    for (int x = tid; x < NR * (D / 4); x += kT) {
-      const int c = x / (D / 4), col = (x % (D / 4)) * 4;
-      if (!row_ok(c)) continue;
+    const int rows = NR << lg_hw;
+    float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + u.slot()) * (rows * (D + 2));
+    for (int x = tid; x < rows * (D / 4); x += kT) {
+      const int row = x / (D / 4), col = (x % (D / 4)) * 4;
+      const int hi = row / NR, c = row % NR, head = h0 + hi;
+      if (!row_ok(head, c)) continue;
       float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
+      for (int w = hi; w < kWarps; w += hw)
         if (s_l[w][c] != 0.f) M = fmaxf(M, s_m[w][c]);
       float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = hi; w < kWarps; w += hw) {
         if (s_l[w][c] == 0.f) continue;  // this warp's keys are not seen
         const float z = ex2(s_m[w][c] - (M == -INFINITY ? 0.f : M));
         const float4 v = *reinterpret_cast<const float4*>(red + (w * NR + c) * D + col);
@@ -485,17 +580,18 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         r.z = fmaf(v.z, z, r.z);
         r.w = fmaf(v.w, z, r.w);
       }
+      const float v_gain = a.v_gain ? a.v_gain[head] : 1.f;
       if (!whole) {
-        put4(slot + c * D + col,
+        put4(slot + row * D + col,
              make_float4(r.x * v_gain, r.y * v_gain, r.z * v_gain, r.w * v_gain));
         if (col == 0) {
-          slot[NR * D + c] = M;
-          slot[NR * (D + 1) + c] = L;
+          slot[rows * D + row] = M;
+          slot[rows * (D + 1) + row] = L;
         }
         continue;
       }
       const long long tok = u.s.q0 + tok0 + a.by_gu.div(c);
-      const int hq = kvh * a.G + e0 + a.by_gu.mod(c);
+      const int hq = head * a.G + e0 + a.by_gu.mod(c);
       float z = L != 0.f ? 1.f : 0.f;
       if (a.sinks) z *= add_sink(a.sinks[hq], M, L);
       z = L != 0.f ? z / L * v_gain : 0.f;
@@ -513,23 +609,72 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       d[4] = u.s.q0;
       d[5] = u.s.nq;
     }
+    fence_proxy_async_shared();
     __syncthreads();  // the rings are free for the next unit
   }
+  // a wait that gave up: what was asked for lands before the CTA leaves
+  if (s_abort && lane == 0)
+    for (int i = 0; i < C::NS; ++i) {
+      drain_wait(&full[i], 0, kDrainNs / 8);
+      drain_wait(&full[i], 1, kDrainNs / 8);
+    }
+}
+
+// Kv heads of a unit (log2).  Where a token's heads lie next to one another,
+// a run of up to 8 heads' rows is read as one piece of memory (8 x 32768 keys,
+// 8 kv heads: see the top of the file); where a head's tokens do, one.
+// A unit of more pieces than the merge takes at once costs more than that saves.
+int unit_heads(const Args& a, int ctas) {
+  int lg = 3;
+  if (a.ks[1] >= a.ks[2] && a.page_size > 1) return 0;
+  while (lg > 0 && (static_cast<long long>(a.B) * a.Hkv >> lg) * 12 < ctas) --lg;
+  // (the last unit's missing heads leave warps idle)
+  while (lg > 0 && (a.Hkv >> lg == 0 || (a.Hkv % (1 << lg) != 0 && a.Hkv < (4 << lg)))) --lg;
+  return lg;
+}
+
+// The tensor map of one cache's codes (strides: page, head, row); a stride of 0
+// becomes an extent of 1.
+bool encode_codes(CUtensorMap* map, const Args& a, const void* base, const long long (&st)[3],
+                  int row_bytes, int lg, int* page_mul, int* head_mul, int* no_page) {
+  const bool flat_page = a.num_pages > 1 && st[0] == 0, flat_head = a.Hkv > 1 && st[1] == 0;
+  *page_mul = flat_page ? 0 : 1;
+  *head_mul = flat_head ? 0 : 1;
+  *no_page = flat_page ? 1 : a.num_pages;
+  auto s = [&](long long x) { return static_cast<uint64_t>(x > 0 ? x : row_bytes); };
+  return encode_tiled_4d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, row_bytes, a.page_size,
+                         flat_head ? 1 : a.Hkv, *no_page, 1, row_bytes, 1u << lg, s(st[2]),
+                         s(st[1]), s(st[0]),
+                         row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, int D, int NT>
 sdpa_status_t launch(Args& a, const LaunchEnv& env) {
   auto kern = paged_fp4_decode_kernel<T, D, NT>;
-  constexpr int smem = std::max(Cfg<D>::SMEM, kWarps * 8 * NT * D * 4);
+  constexpr int smem = std::max(Cfg<D>::SMEM, kWarps * 8 * NT * D * 4 + 512);
   fit_rows(a, 8 * NT);
   a.nctas = std::min(a.max_ctas, (NT == 1 && sizeof(T) == 2 ? 2 : 1) * env.num_sms);
+  const int lg_hw = unit_heads(a, a.nctas);
   if (!allow_smem<paged_fp4_decode_kernel<T, D, NT>>(smem)) return SDPA_ERR_CUDA;
-  kern<<<a.nctas, kT, smem, env.stream>>>(a);
+  CUtensorMap tk = {}, tv = {};
+  CodeMaps cm = {};
+  cm.lg = std::min(box_log2(a.page_size), 5);
+  bool strides = a.num_pages > 0 && cm.lg >= 3;  // that a tensor map takes
+  for (int i = 0; i < 3; ++i)
+    strides = strides && a.ks[i] < (1LL << 40) && a.vs[i] < (1LL << 40);
+  // (rows that lie on one another: the same row for every key)
+  if (a.page_size > 1 && (a.ks[2] == 0 || a.vs[2] == 0)) strides = false;
+  if (!strides ||
+      !encode_codes(&tk, a, a.k, a.ks, D / 2, cm.lg, &cm.page_mul, &cm.head_mul, &cm.no_page) ||
+      !encode_codes(&tv, a, a.v, a.vs, D / 2, cm.lg, &cm.v_page_mul, &cm.v_head_mul,
+                    &cm.v_no_page))
+    cm.lg = -1;
+  kern<<<a.nctas, kT, smem, env.stream>>>(tk, tv, a, cm, lg_hw);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   const int dtype = sizeof(T) == 4                      ? SDPA_F32
                     : std::is_same<T, __half>::value ? SDPA_F16
                                                      : SDPA_BF16;
-  return launch_paged_merge(a, D, dtype, 8 * NT, 1, env.stream);
+  return launch_paged_merge(a, D, dtype, 8 * NT, 1 << lg_hw, env.stream, true);
 }
 
 template <typename T>

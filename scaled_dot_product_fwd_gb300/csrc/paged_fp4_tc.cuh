@@ -1,0 +1,841 @@
+// paged_fp4_tc.cuh — attention of packed new tokens over the 4-bit paged cache
+// on the 5th-generation tensor cores, for more rows a sequence than
+// paged_fp4_decode.cu takes: the kernel and its launch, instantiated per head
+// size in paged_fp4_tc_d64.cu and paged_fp4_tc_d128.cu.
+//
+// The rows, the division of the work, the issue loop and the softmax are those
+// of paged_tc.cuh.  What differs:
+//  - Four warps widen the codes: a lane has a row of a 128-key tile, whose codes
+//    and scales its warp's asynchronous copies brought to a staging ring two
+//    tiles before, and writes it as fp16 where tcgen05.mma reads it (128-byte
+//    swizzle).  Code times scale is exact in fp16 (fp4.cuh).  Rows past the
+//    length, or of a page that the table does not name, become zeros there.
+//  - Both products are in fp16 whatever the type of q.  The same four warps lay
+//    down the query tiles: fp16 rows as they are, bf16 ones times a power of two
+//    a row that brings the row's largest to [2^14, 2^15) (what fp16 then drops
+//    is below 2^-39 of it); fp32 ones likewise as a sum of two fp16 parts (22
+//    bits), each multiplied with K, and so do their weights with V (NT = 1).
+//    A row's score factor, scale * gain / that power, goes to its softmax
+//    thread; its sign into the row, so that the largest raw score is the
+//    largest score.
+//  - Weights are 2^kHead at the reference maximum, so that fp16 holds them to
+//    2^-11 relative down to 2^-18 of the largest.
+// Two query tiles a unit (NT = 2) share each widened tile.  The writes of the
+// widened tiles (64 KB a key tile) come on top of the products' reads of shared
+// memory (192 KB), whose 128 bytes a clock are then all but used up.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "paged.cuh"
+#include "prefill_tc.cuh"
+
+namespace gb300 {
+namespace paged {
+namespace {
+
+template <int D, int NT, bool X2>
+struct F4Cfg {
+  static constexpr int CB = D / 64;        // 128-byte column blocks of a row
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int QN = X2 ? 2 : 1;    // fp16 parts of a query
+  // Ring of widened K and V tiles in the order of their use: K_0 .. K_LA-1, then
+  // V_j, K_j+LA for every j: S runs LA key tiles ahead of P V.
+  static constexpr int NS = D == 64 ? 8 : NT == 2 || X2 ? 4 : 5;
+  static constexpr int LA = NT == 2 ? 1 : 2;
+  static constexpr int RING_OFF = NT * QN * TILE;
+  // staging: a warp's 32 rows of codes and scales, ST stages
+  static constexpr int ROW = D / 2;
+  static constexpr int SC = D / 16;
+  static constexpr int ST = 3;
+  static constexpr int STAGE = 32 * (ROW + SC);
+  static constexpr int STAGE_OFF = RING_OFF + NS * TILE;
+  static constexpr int QF_OFF = STAGE_OFF + 4 * ST * STAGE;  // float[2][NT][128]
+  static constexpr int BAR_OFF = QF_OFF + 2 * NT * 128 * 4;
+  // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain
+  static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int SOFT_WARPS = 4 * NT;
+  static constexpr int WARPS = SOFT_WARPS + 8;
+  static constexpr int THREADS = 32 * WARPS;
+  // registers of a thread by warpgroup (their sum is the launch's)
+  static constexpr uint32_t SOFT_REGS = NT == 2 ? 184 : 232;
+  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 56 : 136;
+  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 88 : 136;
+  static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+  static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
+  static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
+  static constexpr int UNIT_OFF =
+      WALK_OFF + WARPS * static_cast<int>(sizeof(Walk<AttendUnits>));
+  static constexpr int SMEM = UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(STAGE % 16 == 0 && STAGE_OFF % 128 == 0, "alignment");
+  static constexpr uint32_t s_col(int i) { return static_cast<uint32_t>(i * 128); }
+  static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(256 + t * D); }
+  static constexpr int SLOT = 128 * NT * (D + 2);  // floats of a partial result
+};
+
+constexpr int kUnitSteps = 6;    // fixed cost of a unit in key tiles
+constexpr uint32_t kPBar = 1;    // + t: softmax warps of tile t with the MMA warp
+constexpr uint32_t kKBar = 3;    // stage helper with the MMA warp
+constexpr float kHead = 4.f;
+
+// What a role needs of a unit.
+struct TileGeo {
+  int nt;       // active query tiles
+  int s0;       // first key tile
+  int n[2];     // key tiles of each query tile, from s0
+  int nmax;     // key tiles loaded
+  int nk;
+  // ring positions of V_j and K_j, counted from the unit's first slot
+  template <int LA>
+  __device__ __forceinline__ int v_pos(int j) const {
+    const int ahead = min(LA, nmax);
+    return ahead + j + min(j, nmax - ahead);
+  }
+  template <int LA>
+  __device__ __forceinline__ int k_pos(int j) const {
+    return j < LA ? j : v_pos<LA>(j - LA) + 1;
+  }
+};
+template <int NT>
+__device__ __forceinline__ TileGeo tile_geo(const Args& a, const Unit& u) {
+  TileGeo g;
+  g.s0 = u.s0;
+  g.nk = u.s.nk;
+  g.nmax = u.s1 - u.s0;
+  const int tok0 = u.j * a.w * NT;
+  g.nt = NT == 2 && tok0 + a.w < u.s.nq ? 2 : 1;
+  g.n[0] = g.n[1] = g.nmax;
+  if (NT == 2 && a.causal && g.nt == 2) {  // the first tile may see fewer keys
+    const int lim = min(u.s.nk, max(0, u.s.off + tok0 + a.w));
+    g.n[0] = max(0, min(u.s1, (lim + 127) >> 7) - u.s0);
+  }
+  return g;
+}
+
+// Tiles in ring order: the next one is K_k or V_v.
+template <int LA>
+struct Order {
+  int n, k = 0, v = 0;
+  __device__ __forceinline__ explicit Order(int tiles) : n(tiles) {}
+  __device__ __forceinline__ bool more() const { return v < n; }
+  __device__ __forceinline__ bool is_k() const { return k < n && k < v + LA; }
+  __device__ __forceinline__ int tile() const { return is_k() ? k : v; }
+  __device__ __forceinline__ void next() {
+    if (is_k()) ++k; else ++v;
+  }
+};
+
+// 2^(s f - m) of 64 raw scores as fp16 pairs (X2: and what fp16 leaves of
+// them), added to rs.
+template <bool X2>
+__device__ __forceinline__ void weights64(const uint32_t (&s)[64], float f, float m, uint32_t* pk,
+                                          uint32_t* lo, float& rs) {
+  const uint64_t F = f2_pack(f, f), NM = f2_pack(-m, -m);
+  uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint64_t X =
+        f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), F, NM);
+    float x0, x1;
+    f2_unpack(X, x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
+    const __half2 h = __floats2half2_rn(p0, p1);
+    pk[i] = fp4::as_u32(h);
+    if constexpr (X2)
+      lo[i] = fp4::as_u32(__floats2half2_rn(p0 - __low2float(h), p1 - __high2float(h)));
+  }
+  float t0, t1;
+  f2_unpack(f2_add(acc[0], acc[1]), t0, t1);
+  rs += t0 + t1;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
+    paged_fp4_tc_kernel(const Args a) {
+  constexpr bool X2 = sizeof(T) == 4;
+  using C = F4Cfg<D, NT, X2>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + C::RING_OFF;
+  float* sQf = reinterpret_cast<float*>(smem + C::QF_OFF);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
+  uint64_t* empty = full + C::NS;
+  uint64_t* s_full = empty + C::NS;
+  uint64_t* o_done = s_full + 2;
+  uint64_t* pv_done = o_done + 2;
+  uint64_t* drain = pv_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  Share* sh = reinterpret_cast<Share*>(smem + C::SHARE_OFF);
+  constexpr int kMma = C::SOFT_WARPS, kHelp = kMma + 1, kWiden = kMma + 4;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&full[s], 4);
+      mbar_init(&empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  griddep_launch_dependents();
+  griddep_wait();
+  const AttendUnits units{a.by_w, 7, a.causal, kUnitSteps};
+  const int heads = a.Hkv * a.nsub;
+  plan_share<C::THREADS>(a, units, heads, 2,
+                         reinterpret_cast<long long*>(smem + C::SCRATCH_OFF), sh);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{a.wait_ns, abort_flag, a.status};
+  // Each warp walks the share on its own (state in shared memory).
+  using W = Walk<AttendUnits>;
+  W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
+  Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
+  if (lane == 0) *walk = W(*sh);
+  auto next = [&]() {
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = walk->next(a, units, *sh, heads, unit);
+    return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
+  };
+
+  if (warp >= kWiden) {
+    setmaxnreg_dec<C::WIDEN_REGS>();
+    // -------------------------------------------------------------- widening
+    const int w = warp - kWiden;
+    uint8_t* stage = smem + C::STAGE_OFF + w * C::ST * C::STAGE;
+    constexpr int P = C::ROW / 16;  // 16-byte pieces of a row
+    int g = 0;                      // ring slots filled
+    bool ok = true;
+    for (int it = 0; next(); ++it) {
+      const Unit u = *unit;
+      const TileGeo tg = tile_geo<NT>(a, u);
+      const int kvh = a.by_nsub.div(u.h), sub = a.by_nsub.mod(u.h);
+      const int* table = a.table + u.b * a.table_stride;
+      // Copies of a tile's rows w * 32 .. + 31 to the staging ring; the row's
+      // page was looked up a tile before.
+      Order<C::LA> ahead(tg.nmax), now(tg.nmax);
+      int k_page, k_row, v_page, v_row;  // of the next K tile's and the next V tile's row
+      auto lookup = [&](int j, int* page, int* row) {
+        const int key = (tg.s0 + j) * 128 + w * 32 + lane;
+        *page = -1;
+        *row = 0;
+        if (j < tg.nmax && key < tg.nk) {
+          const int i = a.by_page.div(key);
+          *row = key - i * a.page_size;
+          *page = table[i];
+        }
+      };
+      lookup(0, &k_page, &k_row);
+      v_page = k_page;
+      v_row = k_row;
+      int fill = 0, read = 0;  // stages
+      auto copy = [&]() {  // (every call commits one group of copies)
+        if (ahead.more()) {
+          const bool is_k = ahead.is_k();
+          const int page = is_k ? k_page : v_page, row = is_k ? k_row : v_row;
+          const bool named = page >= 0 && page < a.num_pages;
+          const int key = (tg.s0 + ahead.tile()) * 128 + w * 32 + lane;
+          if (!named && key < tg.nk) atomicExch(a.status, kStatusPageTable);
+          const long long* st = is_k ? a.ks : a.vs;
+          const long long* ss = is_k ? a.kss : a.vss;
+          const char* codes = static_cast<const char*>(is_k ? a.k : a.v);
+          const char* scales = is_k ? a.k_scales : a.v_scales;
+          const long long off = named ? page * st[0] + kvh * st[1] + row * st[2] : -1;
+          uint8_t* dst = stage + fill * C::STAGE;
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int x = i * 32 + lane, r = x / P, c = x % P;
+            const long long o = __shfl_sync(0xffffffffu, off, r);
+            // (pieces swapped by row, so that a warp reads 32 rows' pieces
+            // without meeting a bank twice)
+            const int pc = P == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_addr(dst + r * C::ROW + pc * 16)),
+                         "l"(o >= 0 ? codes + o + c * 16 : codes), "r"(o >= 0 ? 16 : 0)
+                         : "memory");
+          }
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                           smem_addr(dst + 32 * C::ROW + lane * C::SC)),
+                       "l"(named ? scales + page * ss[0] + kvh * ss[1] + row * ss[2] : scales),
+                       "n"(C::SC), "r"(named ? C::SC : 0)
+                       : "memory");
+          ahead.next();
+          if (is_k)
+            lookup(ahead.k, &k_page, &k_row);
+          else
+            lookup(ahead.v, &v_page, &v_row);
+          fill = fill + 1 == C::ST ? 0 : fill + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll 1
+      for (int i = 0; i < C::ST - 1; ++i) copy();
+      // ------------------------------------------------------- query tiles
+      {
+        const float gain = a.k_gain ? a.k_gain[kvh] : 1.f;
+        const float sc = a.sl2 * gain;
+        const int r = w * 32 + lane;
+        const int tk = a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
+        auto source = [&](int t) -> const T* {
+          const int tok = (u.j * NT + t) * a.w + tk;
+          const bool is = r < a.w * a.gu && tok < u.s.nq && e < a.G && t < tg.nt;
+          return is ? static_cast<const T*>(a.q) + (u.s.q0 + tok) * a.qs[0] +
+                          static_cast<long long>(kvh * a.G + e) * a.qs[1]
+                    : nullptr;
+        };
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (const T* q = source(t))
+            for (int i = 0; i < D * static_cast<int>(sizeof(T)); i += 128)
+              prefetch_l1(reinterpret_cast<const char*>(q) + i);
+        if (it > 0) ok = ok && mbar_wait(q_empty, (it - 1) & 1, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        constexpr int N = 16 / sizeof(T);  // elements of a load
+#pragma unroll 1
+        for (int t = 0; t < NT; ++t) {
+          const T* q = source(t);
+          float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f, f = sc == 0.f ? 1.f : fabsf(sc);
+          if constexpr (!std::is_same<T, __half>::value) {
+            float top = 0.f;
+            if (q) {
+#pragma unroll 4
+              for (int i = 0; i < D; i += N) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(q + i);
+                const T* x = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(to_float(x[k])));
+              }
+            }
+            // the power of two that brings `top` to [2^14, 2^15) (at most 2^126)
+            const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+            const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
+            mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
+            f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
+          }
+          // (never 0, which would make a hidden score, -inf, NaN)
+          sQf[((it & 1) * NT + t) * 128 + r] = fmaxf(f, 0x1p-149f);
+          uint8_t* row = sQ + t * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll 2
+          for (int c = 0; c < D / 8; ++c) {  // 16-byte pieces of the fp16 row
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = 0.f;
+            if (q) {
+#pragma unroll
+              for (int i = 0; i < 8; i += N) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(q + c * 8 + i);
+                const T* y = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[i + k] = to_float(y[k]) * mul;
+              }
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+              hi[k] = fp4::as_u32(h);
+              if constexpr (X2)
+                lo[k] = fp4::as_u32(__floats2half2_rn(x[2 * k] - __low2float(h),
+                                                      x[2 * k + 1] - __high2float(h)));
+            }
+            uint8_t* dst = row + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) * 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (X2)
+              *reinterpret_cast<uint4*>(dst + NT * C::TILE) =
+                  make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      // ------------------------------------------------------- key tiles
+      for (; now.more(); now.next()) {
+        copy();
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::ST - 1) : "memory");
+        const int s = g % C::NS, use = g / C::NS;
+        ok = __all_sync(0xffffffffu,
+                        ok && (use == 0 || mbar_wait(&empty[s], (use - 1) & 1, wc)));
+        __syncwarp();  // (every lane's copies have landed)
+        const uint8_t* src = stage + read * C::STAGE;
+        read = read + 1 == C::ST ? 0 : read + 1;
+        const int r = w * 32 + lane;
+        uint8_t* dst = sRing + s * C::TILE + (r >> 3) * (C::CB * 1024) + (r & 7) * 128;
+        uint32_t sb[D / 64];  // the row's scales, four a word
+        if constexpr (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2*>(src + 32 * C::ROW + lane * C::SC);
+          sb[0] = x.x;
+          sb[1] = x.y;
+        } else {
+          sb[0] = *reinterpret_cast<const uint32_t*>(src + 32 * C::ROW + lane * C::SC);
+        }
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < P; ++c) {  // 32 codes, two scales
+            const int pc = P == 4 ? c ^ ((lane >> 1) & 3) : c ^ ((lane >> 2) & 1);
+            const uint4 x = *reinterpret_cast<const uint4*>(src + lane * C::ROW + pc * 16);
+            const __half2 sc = fp4::as_half2(fp4::scales_f16(sb[c >> 1] >> (16 * (c & 1))));
+            const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
+            const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 8 elements: a 16-byte piece
+              uint32_t o[4];
+              fp4::codes_f16(wd[k], o);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o[i] = fp4::as_u32(__hmul2(fp4::as_half2(o[i]), k < 2 ? s0 : s1));
+              const int piece = (c & 1) * 4 + k;
+              *reinterpret_cast<uint4*>(dst + (c >> 1) * 1024 + ((piece ^ (r & 7)) * 16)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        ++g;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+  } else if (warp >= C::SOFT_WARPS) {
+    setmaxnreg_dec<C::CONTROL_REGS>();
+    if (warp == kMma) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t idS = idesc_f16(false, 128, 128, false, false);
+      constexpr uint32_t idO = idesc_f16(false, 128, D, false, true);
+      const uint64_t q_desc = sdesc(smem_addr(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = sdesc(smem_addr(sRing), 16, C::CB * 1024, kSwizzle128B);
+      const uint64_t v_desc = sdesc(smem_addr(sRing), 1024, C::CB * 1024, kSwizzle128B);
+      const uint32_t q_hi = static_cast<uint32_t>(q_desc >> 32);
+      const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32);
+      const uint32_t v_hi = static_cast<uint32_t>(v_desc >> 32);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc);
+      const uint32_t k_lo = static_cast<uint32_t>(k_desc);
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc);
+      auto desc = [](uint32_t hi, uint32_t lo) { return (static_cast<uint64_t>(hi) << 32) | lo; };
+      // S (columns of slot i) = Q_t K^T, K in ring slot s
+      auto issue_s = [&](int t, int i, int s) {
+        const uint32_t kd = k_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
+#pragma unroll
+        for (int p = 0; p < C::QN; ++p) {
+          const uint32_t qd = q_lo + static_cast<uint32_t>(((p * NT + t) * C::TILE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qo = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+            const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+            mma_f16_ss_elect(tmem + C::s_col(i), desc(q_hi, qd + qo), desc(k_hi, kd + ko), idS,
+                             kk > 0 || p > 0 ? 1u : 0u, 1u);
+          }
+        }
+      };
+      // O_t += P V, P in slot i (X2: its second part 64 columns on), V in ring
+      // slot s, keys in groups of 16
+      auto issue_pv = [&](int t, int i, int s, bool first, int groups) {
+        const uint32_t vd = v_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
+#pragma unroll
+        for (int p = 0; p < C::QN; ++p)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts_elect(tmem + C::o_col(t), tmem + C::s_col(i) + p * 64 + kk * 8,
+                             desc(v_hi, vd + ((kk * 2 * C::CB * 1024) >> 4)), idO,
+                             (!first || kk > 0 || p > 0) ? 1u : 0u, kk < groups ? 1u : 0u);
+      };
+      int p0 = 0;  // ring slots of earlier units
+      int g0 = 0;  // key tiles of earlier units
+      while (next()) {
+        const TileGeo tg = tile_geo<NT>(a, *unit);
+        auto groups = [&](int j) { return min(8, (tg.nk - (tg.s0 + j) * 128 + 15) >> 4); };
+        auto kslot = [&](int j) { return (p0 + tg.k_pos<C::LA>(j)) % C::NS; };
+        auto vslot = [&](int j) { return (p0 + tg.v_pos<C::LA>(j)) % C::NS; };
+        named_bar_sync(kKBar, 64);  // Q and K_0 are there
+        tc_fence_after();
+        if constexpr (NT == 2) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= tg.nt) continue;
+            if (tg.n[t] > 0) {
+              issue_s(t, t, kslot(0));
+              mma_commit_elect(&s_full[t], 1u);
+            }
+          }
+          if (tg.nmax > 0) mma_commit_elect(&empty[kslot(0)], 1u);
+          if (tg.nmax <= 1) mma_commit_elect(q_empty, 1u);
+          for (int j = 0; j < tg.nmax; ++j) {
+            bool waited = false;
+            const int ks = kslot(j + 1), vs = vslot(j);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t >= tg.nt || j >= tg.n[t]) continue;
+              named_bar_sync(kPBar + t, 32 * 5);
+              if (!waited) {  // V_j and K_j+1 are there
+                named_bar_sync(kKBar, 64);
+                waited = true;
+              }
+              tc_fence_after();
+              issue_pv(t, t, vs, j == 0, groups(j));
+              if (j + 1 < tg.n[t]) {
+                issue_s(t, t, ks);
+                mma_commit_elect(&s_full[t], 1u);
+              } else {
+                mma_commit_elect(&o_done[t], 1u);
+              }
+            }
+            if (j + 1 < tg.nmax) mma_commit_elect(&empty[ks], 1u);
+            if (j == tg.nmax - 2) mma_commit_elect(q_empty, 1u);
+            mma_commit_elect(&empty[vs], 1u);
+          }
+        } else {
+          if (tg.nmax == 0) {
+            mma_commit_elect(q_empty, 1u);
+          } else {
+            issue_s(0, g0 & 1, kslot(0));
+            mma_commit_elect(&s_full[g0 & 1], 1u);
+            mma_commit_elect(&empty[kslot(0)], 1u);
+            if (tg.nmax > 1) {
+              named_bar_sync(kKBar, 64);
+              tc_fence_after();
+              issue_s(0, (g0 + 1) & 1, kslot(1));
+              mma_commit_elect(&s_full[(g0 + 1) & 1], 1u);
+              mma_commit_elect(&empty[kslot(1)], 1u);
+            }
+            if (tg.nmax <= 2) mma_commit_elect(q_empty, 1u);
+            for (int j = 0; j < tg.nmax; ++j) {
+              const int i = (g0 + j) & 1;
+              named_bar_sync(kPBar, 32 * 5);
+              named_bar_sync(kKBar, 64);  // V_j and K_j+2 are there
+              tc_fence_after();
+              issue_pv(0, i, vslot(j), j == 0, groups(j));
+              mma_commit_elect(pv_done, 1u);
+              mma_commit_elect(&empty[vslot(j)], 1u);
+              if (j + 2 < tg.nmax) {
+                issue_s(0, i, kslot(j + 2));
+                mma_commit_elect(&s_full[i], 1u);
+                mma_commit_elect(&empty[kslot(j + 2)], 1u);
+                if (j + 3 == tg.nmax) mma_commit_elect(q_empty, 1u);
+              }
+            }
+            mma_commit_elect(&o_done[0], 1u);
+          }
+        }
+        p0 += 2 * tg.nmax;
+        g0 += tg.nmax;
+      }
+      // every MMA issued by this warp completes before TMEM is freed
+      mma_commit_elect(drain, 1u);
+      if (lane == 0) drain_wait(drain, 0, kDrainNs);
+      __syncwarp();
+    } else if (warp == kHelp) {
+      // ------------------------------------------------------ stage helper
+      // Waits for the tiles that the MMA warp's next products read and meets
+      // the MMA warp (the same number of times, also after a failed wait).
+      bool ok = true;
+      int p0 = 0;
+      auto landed = [&](int p) {
+        ok = ok && mbar_wait(&full[p % C::NS], static_cast<uint32_t>((p / C::NS) & 1), wc);
+      };
+      for (int it = 0; next(); ++it) {
+        const TileGeo tg = tile_geo<NT>(a, *unit);
+        ok = ok && mbar_wait(q_full, static_cast<uint32_t>(it & 1), wc);
+        if (tg.nmax > 0) landed(p0);
+        __syncwarp();
+        named_bar_sync(kKBar, 64);
+        if (NT == 1 && tg.nmax > 1) {
+          landed(p0 + 1);
+          __syncwarp();
+          named_bar_sync(kKBar, 64);
+        }
+        for (int j = 0; j < tg.nmax; ++j) {
+          landed(p0 + tg.v_pos<C::LA>(j));
+          if (j + C::LA < tg.nmax) landed(p0 + tg.k_pos<C::LA>(j + C::LA));
+          __syncwarp();
+          named_bar_sync(kKBar, 64);
+        }
+        p0 += 2 * tg.nmax;
+      }
+    }
+  } else {
+    setmaxnreg_inc<C::SOFT_REGS>();
+    // --------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + lane_off + C::o_col(t);
+    bool ok = true;
+    int g0 = 0;   // steps of earlier units (NT = 2: of this tile)
+    int oph = 0;  // phases of o_done[t] consumed
+    bool began = false;  // this CTA wrote its descriptor
+    for (int it = 0; next(); ++it) {
+      const TileGeo tg = tile_geo<NT>(a, *unit);
+      if (t >= tg.nt) continue;
+      const int tok0 = (unit->j * NT + t) * a.w;  // first token of the tile
+      const int nq = unit->s.nq;
+      const int tok = tok0 + a.by_gu.div(r);
+      // rows of this warp that exist
+      const bool live = (warp & 3) * 32 < min(a.w, nq - tok0) * a.gu;
+      // visible keys of the row, counted from the piece's first key
+      const int limit =
+          (a.causal ? min(tg.nk, unit->s.off + tok + 1) : tg.nk) - tg.s0 * 128;
+      float m = -INFINITY, l = 0.f, f = 1.f;
+      const int n = tg.n[t];
+      for (int j = 0; j < n; ++j) {
+        const int g = g0 + j;
+        const int slot = NT == 2 ? t : g & 1;
+        const uint32_t tS = tmem + lane_off + C::s_col(slot);
+        if (live) {
+          ok = __all_sync(0xffffffffu,
+                          ok && mbar_wait(&s_full[slot], (NT == 2 ? g : g >> 1) & 1, wc));
+          if (ok) {
+            tc_fence_after();
+            if (j == 0) f = sQf[((it & 1) * NT + t) * 128 + r];
+            const int vis = limit - j * 128;  // visible keys of the row in this tile
+            const bool edge = __any_sync(0xffffffffu, vis < 128);
+            uint32_t s[64];
+            auto half = [&](int c) {  // scores c * 64 .. + 63
+              __syncwarp();
+              tmem_ld2x32_sync(tS + c * 64, tS + c * 64 + 32,
+                               *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                               *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+              if (edge) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  if (c * 64 + i >= vis) s[i] = 0xff800000u;  // -inf
+              }
+            };
+            float alpha = 1.f, rs = 0.f;
+            uint32_t pk[64], lo[X2 ? 64 : 1];
+            bool resc = !(m > -INFINITY);
+            if (!__all_sync(0xffffffffu, resc)) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                half(c);
+                weights64<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
+                              rs);
+              }
+              resc = resc || !(rs <= kFusedSumLimit);
+            }
+            if (__any_sync(0xffffffffu, resc)) {
+              float mx = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                half(c);
+                mx = fmaxf(mx, row_max_raw(s));
+              }
+              mx = mx * f - kHead;  // -inf: no visible key
+              if (resc && mx > -INFINITY) {
+                alpha = ex2(m - mx);  // 0 when m = -inf
+                m = mx;
+              }
+              rs = 0.f;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                half(c);
+                weights64<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
+                              rs);
+              }
+            }
+            __syncwarp();
+            l = l * alpha + rs;
+            // O_t through step j - 1 (NT = 2: complete, the commit behind
+            // s_full tracks it); rescaled where a row's max moved
+            if (j > 0 && __any_sync(0xffffffffu, resc)) {
+              if constexpr (NT == 1) {
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(pv_done, (g - 1) & 1, wc));
+                tc_fence_after();
+              }
+              __syncwarp();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t ob[32];
+                tmem_ld32_sync(tO + c * 32, ob);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  ob[i] = __float_as_uint(__uint_as_float(ob[i]) * alpha);
+                tmem_st32(tO + c * 32, ob);
+              }
+            }
+            tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+            if constexpr (X2) {
+              tmem_st32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&lo[0]));
+              tmem_st32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&lo[32]));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+        // hand P_j to the MMA warp; met every step, also after a failed wait
+        named_bar_sync(kPBar + (NT == 2 ? t : 0), 32 * 5);
+      }
+      if (n > 0) {
+        ok = ok && mbar_wait(&o_done[t], static_cast<uint32_t>(oph & 1), wc);
+        ok = __all_sync(0xffffffffu, ok);
+        ++oph;
+      }
+      g0 += n;
+      // ------------------------------------------------------------ epilogue
+      const bool whole = unit->whole();
+      if (!whole && unit->s0 == 0 && threadIdx.x == 0) {
+        int* d = a.desc + blockIdx.x * kDesc;
+        d[0] = pieces_of(*unit, *sh);
+        d[1] = unit->b;
+        d[2] = unit->h;
+        d[3] = unit->j;
+        d[4] = unit->s.q0;
+        d[5] = nq;
+        began = true;
+      }
+      if (!ok || !live) continue;
+      const int kvh = a.by_nsub.div(unit->h), sub = a.by_nsub.mod(unit->h);
+      const int e = sub * a.gu + a.by_gu.mod(r);
+      const bool row_ok = r < a.w * a.gu && tok < nq && e < a.G;
+      const float gain = a.v_gain ? a.v_gain[kvh] : 1.f;
+      tc_fence_after();
+      __syncwarp();
+      if (!whole) {
+        // unnormalised O (relative to 2^m), m and l
+        float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + unit->slot()) * C::SLOT;
+        float* orow = slot + (t * 128 + r) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ob[32];
+          tmem_ld32_sync(tO + c * 32, ob);
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(orow + c * 32)[i] = make_float4(
+                  __uint_as_float(ob[4 * i]) * gain, __uint_as_float(ob[4 * i + 1]) * gain,
+                  __uint_as_float(ob[4 * i + 2]) * gain, __uint_as_float(ob[4 * i + 3]) * gain);
+          }
+        }
+        if (row_ok) {
+          slot[NT * 128 * D + t * 128 + r] = m;
+          slot[NT * 128 * (D + 1) + t * 128 + r] = l;
+        }
+      } else {
+        const int hq = kvh * a.G + e;
+        float z = 1.f;
+        const float own = l;
+        if (a.sinks && row_ok) z = add_sink(a.sinks[hq], m, l);
+        const float inv = own != 0.f ? z / l * gain : 0.f;
+        const long long q = unit->s.q0 + tok;
+        T* orow = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1];
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ob[32];
+          tmem_ld32_sync(tO + c * 32, ob);
+          // (a row that saw no key: O may never have been written)
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = own != 0.f ? __uint_as_float(ob[i]) * inv : 0.f;
+          if (row_ok) {
+            if constexpr (X2) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(orow + c * 32)[i] =
+                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            } else {
+              using E = Elem<std::is_same<T, __nv_bfloat16>::value>;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(orow + c * 32)[i] =
+                    make_uint4(E::pack(x[8 * i], x[8 * i + 1]), E::pack(x[8 * i + 2], x[8 * i + 3]),
+                               E::pack(x[8 * i + 4], x[8 * i + 5]),
+                               E::pack(x[8 * i + 6], x[8 * i + 7]));
+            }
+          }
+        }
+        if (row_ok && a.lse) a.lse[q * a.Hq + hq] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+    if (threadIdx.x == 0 && !began) a.desc[blockIdx.x * kDesc] = 0;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D, int NT>
+sdpa_status_t launch_f4(Args& a, const LaunchEnv& env) {
+  using C = F4Cfg<D, NT, sizeof(T) == 4>;
+  auto kern = paged_fp4_tc_kernel<T, D, NT>;
+  // The setmaxnreg split must fit the registers the kernel is launched with
+  // (an increase beyond them would wait forever).
+  static std::atomic<uint64_t> ready{0};  // devices on which this holds and is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(ready.load() & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SDPA_ERR_CUDA;
+    const long have = static_cast<long>((fa.numRegs + 7) & ~7) * C::THREADS;
+    const long need = 32L * (C::SOFT_WARPS * static_cast<long>(C::SOFT_REGS) +
+                             4L * C::CONTROL_REGS + 4L * C::WIDEN_REGS);
+    if (have < need) return SDPA_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return SDPA_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  a.nctas = a.max_ctas < env.num_sms ? a.max_ctas : env.num_sms;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SDPA_ERR_CUDA;
+  const int dtype = sizeof(T) == 4                      ? SDPA_F32
+                    : std::is_same<T, __half>::value ? SDPA_F16
+                                                     : SDPA_BF16;
+  return launch_paged_merge(a, D, dtype, 128, NT, env.stream);
+}
+
+template <int D>
+sdpa_status_t launch_fp4_tc(Args a, int dtype, const LaunchEnv& env) {
+  fit_rows(a, 128);
+  if (dtype == SDPA_F32) return launch_f4<float, D, 1>(a, env);
+  // More than 128 rows a sequence and head unit on average: two tiles a unit.
+  const bool two = static_cast<long long>(a.T) * a.gu > 128LL * a.B;
+  if (two) fit_rows(a, 128, 2);
+  if (dtype == SDPA_F16)
+    return two ? launch_f4<__half, D, 2>(a, env) : launch_f4<__half, D, 1>(a, env);
+  return two ? launch_f4<__nv_bfloat16, D, 2>(a, env) : launch_f4<__nv_bfloat16, D, 1>(a, env);
+}
+
+}  // namespace
+}  // namespace paged
+
+}  // namespace gb300

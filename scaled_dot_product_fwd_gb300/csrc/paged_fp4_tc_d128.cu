@@ -1,0 +1,11 @@
+// paged_fp4_tc_d128.cu — the head_dim-128 instantiation of paged_fp4_tc.cuh (a
+// translation unit of its own, so that the head sizes compile in parallel).
+#include "paged_fp4_tc.cuh"
+
+namespace gb300 {
+
+sdpa_status_t launch_paged_fp4_tc_d128(paged::Args a, int dtype, const LaunchEnv& env) {
+  return paged::launch_fp4_tc<128>(a, dtype, env);
+}
+
+}  // namespace gb300

@@ -434,7 +434,7 @@ struct MergeVec<64> {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4)
-    paged_merge_kernel(const Args a, int tile_rows, int tiles) {
+    paged_merge_kernel(const Args a, int tile_rows, int tiles, bool by_head) {
   using V = typename MergeVec<D>::V;
   constexpr int E = D / 32;  // columns of a lane
   griddep_wait();
@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(256, 4)
   const int n = d[0];
   if (n == 0) return;
   const int b_h = d[2], j = d[3], q0 = d[4], nq = d[5];
-  const int kvh = a.by_nsub.div(b_h), sub = a.by_nsub.mod(b_h);
+  // the unit's tiles are runs of tokens, or (by_head) consecutive kv heads
+  const int kvh = a.by_nsub.div(b_h) * (by_head ? tiles : 1), sub = a.by_nsub.mod(b_h);
   const int rows = tile_rows * tiles;
   const size_t slot_floats = static_cast<size_t>(rows) * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -455,9 +456,10 @@ __global__ void __launch_bounds__(256, 4)
   auto locate = [&](int rr, int* tok, int* head) {
     const int t = rr >= tile_rows ? rr / tile_rows : 0, r = rr - t * tile_rows;
     const int g = a.by_gu.div(r), e = sub * a.gu + r - g * a.gu;
-    *tok = (j * tiles + t) * a.w + g;
-    *head = kvh * a.G + e;
-    return rr < rows && g < a.w && *tok < nq && e < a.G;
+    *tok = (by_head ? j : j * tiles + t) * a.w + g;
+    const int h = by_head ? kvh + t : kvh;
+    *head = h * a.G + e;
+    return rr < rows && g < a.w && *tok < nq && e < a.G && h < a.Hkv;
   };
   // O, LSE of a row from its joined accumulator
   auto finish = [&](int tok, int hq, float M, float L, const float (&acc)[E]) {
@@ -750,10 +752,12 @@ sdpa_status_t score(Args& a, const LaunchEnv& env) {
 }  // namespace paged
 
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
-                                 int tiles, cudaStream_t stream) {
+                                 int tiles, cudaStream_t stream, bool by_head) {
   using namespace paged;
   const dim3 grid(a.nctas, tile_rows * tiles > 16 ? 16 : 8);
-  auto go = [&](auto kern) { return launch_after(kern, grid, 256, stream, a, tile_rows, tiles); };
+  auto go = [&](auto kern) {
+    return launch_after(kern, grid, 256, stream, a, tile_rows, tiles, by_head);
+  };
   if (head_dim == 64) {
     if (dtype == SDPA_F32) return go(paged_merge_kernel<float, 64>);
     return dtype == SDPA_F16 ? go(paged_merge_kernel<__half, 64>)
