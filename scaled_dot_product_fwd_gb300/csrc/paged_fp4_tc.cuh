@@ -441,28 +441,29 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       auto issue_s = [&](int t, int i, int s) {
         const uint32_t kd = k_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
-        for (int p = 0; p < C::QN; ++p) {
+        for (int p = C::QN - 1; p >= 0; --p) {  // (the small part first)
           const uint32_t qd = q_lo + static_cast<uint32_t>(((p * NT + t) * C::TILE) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t qo = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
             const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
             mma_f16_ss_elect(tmem + C::s_col(i), desc(q_hi, qd + qo), desc(k_hi, kd + ko), idS,
-                             kk > 0 || p > 0 ? 1u : 0u, 1u);
+                             kk > 0 || p < C::QN - 1 ? 1u : 0u, 1u);
           }
         }
       };
-      // O_t += P V, P in slot i (X2: its second part 64 columns on), V in ring
-      // slot s, keys in groups of 16
+      // O_t += P V, P in slot i, V in ring slot s, keys in groups of 16.  X2: the
+      // weights' second part lies 64 columns on and has an O of its own (in the
+      // place of tile 1's), so that half as many sums are rounded at O's size.
       auto issue_pv = [&](int t, int i, int s, bool first, int groups) {
         const uint32_t vd = v_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
         for (int p = 0; p < C::QN; ++p)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts_elect(tmem + C::o_col(t), tmem + C::s_col(i) + p * 64 + kk * 8,
+            mma_f16_ts_elect(tmem + C::o_col(X2 ? p : t), tmem + C::s_col(i) + p * 64 + kk * 8,
                              desc(v_hi, vd + ((kk * 2 * C::CB * 1024) >> 4)), idO,
-                             (!first || kk > 0 || p > 0) ? 1u : 0u, kk < groups ? 1u : 0u);
+                             (!first || kk > 0) ? 1u : 0u, kk < groups ? 1u : 0u);
       };
       int p0 = 0;  // ring slots of earlier units
       int g0 = 0;  // key tiles of earlier units
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
               }
               __syncwarp();
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
+              for (int c = 0; c < C::QN * D / 32; ++c) {
                 uint32_t ob[32];
                 tmem_ld32_sync(tO + c * 32, ob);
 #pragma unroll
@@ -713,6 +714,16 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       const int e = sub * a.gu + a.by_gu.mod(r);
       const bool row_ok = r < a.w * a.gu && tok < nq && e < a.G;
       const float gain = a.v_gain ? a.v_gain[kvh] : 1.f;
+      auto load_o = [&](int c, uint32_t (&x)[32]) {  // columns c * 32 .. + 31
+        tmem_ld32_sync(tO + c * 32, x);
+        if constexpr (X2) {
+          uint32_t y[32];
+          tmem_ld32_sync(tO + D + c * 32, y);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+        }
+      };
       tc_fence_after();
       __syncwarp();
       if (!whole) {
@@ -722,7 +733,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ob[32];
-          tmem_ld32_sync(tO + c * 32, ob);
+          load_o(c, ob);
           if (row_ok) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -746,7 +757,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ob[32];
-          tmem_ld32_sync(tO + c * 32, ob);
+          load_o(c, ob);
           // (a row that saw no key: O may never have been written)
           float x[32];
 #pragma unroll
