@@ -37,8 +37,8 @@
 
 #include "fp4.cuh"
 #include "paged.cuh"
+#include "paged_fp4.cuh"
 #include "ptx.cuh"
-#include "tensor_map.h"
 
 namespace gb300 {
 namespace paged {
@@ -62,17 +62,6 @@ struct Cfg {
   static constexpr int RING = kWarps * NS * CELL;
   static constexpr int SMEM = RING + 512;
   static_assert(CELL % 128 == 0 && (D == 64 || CELL % 512 == 0), "swizzle atoms aligned");
-};
-
-// How the codes of a page reach shared memory: a tensor copy of `box` = 2^lg rows
-// of one head (rows x heads x pages; a dimension whose rows lie on one another
-// has its coordinate times 0), or, where no 8 rows are sure to share a page
-// (lg < 0), 16-byte copies.
-struct CodeMaps {
-  int lg;
-  int page_mul, head_mul;  // K; V's in the next two
-  int v_page_mul, v_head_mul;
-  int no_page, v_no_page;  // coordinates that read zeros
 };
 
 // Row of a 16-key group in which slot s (row of an operand fragment) keeps its
@@ -221,8 +210,8 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             mbar_arrive_expect_tx(&full[fill], static_cast<uint32_t>(boxes * 2 * C::ROW) << cm.lg);
           __syncwarp();
           if ((lane & ((1 << cm.lg) - 1)) == 0 && (lane >> cm.lg) < boxes) {
-            tma_load_4d(cell + lane * C::ROW, &tmK, &full[fill], 0, nx_row, kvh * cm.head_mul,
-                        own ? nx_page * cm.page_mul : cm.no_page);
+            tma_load_4d(cell + lane * C::ROW, &tmK, &full[fill], 0, nx_row, kvh * cm.k_head_mul,
+                        own ? nx_page * cm.k_page_mul : cm.k_no_page);
             tma_load_4d(cell + C::V_OFF + lane * C::ROW, &tmV, &full[fill], 0, nx_row,
                         kvh * cm.v_head_mul, own ? nx_page * cm.v_page_mul : cm.v_no_page);
           }
@@ -633,21 +622,6 @@ int unit_heads(const Args& a, int ctas) {
   return lg;
 }
 
-// The tensor map of one cache's codes (strides: page, head, row); a stride of 0
-// becomes an extent of 1.
-bool encode_codes(CUtensorMap* map, const Args& a, const void* base, const long long (&st)[3],
-                  int row_bytes, int lg, int* page_mul, int* head_mul, int* no_page) {
-  const bool flat_page = a.num_pages > 1 && st[0] == 0, flat_head = a.Hkv > 1 && st[1] == 0;
-  *page_mul = flat_page ? 0 : 1;
-  *head_mul = flat_head ? 0 : 1;
-  *no_page = flat_page ? 1 : a.num_pages;
-  auto s = [&](long long x) { return static_cast<uint64_t>(x > 0 ? x : row_bytes); };
-  return encode_tiled_4d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, row_bytes, a.page_size,
-                         flat_head ? 1 : a.Hkv, *no_page, 1, row_bytes, 1u << lg, s(st[2]),
-                         s(st[1]), s(st[0]),
-                         row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
 template <typename T, int D, int NT>
 sdpa_status_t launch(Args& a, const LaunchEnv& env) {
   auto kern = paged_fp4_decode_kernel<T, D, NT>;
@@ -657,18 +631,8 @@ sdpa_status_t launch(Args& a, const LaunchEnv& env) {
   const int lg_hw = unit_heads(a, a.nctas);
   if (!allow_smem<paged_fp4_decode_kernel<T, D, NT>>(smem)) return SDPA_ERR_CUDA;
   CUtensorMap tk = {}, tv = {};
-  CodeMaps cm = {};
-  cm.lg = std::min(box_log2(a.page_size), 5);
-  bool strides = a.num_pages > 0 && cm.lg >= 3;  // that a tensor map takes
-  for (int i = 0; i < 3; ++i)
-    strides = strides && a.ks[i] < (1LL << 40) && a.vs[i] < (1LL << 40);
-  // (rows that lie on one another: the same row for every key)
-  if (a.page_size > 1 && (a.ks[2] == 0 || a.vs[2] == 0)) strides = false;
-  if (!strides ||
-      !encode_codes(&tk, a, a.k, a.ks, D / 2, cm.lg, &cm.page_mul, &cm.head_mul, &cm.no_page) ||
-      !encode_codes(&tv, a, a.v, a.vs, D / 2, cm.lg, &cm.v_page_mul, &cm.v_head_mul,
-                    &cm.v_no_page))
-    cm.lg = -1;
+  const CodeMaps cm = encode_code_maps(
+      a, D / 2, 5, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, &tk, &tv);
   kern<<<a.nctas, kT, smem, env.stream>>>(tk, tv, a, cm, lg_hw);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   const int dtype = sizeof(T) == 4                      ? SDPA_F32

@@ -5,10 +5,10 @@
 //
 // The rows, the division of the work, the issue loop and the softmax are those
 // of paged_tc.cuh.  What differs:
-//  - Four warps widen the codes: a lane has a row of a 128-key tile, whose codes
-//    and scales its warp's asynchronous copies brought to a staging ring two
-//    tiles before, and writes it as fp16 where tcgen05.mma reads it (128-byte
-//    swizzle).  Code times scale is exact in fp16 (fp4.cuh).  Rows past the
+//  - A loader warp brings the codes of the 128-key tiles to a staging ring
+//    (tensor copies), and four warps widen them: a lane has a row of a tile,
+//    reads its scales a tile ahead and writes it as fp16 where tcgen05.mma
+//    reads it (128-byte swizzle).  Code times scale is exact in fp16 (fp4.cuh).  Rows past the
 //    length, or of a page that the table does not name, become zeros there.
 //  - Both products are in fp16 whatever the type of q.  The same four warps lay
 //    down the query tiles: fp16 rows as they are, bf16 ones times a power of two
@@ -30,6 +30,7 @@
 
 #include "fp4.cuh"
 #include "paged.cuh"
+#include "paged_fp4.cuh"
 #include "prefill_tc.cuh"
 
 namespace gb300 {
@@ -46,24 +47,25 @@ struct F4Cfg {
   static constexpr int NS = D == 64 ? 8 : NT == 2 || X2 ? 4 : 5;
   static constexpr int LA = NT == 2 ? 1 : 2;
   static constexpr int RING_OFF = NT * QN * TILE;
-  // staging: a warp's 32 rows of codes and scales, ST stages
+  // staging: a tile's codes, ST stages
   static constexpr int ROW = D / 2;
-  static constexpr int SC = D / 16;
+  static constexpr int SC = D / 16;  // bytes of a row's scales
   static constexpr int ST = 3;
-  static constexpr int STAGE = 32 * (ROW + SC);
+  static constexpr int STAGE = 128 * ROW;
   static constexpr int STAGE_OFF = RING_OFF + NS * TILE;
-  static constexpr int QF_OFF = STAGE_OFF + 4 * ST * STAGE;  // float[2][NT][128]
+  static constexpr int QF_OFF = STAGE_OFF + ST * STAGE;  // float[2][NT][128]
   static constexpr int BAR_OFF = QF_OFF + 2 * NT * 128 * 4;
-  // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain
-  static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1;
+  // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain,
+  // st_full[ST], st_empty[ST]
+  static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1 + 2 * ST;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int SOFT_WARPS = 4 * NT;
   static constexpr int WARPS = SOFT_WARPS + 8;
   static constexpr int THREADS = 32 * WARPS;
   // registers of a thread by warpgroup (their sum is the launch's)
-  static constexpr uint32_t SOFT_REGS = NT == 2 ? 184 : 232;
-  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 56 : 136;
-  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 88 : 136;
+  static constexpr uint32_t SOFT_REGS = NT == 2 ? 176 : 232;
+  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 80 : 136;
+  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 80 : 136;
   static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
   static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
   static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
@@ -71,7 +73,7 @@ struct F4Cfg {
       WALK_OFF + WARPS * static_cast<int>(sizeof(Walk<AttendUnits>));
   static constexpr int SMEM = UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(STAGE % 16 == 0 && STAGE_OFF % 128 == 0, "alignment");
+  static_assert(STAGE % 512 == 0 && STAGE_OFF % 512 == 0, "swizzle atoms aligned");
   static constexpr uint32_t s_col(int i) { return static_cast<uint32_t>(i * 128); }
   static constexpr uint32_t o_col(int t) { return static_cast<uint32_t>(256 + t * D); }
   static constexpr int SLOT = 128 * NT * (D + 2);  // floats of a partial result
@@ -129,15 +131,15 @@ struct Order {
   }
 };
 
-// 2^(s f - m) of 64 raw scores as fp16 pairs (X2: and what fp16 leaves of
+// 2^(s f - m) of N raw scores as fp16 pairs (X2: and what fp16 leaves of
 // them), added to rs.
-template <bool X2>
-__device__ __forceinline__ void weights64(const uint32_t (&s)[64], float f, float m, uint32_t* pk,
-                                          uint32_t* lo, float& rs) {
+template <bool X2, int N>
+__device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m, uint32_t* pk,
+                                        uint32_t* lo, float& rs) {
   const uint64_t F = f2_pack(f, f), NM = f2_pack(-m, -m);
   uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < N / 2; ++i) {
     const uint64_t X =
         f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), F, NM);
     float x0, x1;
@@ -156,7 +158,9 @@ __device__ __forceinline__ void weights64(const uint32_t (&s)[64], float f, floa
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
-    paged_fp4_tc_kernel(const Args a) {
+    paged_fp4_tc_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const Args a,
+                        const CodeMaps cm) {
   constexpr bool X2 = sizeof(T) == 4;
   using C = F4Cfg<D, NT, X2>;
   extern __shared__ uint8_t smem_raw[];
@@ -172,10 +176,12 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
   uint64_t* o_done = s_full + 2;
   uint64_t* pv_done = o_done + 2;
   uint64_t* drain = pv_done + 1;
+  uint64_t* st_full = drain + 1;
+  uint64_t* st_empty = st_full + C::ST;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   Share* sh = reinterpret_cast<Share*>(smem + C::SHARE_OFF);
-  constexpr int kMma = C::SOFT_WARPS, kHelp = kMma + 1, kWiden = kMma + 4;
+  constexpr int kMma = C::SOFT_WARPS, kHelp = kMma + 1, kLoad = kMma + 2, kWiden = kMma + 4;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -192,6 +198,10 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     }
     mbar_init(pv_done, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < C::ST; ++i) {
+      mbar_init(&st_full[i], cm.lg >= 0 ? 1 : 33);  // (or 32 lanes' copies as well)
+      mbar_init(&st_empty[i], 4);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -221,11 +231,13 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
   };
 
+  int fills = 0;  // loader: stages filled
+
   if (warp >= kWiden) {
     setmaxnreg_dec<C::WIDEN_REGS>();
     // -------------------------------------------------------------- widening
     const int w = warp - kWiden;
-    uint8_t* stage = smem + C::STAGE_OFF + w * C::ST * C::STAGE;
+    const uint8_t* stages = smem + C::STAGE_OFF;
     constexpr int P = C::ROW / 16;  // 16-byte pieces of a row
     int g = 0;                      // ring slots filled
     bool ok = true;
@@ -233,66 +245,43 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       const Unit u = *unit;
       const TileGeo tg = tile_geo<NT>(a, u);
       const int kvh = a.by_nsub.div(u.h), sub = a.by_nsub.mod(u.h);
-      const int* table = a.table + u.b * a.table_stride;
-      // Copies of a tile's rows w * 32 .. + 31 to the staging ring; the row's
-      // page was looked up a tile before.
-      Order<C::LA> ahead(tg.nmax), now(tg.nmax);
-      int k_page, k_row, v_page, v_row;  // of the next K tile's and the next V tile's row
-      auto lookup = [&](int j, int* page, int* row) {
-        const int key = (tg.s0 + j) * 128 + w * 32 + lane;
-        *page = -1;
-        *row = 0;
-        if (j < tg.nmax && key < tg.nk) {
-          const int i = a.by_page.div(key);
-          *row = key - i * a.page_size;
-          *page = table[i];
-        }
-      };
-      lookup(0, &k_page, &k_row);
-      v_page = k_page;
-      v_row = k_row;
-      int fill = 0, read = 0;  // stages
-      auto copy = [&]() {  // (every call commits one group of copies)
-        if (ahead.more()) {
-          const bool is_k = ahead.is_k();
-          const int page = is_k ? k_page : v_page, row = is_k ? k_row : v_row;
-          const bool named = page >= 0 && page < a.num_pages;
-          const int key = (tg.s0 + ahead.tile()) * 128 + w * 32 + lane;
-          if (!named && key < tg.nk) atomicExch(a.status, kStatusPageTable);
-          const long long* st = is_k ? a.ks : a.vs;
-          const long long* ss = is_k ? a.kss : a.vss;
-          const char* codes = static_cast<const char*>(is_k ? a.k : a.v);
-          const char* scales = is_k ? a.k_scales : a.v_scales;
-          const long long off = named ? page * st[0] + kvh * st[1] + row * st[2] : -1;
-          uint8_t* dst = stage + fill * C::STAGE;
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const int x = i * 32 + lane, r = x / P, c = x % P;
-            const long long o = __shfl_sync(0xffffffffu, off, r);
-            // (pieces swapped by row, so that a warp reads 32 rows' pieces
-            // without meeting a bank twice)
-            const int pc = P == 4 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             smem_addr(dst + r * C::ROW + pc * 16)),
-                         "l"(o >= 0 ? codes + o + c * 16 : codes), "r"(o >= 0 ? 16 : 0)
-                         : "memory");
+      // The scales of this lane's row, read a tile before they are needed, and
+      // its page, looked up two before.
+      Order<C::LA> order(tg.nmax), of_scales(tg.nmax), of_pages(tg.nmax);
+      uint32_t sb_next[D / 64];
+      int page = -1, row = 0;
+      auto lookup = [&]() {
+        const int key = (tg.s0 + of_pages.tile()) * 128 + w * 32 + lane;
+        page = -1;
+        if (of_pages.more()) {
+          if (key < tg.nk) {
+            const int i = a.by_page.div(key);
+            row = key - i * a.page_size;
+            page = a.table[u.b * a.table_stride + i];
           }
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
-                           smem_addr(dst + 32 * C::ROW + lane * C::SC)),
-                       "l"(named ? scales + page * ss[0] + kvh * ss[1] + row * ss[2] : scales),
-                       "n"(C::SC), "r"(named ? C::SC : 0)
-                       : "memory");
-          ahead.next();
-          if (is_k)
-            lookup(ahead.k, &k_page, &k_row);
-          else
-            lookup(ahead.v, &v_page, &v_row);
-          fill = fill + 1 == C::ST ? 0 : fill + 1;
+          of_pages.next();
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-#pragma unroll 1
-      for (int i = 0; i < C::ST - 1; ++i) copy();
+      auto fetch_scales = [&]() {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) sb_next[i] = 0;
+        if (page >= 0 && page < a.num_pages) {
+          const bool is_k = of_scales.is_k();
+          const char* src = (is_k ? a.k_scales : a.v_scales) + page * (is_k ? a.kss[0] : a.vss[0]) +
+                            kvh * (is_k ? a.kss[1] : a.vss[1]) + row * (is_k ? a.kss[2] : a.vss[2]);
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            sb_next[0] = y.x;
+            sb_next[1] = y.y;
+          } else {
+            sb_next[0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+        }
+        of_scales.next();
+        lookup();
+      };
+      lookup();
+      fetch_scales();
       // ------------------------------------------------------- query tiles
       {
         const float gain = a.k_gain ? a.k_gain[kvh] : 1.f;
@@ -374,30 +363,29 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
         if (lane == 0) mbar_arrive(q_full);
       }
       // ------------------------------------------------------- key tiles
-      for (; now.more(); now.next()) {
-        copy();
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::ST - 1) : "memory");
+      for (; order.more(); order.next()) {
+        uint32_t sb[D / 64];  // the row's scales, four a word
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) sb[i] = sb_next[i];
+        fetch_scales();
+        const int x = g % C::ST;
         const int s = g % C::NS, use = g / C::NS;
         ok = __all_sync(0xffffffffu,
-                        ok && (use == 0 || mbar_wait(&empty[s], (use - 1) & 1, wc)));
-        __syncwarp();  // (every lane's copies have landed)
-        const uint8_t* src = stage + read * C::STAGE;
-        read = read + 1 == C::ST ? 0 : read + 1;
+                        ok && mbar_wait(&st_full[x], (g / C::ST) & 1, wc) &&
+                            (use == 0 || mbar_wait(&empty[s], (use - 1) & 1, wc)));
         const int r = w * 32 + lane;
+        const uint8_t* src = stages + x * C::STAGE + r * C::ROW;
         uint8_t* dst = sRing + s * C::TILE + (r >> 3) * (C::CB * 1024) + (r & 7) * 128;
-        uint32_t sb[D / 64];  // the row's scales, four a word
-        if constexpr (D == 128) {
-          const uint2 x = *reinterpret_cast<const uint2*>(src + 32 * C::ROW + lane * C::SC);
-          sb[0] = x.x;
-          sb[1] = x.y;
-        } else {
-          sb[0] = *reinterpret_cast<const uint32_t*>(src + 32 * C::ROW + lane * C::SC);
+        uint4 codes[P];
+#pragma unroll
+        for (int c = 0; c < P; ++c) {  // (pieces swapped by row: see the maps' swizzle)
+          const int pc = P == 4 ? c ^ ((lane >> 1) & 3) : c ^ ((lane >> 2) & 1);
+          codes[c] = *reinterpret_cast<const uint4*>(src + pc * 16);
         }
         if (ok) {
 #pragma unroll
           for (int c = 0; c < P; ++c) {  // 32 codes, two scales
-            const int pc = P == 4 ? c ^ ((lane >> 1) & 3) : c ^ ((lane >> 2) & 1);
-            const uint4 x = *reinterpret_cast<const uint4*>(src + lane * C::ROW + pc * 16);
+            const uint4 x = codes[c];
             const __half2 sc = fp4::as_half2(fp4::scales_f16(sb[c >> 1] >> (16 * (c & 1))));
             const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
             const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
@@ -416,10 +404,12 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        if (lane == 0) {
+          mbar_arrive(&full[s]);
+          mbar_arrive(&st_empty[x]);
+        }
         ++g;
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else if (warp >= C::SOFT_WARPS) {
     setmaxnreg_dec<C::CONTROL_REGS>();
@@ -549,6 +539,107 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       mma_commit_elect(drain, 1u);
       if (lane == 0) drain_wait(drain, 0, kDrainNs);
       __syncwarp();
+    } else if (warp == kLoad) {
+      // ---------------------------------------------------------- loader
+      // Codes of the tiles in ring order to the staging ring.  Boxes past the
+      // length are not loaded: scales are zero there, so whatever codes a stage
+      // holds widen to zero.
+      bool ok = true;
+      int g = 0;
+      while (next()) {
+        const Unit u = *unit;
+        const TileGeo tg = tile_geo<NT>(a, u);
+        const int kvh = a.by_nsub.div(u.h);
+        const int* table = a.table + u.b * a.table_stride;
+        struct Box {
+          int page, row;  // as looked up (row -1: past the length); checked():
+        };                // page -1 past the length, -2 not the cache's
+        const int lg = max(cm.lg, 0);
+        const int nbox = cm.lg < 0 ? 0 : 128 >> lg;
+        auto lookup = [&](int j) {  // box `lane` of key tile j
+          Box x{0, -1};
+          const int key = (tg.s0 + j) * 128 + (lane << lg);
+          if (j < tg.nmax && lane < nbox && key < tg.nk) {
+            const int i = a.by_page.div(key);
+            x.row = key - i * a.page_size;
+            x.page = table[i];
+          }
+          return x;
+        };
+        auto checked = [&](Box x) {
+          if (x.row < 0) {
+            x.page = -1;
+          } else if (x.page < 0 || x.page >= a.num_pages) {
+            atomicExch(a.status, kStatusPageTable);
+            x.page = -2;
+          }
+          return x;
+        };
+        auto load = [&](bool is_k, int j, const Box& x) {
+          const int s = g % C::ST, use = g / C::ST;
+          ok = __all_sync(0xffffffffu,
+                          ok && (use == 0 || mbar_wait(&st_empty[s], (use - 1) & 1, wc)));
+          if (!ok) return;
+          uint8_t* dst = smem + C::STAGE_OFF + s * C::STAGE;
+          const int key0 = (tg.s0 + j) * 128;
+          if (cm.lg >= 0) {
+            const int boxes = min(nbox, (tg.nk - key0 + (1 << lg) - 1) >> lg);
+            if (lane == 0)
+              mbar_arrive_expect_tx(&st_full[s], static_cast<uint32_t>(boxes * C::ROW) << lg);
+            __syncwarp();
+            if (x.page != -1)
+              tma_load_4d(dst + (lane * C::ROW << lg), is_k ? &tmK : &tmV, &st_full[s], 0, x.row,
+                          kvh * (is_k ? cm.k_head_mul : cm.v_head_mul),
+                          x.page < 0 ? (is_k ? cm.k_no_page : cm.v_no_page)
+                                     : x.page * (is_k ? cm.k_page_mul : cm.v_page_mul));
+          } else {
+            const char* codes = static_cast<const char*>(is_k ? a.k : a.v);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 32 + lane, key = key0 + r;
+              Box y{0, -1};
+              if (key < tg.nk) {
+                const int n = a.by_page.div(key);
+                y.row = key - n * a.page_size;
+                y.page = table[n];
+              }
+              y = checked(y);
+              const char* src = y.page < 0 ? codes
+                                           : codes + y.page * (is_k ? a.ks[0] : a.vs[0]) +
+                                                 kvh * (is_k ? a.ks[1] : a.vs[1]) +
+                                                 y.row * (is_k ? a.ks[2] : a.vs[2]);
+#pragma unroll 1
+              for (int c = 0; c < C::ROW / 16; ++c) {
+                const int pc = C::ROW == 64 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 smem_addr(dst + r * C::ROW + pc * 16)),
+                             "l"(src + (y.page < 0 ? 0 : c * 16)), "r"(y.page < 0 ? 0 : 16)
+                             : "memory");
+              }
+            }
+            if (lane == 0) mbar_arrive(&st_full[s]);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                             smem_addr(&st_full[s]))
+                         : "memory");
+          }
+          fills = ++g;
+        };
+        Box bx[C::LA + 1];  // boxes of tiles j .. j + LA
+#pragma unroll
+        for (int i = 0; i <= C::LA; ++i) bx[i] = lookup(i);
+#pragma unroll
+        for (int i = 0; i < C::LA; ++i)
+          if (ok && i < tg.nmax) load(true, i, checked(bx[i]));
+        for (int j = 0; ok && j < tg.nmax; ++j) {
+          const Box nx = lookup(j + C::LA + 1);
+          load(false, j, checked(bx[0]));
+          if (ok && j + C::LA < tg.nmax) load(true, j + C::LA, checked(bx[C::LA]));
+#pragma unroll
+          for (int i = 0; i < C::LA; ++i) bx[i] = bx[i + 1];
+          bx[C::LA] = nx;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kHelp) {
       // ------------------------------------------------------ stage helper
       // Waits for the tiles that the MMA warp's next products read and meets
@@ -614,16 +705,26 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
             if (j == 0) f = sQf[((it & 1) * NT + t) * 128 + r];
             const int vis = limit - j * 128;  // visible keys of the row in this tile
             const bool edge = __any_sync(0xffffffffu, vis < 128);
-            uint32_t s[64];
-            auto half = [&](int c) {  // scores c * 64 .. + 63
+            // (the weights take the scores' registers; X2 has none left for
+            // all of them at once, and a moved reference reads them again)
+            constexpr int N = X2 ? 64 : 128;
+            uint32_t s[N];
+            auto scores = [&](int c) {  // scores c * N .. + N - 1
               __syncwarp();
-              tmem_ld2x32_sync(tS + c * 64, tS + c * 64 + 32,
-                               *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
-                               *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+              if constexpr (X2)
+                tmem_ld2x32_sync(tS + c * 64, tS + c * 64 + 32,
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+              else
+                tmem_ld4x32_sync(tS, tS + 32, tS + 64, tS + 96,
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[0]),
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[32]),
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[N - 64]),
+                                 *reinterpret_cast<uint32_t(*)[32]>(&s[N - 32]));
               if (edge) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  if (c * 64 + i >= vis) s[i] = 0xff800000u;  // -inf
+                for (int i = 0; i < N; ++i)
+                  if (c * N + i >= vis) s[i] = 0xff800000u;  // -inf
               }
             };
             float alpha = 1.f, rs = 0.f;
@@ -631,18 +732,18 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
             bool resc = !(m > -INFINITY);
             if (!__all_sync(0xffffffffu, resc)) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                half(c);
-                weights64<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
-                              rs);
+              for (int c = 0; c < 128 / N; ++c) {
+                scores(c);
+                weights<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
+                            rs);
               }
               resc = resc || !(rs <= kFusedSumLimit);
             }
             if (__any_sync(0xffffffffu, resc)) {
               float mx = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                half(c);
+              for (int c = 0; c < 128 / N; ++c) {
+                scores(c);
                 mx = fmaxf(mx, row_max_raw(s));
               }
               mx = mx * f - kHead;  // -inf: no visible key
@@ -652,10 +753,10 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
               }
               rs = 0.f;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                half(c);
-                weights64<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
-                              rs);
+              for (int c = 0; c < 128 / N; ++c) {
+                scores(c);
+                weights<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
+                            rs);
               }
             }
             __syncwarp();
@@ -792,6 +893,11 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (warp == kLoad && lane == 0 && *abort_flag) {
+    // a role gave up: every copy that was asked for lands before the CTA exits
+    for (int i = max(0, fills - C::ST); i < fills; ++i)
+      drain_wait(&st_full[i % C::ST], static_cast<uint32_t>((i / C::ST) & 1), kDrainNs);
+  }
 }
 
 template <typename T, int D, int NT>
@@ -817,6 +923,9 @@ sdpa_status_t launch_f4(Args& a, const LaunchEnv& env) {
     ready.fetch_or(bit);
   }
   a.nctas = a.max_ctas < env.num_sms ? a.max_ctas : env.num_sms;
+  CUtensorMap tk = {}, tv = {};
+  const CodeMaps cm = encode_code_maps(
+      a, D / 2, 7, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, &tk, &tv);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -827,7 +936,7 @@ sdpa_status_t launch_f4(Args& a, const LaunchEnv& env) {
   cfg.stream = env.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a, cm) != cudaSuccess) return SDPA_ERR_CUDA;
   const int dtype = sizeof(T) == 4                      ? SDPA_F32
                     : std::is_same<T, __half>::value ? SDPA_F16
                                                      : SDPA_BF16;
