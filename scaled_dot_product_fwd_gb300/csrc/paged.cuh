@@ -476,7 +476,6 @@ struct Boxes {
 // Launchers (host side).  `a` holds the problem and the workspace; the
 // attention and score launchers fill in the tile's rows (gu, nsub, w).
 sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
-sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
 // Rows of a tile of the 4-bit cache's few-row kernel for this call (8 or 16; 0:
 // the calls of more rows).
 int paged_fp4_decode_rows(const paged::Args& a);
@@ -501,7 +500,7 @@ sdpa_status_t launch_paged_decode_tc(const paged::Args& a, int head_dim, int dty
 sdpa_status_t launch_paged_scores_tc(paged::Args a, int head_dim, int dtype,
                                      const LaunchEnv& env);
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
-                                 int tiles, cudaStream_t stream, bool by_head = false);
+                                 int tiles, cudaStream_t stream);
 sdpa_status_t launch_paged_scores_merge(const paged::Args& a, int tile_keys,
                                         cudaStream_t stream);
 sdpa_status_t launch_paged_write(const paged::Args& a, int row_bytes, const void* k,

@@ -96,6 +96,37 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// The same with nothing to add to.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Issued by one lane of a warp in step: a tensor copy, and the bytes that a
+// barrier's phase waits for (operands the same in every lane; a branch on the
+// lane would have the copy issued in a loop over lanes).
+__device__ __forceinline__ void tma_load_4d_elect(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                  int c1, int c2, int c3) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}\n" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect_elect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(bytes)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t mul2(uint32_t x, __half2 s) {
   return fp4::as_u32(__hmul2(fp4::as_half2(x), s));
 }
@@ -110,6 +141,15 @@ __device__ __forceinline__ float wide(__half x) { return __half2float(x); }
 __device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put4(float* p, const float4& v) {
   *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void put2(float* p, const float2& v) {
+  *reinterpret_cast<float2*>(p) = v;
+}
+__device__ __forceinline__ void put2(__half* p, const float2& v) {
+  *reinterpret_cast<__half2*>(p) = __floats2half2_rn(v.x, v.y);
+}
+__device__ __forceinline__ void put2(__nv_bfloat16* p, const float2& v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 __device__ __forceinline__ void put4(__half* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) =
@@ -206,14 +246,16 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         if (cm.lg >= 0) {
           const int keys = head_ok ? u.s.nk - ((step << lg_tile) + sub * 32) : 0;
           const int boxes = keys <= 0 ? 0 : min(32 >> cm.lg, (keys + (1 << cm.lg) - 1) >> cm.lg);
-          if (lane == 0)
-            mbar_arrive_expect_tx(&full[fill], static_cast<uint32_t>(boxes * 2 * C::ROW) << cm.lg);
-          __syncwarp();
-          if ((lane & ((1 << cm.lg) - 1)) == 0 && (lane >> cm.lg) < boxes) {
-            tma_load_4d(cell + lane * C::ROW, &tmK, &full[fill], 0, nx_row, kvh * cm.k_head_mul,
-                        own ? nx_page * cm.k_page_mul : cm.k_no_page);
-            tma_load_4d(cell + C::V_OFF + lane * C::ROW, &tmV, &full[fill], 0, nx_row,
-                        kvh * cm.v_head_mul, own ? nx_page * cm.v_page_mul : cm.v_no_page);
+          mbar_expect_elect(&full[fill], static_cast<uint32_t>(boxes * 2 * C::ROW) << cm.lg);
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i) {
+            const int page = __shfl_sync(0xffffffffu, nx_page, i << cm.lg);
+            const int row = __shfl_sync(0xffffffffu, nx_row, i << cm.lg);
+            uint8_t* dst = cell + (i << cm.lg) * C::ROW;
+            tma_load_4d_elect(dst, &tmK, &full[fill], row, kvh * cm.k_head_mul,
+                              page >= 0 ? page * cm.k_page_mul : cm.k_no_page);
+            tma_load_4d_elect(dst + C::V_OFF, &tmV, &full[fill], row, kvh * cm.v_head_mul,
+                              page >= 0 ? page * cm.v_page_mul : cm.v_no_page);
           }
         } else {
           constexpr int P = C::ROW / 16;  // 16-byte pieces of a row
@@ -340,7 +382,7 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll 1
     for (int step = u.s0; step < u.s1; ++step) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::NS - 2) : "memory");
-      ok_wait = __all_sync(0xffffffffu, ok_wait && mbar_wait(&full[read], read_par, wc));
+      ok_wait = ok_wait && mbar_wait(&full[read], read_par, wc);
       __syncwarp();  // every lane's copies of this step have landed, and the last step is read
       copy(step + C::NS - 1);
       const int key0 = (step << lg_tile) + sub * 32;
@@ -378,16 +420,6 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
                   __low2half2(fp4::as_half2(fp4::scales_f16(st[ks_off + row * C::SC])));
             }
           }
-        // two sums each, so that products wait less for one another
-        float z[2][2][NT][4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) z[x][kg][n][k] = 0.f;
 #pragma unroll
         for (int i = 0; i < KW; ++i)
 #pragma unroll
@@ -396,20 +428,18 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             widen4(w[kg][0][i], sc[kg][0][i >> 1], x);
             widen4(w[kg][1][i], sc[kg][1][i >> 1], y);
 #pragma unroll
-            for (int p = 0; p < QN; ++p)
+            for (int p = QN - 1; p >= 0; --p)  // (the small part first)
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma16816(z[0][kg][n], x[0], y[0], x[1], y[1], q[p][n][2 * i][0], q[p][n][2 * i][1]);
-                mma16816(z[1][kg][n], x[2], y[2], x[3], y[3], q[p][n][2 * i + 1][0],
+                if (i == 0 && p == QN - 1)
+                  mma16816_first(s[kg][n], x[0], y[0], x[1], y[1], q[p][n][0][0], q[p][n][0][1]);
+                else
+                  mma16816(s[kg][n], x[0], y[0], x[1], y[1], q[p][n][2 * i][0],
+                           q[p][n][2 * i][1]);
+                mma16816(s[kg][n], x[2], y[2], x[3], y[3], q[p][n][2 * i + 1][0],
                          q[p][n][2 * i + 1][1]);
               }
           }
-#pragma unroll
-        for (int kg = 0; kg < 2; ++kg)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[kg][n][k] = z[0][kg][n][k] + z[1][kg][n][k];
       }
       // exponents of the weights, x - mb; element k of a fragment: slot g + 8 (k / 2), column k & 1
       bool over = false;
@@ -609,14 +639,155 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     }
 }
 
+constexpr int kMaxUnits = 1024;  // CTAs of a call, at most
+
+// Joins the partial results of the units that CTAs began and did not finish
+// (their descriptors are compacted first): M = max of the m's, weights 2^(m -
+// M), in the order of the pieces.  Bound by the latency of its three dependent
+// loads, so a row is spread over as many warps of a block as leave all warps of
+// the grid with at most one row: 32 rows of 38 pieces 19 us with a block a unit
+// and 16th of its rows, 4 so.
+template <typename T, int D>
+__global__ void __launch_bounds__(kT) paged_fp4_merge_kernel(const Args a, const int nr,
+                                                             const int lg_hw) {
+  constexpr int E = D / 32;  // columns of a lane
+  __shared__ short s_unit[kMaxUnits];
+  __shared__ bool s_cut[kMaxUnits];
+  __shared__ int s_count;
+  __shared__ float s_ml[kWarps][2], s_o[kWarps][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  for (int c = tid; c < a.nctas; c += kT) s_cut[c] = a.desc[c * kDesc] != 0;
+  __syncthreads();
+  if (warp == 0) {  // (the same order in every block)
+    int count = 0;
+    for (int c0 = 0; c0 < a.nctas; c0 += 32) {
+      const int c = c0 + lane;
+      const bool cut = c < a.nctas && s_cut[c];
+      const uint32_t all = __ballot_sync(0xffffffffu, cut);
+      if (cut) s_unit[count + __popc(all & ((1u << lane) - 1))] = static_cast<short>(c);
+      count += __popc(all);
+    }
+    if (lane == 0) s_count = count;
+  }
+  __syncthreads();
+  const int live = a.gu * a.w;  // rows of a head's tile
+  const int per = live << lg_hw;
+  const int tasks = s_count * per, warps = gridDim.x * kWarps;
+  int lg = 3;  // log2 of the warps of a row
+  while (lg > 0 && (tasks << lg) > warps) --lg;
+  const int part = warp & ((1 << lg) - 1), step = 1 << lg;
+  const int rows = nr << lg_hw;
+  const size_t slot_floats = static_cast<size_t>(rows) * (D + 2);
+  for (int base = blockIdx.x * (kWarps >> lg); base < tasks; base += warps >> lg) {
+    const int task = base + (warp >> lg);
+    bool ok = task < tasks;
+    int c = 0, row = 0, tok = 0, hq = 0, head = 0, n = 0;
+    const int* d = a.desc;
+    if (ok) {
+      const int unit = task / per, x = task - unit * per;
+      c = s_unit[unit];
+      d = a.desc + c * kDesc;
+      n = d[0];
+      const int hi = x / live, r = x - hi * live;
+      row = hi * nr + r;
+      const int g = a.by_gu.div(r), e = a.by_nsub.mod(d[2]) * a.gu + r - g * a.gu;
+      head = (a.by_nsub.div(d[2]) << lg_hw) + hi;
+      tok = d[3] * a.w + g;
+      hq = head * a.G + e;
+      ok = tok < d[5] && e < a.G && head < a.Hkv;
+    }
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+    if (ok) {
+      auto piece = [&](int p) {
+        return a.ws +
+               (p == 0 ? static_cast<size_t>(c * 2 + 1) : static_cast<size_t>((c + p) * 2)) *
+                   slot_floats;
+      };
+      for (int p0 = part; p0 < n; p0 += 32 * step) {  // 32 pieces of this warp's
+        const int mine = p0 + lane * step;
+        float m = -INFINITY, l = 0.f;
+        if (mine < n) {
+          const float* s = piece(mine);
+          m = s[static_cast<size_t>(rows) * D + row];
+          l = s[static_cast<size_t>(rows) * (D + 1) + row];
+        }
+        if (l == 0.f) m = -INFINITY;  // (a piece whose keys the row does not see)
+        float mn = m;
+#pragma unroll
+        for (int i = 16; i >= 1; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, i));
+        mn = fmaxf(mn, M);
+        const float fall = M == -INFINITY ? 0.f : ex2(M - mn);
+        M = mn;
+        const float wgt = l != 0.f ? ex2(m - (mn == -INFINITY ? 0.f : mn)) : 0.f;
+        L *= fall;
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] *= fall;
+        const int count = min(32, (n - p0 + step - 1) >> lg);
+#pragma unroll 5
+        for (int k = 0; k < count; ++k) {
+          const float w = __shfl_sync(0xffffffffu, wgt, k), lk = __shfl_sync(0xffffffffu, l, k);
+          if (lk != 0.f) {
+            const float* s = piece(p0 + k * step) + static_cast<size_t>(row) * D + lane * E;
+            L = fmaf(lk, w, L);
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(s + i);
+              acc[i] = fmaf(v.x, w, acc[i]);
+              acc[i + 1] = fmaf(v.y, w, acc[i + 1]);
+            }
+          }
+        }
+      }
+    }
+    if (lg > 0) {  // the parts of a row meet
+      if (lane == 0) {
+        s_ml[warp][0] = M;
+        s_ml[warp][1] = L;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = acc[i];
+      __syncthreads();
+      if (part == 0) {
+        for (int w = 1; w < step; ++w) {
+          const float m = s_ml[warp + w][0], l = s_ml[warp + w][1];
+          if (l == 0.f) continue;
+          const float mn = fmaxf(M, m);
+          const float f = M == -INFINITY ? 0.f : ex2(M - mn), z = ex2(m - (mn == -INFINITY ? 0.f : mn));
+          L = L * f + l * z;
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + s_o[warp + w][lane * E + i] * z;
+          M = mn;
+        }
+      }
+    }
+    if (ok && part == 0) {
+      const bool any = L != 0.f;
+      float f = 1.f;
+      if (a.sinks) f = add_sink(a.sinks[hq], M, L);
+      const float inv = any ? f / L : 0.f;
+      const long long q = d[4] + tok;
+      T* o = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1] + lane * E;
+      if constexpr (E == 4) {
+        put4(o, make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
+      } else {
+        put2(o, make_float2(acc[0] * inv, acc[1] * inv));
+      }
+      if (a.lse && lane == 0) a.lse[q * a.Hq + hq] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    }
+    if (lg > 0) __syncthreads();  // (the meeting place is read)
+  }
+}
+
 // Kv heads of a unit (log2).  Where a token's heads lie next to one another,
-// a run of up to 8 heads' rows is read as one piece of memory (8 x 32768 keys,
-// 8 kv heads: see the top of the file); where a head's tokens do, one.
-// A unit of more pieces than the merge takes at once costs more than that saves.
-int unit_heads(const Args& a, int ctas) {
-  int lg = 3;
+// a run of up to 4 heads' rows is read as one piece of memory (8 x 32768 keys of
+// 8 kv heads, 1, 2, 4 and 8 heads a unit: 128, 88, 81 and 87 us); where a head's
+// tokens do, one.
+int unit_heads(const Args& a) {
+  int lg = 2;
   if (a.ks[1] >= a.ks[2] && a.page_size > 1) return 0;
-  while (lg > 0 && (static_cast<long long>(a.B) * a.Hkv >> lg) * 12 < ctas) --lg;
   // (the last unit's missing heads leave warps idle)
   while (lg > 0 && (a.Hkv >> lg == 0 || (a.Hkv % (1 << lg) != 0 && a.Hkv < (4 << lg)))) --lg;
   return lg;
@@ -628,17 +799,26 @@ sdpa_status_t launch(Args& a, const LaunchEnv& env) {
   constexpr int smem = std::max(Cfg<D>::SMEM, kWarps * 8 * NT * D * 4 + 512);
   fit_rows(a, 8 * NT);
   a.nctas = std::min(a.max_ctas, (NT == 1 && sizeof(T) == 2 ? 2 : 1) * env.num_sms);
-  const int lg_hw = unit_heads(a, a.nctas);
+  if (a.nctas > kMaxUnits) a.nctas = kMaxUnits;
+  const int lg_hw = unit_heads(a);
   if (!allow_smem<paged_fp4_decode_kernel<T, D, NT>>(smem)) return SDPA_ERR_CUDA;
   CUtensorMap tk = {}, tv = {};
   const CodeMaps cm = encode_code_maps(
       a, D / 2, 5, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, &tk, &tv);
   kern<<<a.nctas, kT, smem, env.stream>>>(tk, tv, a, cm, lg_hw);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
-  const int dtype = sizeof(T) == 4                      ? SDPA_F32
-                    : std::is_same<T, __half>::value ? SDPA_F16
-                                                     : SDPA_BF16;
-  return launch_paged_merge(a, D, dtype, 8 * NT, 1 << lg_hw, env.stream, true);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * env.num_sms));
+  cfg.blockDim = dim3(kT);
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_fp4_merge_kernel<T, D>, a, 8 * NT, lg_hw) == cudaSuccess
+             ? SDPA_OK
+             : SDPA_ERR_CUDA;
 }
 
 template <typename T>

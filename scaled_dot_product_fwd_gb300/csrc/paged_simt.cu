@@ -27,15 +27,12 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "fp4.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
 namespace gb300 {
 namespace paged {
 namespace {
-
-struct Fp4 {};  // the element of a 4-bit cache
 
 constexpr int kT = 256;   // threads of a CTA
 constexpr int kKT = 64;   // keys of a tile
@@ -94,38 +91,6 @@ __device__ void load_rows(const void* base, const long long* off, float* dst, in
     const int r = i / C, c = (i % C) * N;
     const long long o = off[r];
     widen16<T>(dst + r * pitch + c, o >= 0 ? static_cast<const T*>(base) + o + c : nullptr);
-  }
-}
-
-// The rows of a 4-bit cache tile as fp32: a thread takes the 16 codes of a
-// scale.  `codes`, `scales`: the kv head's; off: page and row (-1: none).
-template <int D>
-__device__ void load_rows_fp4(const char* codes, const char* scales, const long long* st,
-                              const long long* ss, const int2* off, float gain, float* dst,
-                              int pitch) {
-  constexpr int C = D / 16;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < kKT * C; i += kT) {
-    const int r = i / C, c = i % C;
-    const int2 at = off[r];
-    float* x = dst + r * pitch + 16 * c;
-    uint2 w = make_uint2(0, 0);
-    uint32_t sb = 0;
-    if (at.x >= 0) {
-      w = *reinterpret_cast<const uint2*>(codes + at.x * st[0] + at.y * st[2] + 8 * c);
-      sb = static_cast<uint8_t>(scales[at.x * ss[0] + at.y * ss[2] + c]);
-    }
-    const float g = __low2float(fp4::as_half2(fp4::scales_f16(sb)));
-    uint32_t f[8];
-    fp4::codes_f16(w.x, reinterpret_cast<uint32_t(&)[4]>(f[0]));
-    fp4::codes_f16(w.y, reinterpret_cast<uint32_t(&)[4]>(f[4]));
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float2 a = __half22float2(fp4::as_half2(f[k]));
-      const float2 b = __half22float2(fp4::as_half2(f[k + 1]));
-      *reinterpret_cast<float4*>(x + 2 * k) =
-          make_float4(a.x * g * gain, a.y * g * gain, b.x * g * gain, b.y * g * gain);
-    }
   }
 }
 
@@ -195,9 +160,8 @@ __device__ __forceinline__ void scores_tile(const float* sQ, const float* sK, in
 // fp32 tiles are double-buffered (copies of the next beside the arithmetic on
 // this one)
 template <typename T, int D, int RM>
-constexpr int attend_smem() {  // T: the cache's
-  return (RM * D + (std::is_same<T, float>::value ? 2 : 1) * kKT * (2 * D + 4) + RM * (kKT + 4)) *
-         4;
+constexpr int attend_smem() {
+  return (RM * D + (sizeof(T) == 4 ? 2 : 1) * kKT * (2 * D + 4) + RM * (kKT + 4)) * 4;
 }
 
 // CTAs an SM: what the shared memory and the registers of a tile allow (one of
@@ -212,17 +176,15 @@ constexpr int scores_ctas() {
   return RM == 16 ? 4 : D == 64 ? 3 : 2;
 }
 
-// T: the type of q and o, CT: the cache's.
-template <typename T, int D, int RM, typename CT = T>
-__global__ void __launch_bounds__(kT, attend_ctas<CT, D, RM>()) paged_simt_kernel(const Args a) {
+template <typename T, int D, int RM>
+__global__ void __launch_bounds__(kT, attend_ctas<T, D, RM>()) paged_simt_kernel(const Args a) {
   constexpr int RPT = RM / 16;
   constexpr int CG = D / 64;  // float4 column groups of a thread
   constexpr int kSlot = RM * (D + 2);
   extern __shared__ float smem[];
   float* sQ = smem;
   float* sK = sQ + RM * D;
-  constexpr bool kAsync = std::is_same<CT, float>::value;
-  constexpr bool kFp4 = std::is_same<CT, Fp4>::value;
+  constexpr bool kAsync = sizeof(T) == 4;
   constexpr int kTile = kKT * (2 * D + 4);  // a K and a V tile
   float* sP = sK + (kAsync ? 2 : 1) * kTile;
   __shared__ long long off_k[2][kKT], off_v[2][kKT];
@@ -241,14 +203,7 @@ __global__ void __launch_bounds__(kT, attend_ctas<CT, D, RM>()) paged_simt_kerne
     const int tok0 = u.j * a.w;
     __syncthreads();  // the previous unit's tiles are read
     load_queries<T, D, RM>(a, u.s, tok0, kvh, sub, sQ);
-    int2* at = reinterpret_cast<int2*>(off_k);  // (4-bit cache) pages and rows of a tile
-    auto places = [&](int key0) {
-      if (tid < kKT) {
-        const int key = key0 + tid;
-        at[tid] = make_int2(key < u.s.nk ? page_of(a, u.b, key) : -1, a.by_page.mod(key));
-      }
-    };
-    if constexpr (!kFp4) row_offsets(a, u.b, kvh, u.s0 * kKT, u.s.nk, off_k[0], off_v[0]);
+    row_offsets(a, u.b, kvh, u.s0 * kKT, u.s.nk, off_k[0], off_v[0]);
     __syncthreads();
     int limit[RPT];  // keys below it are visible to the row
     float m[RPT], l[RPT], o[RPT][CG][4];
@@ -286,17 +241,6 @@ __global__ void __launch_bounds__(kT, attend_ctas<CT, D, RM>()) paged_simt_kerne
         if (t + 1 < u.s1) copy_tile(par ^ 1);
         if (t + 2 < u.s1)
           row_offsets(a, u.b, kvh, key0 + 2 * kKT, u.s.nk, off_k[par], off_v[par]);
-      } else if constexpr (kFp4) {
-        if (t > u.s0) __syncthreads();
-        places(key0);
-        __syncthreads();
-        load_rows_fp4<D>(static_cast<const char*>(a.k) + kvh * a.ks[1],
-                         a.k_scales + kvh * a.kss[1], a.ks, a.kss, at,
-                         a.k_gain ? a.k_gain[kvh] : 1.f, sK, D + 4);
-        load_rows_fp4<D>(static_cast<const char*>(a.v) + kvh * a.vs[1],
-                         a.v_scales + kvh * a.vss[1], a.vs, a.vss, at,
-                         a.v_gain ? a.v_gain[kvh] : 1.f, sK + kKT * (D + 4), D);
-        __syncthreads();
       } else {
         if (t > u.s0) __syncthreads();
         load_rows<T, D>(a.k, off_k[par], sK, D + 4);
@@ -434,7 +378,7 @@ struct MergeVec<64> {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4)
-    paged_merge_kernel(const Args a, int tile_rows, int tiles, bool by_head) {
+    paged_merge_kernel(const Args a, int tile_rows, int tiles) {
   using V = typename MergeVec<D>::V;
   constexpr int E = D / 32;  // columns of a lane
   griddep_wait();
@@ -443,8 +387,7 @@ __global__ void __launch_bounds__(256, 4)
   const int n = d[0];
   if (n == 0) return;
   const int b_h = d[2], j = d[3], q0 = d[4], nq = d[5];
-  // the unit's tiles are runs of tokens, or (by_head) consecutive kv heads
-  const int kvh = a.by_nsub.div(b_h) * (by_head ? tiles : 1), sub = a.by_nsub.mod(b_h);
+  const int kvh = a.by_nsub.div(b_h), sub = a.by_nsub.mod(b_h);
   const int rows = tile_rows * tiles;
   const size_t slot_floats = static_cast<size_t>(rows) * (D + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -456,10 +399,9 @@ __global__ void __launch_bounds__(256, 4)
   auto locate = [&](int rr, int* tok, int* head) {
     const int t = rr >= tile_rows ? rr / tile_rows : 0, r = rr - t * tile_rows;
     const int g = a.by_gu.div(r), e = sub * a.gu + r - g * a.gu;
-    *tok = (by_head ? j : j * tiles + t) * a.w + g;
-    const int h = by_head ? kvh + t : kvh;
-    *head = h * a.G + e;
-    return rr < rows && g < a.w && *tok < nq && e < a.G && h < a.Hkv;
+    *tok = (j * tiles + t) * a.w + g;
+    *head = kvh * a.G + e;
+    return rr < rows && g < a.w && *tok < nq && e < a.G;
   };
   // O, LSE of a row from its joined accumulator
   auto finish = [&](int tok, int hq, float M, float L, const float (&acc)[E]) {
@@ -718,19 +660,16 @@ sdpa_status_t start(Args& a, int smem, int ctas, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
-template <typename T, int D, typename CT = T>
+template <typename T, int D>
 sdpa_status_t attend(Args& a, const LaunchEnv& env) {
   // few rows a sequence (decode): the 16-row tile, see the top of the file
   const int rows = a.G <= 16 && call_rows(a) <= 16 ? 16 : 64;
   fit_rows(a, rows);
   const sdpa_status_t st =
-      rows == 16
-          ? start<paged_simt_kernel<T, D, 16, CT>>(a, attend_smem<CT, D, 16>(),
-                                                   attend_ctas<CT, D, 16>() * env.num_sms,
-                                                   env.stream)
-          : start<paged_simt_kernel<T, D, 64, CT>>(a, attend_smem<CT, D, 64>(),
-                                                   attend_ctas<CT, D, 64>() * env.num_sms,
-                                                   env.stream);
+      rows == 16 ? start<paged_simt_kernel<T, D, 16>>(
+                       a, attend_smem<T, D, 16>(), attend_ctas<T, D, 16>() * env.num_sms, env.stream)
+                 : start<paged_simt_kernel<T, D, 64>>(
+                       a, attend_smem<T, D, 64>(), attend_ctas<T, D, 64>() * env.num_sms, env.stream);
   if (st != SDPA_OK) return st;
   const int dtype = sizeof(T) == 4 ? SDPA_F32 : std::is_same<T, __half>::value ? SDPA_F16 : SDPA_BF16;
   return launch_paged_merge(a, D, dtype, rows, 1, env.stream);
@@ -752,12 +691,10 @@ sdpa_status_t score(Args& a, const LaunchEnv& env) {
 }  // namespace paged
 
 sdpa_status_t launch_paged_merge(const paged::Args& a, int head_dim, int dtype, int tile_rows,
-                                 int tiles, cudaStream_t stream, bool by_head) {
+                                 int tiles, cudaStream_t stream) {
   using namespace paged;
   const dim3 grid(a.nctas, tile_rows * tiles > 16 ? 16 : 8);
-  auto go = [&](auto kern) {
-    return launch_after(kern, grid, 256, stream, a, tile_rows, tiles, by_head);
-  };
+  auto go = [&](auto kern) { return launch_after(kern, grid, 256, stream, a, tile_rows, tiles); };
   if (head_dim == 64) {
     if (dtype == SDPA_F32) return go(paged_merge_kernel<float, 64>);
     return dtype == SDPA_F16 ? go(paged_merge_kernel<__half, 64>)
@@ -782,19 +719,6 @@ sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const La
   }
   if (dtype == SDPA_F32) return attend<float, 128>(a, env);
   return dtype == SDPA_F16 ? attend<__half, 128>(a, env) : attend<__nv_bfloat16, 128>(a, env);
-}
-
-sdpa_status_t launch_paged_simt_fp4(paged::Args a, int head_dim, int dtype,
-                                    const LaunchEnv& env) {
-  using namespace paged;
-  if (head_dim == 64) {
-    if (dtype == SDPA_F32) return attend<float, 64, Fp4>(a, env);
-    return dtype == SDPA_F16 ? attend<__half, 64, Fp4>(a, env)
-                             : attend<__nv_bfloat16, 64, Fp4>(a, env);
-  }
-  if (dtype == SDPA_F32) return attend<float, 128, Fp4>(a, env);
-  return dtype == SDPA_F16 ? attend<__half, 128, Fp4>(a, env)
-                           : attend<__nv_bfloat16, 128, Fp4>(a, env);
 }
 
 sdpa_status_t launch_paged_scores_simt(paged::Args a, int head_dim, int dtype,
