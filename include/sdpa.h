@@ -663,7 +663,8 @@ typedef struct {
   void* v_scales;
   int64_t k_scale_stride[3];
   int64_t v_scale_stride[3];
-  const float* k_gain; /* NULL (1), or device float32 [Hkv], finite, not 0 */
+  const float* k_gain; /* NULL (1), or device float32 [Hkv] of magnitudes
+                          between 2^-100 and 2^100 */
   const float* v_gain;
 } sdpa_fp4_cache_t;
 

@@ -376,10 +376,13 @@ def _torch():
 
 
 def dtype_code(t) -> int:
-    _torch()
-    if t not in _dtype_codes:
-        raise TypeError("unsupported dtype %s" % t)
-    return _dtype_codes[t]
+    code = _dtype_codes.get(t)
+    if code is None:
+        _torch()
+        if t not in _dtype_codes:
+            raise TypeError("unsupported dtype %s" % t)
+        code = _dtype_codes[t]
+    return code
 
 
 def _workspace(nbytes: int, device):
@@ -569,7 +572,7 @@ def sdpa_forward_host(q, k, v, scale=None, causal=False, mask=None, sinks=None, 
 # SdpaPagedParams as one struct.pack call: filling the ctypes fields one by one
 # costs several times as much, and single-token calls are bound by the host.
 _PAGED = struct.Struct("<6ifi3iIQqQQQ10q")
-_STRIDE2 = ctypes.c_int64 * 2
+_STRIDE2 = struct.Struct("<2q").pack  # two strides as a C array
 _paged_fn = {}
 _PAGED_KEPT = 4  # workspaces (some 20 or 40 MB each) that a thread keeps at most
 
@@ -1156,38 +1159,42 @@ def sdpa_paged_append(q, k, v, k_pages, v_pages, page_table, seq_lens_kv, rope_t
 
 
 # ---------------------------------------------------------- 4-bit paged KV cache
+def _fp4_scales(t, want, dev):
+    """The strides of k_scales or v_scales."""
+    torch = _torch()
+    dtype, st = t.dtype, t.stride()
+    if dtype is not torch.uint8 and dtype is not torch.float8_e4m3fn:
+        raise TypeError("k_scales and v_scales must be uint8 or float8_e4m3fn")
+    if t.shape != want or t.get_device() != dev or st[3] != 1:
+        raise ValueError("k_scales and v_scales must be [pages, kv heads, page_size, D / 16] "
+                         "on the same device with a contiguous last dimension")
+    return st
+
+
+def _fp4_gain(g, heads, dev):
+    """The address of a gain tensor."""
+    if (g.dtype is not _torch().float32 or g.get_device() != dev or g.numel() != heads
+            or not g.is_contiguous()):
+        raise ValueError("k_gain and v_gain must be contiguous float32 CUDA tensors of one "
+                         "number a kv head")
+    return g.data_ptr()
+
+
 def _fp4_cache(dev, dtype, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv,
                cu_seqlens_q, k_gain, v_gain):
     """Checks of a 4-bit cache: the fields of _paged_cache for rows of `dtype`,
     and SdpaFp4Cache packed."""
-    torch = _torch()
-    if k_pages.dtype is not torch.uint8:
+    if k_pages.dtype is not _torch().uint8:
         raise TypeError("k_pages and v_pages must be uint8 (two codes a byte)")
-    c = _paged_cache(dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q,
-                     dtype_code(dtype))
-    shape = k_pages.shape
-    D = 2 * shape[3]
-    want = (shape[0], shape[1], shape[2], D // 16)
-    for t in (k_scales, v_scales):
-        if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
-            raise TypeError("k_scales and v_scales must be uint8 or float8_e4m3fn")
-        if t.shape != want or t.get_device() != dev or (t.stride(3) != 1 and want[3] > 1):
-            raise ValueError("k_scales and v_scales must be [pages, kv heads, page_size, D / 16] "
-                             "on the same device with a contiguous last dimension")
-    gains = []
-    for g in (k_gain, v_gain):
-        if g is None:
-            gains.append(0)
-            continue
-        if (g.dtype is not torch.float32 or g.get_device() != dev or g.numel() != shape[1]
-                or not g.is_contiguous()):
-            raise ValueError("k_gain and v_gain must be contiguous float32 CUDA tensors of one "
-                             "number a kv head")
-        gains.append(g.data_ptr())
-    ks, vs = k_scales.stride(), v_scales.stride()
-    return (c[0], D) + c[2:], _FP4.pack(
-        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ks[0],
-        ks[1], ks[2], vs[0], vs[1], vs[2], gains[0], gains[1])
+    heads, half, code, pages, page, B, cols, table, tst, cu, lens, ks, vs = _paged_cache(
+        dev, k_pages, v_pages, page_table, seq_lens_kv, cu_seqlens_q, dtype_code(dtype))
+    want = (pages, heads, page, half // 8)
+    kss, vss = _fp4_scales(k_scales, want, dev), _fp4_scales(v_scales, want, dev)
+    return (heads, 2 * half, code, pages, page, B, cols, table, tst, cu, lens, ks, vs), _FP4.pack(
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), kss[0],
+        kss[1], kss[2], vss[0], vss[1], vss[2],
+        0 if k_gain is None else _fp4_gain(k_gain, heads, dev),
+        0 if v_gain is None else _fp4_gain(v_gain, heads, dev))
 
 
 def sdpa_paged_append_fp4(q, k, v, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens_kv,

@@ -48,18 +48,19 @@ __device__ __forceinline__ uint32_t scale_of(float top, float* value) {
   return s;
 }
 // Eight numbers as codes, ties to even, at most 6 in magnitude: a word, the
-// first in its low four bits.
+// first in its low four bits.  (Each byte through a register of its own: joined
+// as 8-bit registers in one move, the first two came out wrong in one caller,
+// nvcc 13.0.88.)
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8]) {
-  uint32_t w;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(w)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
-  return w;
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b8 c;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\t"
+        "cvt.u32.u8 %0, c;\n\t}"
+        : "=r"(b[i])
+        : "f"(x[2 * i]), "f"(x[2 * i + 1]));
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
 }  // namespace fp4

@@ -43,6 +43,38 @@ struct AppendArgs {
   long long vo[2];
 };
 
+__device__ __forceinline__ void put8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void get8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = a.z;
+  x[3] = a.w;
+  x[4] = b.x;
+  x[5] = b.y;
+  x[6] = b.z;
+  x[7] = b.w;
+}
+
+// x / d for r the reciprocal of d rounded once: the quotient x r, corrected by
+// its exact remainder (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990).  One correction is within a unit of
+// a product of two rounded numbers and, where d has 4 significant bits, meets
+// every number of few bits that the quotient equals and passes none; the
+// second leaves the quotient rounded to nearest.
+template <int kSteps>
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float q0 = __fmul_rn(x, r);
+  float q = q0;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) q = __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+  if (kSteps > 1) return fabsf(q0) < INFINITY ? q : q0;  // (an infinity has no remainder)
+  return q;
+}
+
 template <typename T, int D, bool kFp4>
 __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendArgs w) {
   constexpr int U = D / 16;    // pieces of a row
@@ -52,27 +84,28 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
   const int u = lane % U;
   // a warp's rows in fp32 where 16 consecutive elements of a rotated row come
   // from two lanes
-  __shared__ float s_rows[kFp4 ? kWarps * 512 : 1];
+  __shared__ __align__(16) float s_rows[kFp4 ? kWarps * 512 : 4];
   const long long tt = static_cast<long long>(blockIdx.x) * kWarps + warp;
   if (tt >= a.T) return;
   const int t = static_cast<int>(tt);
   const int row0 = blockIdx.y * w.times * RW + lane / U;
-  const Piece pc = piece_of(w.rot, u);
-  const Piece straight{16 * u, 16 * u + 8, false};
+  // (a group of the 4-bit cache is 16 consecutive elements)
+  const Piece pc = piece_of<kFp4>(w.rot, D, u);
+  const Piece plain = kFp4 ? Piece{16 * u, 16 * u + 8, false} : Piece{8 * u, D / 2 + 8 * u, false};
   // what row r is: 0 a query, 1 a key, 2 a value
   auto kind = [&](int r) { return r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2; };
-  Raw<T> lo, hi;
-  auto load = [&](int r) {
+  Raw<T> lo, hi, nlo, nhi;
+  auto load = [&](int r, Raw<T>& x0, Raw<T>& x1) {
     if (r >= w.rows) return;
     const int kd = kind(r);
     const char* x = kd == 0   ? static_cast<const char*>(a.q) + t * w.qi[0] + r * w.qi[1]
                     : kd == 1 ? w.k + t * w.kn[0] + (r - a.Hq) * w.kn[1]
                               : w.v + t * w.vn[0] + (r - a.Hq - a.Hkv) * w.vn[1];
-    const Piece p = kd == 2 ? straight : pc;
-    lo = load8(reinterpret_cast<const T*>(x) + p.lo);
-    hi = load8(reinterpret_cast<const T*>(x) + p.hi);
+    const Piece p = kd == 2 ? plain : pc;
+    x0 = load8(reinterpret_cast<const T*>(x) + p.lo);
+    x1 = load8(reinterpret_cast<const T*>(x) + p.hi);
   };
-  load(row0);
+  load(row0, lo, hi);
   const int b = find_seq(a, t, lane);
   if (b < 0) return;
   const Seq s = seq_of(a, b);
@@ -81,7 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
   const long long pos = w.rot.positions ? w.rot.positions[t] : own;
   Angles ang = {};
   bool turned = pc.turned && pos >= 0 && pos < w.rot.len;
-  if (turned) ang = load_angles(w.rot, pos, u);
+  if (turned) ang = load_angles(w.rot, pos, pc);
   if (pc.turned && !turned && u == 0 && (w.rot.positions || pos >= 0))
     atomicExch(a.status, kStatusPosition);
   int page = -1, prow = 0;
@@ -91,12 +124,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
   }
   for (int i = 0; i < w.times; ++i) {
     const int r = row0 + i * RW;
-    if (i > 0) load(r);
+    if (i + 1 < w.times) load(r + RW, nlo, nhi);  // (on their way meanwhile)
     const bool live = r < w.rows;
-    if (!kFp4 && !live) break;
+    if (!kFp4 && !live) break;  // (so are the lane's later rows)
     const int kd = kind(r);
     const int h = r - (kd == 0 ? 0 : kd == 1 ? a.Hq : a.Hq + a.Hkv);
-    const Piece p = kd == 2 ? straight : pc;
+    const Piece p = kd == 2 ? plain : pc;
     Values x;
     const bool tn = turned && kd != 2;
     if (live && (tn || (kFp4 && kd != 0))) {
@@ -130,19 +163,13 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
         float* row = s_rows + warp * 512 + (lane / U) * D;
         __syncwarp();
         if (mine) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            row[p.lo + k] = x.lo[k];
-            row[p.hi + k] = x.hi[k];
-          }
+          put8(row + p.lo, x.lo);
+          put8(row + p.hi, x.hi);
         }
         __syncwarp();
         if (mine) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x.lo[k] = row[16 * u + k];
-            x.hi[k] = row[16 * u + 8 + k];
-          }
+          get8(row + 16 * u, x.lo);
+          get8(row + 16 * u + 8, x.hi);
         }
       }
       if (mine) {
@@ -150,21 +177,22 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
         const float g = w.gain[c] ? w.gain[c][h] : 1.f;
         float top = 0.f;
         if (w.gain[c]) {
+          const float rg = __frcp_rn(g);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            x.lo[k] = __fdiv_rn(x.lo[k], g);
-            x.hi[k] = __fdiv_rn(x.hi[k], g);
+            x.lo[k] = quotient<2>(x.lo[k], g, rg);
+            x.hi[k] = quotient<2>(x.hi[k], g, rg);
           }
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaxf(fabsf(x.lo[k]), fabsf(x.hi[k])));
         float sc;
         const uint32_t sbyte = fp4::scale_of(top, &sc);
-        // (true quotients: a tie between two codes is found exactly)
+        const float rs = __frcp_rn(sc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x.lo[k] = __fdiv_rn(x.lo[k], sc);
-          x.hi[k] = __fdiv_rn(x.hi[k], sc);
+        for (int k = 0; k < 8; ++k) {  // (what is past the largest value ends there)
+          x.lo[k] = quotient<1>(fminf(fmaxf(x.lo[k], -4096.f), 4096.f), sc, rs);
+          x.hi[k] = quotient<1>(fminf(fmaxf(x.hi[k], -4096.f), 4096.f), sc, rs);
         }
         const uint32_t c0 = fp4::codes_of(x.lo), c1 = fp4::codes_of(x.hi);
         if (page >= 0) {
@@ -193,6 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
         }
       }
     }
+    lo = nlo;
+    hi = nhi;
   }
 }
 

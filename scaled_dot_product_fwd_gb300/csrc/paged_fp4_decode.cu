@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int KS_OFF = 2 * V_OFF;
   static constexpr int VS_OFF = KS_OFF + 32 * SC;
   static constexpr int CELL = VS_OFF + 32 * SC;
-  static constexpr int NS = D == 128 ? 3 : 5;
+  static constexpr int NS = D == 128 ? 2 : 4;
   static constexpr int RING = kWarps * NS * CELL;
   static constexpr int SMEM = RING + 512;
   static_assert(CELL % 128 == 0 && (D == 64 || CELL % 512 == 0), "swizzle atoms aligned");

@@ -51,8 +51,22 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
   if (t >= a.n) return;
   const int b = a.by_len.div(static_cast<int>(t));
   const int l = static_cast<int>(t) - b * static_cast<int>(a.by_len.d);
-  const Piece pc = piece_of(a.rot, u);
+  const Piece pc = piece_of<false>(a.rot, 16 << a.lg_u, u);
   const int h0 = blockIdx.y * a.per * (1 << lg_h) + (r >> a.lg_t);
+  constexpr int U = sizeof(T) == 4 ? 1 : 2;  // heads at a time
+  Raw<T> lo[U], hi[U];
+  auto load = [&](int i, Raw<T>& x0, Raw<T>& x1) {  // head number i of this thread
+    const int h = h0 + (i << lg_h);
+    if (i < a.per && h < a.H) {
+      const int w = h >= a.Hq, g = w ? h - a.Hq : h;
+      const T* x = reinterpret_cast<const T*>(a.in[w] + b * a.is[w][0] + g * a.is[w][1] +
+                                              l * a.is[w][2]);
+      x0 = load8(x + pc.lo);
+      x1 = load8(x + pc.hi);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < U; ++k) load(k, lo[k], hi[k]);
   bool turned = pc.turned;
   Angles ang = {};
   {
@@ -61,33 +75,17 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
       if (u == 0 && turned) atomicExch(a.status, kStatusPosition);
       turned = false;
     }
-    if (turned) ang = load_angles(a.rot, pos, u);
+    if (turned) ang = load_angles(a.rot, pos, pc);
   }
-  auto at = [&](int h, int* which, int* head) {
-    *which = h >= a.Hq;
-    *head = *which ? h - a.Hq : h;
-  };
-  constexpr int U = 2;  // heads in flight
   for (int i = 0; i < a.per; i += U) {
-    Raw<T> lo[U], hi[U];
+    Raw<T> nlo[U], nhi[U];  // the next heads' pieces are on their way meanwhile
+#pragma unroll
+    for (int k = 0; k < U; ++k) load(i + U + k, nlo[k], nhi[k]);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int h = h0 + ((i + k) << lg_h);
       if (i + k < a.per && h < a.H) {
-        int w, g;
-        at(h, &w, &g);
-        const T* x = reinterpret_cast<const T*>(a.in[w] + b * a.is[w][0] + g * a.is[w][1] +
-                                                l * a.is[w][2]);
-        lo[k] = load8(x + pc.lo);
-        hi[k] = load8(x + pc.hi);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int h = h0 + ((i + k) << lg_h);
-      if (i + k < a.per && h < a.H) {
-        int w, g;
-        at(h, &w, &g);
+        const int w = h >= a.Hq, g = w ? h - a.Hq : h;
         T* x = reinterpret_cast<T*>(a.out[w] + b * a.os[w][0] + g * a.os[w][1] + l * a.os[w][2]);
         if (turned) {
           Values v;
@@ -100,6 +98,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
         store8(x + pc.lo, lo[k]);
         store8(x + pc.hi, hi[k]);
       }
+      lo[k] = nlo[k];
+      hi[k] = nhi[k];
     }
   }
 }
@@ -173,6 +173,7 @@ sdpa_status_t launch_rope(const sdpa_rope_params_t& p, const void* q, const void
   int per = 8;
   while (per > 1 && warps * ((heads + per - 1) / per) < 32LL * env.num_sms) per >>= 1;
   per = std::max(per, (heads + 65534) / 65535);
+  per = (heads + (heads + per - 1) / per - 1) / ((heads + per - 1) / per);  // (even shares)
   a.per = per;
   const dim3 grid(static_cast<unsigned>((warps + kWarps - 1) / kWarps),
                   static_cast<unsigned>((heads + per - 1) / per));

@@ -1,10 +1,10 @@
 // rotate.cuh — the rotation of a head's pairs as the rotary kernels share it.
 //
-// A row of D elements is D / 16 pieces of 16 elements, one a thread: of the
-// rotated R elements a piece holds 8 whole pairs (16 consecutive elements of
-// the interleaved form, 8 of each half else), so a thread reads and writes two
-// runs of 8 elements and needs 64 bytes of the table; behind them a piece is
-// 16 consecutive elements.
+// A row of D elements is D / 16 pieces, one a thread: two runs of 8 elements,
+// half of the rotated (or of the other) elements apart, so that neighbouring
+// lanes' 16-byte accesses are neighbours in memory.  In the halves form the
+// runs are each other's partners, in the interleaved form each holds whole
+// pairs; either way a thread needs 64 bytes of the table.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,15 +33,19 @@ inline Rotation make_rotation(const sdpa_rotation_t* r) {
   return x;
 }
 
-// Elements of piece u: the runs of 8 from lo and from hi.
+// Elements of piece u of a row of D: the runs of 8 from lo and from hi.
+// kWhole: 16 consecutive elements where the pairs allow it.
 struct Piece {
   int lo, hi;
   bool turned;
 };
-__device__ __forceinline__ Piece piece_of(const Rotation& r, int u) {
+template <bool kWhole>
+__device__ __forceinline__ Piece piece_of(const Rotation& r, int D, int u) {
   const bool turned = 16 * u < r.R;
-  if (turned && !r.interleaved) return Piece{8 * u, r.R / 2 + 8 * u, true};
-  return Piece{16 * u, 16 * u + 8, turned};
+  if (kWhole && !(turned && !r.interleaved)) return Piece{16 * u, 16 * u + 8, turned};
+  const int first = turned ? 0 : r.R, count = turned ? r.R : D - r.R;
+  const int lo = first + 8 * (u - first / 16);
+  return Piece{lo, lo + count / 2, turned};
 }
 
 // Eight elements of a row in fp32 (lo, hi: the piece's runs).
@@ -115,11 +119,16 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
 struct Angles {
   float4 cs[4];
 };
-__device__ __forceinline__ Angles load_angles(const Rotation& r, long long pos, int u) {
+__device__ __forceinline__ Angles load_angles(const Rotation& r, long long pos, const Piece& p) {
   Angles a;
-  const float4* p = reinterpret_cast<const float4*>(r.table + pos * r.R + 16 * u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a.cs[i] = __ldg(p + i);
+  // pair i of the halves form at 2 i, of the interleaved form at its element
+  const float* t = r.table + pos * r.R;
+  const float4* lo = reinterpret_cast<const float4*>(t + (r.interleaved ? p.lo : 2 * p.lo));
+  const float4* hi = r.interleaved ? reinterpret_cast<const float4*>(t + p.hi) : lo + 2;
+  a.cs[0] = __ldg(lo);
+  a.cs[1] = __ldg(lo + 1);
+  a.cs[2] = __ldg(hi);
+  a.cs[3] = __ldg(hi + 1);
   return a;
 }
 template <bool kExact>
