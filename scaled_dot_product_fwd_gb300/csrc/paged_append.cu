@@ -76,7 +76,7 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
 }
 
 template <typename T, int D, bool kFp4>
-__global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendArgs w) {
+__global__ void __launch_bounds__(kWarps * 32, kFp4 ? 3 : 4) paged_append_kernel(const AppendArgs w) {
   constexpr int U = D / 16;    // pieces of a row
   constexpr int RW = 32 / U;   // rows of a warp at a time
   const Args& a = w.a;
@@ -136,7 +136,10 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const AppendA
       widen8(lo, x.lo);
       widen8(hi, x.hi);
       if (tn) {
-        turn_piece<kFp4>(x, ang, w.rot.interleaved, 1.f);
+        if (kFp4 && kd == 1)
+          turn_piece<kFp4>(x, ang, w.rot.interleaved, 1.f);
+        else
+          turn_piece<false>(x, ang, w.rot.interleaved, 1.f);
         lo = narrow8<T>(x.lo);
         hi = narrow8<T>(x.hi);
       }
@@ -232,10 +235,14 @@ sdpa_status_t launch(AppendArgs& w, const LaunchEnv& env) {
   const long long blocks = (static_cast<long long>(w.a.T) + kWarps - 1) / kWarps;
   const int groups = (w.rows + RW - 1) / RW;
   // Groups of rows of a warp: one where the call is small (the shortest
-  // chain), up to four where that still fills the GPU.
-  int times = 4;
+  // chain), more where that still fills the GPU.  Four chunks of up to 2048
+  // tokens, 32 heads over 8, head_dim 128: 2, 4, 6 and 12 groups 27.6, 27.4, 28.2
+  // and 28.5 us, into the 4-bit cache, whose rows cost more, 44, 42, 40 and 40.
+  int times = kFp4 ? 8 : 4;
   while (times > 1 && blocks * ((groups + times - 1) / times) < 8LL * env.num_sms) times >>= 1;
   times = std::max(times, (groups + 65534) / 65535);
+  const int parts = (groups + times - 1) / times;
+  times = (groups + parts - 1) / parts;  // (even shares)
   w.times = times;
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((groups + times - 1) / times));
