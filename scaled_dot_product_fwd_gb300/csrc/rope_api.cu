@@ -39,7 +39,8 @@ sdpa_status_t check_pair(const sdpa_rope_params_t& p, int heads, const void* x, 
 }  // namespace
 
 sdpa_status_t check_rotation(const sdpa_rotation_t& r, int head_dim) {
-  if (r.rotary_dim < 1 || r.rotary_dim > head_dim || r.table_len < 0 || !r.table)
+  if (r.rotary_dim < 1 || r.rotary_dim > head_dim || r.table_len < 0 ||
+      (r.table_len > 0 && !r.table))
     return SDPA_ERR_INVALID_ARGUMENT;
   if (r.rotary_dim % 16 != 0 || r.table_len > (int64_t(1) << 40)) return SDPA_ERR_UNSUPPORTED;
   if (!aligned(r.table, 16) || !aligned(r.positions, 4)) return SDPA_ERR_MISALIGNED;

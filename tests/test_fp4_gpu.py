@@ -23,6 +23,9 @@ pytestmark = pytest.mark.gpu
 
 DT = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
 VALUES = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+# every scale byte's value (a table: powers computed on the GPU are not exact)
+SCALES = [math.ldexp(b & 7, -9) if not b >> 3 & 15 else math.ldexp(8 + (b & 7), (b >> 3 & 15) - 10)
+          for b in range(128)]
 
 
 @pytest.fixture
@@ -51,9 +54,8 @@ def values_of(torch, codes, scales):
     """What rows of code and scale bytes stand for, in float64."""
     lut = torch.tensor(VALUES + [-v for v in VALUES], dtype=torch.float64, device=codes.device)
     c = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
-    e, m = (scales >> 3 & 15).double(), (scales & 7).double()
-    s = torch.where(e == 0, m * 2.0**-9, (1 + m / 8) * 2.0**(e - 7))
-    s = torch.where(scales >= 128, -s, s)
+    s = torch.tensor(SCALES + [-v for v in SCALES], dtype=torch.float64,
+                     device=codes.device)[scales.long()]
     return lut[c.long()] * s.repeat_interleave(16, -1)
 
 
@@ -197,3 +199,206 @@ def test_forward(cuda, S, shape, layout, dtype):
     check(t, o, lse, 1 / math.sqrt(t.D))
     # rows behind the last sequence are left as they were
     assert (o[-3:] == 7).all() and (lse[-3:] == 7).all()
+
+
+OPTIONS = [dict(causal=False), dict(scale=-0.2), dict(scale=0.0), dict(sinks=True),
+           dict(sinks=True, scale=0.5, causal=False)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kw", OPTIONS, ids=str)
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[5], SHAPES[8], SHAPES[9]], ids=str)
+def test_options(cuda, S, shape, kw, dtype):
+    t = Cache4(cuda, *shape[:5], dtype, shape[5])
+    kw = dict(kw)
+    sinks = t.sinks if kw.pop("sinks", False) else None
+    o, lse = forward(S, t, sinks=sinks, **kw)
+    check(t, o, lse, kw.get("scale", 1 / math.sqrt(t.D)), kw.get("causal", True), sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ctas", [1, 2, 5, 37])
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[3], SHAPES[6], SHAPES[9]], ids=str)
+def test_shared_out_differently(cuda, S, hook, shape, ctas, dtype):
+    hook("paged_ctas", ctas)
+    t = Cache4(cuda, *shape[:5], dtype, shape[5])
+    o, lse = forward(S, t, sinks=t.sinks)
+    check(t, o, lse, 1 / math.sqrt(t.D), sinks=t.sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("hq,hkv,nq", [(4, 1, 1), (12, 1, 1), (20, 1, 3), (20, 1, 40), (8, 8, 1)])
+@pytest.mark.parametrize("ctas", [1, 2, 0])
+def test_sequences_without_keys_among_others(cuda, S, hook, ctas, hq, hkv, nq, dtype):
+    hook("paged_ctas", ctas)
+    ks = [0, 300, 0, 5, 0, 0, 140, 128, 0, 0, 0, 17, 2, 0]
+    t = Cache4(cuda, [nq] * len(ks), ks, hq, hkv, 64, dtype, 16)
+    for causal in (True, False):
+        o, lse = forward(S, t, causal=causal)
+        check(t, o, lse, 1 / 8, causal)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_empty_rows(cuda, S, dtype):
+    """More new tokens than keys: the first see none; a sequence of no keys; no page at all."""
+    t = Cache4(cuda, [6, 3, 1, 200], [4, 0, 0, 150], 8, 2, 64, dtype, 16)
+    o, lse = forward(S, t)
+    check(t, o, lse, 1 / 8)
+    o, lse = forward(S, t, sinks=t.sinks)
+    assert (o[:2] == 0).all() and (o[6:10] == 0).all()
+    assert ((lse[6:10] - t.sinks).abs() <= t.sinks.abs() * 2.0**-21 + 2.0**-22).all()
+    o, lse = S.sdpa_paged_forward_fp4(t.q, *t.codes, *t.scales, t.table[:, :0], t.lens,
+                                      cu_seqlens_q=t.cu)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("nq", [1, 6, 150])
+def test_growing_scores(cuda, S, nq, dtype):
+    """Keys that grow along the sequence: the reference maximum moves again and again."""
+    t = Cache4(cuda, [nq], [1500], 4, 2, 128, dtype, 16, gains=False)
+    b, n = 0, 1500
+    pos = cuda.arange(n, device="cuda")
+    pg = t.table[0, pos // 16].long()
+    step = (0x28 + pos * 0x20 // n).to(cuda.uint8)  # scales from 2^-2 to 2^2
+    t.scales[0][pg, :, pos % 16] = step[:, None, None].expand(n, 2, 8).contiguous()
+    codes = t.codes[0][pg, :, pos % 16] & 0x77  # all positive
+    t.codes[0][pg, :, pos % 16] = codes
+    t.KV[0][0] = values_of(cuda, codes, t.scales[0][pg, :, pos % 16])
+    t.q = t.q.abs()
+    o, lse = forward(S, t)
+    check(t, o, lse, 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("nq", [1, 140])
+def test_small_and_large_queries(cuda, S, nq):
+    """bf16 rows whose elements lie far outside fp16's range, up and down."""
+    for factor, scale in ((2.0**60, 2.0**-64), (2.0**-100, 2.0**96), (2.0**-130, 1.0)):
+        t = Cache4(cuda, [nq], [300], 8, 2, 64, "bf16", 16)
+        t.q = (t.q.float() * factor).to(cuda.bfloat16)
+        o, lse = forward(S, t, scale=scale)
+        check(t, o, lse, scale)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_strides(cuda, S, nq, dtype):
+    """Rows inside wider rows, K and V of one tensor, a page table with spare columns."""
+    t = Cache4(cuda, [nq, nq], [70, 300], 8, 2, 64, dtype, 16)
+    wide = cuda.zeros(t.q.shape[0], 3, 8, 64, device="cuda", dtype=t.dtype)
+    wide[:, 1] = t.q
+    P = t.codes[0].shape[0]
+    codes = cuda.zeros(P, 16, 2, 2, 48, device="cuda", dtype=cuda.uint8)
+    scales = cuda.full((P, 16, 2, 2, 12), 0x7F, device="cuda", dtype=cuda.uint8)
+    for i in range(2):
+        codes[:, :, i, :, :32] = t.codes[i].transpose(1, 2)
+        scales[:, :, i, :, 4:8] = t.scales[i].transpose(1, 2)
+    kc, vc = (codes[:, :, i, :, :32].transpose(1, 2) for i in range(2))
+    ks, vs = (scales[:, :, i, :, 4:8].transpose(1, 2) for i in range(2))
+    out = cuda.zeros(8, t.q.shape[0], 64, device="cuda", dtype=t.dtype).transpose(0, 1)
+    tab = cuda.full((2, 99), -1, dtype=cuda.int32, device="cuda")
+    tab[:, :t.table.shape[1]] = t.table
+    o, lse = S.sdpa_paged_forward_fp4(
+        wide[:, 1], kc, vc, ks.view(cuda.float8_e4m3fn), vs.view(cuda.float8_e4m3fn),
+        tab[:, :t.table.shape[1]], t.lens, cu_seqlens_q=t.cu, k_gain=t.gain[0], v_gain=t.gain[1],
+        out=out)
+    check(t, o, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_offsets_past_32_bits(cuda, S, nq):
+    """Pages further apart than 2^31 bytes, codes and scales."""
+    t = Cache4(cuda, [nq], [3 * 64], 4, 2, 128, "bf16", 64, extra_cols=0)
+    far = (2**31 + 4096) // 64 * 64
+    room = cuda.zeros(2 * 4 * far + 2**20, dtype=cuda.uint8, device="cuda")
+    big = []
+    for i, (x, n) in enumerate(((t.codes[0], 64), (t.codes[1], 64))):
+        v = room.as_strided((5, 2, 64, n), (far // 2, 64 * n, n, 1), i * 2**14)
+        v.copy_(x)
+        big.append(v)
+    for i, x in enumerate(t.scales):
+        v = room.as_strided((5, 2, 64, 8), (far // 2, 512, 8, 1), 2**16 + i * 2**14)
+        v.copy_(x)
+        big.append(v)
+    assert 4 * big[0].stride(0) > 2**32
+    o, lse = S.sdpa_paged_forward_fp4(t.q, *big, t.table, t.lens, cu_seqlens_q=t.cu,
+                                      k_gain=t.gain[0], v_gain=t.gain[1])
+    check(t, o, lse, 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_bad_pages(cuda, nq, dtype):
+    """An entry that names no page reads as zero keys and values and is reported."""
+    import scaled_dot_product_fwd_gb300 as S
+    for page in (16, 5):
+        t = Cache4(cuda, [nq, nq], [100, 90], 8, 2, 64, dtype, page)
+        t.table[0, 1] = 10**6
+        t.table[1, 2] = -1
+        for i in range(2):
+            t.KV[0][i][page:2 * page] = 0
+            t.KV[1][i][2 * page:3 * page] = 0
+        o, lse = forward(S, t)
+        cuda.cuda.synchronize()
+        assert S.sdpa_device_status() == 7
+        check(t, o, lse, 1 / 8)
+    assert S.sdpa_device_status() == 0
+
+
+def test_streams_graphs_and_repeats(cuda, S):
+    """A call under capture and its replays, on other streams, again and again: the same bits."""
+    ts = [Cache4(cuda, [1, 1], [3000, 900], 8, 2, 64, "bf16", 16),
+          Cache4(cuda, [9, 300], [900, 1500], 8, 2, 128, "f16", 16),
+          Cache4(cuda, [40], [700], 8, 2, 64, "f32", 16)]
+    refs = [forward(S, t) for t in ts]
+    for t, ref in zip(ts, refs):
+        for _ in range(3):
+            o, lse = forward(S, t)
+            assert cuda.equal(o, ref[0]) and cuda.equal(lse, ref[1])
+        side = cuda.cuda.Stream()
+        side.wait_stream(cuda.cuda.current_stream())
+        with cuda.cuda.stream(side):
+            o, lse = forward(S, t)
+        o2, lse2 = forward(S, t, stream=side.cuda_stream)
+        side.synchronize()
+        assert cuda.equal(o, ref[0]) and cuda.equal(o2, ref[0]) and cuda.equal(lse2, ref[1])
+    graphs = []
+    for t in ts:
+        g = cuda.cuda.CUDAGraph()
+        with cuda.cuda.graph(g):
+            out = forward(S, t)
+        graphs.append((g, out))
+    for _ in range(3):
+        for (g, out), ref in zip(graphs, refs):
+            out[0].zero_()
+            g.replay()
+        for (g, out), ref in zip(graphs, refs):
+            assert cuda.equal(out[0], ref[0]) and cuda.equal(out[1], ref[1])
+
+
+def test_one_token_each_without_offsets(cuda, S):
+    t = Cache4(cuda, [1] * 5, [3, 99, 1, 500, 64], 8, 4, 128, "bf16", 16, pad=2)
+    o, lse = forward(S, t)
+    o2, lse2 = S.sdpa_paged_forward_fp4(t.q, *t.codes, *t.scales, t.table, t.lens,
+                                        k_gain=t.gain[0], v_gain=t.gain[1])
+    assert cuda.equal(o[:5], o2[:5]) and cuda.equal(lse[:5], lse2[:5])
+
+
+def test_long_sequence(cuda, S):
+    t = Cache4(cuda, [1, 20], [70001, 33333], 4, 1, 128, "bf16", 64)
+    o, lse = forward(S, t)
+    check(t, o, lse, 1 / math.sqrt(128))
+
+
+def test_against_the_16_bit_cache(cuda, S):
+    """The same values in a 16-bit cache (exact there too: six significant bits) give the same
+    results within both operators' bounds."""
+    t = Cache4(cuda, [1, 30], [500, 300], 8, 2, 64, "f16", 16, gains=False)
+    kp, vp = (values_of(cuda, c, cuda.where(s == 0x7F, cuda.zeros_like(s), s)).to(cuda.float16)
+              for c, s in zip(t.codes, t.scales))
+    o, lse = forward(S, t)
+    o2, lse2 = S.sdpa_paged_forward(t.q, kp, vp, t.table, t.lens, cu_seqlens_q=t.cu)
+    assert ((lse - lse2).abs() <= 2.0**-12).all()
+    # 2^-11 of sum w |v| <= max |v| for each side's weights, and both roundings of o
+    tol = 2 * 2.0**-11 * float(vp.abs().max()) + 2.0**-11 * o.abs().float() + 2.0**-10
+    assert ((o.float() - o2.float()).abs() <= tol).all()
