@@ -646,8 +646,9 @@ SDPA_API sdpa_status_t sdpa_paged_append(const sdpa_paged_params_t* params,
  * A row x in its own type is written as follows: y = x / g in fp32; the scale
  * is max |y| over the 16 elements, divided by 6 and rounded to e4m3, at least
  * 2^-9 and at most 448; the code is y / scale rounded to the nearest code, ties
- * to even, at most 6 in magnitude.  Rows hold finite values (an infinity is
- * stored as the largest value, a NaN as some finite one).
+ * to even, at most 6 in magnitude (zeros are stored as code 0).  Rows hold
+ * finite values (an infinity is stored as the largest value, a NaN as some
+ * finite one).
  *
  * Codes and scales are two tensors of bytes for K and two for V, [num_pages,
  * Hkv, page_size, D / 2] and [num_pages, Hkv, page_size, D / 16] by shape; the

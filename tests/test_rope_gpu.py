@@ -262,7 +262,8 @@ def quantised(torch, x, gain):
     # borders between codes; those whose lower code is even keep the tie
     n = sum(((a > b) if even else (a >= b)).int() for b, even in
             ((0.25, 1), (0.75, 0), (1.25, 1), (1.75, 0), (2.5, 1), (3.5, 0), (5.0, 1)))
-    code = (n + 8 * torch.signbit(y).int()).to(torch.uint8).flatten(-2)
+    # (the sign of a number that rounds to 0 is kept, a zero's is not)
+    code = (n + 8 * (y < 0).int()).to(torch.uint8).flatten(-2)
     codes = code[..., 0::2] | (code[..., 1::2] << 4)
     value = values_of(torch, codes, sb)
     value = value.float() if gain is None else value.float() * gain[:, None]
@@ -506,7 +507,9 @@ def test_streams_and_graphs(cuda, S):
     at, page, row = t.places()
     assert cuda.equal(t.pages[1][page, :, row], t.v[at])
     # a raw stream handle
-    r2, _ = S.sdpa_rope(t.q.transpose(0, 1)[None], None, table, positions=t.pos.to(cuda.int32),
+    at = t.pos.to(cuda.int32)
+    cuda.cuda.synchronize()
+    r2, _ = S.sdpa_rope(t.q.transpose(0, 1)[None], None, table, positions=at,
                         stream=side.cuda_stream)
     side.synchronize()
     assert cuda.equal(r2, ref[3])
