@@ -10,14 +10,14 @@
 //    reads its scales a tile ahead and writes it as fp16 where tcgen05.mma
 //    reads it (128-byte swizzle).  Code times scale is exact in fp16 (fp4.cuh).  Rows past the
 //    length, or of a page that the table does not name, become zeros there.
-//  - Both products are in fp16 whatever the type of q.  The same four warps lay
-//    down the query tiles: fp16 rows as they are, bf16 ones times a power of two
+//  - Both products are in fp16 whatever the type of q.  The softmax warps lay
+//    down the query tiles, a row a thread, while the products of the unit before
+//    end: fp16 rows as they are, bf16 ones times a power of two
 //    a row that brings the row's largest to [2^14, 2^15) (what fp16 then drops
 //    is below 2^-39 of it); fp32 ones likewise as a sum of two fp16 parts (22
 //    bits), each multiplied with K, and so do their weights with V (NT = 1).
-//    A row's score factor, scale * gain / that power, goes to its softmax
-//    thread; its sign into the row, so that the largest raw score is the
-//    largest score.
+//    A row's score factor is scale * gain / that power; its sign goes into the
+//    row, so that the largest raw score is the largest score.
 //  - Weights are 2^kHead at the reference maximum, so that fp16 holds them to
 //    2^-11 relative down to 2^-18 of the largest.
 // Two query tiles a unit (NT = 2) share each widened tile.  The writes of the
@@ -53,8 +53,7 @@ struct F4Cfg {
   static constexpr int ST = 3;
   static constexpr int STAGE = 128 * ROW;
   static constexpr int STAGE_OFF = RING_OFF + NS * TILE;
-  static constexpr int QF_OFF = STAGE_OFF + ST * STAGE;  // float[2][NT][128]
-  static constexpr int BAR_OFF = QF_OFF + 2 * NT * 128 * 4;
+  static constexpr int BAR_OFF = STAGE_OFF + ST * STAGE;
   // q_full, q_empty, full[NS], empty[NS], s_full[2], o_done[2], pv_done, drain,
   // st_full[ST], st_empty[ST]
   static constexpr int NBARS = 2 + 2 * NS + 2 + 2 + 1 + 1 + 2 * ST;
@@ -71,7 +70,9 @@ struct F4Cfg {
   static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
   static constexpr int UNIT_OFF =
       WALK_OFF + WARPS * static_cast<int>(sizeof(Walk<AttendUnits>));
-  static constexpr int SMEM = UNIT_OFF + WARPS * static_cast<int>(sizeof(Unit)) + 1024;
+  // (a softmax warp has its unit and the next one)
+  static constexpr int SMEM =
+      UNIT_OFF + (WARPS + SOFT_WARPS) * static_cast<int>(sizeof(Unit)) + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(STAGE % 512 == 0 && STAGE_OFF % 512 == 0, "swizzle atoms aligned");
   static constexpr uint32_t s_col(int i) { return static_cast<uint32_t>(i * 128); }
@@ -156,6 +157,13 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m
   rs += t0 + t1;
 }
 
+// 32 bytes, a whole sector (p 32-byte aligned).
+__device__ __forceinline__ void store32(float* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     paged_fp4_tc_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -167,7 +175,6 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::RING_OFF;
-  float* sQf = reinterpret_cast<float*>(smem + C::QF_OFF);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* q_empty = q_full + 1;
   uint64_t* full = q_empty + 1;
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);
+    mbar_init(q_full, C::SOFT_WARPS);
     mbar_init(q_empty, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&full[s], 4);
@@ -224,12 +231,13 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
   W* walk = reinterpret_cast<W*>(smem + C::WALK_OFF) + warp;
   Unit* unit = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
   if (lane == 0) *walk = W(*sh);
-  auto next = [&]() {
+  auto next_to = [&](Unit* u) {
     __syncwarp();
     bool more = false;
-    if (lane == 0) more = walk->next(a, units, *sh, heads, unit);
+    if (lane == 0) more = walk->next(a, units, *sh, heads, u);
     return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
   };
+  auto next = [&]() { return next_to(unit); };
 
   int fills = 0;  // loader: stages filled
 
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     for (int it = 0; next(); ++it) {
       const Unit u = *unit;
       const TileGeo tg = tile_geo<NT>(a, u);
-      const int kvh = a.by_nsub.div(u.h), sub = a.by_nsub.mod(u.h);
+      const int kvh = a.by_nsub.div(u.h);
       // The scales of this lane's row, read a tile before they are needed, and
       // its page, looked up two before.
       Order<C::LA> order(tg.nmax), of_scales(tg.nmax), of_pages(tg.nmax);
@@ -282,86 +290,6 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       };
       lookup();
       fetch_scales();
-      // ------------------------------------------------------- query tiles
-      {
-        const float gain = a.k_gain ? a.k_gain[kvh] : 1.f;
-        const float sc = a.sl2 * gain;
-        const int r = w * 32 + lane;
-        const int tk = a.by_gu.div(r), e = sub * a.gu + a.by_gu.mod(r);
-        auto source = [&](int t) -> const T* {
-          const int tok = (u.j * NT + t) * a.w + tk;
-          const bool is = r < a.w * a.gu && tok < u.s.nq && e < a.G && t < tg.nt;
-          return is ? static_cast<const T*>(a.q) + (u.s.q0 + tok) * a.qs[0] +
-                          static_cast<long long>(kvh * a.G + e) * a.qs[1]
-                    : nullptr;
-        };
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (const T* q = source(t))
-            for (int i = 0; i < D * static_cast<int>(sizeof(T)); i += 128)
-              prefetch_l1(reinterpret_cast<const char*>(q) + i);
-        if (it > 0) ok = ok && mbar_wait(q_empty, (it - 1) & 1, wc);
-        ok = __all_sync(0xffffffffu, ok);
-        constexpr int N = 16 / sizeof(T);  // elements of a load
-#pragma unroll 1
-        for (int t = 0; t < NT; ++t) {
-          const T* q = source(t);
-          float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f, f = sc == 0.f ? 1.f : fabsf(sc);
-          if constexpr (!std::is_same<T, __half>::value) {
-            float top = 0.f;
-            if (q) {
-#pragma unroll 4
-              for (int i = 0; i < D; i += N) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(q + i);
-                const T* x = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-                for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(to_float(x[k])));
-              }
-            }
-            // the power of two that brings `top` to [2^14, 2^15) (at most 2^126)
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-            const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
-            mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
-            f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
-          }
-          // (never 0, which would make a hidden score, -inf, NaN)
-          sQf[((it & 1) * NT + t) * 128 + r] = fmaxf(f, 0x1p-149f);
-          uint8_t* row = sQ + t * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll 2
-          for (int c = 0; c < D / 8; ++c) {  // 16-byte pieces of the fp16 row
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = 0.f;
-            if (q) {
-#pragma unroll
-              for (int i = 0; i < 8; i += N) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(q + c * 8 + i);
-                const T* y = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-                for (int k = 0; k < N; ++k) x[i + k] = to_float(y[k]) * mul;
-              }
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-              hi[k] = fp4::as_u32(h);
-              if constexpr (X2)
-                lo[k] = fp4::as_u32(__floats2half2_rn(x[2 * k] - __low2float(h),
-                                                      x[2 * k + 1] - __high2float(h)));
-            }
-            uint8_t* dst = row + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) * 16);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (X2)
-              *reinterpret_cast<uint4*>(dst + NT * C::TILE) =
-                  make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-      }
       // ------------------------------------------------------- key tiles
       for (; order.more(); order.next()) {
         uint32_t sb[D / 64];  // the row's scales, four a word
@@ -680,9 +608,98 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
     int g0 = 0;   // steps of earlier units (NT = 2: of this tile)
     int oph = 0;  // phases of o_done[t] consumed
     bool began = false;  // this CTA wrote its descriptor
-    for (int it = 0; next(); ++it) {
+    // Row r of the unit's query tile t as fp16 (see the top), while the products
+    // of the unit before end; returns the row's score factor.
+    auto load_q = [&](const Unit& u, int it) {
+      const TileGeo tg = tile_geo<NT>(a, u);
+      const int kvh = a.by_nsub.div(u.h), e = a.by_nsub.mod(u.h) * a.gu + a.by_gu.mod(r);
+      const int tok = (u.j * NT + t) * a.w + a.by_gu.div(r);
+      const T* q = r < a.w * a.gu && tok < u.s.nq && e < a.G
+                       ? static_cast<const T*>(a.q) + (u.s.q0 + tok) * a.qs[0] +
+                             static_cast<long long>(kvh * a.G + e) * a.qs[1]
+                       : nullptr;
+      constexpr int N = 16 / sizeof(T);  // elements of a load
+      constexpr int R = D / N < 4 ? D / N : 4;  // loads on their way
+      constexpr bool kAll = R == D / N;
+      const float sc = a.sl2 * (a.k_gain ? a.k_gain[kvh] : 1.f);
+      float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f, f = sc == 0.f ? 1.f : fabsf(sc);
+      if (it > 0) ok = ok && mbar_wait(q_empty, (it - 1) & 1, wc);
+      ok = __all_sync(0xffffffffu, ok);
+      if (t < tg.nt) {
+        uint4 raw[R];
+        auto load = [&](int i0) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (q) raw[i] = *reinterpret_cast<const uint4*>(q + (i0 + i) * N);
+          }
+        };
+        if (kAll) load(0);
+        if constexpr (!std::is_same<T, __half>::value) {
+          float top = 0.f;
+#pragma unroll 1
+          for (int i0 = 0; i0 < D / N; i0 += R) {
+            if (!kAll) load(i0);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const T* x = reinterpret_cast<const T*>(&raw[i]);
+#pragma unroll
+              for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(to_float(x[k])));
+            }
+          }
+          // the power of two that brings `top` to [2^14, 2^15) (at most 2^126)
+          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+          const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
+          mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
+          f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
+        }
+        uint8_t* row = sQ + t * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / N; i0 += R) {
+          if (!kAll) load(i0);
+#pragma unroll
+          for (int c = 0; c < R * N / 8; ++c) {  // 16-byte pieces of the fp16 row
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = c * 8 + 2 * k;
+              const T* x = reinterpret_cast<const T*>(&raw[at / N]) + at % N;
+              const float x0 = to_float(x[0]) * mul, x1 = to_float(x[1]) * mul;
+              const __half2 h = __floats2half2_rn(x0, x1);
+              hi[k] = fp4::as_u32(h);
+              if constexpr (X2)
+                lo[k] = fp4::as_u32(__floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h)));
+            }
+            const int piece = i0 * N / 8 + c;
+            uint8_t* dst = row + (piece >> 3) * (128 * 128) + (((piece & 7) ^ (r & 7)) * 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (X2)
+              *reinterpret_cast<uint4*>(dst + NT * C::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        fence_proxy_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      return fmaxf(f, 0x1p-149f);  // (never 0, which would make a hidden score, -inf, NaN)
+    };
+    Unit* const units2 = reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + C::WARPS;
+    bool more = next_to(unit);
+    float f_next = 1.f;
+    if (more) f_next = load_q(*unit, 0);
+    for (int it = 0; more; ++it) {
+      Unit* const unit = (it & 1) ? units2 + warp
+                                  : reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp;
+      Unit* const after = (it & 1) ? reinterpret_cast<Unit*>(smem + C::UNIT_OFF) + warp
+                                   : units2 + warp;
       const TileGeo tg = tile_geo<NT>(a, *unit);
-      if (t >= tg.nt) continue;
+      const float f = f_next;
+      if (t >= tg.nt) {
+        more = next_to(after);
+        if (more) f_next = load_q(*after, it + 1);
+        continue;
+      }
       const int tok0 = (unit->j * NT + t) * a.w;  // first token of the tile
       const int nq = unit->s.nq;
       const int tok = tok0 + a.by_gu.div(r);
@@ -691,7 +708,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       // visible keys of the row, counted from the piece's first key
       const int limit =
           (a.causal ? min(tg.nk, unit->s.off + tok + 1) : tg.nk) - tg.s0 * 128;
-      float m = -INFINITY, l = 0.f, f = 1.f;
+      float m = -INFINITY, l = 0.f;
       const int n = tg.n[t];
       for (int j = 0; j < n; ++j) {
         const int g = g0 + j;
@@ -702,7 +719,6 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                           ok && mbar_wait(&s_full[slot], (NT == 2 ? g : g >> 1) & 1, wc));
           if (ok) {
             tc_fence_after();
-            if (j == 0) f = sQf[((it & 1) * NT + t) * 128 + r];
             const int vis = limit - j * 128;  // visible keys of the row in this tile
             const bool edge = __any_sync(0xffffffffu, vis < 128);
             // (the weights take the scores' registers; X2 has none left for
@@ -792,6 +808,8 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
         // hand P_j to the MMA warp; met every step, also after a failed wait
         named_bar_sync(kPBar + (NT == 2 ? t : 0), 32 * 5);
       }
+      more = next_to(after);
+      if (more) f_next = load_q(*after, it + 1);
       if (n > 0) {
         ok = ok && mbar_wait(&o_done[t], static_cast<uint32_t>(oph & 1), wc);
         ok = __all_sync(0xffffffffu, ok);
@@ -837,10 +855,10 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
           load_o(c, ob);
           if (row_ok) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(orow + c * 32)[i] = make_float4(
-                  __uint_as_float(ob[4 * i]) * gain, __uint_as_float(ob[4 * i + 1]) * gain,
-                  __uint_as_float(ob[4 * i + 2]) * gain, __uint_as_float(ob[4 * i + 3]) * gain);
+            for (int i = 0; i < 32; ++i)
+              ob[i] = __float_as_uint(__uint_as_float(ob[i]) * gain);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) store32(orow + c * 32 + i, ob + i);
           }
         }
         if (row_ok) {
