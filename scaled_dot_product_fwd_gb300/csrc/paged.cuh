@@ -563,6 +563,26 @@ bool allow_smem(int bytes) {
   return true;
 }
 
+// Launch with programmatic stream serialization: the grid may start while the
+// one before it ends, and waits for that one itself (griddep_wait), before it
+// touches global memory.  Between two calls that are launched so a stream is
+// idle for some 2 us less.
+template <typename... P, typename... V>
+sdpa_status_t launch_overlapped(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t stream, const V&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
 // Query rows (tokens times heads of a kv head) of a sequence on average, by
 // which a kernel is chosen: the offsets are on the device.  A chunk among
 // single tokens is read in passes of few rows then.  Where the chunk's keys are

@@ -13,6 +13,7 @@
 #include "fp4.cuh"
 #include "paged.cuh"
 #include "paged_append.cuh"
+#include "ptx.cuh"
 #include "rotate.cuh"
 
 namespace gb300 {
@@ -85,6 +86,8 @@ __global__ void __launch_bounds__(kWarps * 32, kFp4 ? 3 : 4) paged_append_kernel
   // a warp's rows in fp32 where 16 consecutive elements of a rotated row come
   // from two lanes
   __shared__ __align__(16) float s_rows[kFp4 ? kWarps * 512 : 4];
+  griddep_launch_dependents();
+  griddep_wait();
   const long long tt = static_cast<long long>(blockIdx.x) * kWarps + warp;
   if (tt >= a.T) return;
   const int t = static_cast<int>(tt);
@@ -246,8 +249,7 @@ sdpa_status_t launch(AppendArgs& w, const LaunchEnv& env) {
   w.times = times;
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((groups + times - 1) / times));
-  paged_append_kernel<T, D, kFp4><<<grid, kWarps * 32, 0, env.stream>>>(w);
-  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  return launch_overlapped(paged_append_kernel<T, D, kFp4>, grid, kWarps * 32, 0, env.stream, w);
 }
 
 template <typename T>

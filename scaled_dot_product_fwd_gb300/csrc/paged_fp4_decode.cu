@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   }
   const WaitCtl wc{a.wait_ns, &s_abort, a.status};
   griddep_launch_dependents();
+  griddep_wait();
   const AttendUnits units{a.by_w, lg_tile, a.causal, 1};
   const int heads = ((a.Hkv + hw - 1) >> lg_hw) * a.nsub;
   plan_share<kT>(a, units, heads, 1, scratch, &sh);  // (ends with a CTA barrier)
@@ -805,20 +806,11 @@ sdpa_status_t launch(Args& a, const LaunchEnv& env) {
   CUtensorMap tk = {}, tv = {};
   const CodeMaps cm = encode_code_maps(
       a, D / 2, 5, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, &tk, &tv);
-  kern<<<a.nctas, kT, smem, env.stream>>>(tk, tv, a, cm, lg_hw);
-  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * env.num_sms));
-  cfg.blockDim = dim3(kT);
-  cfg.stream = env.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_fp4_merge_kernel<T, D>, a, 8 * NT, lg_hw) == cudaSuccess
-             ? SDPA_OK
-             : SDPA_ERR_CUDA;
+  const sdpa_status_t st =
+      launch_overlapped(kern, dim3(a.nctas), kT, smem, env.stream, tk, tv, a, cm, lg_hw);
+  if (st != SDPA_OK) return st;
+  return launch_overlapped(paged_fp4_merge_kernel<T, D>, dim3(2 * env.num_sms), kT, 0, env.stream,
+                           a, 8 * NT, lg_hw);
 }
 
 template <typename T>

@@ -944,17 +944,9 @@ sdpa_status_t launch_f4(Args& a, const LaunchEnv& env) {
   CUtensorMap tk = {}, tv = {};
   const CodeMaps cm = encode_code_maps(
       a, D / 2, 7, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, &tk, &tv);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.nctas));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = env.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a, cm) != cudaSuccess) return SDPA_ERR_CUDA;
+  const sdpa_status_t st = launch_overlapped(kern, dim3(static_cast<unsigned>(a.nctas)), C::THREADS,
+                                             C::SMEM, env.stream, tk, tv, a, cm);
+  if (st != SDPA_OK) return st;
   const int dtype = sizeof(T) == 4                      ? SDPA_F32
                     : std::is_same<T, __half>::value ? SDPA_F16
                                                      : SDPA_BF16;

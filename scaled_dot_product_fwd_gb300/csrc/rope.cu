@@ -46,6 +46,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int u = lane & ((1 << a.lg_u) - 1), r = lane >> a.lg_u;
   const int lg_h = 5 - a.lg_u - a.lg_t;  // log2 of heads at a time
+  griddep_launch_dependents();
+  griddep_wait();
   const long long t =
       ((static_cast<long long>(blockIdx.x) * kWarps + warp) << a.lg_t) + (r & ((1 << a.lg_t) - 1));
   if (t >= a.n) return;
@@ -177,13 +179,11 @@ sdpa_status_t launch_rope(const sdpa_rope_params_t& p, const void* q, const void
   a.per = per;
   const dim3 grid(static_cast<unsigned>((warps + kWarps - 1) / kWarps),
                   static_cast<unsigned>((heads + per - 1) / per));
-  if (p.dtype == SDPA_F32)
-    rope_kernel<float><<<grid, kWarps * 32, 0, env.stream>>>(a);
-  else if (p.dtype == SDPA_F16)
-    rope_kernel<__half><<<grid, kWarps * 32, 0, env.stream>>>(a);
-  else
-    rope_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, env.stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  auto go = [&](auto kern) {
+    return paged::launch_overlapped(kern, grid, kWarps * 32, 0, env.stream, a);
+  };
+  if (p.dtype == SDPA_F32) return go(rope_kernel<float>);
+  return p.dtype == SDPA_F16 ? go(rope_kernel<__half>) : go(rope_kernel<__nv_bfloat16>);
 }
 
 }  // namespace gb300
