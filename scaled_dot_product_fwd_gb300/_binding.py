@@ -1003,56 +1003,67 @@ def _check_table(table, dev):
     return s[0], 2 * s[1]
 
 
+def _rope_out(out, x, shape, dtype, dev):
+    """The strides of a given output."""
+    st = out.stride()
+    if out.shape != shape or out.dtype is not dtype or out.get_device() != dev or st[3] != 1:
+        raise ValueError("q_out and k_out must be like their inputs with a contiguous last "
+                         "dimension")
+    return st
+
+
 def _rope(q, k, table, positions, interleaved, q_out, k_out, stream, transpose):
     torch = _torch()
     dev = q.get_device()
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    shape, dtype = q.shape, q.dtype
-    qs = q.stride()
+    shape, dtype, qs = q.shape, q.dtype, q.stride()
     if len(shape) != 4 or qs[3] != 1:
         raise ValueError("q must be [batch, heads, length, D] with a contiguous last dimension")
     B, H, L, D = shape
-    if k is not None and (k.dim() != 4 or k.get_device() != dev or k.stride(3) != 1
-                          or k.shape[0] != B or k.shape[2:] != shape[2:]):
-        raise ValueError("k must be [batch, kv heads, length, D] like q")
-    if k is not None and k.dtype is not dtype:
-        raise TypeError("q and k must share a dtype")
+    heads, kp, kop, ks, ko = 0, None, None, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        kshape, ks = k.shape, k.stride()
+        if (len(kshape) != 4 or kshape[0] != B or kshape[2] != L or kshape[3] != D or ks[3] != 1
+                or k.get_device() != dev):
+            raise ValueError("k must be [batch, kv heads, length, D] like q")
+        if k.dtype is not dtype:
+            raise TypeError("q and k must share a dtype")
+        heads, kp = kshape[1], k.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     P, R = _check_table(table, dev)
     pos, pstride = 0, 0
     if positions is not None:
         if positions.dtype is not torch.int32 or positions.get_device() != dev:
             raise TypeError("positions must be an int32 CUDA tensor on the same device")
         ps, pst = positions.shape, positions.stride()
-        if ps[-1:] != (L,) or len(ps) > 2 or (len(ps) == 2 and ps[0] not in (1, B)) \
-                or (L > 1 and pst[-1] != 1):
+        n = len(ps)
+        if (n not in (1, 2) or ps[-1] != L or (n == 2 and ps[0] != B and ps[0] != 1)
+                or (L > 1 and pst[-1] != 1)):
             raise ValueError("positions must be [length] or [batch, length] with contiguous rows")
         pos = positions.data_ptr()
-        pstride = pst[0] if len(ps) == 2 and ps[0] > 1 else 0
+        pstride = pst[0] if n == 2 and ps[0] > 1 else 0
     if stream is not None or torch._C._cuda_getDevice() != dev:
         return _elsewhere(dev, stream, lambda: _rope(q, k, table, positions, interleaved, q_out,
                                                      k_out, None, transpose))
-    outs = []
-    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is None:
-            if out is not None:
-                raise ValueError("%s without its input" % name)
-        elif out is None:
-            out = torch.empty_like(x)
-        elif (out.shape != x.shape or out.dtype is not dtype or out.get_device() != dev
-              or out.stride(3) != 1):
-            raise ValueError("%s must be like its input with a contiguous last dimension" % name)
-        outs.append(out)
-    q_out, k_out = outs
-    zero = (0, 0, 0)
-    qo = q_out.stride()
-    ks, ko = (zero, zero) if k is None else (k.stride(), k_out.stride())
-    p = _ROPE.pack(B, H, 0 if k is None else k.shape[1], L, D, dtype_code(dtype), transpose, 0,
-                   table.data_ptr(), P, R, 1 if interleaved else 0, pos, pstride, qs[0], qs[1],
-                   qs[2], ks[0], ks[1], ks[2], qo[0], qo[1], qo[2], ko[0], ko[1], ko[2])
-    _paged_status(_paged_call("sdpa_rope")(
-        p, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-        None if k is None else k_out.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)))
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        qo = q_out.stride()
+    else:
+        qo = _rope_out(q_out, q, shape, dtype, dev)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k)
+            ko = k_out.stride()
+        else:
+            ko = _rope_out(k_out, k, kshape, dtype, dev)
+        kop = k_out.data_ptr()
+    p = _ROPE.pack(B, H, heads, L, D, dtype_code(dtype), transpose, 0, table.data_ptr(), P, R,
+                   1 if interleaved else 0, pos, pstride, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
+                   qo[0], qo[1], qo[2], ko[0], ko[1], ko[2])
+    _paged_status(_paged_call("sdpa_rope")(p, q.data_ptr(), kp, q_out.data_ptr(), kop,
+                                           torch._C._cuda_getCurrentRawStream(dev)))
     return q_out, k_out
 
 

@@ -478,7 +478,7 @@ struct Boxes {
 sdpa_status_t launch_paged_simt(paged::Args a, int head_dim, int dtype, const LaunchEnv& env);
 // Rows of a tile of the 4-bit cache's few-row kernel for this call (8 or 16; 0:
 // the calls of more rows).
-int paged_fp4_decode_rows(const paged::Args& a);
+int paged_fp4_decode_rows(const paged::Args& a, int dtype);
 sdpa_status_t launch_paged_fp4_decode(paged::Args a, int head_dim, int dtype, int rows,
                                       const LaunchEnv& env);
 sdpa_status_t launch_paged_fp4_tc_d64(paged::Args a, int dtype, const LaunchEnv& env);

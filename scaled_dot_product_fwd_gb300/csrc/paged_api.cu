@@ -512,7 +512,7 @@ sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* p, const sdpa_fp
   }
   a.k_gain = cache->k_gain;
   a.v_gain = cache->v_gain;
-  if (const int rows = paged_fp4_decode_rows(a))
+  if (const int rows = paged_fp4_decode_rows(a, p->dtype))
     st = launch_paged_fp4_decode(a, p->head_dim, p->dtype, rows, env);
   else
     st = p->head_dim == 64 ? launch_paged_fp4_tc_d64(a, p->dtype, env)

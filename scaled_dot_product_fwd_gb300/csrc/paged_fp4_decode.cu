@@ -1,6 +1,6 @@
 // paged_fp4_decode.cu — attention over the 4-bit paged cache where a sequence
-// has few query rows (single tokens: the heads of a kv head), up to 8 or 16
-// rows of (token, head) a unit; every element type, head_dim 64/128.
+// has few query rows (single tokens: the heads of a kv head), 8 or 16 rows of
+// (token, head) a unit; every element type, head_dim 64/128.
 //
 // A key and kv head is 2 (D / 2 + D / 16) bytes, 3.6 times fewer than in 16
 // bits, so the widening of its 2 D codes is what a kernel has to keep beside
@@ -29,6 +29,16 @@
 // warp has 32 keys of a tile and a ring of its own in shared memory, filled by
 // asynchronous copies two steps ahead, so nothing but the end of a unit meets
 // a CTA barrier.
+//
+// 8 sequences of 32768 keys, 32 heads over 8, head_dim 128, bf16: 77 us a call,
+// 3.9 TB/s, of which this kernel 72.  Bound by instruction issue: 380 a warp
+// for 16 keys (110 scores, 124 values, 29 softmax, the rest copies and lookups),
+// 2.5 a clock and SM; the ALU pipe, which converts the codes, 55 % busy, DRAM 62 %
+// of the copy rate.  What brought it there (us): cp.async by each lane 115, by
+// rows of neighbouring heads 102, tensor copies 90, copies issued without a loop
+// over lanes and a merge over the whole grid 81, overlapped launches 77.  A ring
+// of three stages instead of two, three CTAs an SM (80 registers, spills) and
+// the next unit's copies beside the last one's end gave nothing or cost time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -646,8 +656,9 @@ constexpr int kMaxUnits = 1024;  // CTAs of a call, at most
 // (their descriptors are compacted first): M = max of the m's, weights 2^(m -
 // M), in the order of the pieces.  Bound by the latency of its three dependent
 // loads, so a row is spread over as many warps of a block as leave all warps of
-// the grid with at most one row: 32 rows of 38 pieces 19 us with a block a unit
-// and 16th of its rows, 4 so.
+// the grid with at most one row (8 units of 32 rows in 38 pieces, cold: 13 us
+// against 19 with 16 blocks a unit; 16 units of 16 rows in 19 pieces: 10 against
+// 13).
 template <typename T, int D>
 __global__ void __launch_bounds__(kT) paged_fp4_merge_kernel(const Args a, const int nr,
                                                              const int lg_hw) {
@@ -822,9 +833,15 @@ sdpa_status_t by_size(Args& a, int head_dim, int rows, const LaunchEnv& env) {
 }  // namespace
 }  // namespace paged
 
-int paged_fp4_decode_rows(const paged::Args& a) {
+int paged_fp4_decode_rows(const paged::Args& a, int dtype) {
+  // 16 sequences of 4096 keys (us): 8 rows a tile, 16 rows, the kernel of many
+  // rows.  32 heads over 8, head_dim 128, bf16: 8 rows a sequence and kv head 35,
+  // 42, 56; 16 rows 52, 46, 56; 24 rows 71, 71, 56.  16 heads over 4, head_dim 64,
+  // fp32, whose many-row kernel does twice the work: 8 rows 21, 27, 46; 16 rows
+  // 29, 28, 46; 32 rows 45, 38, 47.
   const long long rows = paged::call_rows(a);
-  return a.G > 16 ? 0 : a.G <= 8 && rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
+  const int most = dtype == SDPA_F32 ? 32 : 16;
+  return a.G > 16 ? 0 : a.G <= 8 && rows <= 8 ? 8 : rows <= most ? 16 : 0;
 }
 
 sdpa_status_t launch_paged_fp4_decode(paged::Args a, int head_dim, int dtype, int rows,
