@@ -8,14 +8,16 @@
 //  - A loader warp brings the codes of the 128-key tiles to a staging ring
 //    (tensor copies), and four warps widen them: a lane has a row of a tile,
 //    reads its scales a tile ahead and writes it as fp16 where tcgen05.mma
-//    reads it (128-byte swizzle).  Code times scale is exact in fp16 (fp4.cuh).  Rows past the
-//    length, or of a page that the table does not name, become zeros there.
+//    reads it (128-byte swizzle).  Code times scale is exact in fp16 (fp4.cuh).
+//    Rows past the length, or of a page that the table does not name, become
+//    zeros there.
 //  - Both products are in fp16 whatever the type of q.  The softmax warps lay
-//    down the query tiles, a row a thread, while the products of the unit before
-//    end: fp16 rows as they are, bf16 ones times a power of two
-//    a row that brings the row's largest to [2^14, 2^15) (what fp16 then drops
-//    is below 2^-39 of it); fp32 ones likewise as a sum of two fp16 parts (22
-//    bits), each multiplied with K, and so do their weights with V (NT = 1).
+//    down the query tiles while the products of the unit before end (whole rows
+//    by asynchronous copies, then each lane its own row in place): fp16 rows as
+//    they are, bf16 ones times a power of two a row that brings the row's
+//    largest to [2^14, 2^15) (what fp16 then drops is below 2^-39 of it); fp32
+//    ones likewise as a sum of two fp16 parts (22 bits), each multiplied with K,
+//    and so do their weights with V (NT = 1).
 //    A row's score factor is scale * gain / that power; its sign goes into the
 //    row, so that the largest raw score is the largest score.
 //  - Weights are 2^kHead at the reference maximum, so that fp16 holds them to
@@ -24,15 +26,19 @@
 // widened tiles (64 KB a key tile) come on top of the products' reads of shared
 // memory (192 KB), at 128 bytes a clock 2300 of the 3200 that a key tile takes.
 //
-// 4096 tokens over 32768 keys, 32 heads over 8, head_dim 128, bf16: 1460 us, 1410
+// 4096 tokens over 32768 keys, 32 heads over 8, head_dim 128, bf16: 1530 us, 1350
 // TFLOP/s (the 16-bit cache's kernel 1190 to 1374 us); tensor pipe 56 % active on
 // 2048 tokens over 16384 keys.  Four ragged chunks of up to 700 tokens over 5000
-// keys: 154 us, 720 TFLOP/s; of a CTA's 190 us at 4 x 700 tokens, 12 go before the
-// first product and 5 a unit between units.  The steps (us, the first case): copies
-// and widening by the same four warps 1975; a loader warp, scales read by the
-// widening lanes, all scores in one load, and the registers split anew 1505 (of
-// 176 / 80 / 80, 184 / 72 / 72, 184 / 64 / 80 and 168 / 96 / 80 a thread the first);
-// queries by the softmax warps, 4 loads on their way, 1460 (8 and 16: 1550).
+// keys: 151 us, 735 TFLOP/s.  The steps (us, the first case): copies and widening
+// by the same four warps 1975; a loader warp, scales read by the widening lanes,
+// all scores in one load, and the registers split anew 1505; queries by the
+// softmax warps, a row a lane in 16-byte loads, 1465; queries by asynchronous
+// copies of whole rows 1530, but the chunks 156 -> 151, 300 tokens over themselves
+// 28 -> 24, 8 x 16 tokens over 4096 keys 45 -> 37 and head_dim 64 (4 x 700 over
+// 5000) 222 -> 200.  The compiler's schedule of the softmax turns on the split of
+// the registers and on what else that role holds: 176 / 80 / 80 a thread 1600 and
+// 159 (chunks), 192 / 64 / 64 1912 and 168; the query loops unrolled by 1, 3 and 4
+// instead of 2: 1587, 1637 and 1796.
 #pragma once
 
 #include <atomic>
@@ -72,9 +78,9 @@ struct F4Cfg {
   static constexpr int WARPS = SOFT_WARPS + 8;
   static constexpr int THREADS = 32 * WARPS;
   // registers of a thread by warpgroup (their sum is the launch's)
-  static constexpr uint32_t SOFT_REGS = NT == 2 ? 176 : 232;
-  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 80 : 136;
-  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 80 : 136;
+  static constexpr uint32_t SOFT_REGS = NT == 2 ? 184 : 232;
+  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 72 : 136;
+  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 72 : 136;
   static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
   static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
   static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
@@ -628,61 +634,84 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                        ? static_cast<const T*>(a.q) + (u.s.q0 + tok) * a.qs[0] +
                              static_cast<long long>(kvh * a.G + e) * a.qs[1]
                        : nullptr;
-      constexpr int N = 16 / sizeof(T);  // elements of a load
-      constexpr int R = D / N < 4 ? D / N : 4;  // loads on their way
-      constexpr bool kAll = R == D / N;
       const float sc = a.sl2 * (a.k_gain ? a.k_gain[kvh] : 1.f);
       float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f, f = sc == 0.f ? 1.f : fabsf(sc);
+      // the power of two that brings `top` to [2^14, 2^15) (at most 2^126), into
+      // mul and, inverted, f
+      auto scale_by = [&](float top) {
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+        const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
+        mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
+        f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
+      };
       if (it > 0) ok = ok && mbar_wait(q_empty, (it - 1) & 1, wc);
       ok = __all_sync(0xffffffffu, ok);
       if (t < tg.nt) {
-        uint4 raw[R];
-        auto load = [&](int i0) {
+        // 16-byte piece c of the fp16 row rr
+        auto at = [&](int rr, int c) {
+          return sQ + t * C::TILE + (c >> 3) * (128 * 128) + (rr >> 3) * 1024 + (rr & 7) * 128 +
+                 (((c & 7) ^ (rr & 7)) * 16);
+        };
+        // The warp's rows as they are, whole rows at a time (zeros where there is
+        // none), then each lane's own in place.  Pieces 2 c and 2 c + 1 of an fp32
+        // row come where its fp16 parts' pieces c will be.
+        constexpr int LR = D * sizeof(T) / 16;  // pieces of a row
+        const unsigned long long src = reinterpret_cast<unsigned long long>(q);
+#pragma unroll 2
+        for (int i = 0; i < LR; ++i) {
+          const int from = i * (32 / LR) + lane / LR, p = lane % LR;
+          const unsigned long long s = __shfl_sync(0xffffffffu, src, from);
+          const uint8_t* dst = X2 ? at((warp & 3) * 32 + from, p >> 1) + (p & 1) * NT * C::TILE
+                                  : at((warp & 3) * 32 + from, p);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+                       "l"(s ? s + p * 16 : reinterpret_cast<unsigned long long>(a.q)),
+                       "r"(s ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        // the 8 elements of piece c
+        auto load = [&](int c, float (&x)[8]) {
+          if constexpr (X2) {
 #pragma unroll
-          for (int i = 0; i < R; ++i) {
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (q) raw[i] = *reinterpret_cast<const uint4*>(q + (i0 + i) * N);
+            for (int h = 0; h < 2; ++h) {
+              const float4 v = *reinterpret_cast<const float4*>(at(r, c) + h * NT * C::TILE);
+              x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+            }
+          } else {
+            const uint4 raw = *reinterpret_cast<const uint4*>(at(r, c));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = to_float(reinterpret_cast<const T*>(&raw)[k]);
           }
         };
-        if (kAll) load(0);
-        if constexpr (!std::is_same<T, __half>::value) {
+        constexpr bool kHalf = std::is_same<T, __half>::value;
+        if constexpr (!kHalf) {
           float top = 0.f;
-#pragma unroll 1
-          for (int i0 = 0; i0 < D / N; i0 += R) {
-            if (!kAll) load(i0);
+#pragma unroll 2
+          for (int c = 0; c < D / 8; ++c) {
+            float x[8];
+            load(c, x);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const T* x = reinterpret_cast<const T*>(&raw[i]);
-#pragma unroll
-              for (int k = 0; k < N; ++k) top = fmaxf(top, fabsf(to_float(x[k])));
-            }
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
           }
-          // the power of two that brings `top` to [2^14, 2^15) (at most 2^126)
-          const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-          const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
-          mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
-          f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
+          scale_by(top);
         }
-        uint8_t* row = sQ + t * C::TILE + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / N; i0 += R) {
-          if (!kAll) load(i0);
-#pragma unroll
-          for (int c = 0; c < R * N / 8; ++c) {  // 16-byte pieces of the fp16 row
+        if (!kHalf || mul != 1.f) {
+#pragma unroll 2
+          for (int c = 0; c < D / 8; ++c) {
+            float x[8];
+            load(c, x);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int at = c * 8 + 2 * k;
-              const T* x = reinterpret_cast<const T*>(&raw[at / N]) + at % N;
-              const float x0 = to_float(x[0]) * mul, x1 = to_float(x[1]) * mul;
+              const float x0 = x[2 * k] * mul, x1 = x[2 * k + 1] * mul;
               const __half2 h = __floats2half2_rn(x0, x1);
               hi[k] = fp4::as_u32(h);
               if constexpr (X2)
                 lo[k] = fp4::as_u32(__floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h)));
             }
-            const int piece = i0 * N / 8 + c;
-            uint8_t* dst = row + (piece >> 3) * (128 * 128) + (((piece & 7) ^ (r & 7)) * 16);
+            uint8_t* dst = at(r, c);
             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             if constexpr (X2)
               *reinterpret_cast<uint4*>(dst + NT * C::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
