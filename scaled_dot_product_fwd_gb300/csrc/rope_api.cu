@@ -91,6 +91,8 @@ sdpa_status_t sdpa_rope(const sdpa_rope_params_t* p, const void* q, const void* 
   if (st == SDPA_OK)
     st = check_pair(*p, p->num_kv_heads, k, k_out, p->k_stride, p->k_out_stride);
   if (st != SDPA_OK) return st;
+  if (p->num_q_heads > 0 && p->num_kv_heads > 0 && q_out == k_out)
+    return SDPA_ERR_INVALID_ARGUMENT;
   LaunchEnv env;
   env.wait_limit_ns = current_wait_limit_ns();
   env.stream = static_cast<cudaStream_t>(stream);

@@ -62,6 +62,11 @@ def test_rope_rejects_pointers(sdpa_lib):
     assert rope(sdpa_lib, R(q_out_stride=(2560, 64, 512)), q_out=1024) == 1
 
 
+def test_rope_rejects_one_output_for_both(sdpa_lib):
+    assert rope(sdpa_lib, R(), q_out=4096, k_out=4096) == 1
+    assert rope(sdpa_lib, R(), q=1024, k=1024, q_out=1024, k_out=1024) == 1
+
+
 def test_rope_nothing_to_do(sdpa_lib):
     for kw in (dict(batch=0), dict(seq_len=0), dict(num_q_heads=0, num_kv_heads=0)):
         assert rope(sdpa_lib, R(**kw), None, None, None, None) == 0
