@@ -586,7 +586,7 @@ SDPA_API sdpa_status_t sdpa_rope_table(float* table, int64_t length, int32_t rot
  * or 512, element strides {batch, head, row} (D contiguous; times the element
  * size multiples of 16 bytes); q_out and k_out likewise, either the input
  * itself (same pointer and strides) or without a common element with the
- * inputs.  num_kv_heads 0 (k and k_out unused) rotates q alone.
+ * inputs and each other.  num_kv_heads 0 (k and k_out unused) rotates q alone.
  * rotation.positions: int32, token (b, l) at b * position_stride + l (a stride
  * of 0 shares them among the batches); NULL: l itself.  A position outside
  * [0, table_len) leaves its row as it is and sets the device status word to
