@@ -512,6 +512,10 @@ sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* p, const sdpa_fp
   }
   a.k_gain = cache->k_gain;
   a.v_gain = cache->v_gain;
+  if (p->num_pages == 0) {  // (nothing is read there, but copies of no bytes name an address)
+    a.k = a.v = q;
+    a.k_scales = a.v_scales = static_cast<const char*>(q);
+  }
   if (const int rows = paged_fp4_decode_rows(a, p->dtype))
     st = launch_paged_fp4_decode(a, p->head_dim, p->dtype, rows, env);
   else

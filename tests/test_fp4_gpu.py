@@ -328,6 +328,22 @@ def test_offsets_past_32_bits(cuda, S, nq):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("nq", [1, 40])
+def test_cache_of_no_pages(cuda, nq, dtype):
+    """Every entry of the table names no page then."""
+    import scaled_dot_product_fwd_gb300 as S
+    t = Cache4(cuda, [nq, nq], [100, 0], 8, 2, 64, dtype, 16)
+    none = [x[:0] for x in t.codes + t.scales]
+    for x in t.KV[0]:
+        x[:] = 0
+    o, lse = S.sdpa_paged_forward_fp4(t.q, *none, t.table, t.lens, cu_seqlens_q=t.cu)
+    cuda.cuda.synchronize()
+    assert S.sdpa_device_status() == 7
+    check(t, o, lse, 1 / 8)
+    assert S.sdpa_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nq", [1, 40])
 def test_bad_pages(cuda, nq, dtype):
     """An entry that names no page reads as zero keys and values and is reported."""
     import scaled_dot_product_fwd_gb300 as S
