@@ -26,19 +26,19 @@
 // widened tiles (64 KB a key tile) come on top of the products' reads of shared
 // memory (192 KB), at 128 bytes a clock 2300 of the 3200 that a key tile takes.
 //
-// 4096 tokens over 32768 keys, 32 heads over 8, head_dim 128, bf16: 1530 us, 1350
+// 4096 tokens over 32768 keys, 32 heads over 8, head_dim 128, bf16: 1450 us, 1420
 // TFLOP/s (the 16-bit cache's kernel 1190 to 1374 us); tensor pipe 56 % active on
 // 2048 tokens over 16384 keys.  Four ragged chunks of up to 700 tokens over 5000
-// keys: 151 us, 735 TFLOP/s.  The steps (us, the first case): copies and widening
+// keys: 150 us, 737 TFLOP/s.  The steps (us, the first case): copies and widening
 // by the same four warps 1975; a loader warp, scales read by the widening lanes,
 // all scores in one load, and the registers split anew 1505; queries by the
 // softmax warps, a row a lane in 16-byte loads, 1465; queries by asynchronous
 // copies of whole rows 1530, but the chunks 156 -> 151, 300 tokens over themselves
 // 28 -> 24, 8 x 16 tokens over 4096 keys 45 -> 37 and head_dim 64 (4 x 700 over
-// 5000) 222 -> 200.  The compiler's schedule of the softmax turns on the split of
-// the registers and on what else that role holds: 176 / 80 / 80 a thread 1600 and
-// 159 (chunks), 192 / 64 / 64 1912 and 168; the query loops unrolled by 1, 3 and 4
-// instead of 2: 1587, 1637 and 1796.
+// 5000) 222 -> 200; these in a function of their own 1450.  The split of the
+// registers counts (spills of the softmax or of the issuing warps): 184 / 72 / 72 a
+// thread 1470, 176 / 80 / 80 1471, 176 / 88 / 72 1500, 192 / 64 / 64 1725, 168 / 88 / 88
+// 1750.
 #pragma once
 
 #include <atomic>
@@ -79,8 +79,8 @@ struct F4Cfg {
   static constexpr int THREADS = 32 * WARPS;
   // registers of a thread by warpgroup (their sum is the launch's)
   static constexpr uint32_t SOFT_REGS = NT == 2 ? 184 : 232;
-  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 72 : 136;
-  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 72 : 136;
+  static constexpr uint32_t CONTROL_REGS = NT == 2 ? 80 : 136;
+  static constexpr uint32_t WIDEN_REGS = NT == 2 ? 64 : 136;
   static constexpr int SHARE_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
   static constexpr int SCRATCH_OFF = SHARE_OFF + static_cast<int>(sizeof(Share));
   static constexpr int WALK_OFF = (SCRATCH_OFF + (WARPS + 1) * 8 + 15) / 16 * 16;
@@ -178,6 +178,107 @@ __device__ __forceinline__ void store32(float* p, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
                "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                : "memory");
+}
+
+// A warp's 32 query rows (q: this lane's, or null; any: an address to name where
+// there is none) times mul, -1, 0 or 1, as fp16 rows of the query tile `tile`.
+// Returns two factors that a row's scores take for it (as one, 2^-127 would be
+// subnormal).
+template <typename T, int D, int NT>
+__device__ __forceinline__ float2 lay_down(uint8_t* tile, int quarter, const T* q, const void* any,
+                                        float mul) {
+  constexpr bool X2 = sizeof(T) == 4;
+  using C = F4Cfg<D, NT, X2>;
+  const int lane = threadIdx.x & 31, r = quarter * 32 + lane;
+  float f = 1.f, f2 = 1.f;
+  // the power of two that brings `top` to [2^14, 2^15) (at most 2^126), into mul
+  // and, inverted, f f2
+  auto scale_by = [&](float top) {
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+    const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
+    mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    f = __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
+    f2 = __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
+  };
+  // 16-byte piece c of the fp16 row rr
+  auto at = [&](int rr, int c) {
+    return tile + (c >> 3) * (128 * 128) + (rr >> 3) * 1024 + (rr & 7) * 128 +
+           (((c & 7) ^ (rr & 7)) * 16);
+  };
+  // The warp's rows as they are, whole rows at a time (zeros where there is
+  // none), then each lane's own in place.  Pieces 2 c and 2 c + 1 of an fp32
+  // row come where its fp16 parts' pieces c will be.
+  constexpr int LR = D * sizeof(T) / 16;  // pieces of a row
+  const unsigned long long src = reinterpret_cast<unsigned long long>(q);
+#pragma unroll 2
+  for (int i = 0; i < LR; ++i) {
+    const int from = i * (32 / LR) + lane / LR, p = lane % LR;
+    const unsigned long long s = __shfl_sync(0xffffffffu, src, from);
+    const uint8_t* dst = X2 ? at(quarter * 32 + from, p >> 1) + (p & 1) * NT * C::TILE
+                            : at(quarter * 32 + from, p);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
+                 "l"(s ? s + p * 16 : reinterpret_cast<unsigned long long>(any)),
+                 "r"(s ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  // the 8 elements of piece c
+  auto load = [&](int c, float (&x)[8]) {
+    if constexpr (X2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 v = *reinterpret_cast<const float4*>(at(r, c) + h * NT * C::TILE);
+        x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+      }
+    } else {
+      const uint4 raw = *reinterpret_cast<const uint4*>(at(r, c));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = to_float(reinterpret_cast<const T*>(&raw)[k]);
+    }
+  };
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  if constexpr (!kHalf) {
+    float top = 0.f;
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+      float x[8];
+      load(c, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+    }
+    scale_by(top);
+  }
+  if (!kHalf || mul != 1.f) {
+#pragma unroll 2
+    for (int c = 0; c < D / 8; ++c) {
+      float x[8];
+      load(c, x);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = x[2 * k] * mul, x1 = x[2 * k + 1] * mul;
+        const __half2 h = __floats2half2_rn(x0, x1);
+        hi[k] = fp4::as_u32(h);
+        if constexpr (X2)
+          lo[k] = fp4::as_u32(__floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h)));
+      }
+      uint8_t* dst = at(r, c);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (X2)
+        *reinterpret_cast<uint4*>(dst + NT * C::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
+  return make_float2(f, f2);
+}
+// Two tiles of head_dim 128 have it in a function of its own: the compiler's
+// schedule of the softmax turns on what else that role's loop holds.  Apart and
+// inside: 4096 tokens over 32768 keys 1450 and 1530 us; head_dim 64, 2048 tokens
+// over 16384 keys 402 and 316; one tile, 8 x 16 tokens over 4096 keys 41 and 38.
+template <typename T, int D, int NT>
+__device__ __noinline__ float2 lay_down_apart(uint8_t* tile, int quarter, const T* q,
+                                              const void* any, float mul) {
+  return lay_down<T, D, NT>(tile, quarter, q, any, mul);
 }
 
 template <typename T, int D, int NT>
@@ -635,88 +736,14 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                              static_cast<long long>(kvh * a.G + e) * a.qs[1]
                        : nullptr;
       const float sc = a.sl2 * (a.k_gain ? a.k_gain[kvh] : 1.f);
-      float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f, f = sc == 0.f ? 1.f : fabsf(sc);
-      // the power of two that brings `top` to [2^14, 2^15) (at most 2^126), into
-      // mul and, inverted, f
-      auto scale_by = [&](float top) {
-        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-        const int up = ex == 0 ? 126 : ex == 255 ? 0 : min(127 + 14 - ex, 126);
-        mul *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        f *= __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
-        f *= __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
-      };
+      const float mul = sc < 0.f ? -1.f : sc == 0.f ? 0.f : 1.f;
+      float f = sc == 0.f ? 1.f : fabsf(sc);
       if (it > 0) ok = ok && mbar_wait(q_empty, (it - 1) & 1, wc);
       ok = __all_sync(0xffffffffu, ok);
       if (t < tg.nt) {
-        // 16-byte piece c of the fp16 row rr
-        auto at = [&](int rr, int c) {
-          return sQ + t * C::TILE + (c >> 3) * (128 * 128) + (rr >> 3) * 1024 + (rr & 7) * 128 +
-                 (((c & 7) ^ (rr & 7)) * 16);
-        };
-        // The warp's rows as they are, whole rows at a time (zeros where there is
-        // none), then each lane's own in place.  Pieces 2 c and 2 c + 1 of an fp32
-        // row come where its fp16 parts' pieces c will be.
-        constexpr int LR = D * sizeof(T) / 16;  // pieces of a row
-        const unsigned long long src = reinterpret_cast<unsigned long long>(q);
-#pragma unroll 2
-        for (int i = 0; i < LR; ++i) {
-          const int from = i * (32 / LR) + lane / LR, p = lane % LR;
-          const unsigned long long s = __shfl_sync(0xffffffffu, src, from);
-          const uint8_t* dst = X2 ? at((warp & 3) * 32 + from, p >> 1) + (p & 1) * NT * C::TILE
-                                  : at((warp & 3) * 32 + from, p);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
-                       "l"(s ? s + p * 16 : reinterpret_cast<unsigned long long>(a.q)),
-                       "r"(s ? 16 : 0)
-                       : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-        // the 8 elements of piece c
-        auto load = [&](int c, float (&x)[8]) {
-          if constexpr (X2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 v = *reinterpret_cast<const float4*>(at(r, c) + h * NT * C::TILE);
-              x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
-            }
-          } else {
-            const uint4 raw = *reinterpret_cast<const uint4*>(at(r, c));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = to_float(reinterpret_cast<const T*>(&raw)[k]);
-          }
-        };
-        constexpr bool kHalf = std::is_same<T, __half>::value;
-        if constexpr (!kHalf) {
-          float top = 0.f;
-#pragma unroll 2
-          for (int c = 0; c < D / 8; ++c) {
-            float x[8];
-            load(c, x);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-          }
-          scale_by(top);
-        }
-        if (!kHalf || mul != 1.f) {
-#pragma unroll 2
-          for (int c = 0; c < D / 8; ++c) {
-            float x[8];
-            load(c, x);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x0 = x[2 * k] * mul, x1 = x[2 * k + 1] * mul;
-              const __half2 h = __floats2half2_rn(x0, x1);
-              hi[k] = fp4::as_u32(h);
-              if constexpr (X2)
-                lo[k] = fp4::as_u32(__floats2half2_rn(x0 - __low2float(h), x1 - __high2float(h)));
-            }
-            uint8_t* dst = at(r, c);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (X2)
-              *reinterpret_cast<uint4*>(dst + NT * C::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
+        constexpr auto lay = D == 128 && NT == 2 ? lay_down_apart<T, D, NT> : lay_down<T, D, NT>;
+        const float2 x = lay(sQ + t * C::TILE, warp & 3, q, a.q, mul);
+        f = f * x.x * x.y;
         fence_proxy_async_shared();
       }
       __syncwarp();
