@@ -97,7 +97,8 @@ __device__ __forceinline__ Raw<T> narrow8(const float (&v)[8]) {
 // (x, y) turned by (c, s).  kExact: the two sums of products rounded once from
 // about 48 bits (the products' and the sum's rounding errors are computed with
 // fma and added up: Dekker 1971, Knuth's two-sum), so that a 4-bit code next to
-// a border does not turn on the order of operations.
+// a border does not turn on the order of operations.  A sum that is not finite
+// has no such errors (inf - inf): it is what the plain form makes of it.
 template <bool kExact>
 __device__ __forceinline__ float dot2(float x, float c, float y, float s) {  // x c + y s
   if constexpr (!kExact) return fmaf(x, c, y * s);
@@ -106,7 +107,8 @@ __device__ __forceinline__ float dot2(float x, float c, float y, float s) {  // 
   const float t = __fadd_rn(p, q);
   const float b = __fsub_rn(t, p);
   const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(t, b)), __fsub_rn(q, b));
-  return __fadd_rn(t, __fadd_rn(e, __fadd_rn(pe, qe)));
+  const float r = __fadd_rn(t, __fadd_rn(e, __fadd_rn(pe, qe)));
+  return fabsf(t) < INFINITY ? r : __fmaf_rn(x, c, q);
 }
 template <bool kExact>
 __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
