@@ -10,6 +10,14 @@
 namespace gb300 {
 namespace paged {
 
+// fp32 calls multiply a softmax weight with its value as two fp16 parts.  The
+// second, what the first leaves, is this times larger than the first before it
+// is rounded: below 2^-14 the first part's steps stay 2^-24, and the second, at
+// the same scale, would be 0.  (The first is at most 2^15, so what it leaves at
+// most 2^3, and the second at most 2^15.)  The two hold a weight to 2^-22 of
+// itself, or to 2^-37 of the first part's unit where it is small.
+constexpr float kRestScale = 0x1p12f;
+
 // How codes reach shared memory: a tensor copy of 2^lg rows of one head at
 // coordinates {0, row, head, page}, or, where no 8 rows are sure to share a page
 // (lg < 0), 16-byte copies.  A dimension of stride 0 has an extent of 1 and its

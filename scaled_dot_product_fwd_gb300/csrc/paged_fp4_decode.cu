@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             p[0][kg][n][h] = transpose8(fp4::as_u32(hi));
             if constexpr (kSplit)
               p[1][kg][n][h] = transpose8(
-                  fp4::as_u32(__floats2half2_rn(p0 - __low2float(hi), p1 - __high2float(hi))));
+                  fp4::as_u32(__floats2half2_rn((p0 - __low2float(hi)) * kRestScale,
+                                                (p1 - __high2float(hi)) * kRestScale)));
           }
 #pragma unroll
       for (int kg = 0; kg < 2; ++kg) {
@@ -552,13 +553,22 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           widen4((w[2][i] & L) | ((w[3][i] << 4) & H), s1, e1_);
           widen4(((w[2][i] >> 4) & L) | (w[3][i] & H), s1, o1_);
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4; ++b) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
+              mma16816(o[n][4 * i + b], e0_[b], o0_[b], e1_[b], o1_[b], p[0][kg][n][0],
+                       p[0][kg][n][1]);
+            if constexpr (kSplit) {
+              // the weights' second part, times values scaled back (multiples of
+              // 2^-10 below 2^12: exact in fp16 at 2^-12 of them too)
+              const __half2 z = __float2half2_rn(1.f / kRestScale);
+              const uint32_t e0 = mul2(e0_[b], z), o0 = mul2(o0_[b], z), e1 = mul2(e1_[b], z),
+                             o1 = mul2(o1_[b], z);
 #pragma unroll
-              for (int y = 0; y < QN; ++y)
-                mma16816(o[n][4 * i + b], e0_[b], o0_[b], e1_[b], o1_[b], p[y][kg][n][0],
-                         p[y][kg][n][1]);
+              for (int n = 0; n < NT; ++n)
+                mma16816(o[n][4 * i + b], e0, o0, e1, o1, p[1][kg][n][0], p[1][kg][n][1]);
+            }
+          }
         }
       }
     }

@@ -21,7 +21,8 @@
 //    A row's score factor is scale * gain / that power; its sign goes into the
 //    row, so that the largest raw score is the largest score.
 //  - Weights are 2^kHead at the reference maximum, so that fp16 holds them to
-//    2^-11 relative down to 2^-18 of the largest.
+//    2^-11 relative down to 2^-18 of the largest, and to 2^-29 of it below that;
+//    the two parts of fp32 calls (kRestScale) to 2^-22, and to 2^-41.
 // Two query tiles a unit (NT = 2) share each widened tile.  The writes of the
 // widened tiles (64 KB a key tile) come on top of the products' reads of shared
 // memory (192 KB), at 128 bytes a clock 2300 of the 3200 that a key tile takes.
@@ -99,7 +100,12 @@ struct F4Cfg {
 constexpr int kUnitSteps = 6;    // fixed cost of a unit in key tiles
 constexpr uint32_t kPBar = 1;    // + t: softmax warps of tile t with the MMA warp
 constexpr uint32_t kKBar = 3;    // stage helper with the MMA warp
-constexpr float kHead = 4.f;
+// A row's weights are 2^kHead at its reference maximum (fp32 calls: kRestScale
+// times that, see weights()), and their sum over a key tile at most kMostSum.
+template <bool X2>
+constexpr float kHead = X2 ? 16.f : 4.f;
+template <bool X2>
+constexpr float kMostSum = X2 ? kFusedSumLimit * kRestScale : kFusedSumLimit;
 
 // What a role needs of a unit.
 struct TileGeo {
@@ -148,8 +154,18 @@ struct Order {
   }
 };
 
-// 2^(s f - m) of N raw scores as fp16 pairs (X2: and what fp16 leaves of
-// them), added to rs.
+// p - kRestScale h: exact where h is p / kRestScale rounded.
+__device__ __forceinline__ float rest_of(float p, __half h) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "h"(__half_as_ushort(h)), "h"(__half_as_ushort(__float2half_rn(-kRestScale))), "f"(p));
+  return r;
+}
+// p = 2^(s f - m) of N raw scores, added to rs, as fp16 pairs.  X2: p / kRestScale
+// as fp16 pairs, and what they leave of p.  (With a multiplication of the rest
+// instead, 4 x 300 fp32 tokens over 3000 keys take 60.2 us, head_dim 64 and 8
+// heads, and 187, head_dim 128 and 32 over 8; so 56.4 and 179.)
 template <bool X2, int N>
 __device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m, uint32_t* pk,
                                         uint32_t* lo, float& rs) {
@@ -163,10 +179,14 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m
     f2_unpack(X, x0, x1);
     const float p0 = ex2(x0), p1 = ex2(x1);
     acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
-    const __half2 h = __floats2half2_rn(p0, p1);
-    pk[i] = fp4::as_u32(h);
-    if constexpr (X2)
-      lo[i] = fp4::as_u32(__floats2half2_rn(p0 - __low2float(h), p1 - __high2float(h)));
+    if constexpr (X2) {
+      const __half2 h = __floats2half2_rn(p0 * (1.f / kRestScale), p1 * (1.f / kRestScale));
+      pk[i] = fp4::as_u32(h);
+      lo[i] = fp4::as_u32(
+          __floats2half2_rn(rest_of(p0, __low2half(h)), rest_of(p1, __high2half(h))));
+    } else {
+      pk[i] = fp4::as_u32(__floats2half2_rn(p0, p1));
+    }
   }
   float t0, t1;
   f2_unpack(f2_add(acc[0], acc[1]), t0, t1);
@@ -489,7 +509,8 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       };
       // O_t += P V, P in slot i, V in ring slot s, keys in groups of 16.  X2: the
       // weights' second part lies 64 columns on and has an O of its own (in the
-      // place of tile 1's), so that half as many sums are rounded at O's size.
+      // place of tile 1's): the first part is kRestScale smaller, and half as many
+      // sums are rounded at O's size.
       auto issue_pv = [&](int t, int i, int s, bool first, int groups) {
         const uint32_t vd = v_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
@@ -819,7 +840,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                 weights<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
                             rs);
               }
-              resc = resc || !(rs <= kFusedSumLimit);
+              resc = resc || !(rs <= kMostSum<X2>);
             }
             if (__any_sync(0xffffffffu, resc)) {
               float mx = -INFINITY;
@@ -828,7 +849,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                 scores(c);
                 mx = fmaxf(mx, row_max_raw(s));
               }
-              mx = mx * f - kHead;  // -inf: no visible key
+              mx = mx * f - kHead<X2>;  // -inf: no visible key
               if (resc && mx > -INFINITY) {
                 alpha = ex2(m - mx);  // 0 when m = -inf
                 m = mx;
@@ -906,7 +927,8 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
           tmem_ld32_sync(tO + D + c * 32, y);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+            x[i] = __float_as_uint(
+                fmaf(__uint_as_float(x[i]), kRestScale, __uint_as_float(y[i])));
         }
       };
       tc_fence_after();
