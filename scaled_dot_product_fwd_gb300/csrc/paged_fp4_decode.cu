@@ -620,10 +620,8 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         r.z = fmaf(v.z, z, r.z);
         r.w = fmaf(v.w, z, r.w);
       }
-      const float v_gain = a.v_gain ? a.v_gain[head] : 1.f;
-      if (!whole) {
-        put4(slot + row * D + col,
-             make_float4(r.x * v_gain, r.y * v_gain, r.z * v_gain, r.w * v_gain));
+      if (!whole) {  // (without the gain, which may be large)
+        put4(slot + row * D + col, r);
         if (col == 0) {
           slot[rows * D + row] = M;
           slot[rows * (D + 1) + row] = L;
@@ -634,9 +632,10 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       const int hq = head * a.G + e0 + a.by_gu.mod(c);
       float z = L != 0.f ? 1.f : 0.f;
       if (a.sinks) z *= add_sink(a.sinks[hq], M, L);
-      z = L != 0.f ? z / L * v_gain : 0.f;
+      z = L != 0.f ? z / L : 0.f;
+      const float gain = a.v_gain ? a.v_gain[head] : 1.f;
       put4(static_cast<T*>(a.o) + tok * a.os[0] + hq * a.os[1] + col,
-           make_float4(r.x * z, r.y * z, r.z * z, r.w * z));
+           make_float4(r.x * z * gain, r.y * z * gain, r.z * z * gain, r.w * z * gain));
       if (a.lse && col == 0)
         a.lse[tok * a.Hq + hq] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
@@ -790,12 +789,15 @@ __global__ void __launch_bounds__(kT) paged_fp4_merge_kernel(const Args a, const
       float f = 1.f;
       if (a.sinks) f = add_sink(a.sinks[hq], M, L);
       const float inv = any ? f / L : 0.f;
+      const float gain = a.v_gain ? a.v_gain[head] : 1.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] *= inv;
       const long long q = d[4] + tok;
       T* o = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1] + lane * E;
       if constexpr (E == 4) {
-        put4(o, make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
+        put4(o, make_float4(acc[0] * gain, acc[1] * gain, acc[2] * gain, acc[3] * gain));
       } else {
-        put2(o, make_float2(acc[0] * inv, acc[1] * inv));
+        put2(o, make_float2(acc[0] * gain, acc[1] * gain));
       }
       if (a.lse && lane == 0) a.lse[q * a.Hq + hq] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }

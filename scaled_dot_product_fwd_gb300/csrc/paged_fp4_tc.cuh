@@ -919,7 +919,6 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       const int kvh = a.by_nsub.div(unit->h), sub = a.by_nsub.mod(unit->h);
       const int e = sub * a.gu + a.by_gu.mod(r);
       const bool row_ok = r < a.w * a.gu && tok < nq && e < a.G;
-      const float gain = a.v_gain ? a.v_gain[kvh] : 1.f;
       auto load_o = [&](int c, uint32_t (&x)[32]) {  // columns c * 32 .. + 31
         tmem_ld32_sync(tO + c * 32, x);
         if constexpr (X2) {
@@ -934,7 +933,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       tc_fence_after();
       __syncwarp();
       if (!whole) {
-        // unnormalised O (relative to 2^m), m and l
+        // unnormalised O (relative to 2^m, without the gain), m and l
         float* slot = a.ws + static_cast<size_t>(blockIdx.x * 2 + unit->slot()) * C::SLOT;
         float* orow = slot + (t * 128 + r) * D;
 #pragma unroll 1
@@ -942,9 +941,6 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
           uint32_t ob[32];
           load_o(c, ob);
           if (row_ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              ob[i] = __float_as_uint(__uint_as_float(ob[i]) * gain);
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store32(orow + c * 32 + i, ob + i);
           }
@@ -958,7 +954,10 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
         float z = 1.f;
         const float own = l;
         if (a.sinks && row_ok) z = add_sink(a.sinks[hq], m, l);
-        const float inv = own != 0.f ? z / l * gain : 0.f;
+        // (apart from the gain: a sum of weights times its inverse, or over it,
+        // would be past fp32's range where O is not)
+        const float inv = own != 0.f ? z / l : 0.f;
+        const float gain = a.v_gain ? a.v_gain[kvh] : 1.f;
         const long long q = unit->s.q0 + tok;
         T* orow = static_cast<T*>(a.o) + q * a.os[0] + hq * a.os[1];
 #pragma unroll 1
@@ -968,7 +967,8 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
           // (a row that saw no key: O may never have been written)
           float x[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = own != 0.f ? __uint_as_float(ob[i]) * inv : 0.f;
+          for (int i = 0; i < 32; ++i)
+            x[i] = own != 0.f ? __uint_as_float(ob[i]) * inv * gain : 0.f;
           if (row_ok) {
             if constexpr (X2) {
 #pragma unroll

@@ -409,10 +409,11 @@ __global__ void __launch_bounds__(256, 4)
     float f = 1.f;
     if (a.sinks) f = add_sink(a.sinks[hq], M, L);
     const float inv = any ? f / L : 0.f;
+    const float gain = a.v_gain ? a.v_gain[kvh] : 1.f;  // (of a 4-bit cache)
     T* orow = static_cast<T*>(a.o) + static_cast<long long>(q0 + tok) * a.os[0] + hq * a.os[1];
     T x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = narrow<T>(acc[i] * inv);
+    for (int i = 0; i < E; ++i) x[i] = narrow<T>(acc[i] * inv * gain);
     if constexpr (E * sizeof(T) == 16)
       *reinterpret_cast<uint4*>(orow + lane * E) = *reinterpret_cast<uint4*>(x);
     else if constexpr (E * sizeof(T) == 8)
