@@ -944,9 +944,9 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origina
     if scaling != "yarn":
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     if original_length is None or original_length < 1 or not beta_fast > beta_slow > 0.0 \
-            or base == 1.0:
+            or base <= 1.0:
         raise ValueError("scaling='yarn' needs original_length >= 1, beta_fast > beta_slow > 0 "
-                         "and a base other than 1")
+                         "and a base above 1")
 
     def pair_of(turns):  # the (fractional) pair that turns so often in original_length
         return R * math.log(original_length / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
