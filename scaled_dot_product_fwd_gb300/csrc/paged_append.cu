@@ -34,7 +34,6 @@ constexpr int kWarps = 8;
 struct AppendArgs {
   Args a;
   Rotation rot;
-  int lg_u;    // log2 of the pieces of a row
   int times;   // groups of 32 * 16 / D rows that a warp takes
   int rows;    // rows of a token: q heads, k heads, v heads
   const char* k;

@@ -4,8 +4,8 @@
 //
 // Rotation: bound by HBM (q and k in and out).  A thread takes a 16-element
 // piece of a row (rotate.cuh), holds its 8 cosines and sines in registers and
-// walks over heads with them, so that the table costs 4 bytes a pair and
-// kHeads heads rather than 8 bytes a pair of elements.  A warp's D / 16 lanes a
+// walks over `per` heads with them (RopeArgs, chosen at the launch), so that a
+// pair's 8 bytes of the table are read once for `per` heads.  A warp's D / 16 lanes a
 // row leave it 32 * 16 / D rows at a time: consecutive tokens where a head's
 // tokens lie next to one another, consecutive heads where a token's heads do,
 // so that a warp's accesses are runs of 1 KB in either order.
