@@ -692,6 +692,11 @@ SDPA_API sdpa_status_t sdpa_paged_append_fp4(const sdpa_paged_params_t* params,
  * sdpa_paged_forward_fp4 — sdpa_paged_forward over a 4-bit cache.  q, o and
  * lse as there, in params->dtype; workspace of sdpa_paged_workspace_size bytes.
  * A scale byte of NaN below a sequence's length gives NaN.
+ * Rounding: scores, sums and lse are fp32.  bf16 queries lose what is below 2^-39
+ * of their row's largest element; fp32 ones are held to 2^-22 of an element, or
+ * 2^-39 of that.  A softmax weight meets its value as an fp16 number (2^-11 of it,
+ * or 2^-29 of the row's largest weight, whichever is more), in fp32 calls as two
+ * (2^-22, or 2^-41).  o is rounded once.
  */
 SDPA_API sdpa_status_t sdpa_paged_forward_fp4(const sdpa_paged_params_t* params,
                                               const sdpa_fp4_cache_t* cache, const void* q,

@@ -8,11 +8,14 @@
 // (rotate.cuh), so the lookups are made once a warp, beside the rows' loads.
 //
 // Four chunks of up to 2048 tokens, 32 heads over 8, head_dim 128, fp16: 26 us
-// (131 MB, 5.0 TB/s; the kernel alone 24), into the 4-bit cache 35 us (139 MB with
+// (131 MB, 5.0 TB/s; the kernel alone 24), into the 4-bit cache 36 us (139 MB with
 // the values read back, 3.9 TB/s), where the exact rotation of k and the quotients
 // count too: true divisions 62, corrected products 47, three CTAs an SM 40, queries
-// without the exact sums 38, overlapped launches 35.  64 single tokens: 10 and 14
-// us a call, the host's.
+// without the exact sums 38, overlapped launches 35 (35.8 with sums that are not
+// finite kept apart).  There the issue slots are 70 % busy and no pipe above 51 %;
+// the 20 resident warps an SM wait for their turn (1.9 for each instruction issued),
+// the sums' and quotients' fixed latencies (1.4) and memory (0.9).  64 single tokens:
+// 10 and 14 us a call, the host's.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -20,24 +20,30 @@
 // Products of codes and scales are exact in fp16 (fp4.cuh).  fp16 queries enter
 // as they are; bf16 ones times a power of two a row that brings the row's
 // largest to 2^14 (what fp16 then drops is below 2^-39 of it); fp32 ones as a
-// sum of two fp16 parts, likewise scaled (22 bits), and so do their weights.
+// sum of two fp16 parts, likewise scaled (2^-22 of an element, or 2^-39 of the
+// row's largest), and so do their weights.
 // Weights are 2^(x - m + 7) against a reference maximum m that moves only when a
-// score passes it by 8 (fp16 then holds them to 2^-11 relative down to 2^-21 of
-// the largest).  The gains enter with the score factor and the output.
+// score passes it by 8.  fp16 then holds them to 2^-11 relative down to 2^-21 of
+// the largest, and to 2^-32 of it below; two parts (kRestScale) to 2^-22 relative,
+// or 2^-44.  (A second part for 16-bit calls too would be half as many
+// mma.sync again, for an O that is then rounded to 16 bits.)
+// The gains enter with the score factor and, last, with the output.
 //
 // A CTA of 8 warps walks its share of the line of 256-key tiles (paged.cuh); a
 // warp has 32 keys of a tile and a ring of its own in shared memory, filled by
 // asynchronous copies one step ahead (head_dim 128; 64: three, in as many
 // bytes), so nothing but the end of a unit meets a CTA barrier.
 //
-// 8 sequences of 32768 keys, 32 heads over 8, head_dim 128, bf16: 77 us a call,
-// 3.9 TB/s, of which this kernel 72.  Bound by instruction issue: 380 a warp
-// for 16 keys (110 scores, 124 values, 29 softmax, the rest copies and lookups),
-// 2.5 a clock and SM; the ALU pipe, which converts the codes, 55 % busy, DRAM 62 %
-// of the copy rate.  What brought it there (us): cp.async by each lane 115, by
-// rows of neighbouring heads 102, tensor copies 90, copies issued without a loop
-// over lanes and a merge over the whole grid 81, overlapped launches 77.  A ring
-// of three stages instead of two, three CTAs an SM (80 registers, spills) and
+// 8 sequences of 32768 keys, 32 heads over 8, head_dim 128, bf16: 75.5 us a call,
+// 4.0 TB/s, of which this kernel 71.5.  No unit is full: issue 62 % of the slots
+// (380 instructions a warp for 16 keys: 110 scores, 124 values, 29 softmax, the
+// rest copies and lookups), the ALU pipe, which converts the codes, 56 %, DRAM
+// 62 % of the copy rate; of 14.7 resident warps an SM most wait for their turn
+// (1.2 for each instruction issued), fixed latencies (1.1) or the conversions'
+// pipe (0.9), memory least (0.3).  What brought it there (us): cp.async by each
+// lane 115, by rows of neighbouring heads 102, tensor copies 90, copies issued
+// without a loop over lanes and a merge over the whole grid 81, overlapped launches
+// 77.  A ring of three stages instead of two, three CTAs an SM (80 registers, spills) and
 // the next unit's copies beside the last one's end gave nothing or cost time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -850,7 +856,11 @@ int paged_fp4_decode_rows(const paged::Args& a, int dtype) {
   // rows.  32 heads over 8, head_dim 128, bf16: 8 rows a sequence and kv head 35,
   // 42, 56; 16 rows 52, 46, 56; 24 rows 71, 71, 56.  16 heads over 4, head_dim 64,
   // fp32, whose many-row kernel does twice the work: 8 rows 21, 27, 46; 16 rows
-  // 29, 28, 46; 32 rows 45, 38, 47.
+  // 29, 28, 46; 32 rows 45, 38, 47 (before fp32 weights kept their small parts;
+  // since then, on other inputs, 4, 16 and 32 rows 21, 29 and 42, 36 rows, by the
+  // other kernel, 47).  A step of single tokens and a long chunk goes by the average
+  // and loses by it: 128 tokens over 512 keys and a chunk of 384 over 32768, 32 heads
+  // over 8, bf16, 1434, in two calls 40 and 172.
   const long long rows = paged::call_rows(a);
   const int most = dtype == SDPA_F32 ? 32 : 16;
   return a.G > 16 ? 0 : a.G <= 8 && rows <= 8 ? 8 : rows <= most ? 16 : 0;

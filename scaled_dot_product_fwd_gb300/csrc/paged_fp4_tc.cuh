@@ -16,30 +16,38 @@
 //    by asynchronous copies, then each lane its own row in place): fp16 rows as
 //    they are, bf16 ones times a power of two a row that brings the row's
 //    largest to [2^14, 2^15) (what fp16 then drops is below 2^-39 of it); fp32
-//    ones likewise as a sum of two fp16 parts (22 bits), each multiplied with K,
-//    and so do their weights with V (NT = 1).
+//    ones likewise as a sum of two fp16 parts (2^-22 of an element, or 2^-39 of
+//    the row's largest), each multiplied with K, and so do their weights with V
+//    (NT = 1).
 //    A row's score factor is scale * gain / that power; its sign goes into the
 //    row, so that the largest raw score is the largest score.
 //  - Weights are 2^kHead at the reference maximum, so that fp16 holds them to
 //    2^-11 relative down to 2^-18 of the largest, and to 2^-29 of it below that;
 //    the two parts of fp32 calls (kRestScale) to 2^-22, and to 2^-41.
-// Two query tiles a unit (NT = 2) share each widened tile.  The writes of the
-// widened tiles (64 KB a key tile) come on top of the products' reads of shared
-// memory (192 KB), at 128 bytes a clock 2300 of the 3200 that a key tile takes.
+// Two query tiles a unit (NT = 2) share each widened tile.
+//
+// What bounds it: no unit is full (2048 tokens over 16384 keys, head_dim 128 /
+// 64: tensor pipe 58 / 33 % active, issue 50 / 49 %, XU 29 / 33 %, ALU 34 / 31 %,
+// shared-memory wavefronts 27 / 17 %).  In a build with clock stamps, which takes
+// 1.5 and 1.1 times as long, the issuing warp waits for widened tiles (700 of 5000
+// clocks a key tile, 910 of 2900) and never for weights (14, 16), and the widening
+// warps are busy all the time, with their rows' pages and scales for a third of
+// it: the chain of a widened tile sets the pace.
 //
 // 4096 tokens over 32768 keys, 32 heads over 8, head_dim 128, bf16: 1450 us, 1420
-// TFLOP/s (the 16-bit cache's kernel 1190 to 1374 us); tensor pipe 56 % active on
-// 2048 tokens over 16384 keys.  Four ragged chunks of up to 700 tokens over 5000
-// keys: 150 us, 737 TFLOP/s.  The steps (us, the first case): copies and widening
+// TFLOP/s (the 16-bit cache's kernel 1190 to 1374 us).  Four ragged chunks of up to
+// 700 tokens over 5000 keys: 150 us, 737 TFLOP/s.  Head_dim 64, 2048 tokens over
+// 16384 keys: bf16 344 us (750 TFLOP/s), fp16 307 (840).  fp32, 4 x 300 tokens over
+// 3000 keys: 181 us, and 57 for 8 heads of head_dim 64.  The steps (us, the first case): copies and widening
 // by the same four warps 1975; a loader warp, scales read by the widening lanes,
 // all scores in one load, and the registers split anew 1505; queries by the
 // softmax warps, a row a lane in 16-byte loads, 1465; queries by asynchronous
 // copies of whole rows 1530, but the chunks 156 -> 151, 300 tokens over themselves
 // 28 -> 24, 8 x 16 tokens over 4096 keys 45 -> 37 and head_dim 64 (4 x 700 over
 // 5000) 222 -> 200; these in a function of their own 1450.  The split of the
-// registers counts (spills of the softmax or of the issuing warps): 184 / 72 / 72 a
-// thread 1470, 176 / 80 / 80 1471, 176 / 88 / 72 1500, 192 / 64 / 64 1725, 168 / 88 / 88
-// 1750.
+// registers counts (spills of the softmax or of the issuing warps; a thread of the
+// softmax, control and widening warps): 184 / 80 / 64 (kept) 1452, 176 / 80 / 80 1449,
+// 184 / 72 / 72 1473, 176 / 88 / 72 1519 to 1529; the four chunks 149, 148, 148, 152.
 #pragma once
 
 #include <atomic>
@@ -294,7 +302,8 @@ __device__ __forceinline__ float2 lay_down(uint8_t* tile, int quarter, const T* 
 // Two tiles of head_dim 128 have it in a function of its own: the compiler's
 // schedule of the softmax turns on what else that role's loop holds.  Apart and
 // inside: 4096 tokens over 32768 keys 1450 and 1530 us; head_dim 64, 2048 tokens
-// over 16384 keys 402 and 316; one tile, 8 x 16 tokens over 4096 keys 41 and 38.
+// over 16384 keys, bf16 395 and 344, fp16 404 and 307; one tile, 8 x 16 tokens over
+// 4096 keys 41 and 38.
 template <typename T, int D, int NT>
 __device__ __noinline__ float2 lay_down_apart(uint8_t* tile, int quarter, const T* q,
                                               const void* any, float mul) {
