@@ -109,7 +109,11 @@ constexpr int kUnitSteps = 6;    // fixed cost of a unit in key tiles
 constexpr uint32_t kPBar = 1;    // + t: softmax warps of tile t with the MMA warp
 constexpr uint32_t kKBar = 3;    // stage helper with the MMA warp
 // A row's weights are 2^kHead at its reference maximum (fp32 calls: kRestScale
-// times that, see weights()), and their sum over a key tile at most kMostSum.
+// times that, see weights()), and their sum over a key tile at most kMostSum, past
+// which the reference moves.  With 2^7 small weights were held to 2^-32 of the
+// largest, but scores that grow along the keys would move it more often: 2 x 1024
+// tokens over 8192 such keys, 16 heads over 4, head_dim 128, 178 us and 203; where
+// they do not grow, or grow at once, both take the same.
 template <bool X2>
 constexpr float kHead = X2 ? 16.f : 4.f;
 template <bool X2>
