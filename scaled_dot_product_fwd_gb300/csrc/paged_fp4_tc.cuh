@@ -38,7 +38,7 @@
 // TFLOP/s (the 16-bit cache's kernel 1190 to 1374 us).  Four ragged chunks of up to
 // 700 tokens over 5000 keys: 150 us, 737 TFLOP/s.  Head_dim 64, 2048 tokens over
 // 16384 keys: bf16 344 us (750 TFLOP/s), fp16 307 (840).  fp32, 4 x 300 tokens over
-// 3000 keys: 181 us, and 57 for 8 heads of head_dim 64.  The steps (us, the first case): copies and widening
+// 3000 keys: 180 us, and 54 for 8 heads of head_dim 64.  The steps (us, the first case): copies and widening
 // by the same four warps 1975; a loader warp, scales read by the widening lanes,
 // all scores in one load, and the registers split anew 1505; queries by the
 // softmax warps, a row a lane in 16-byte loads, 1465; queries by asynchronous
@@ -108,16 +108,13 @@ struct F4Cfg {
 constexpr int kUnitSteps = 6;    // fixed cost of a unit in key tiles
 constexpr uint32_t kPBar = 1;    // + t: softmax warps of tile t with the MMA warp
 constexpr uint32_t kKBar = 3;    // stage helper with the MMA warp
-// A row's weights are 2^kHead at its reference maximum (fp32 calls: kRestScale
-// times that, see weights()), and their sum over a key tile at most kMostSum, past
-// which the reference moves.  With 2^7 small weights were held to 2^-32 of the
-// largest, but scores that grow along the keys would move it more often: 2 x 1024
-// tokens over 8192 such keys, 16 heads over 4, head_dim 128, 178 us and 203; where
-// they do not grow, or grow at once, both take the same.
-template <bool X2>
-constexpr float kHead = X2 ? 16.f : 4.f;
-template <bool X2>
-constexpr float kMostSum = X2 ? kFusedSumLimit * kRestScale : kFusedSumLimit;
+// A row's weights are 2^kHead at its reference maximum, and their sum over a key
+// tile at most kFusedSumLimit, past which the reference moves.  With 2^7 small
+// weights were held to 2^-32 of the largest, but scores that grow along the keys
+// would move it more often: 2 x 1024 tokens over 8192 such keys, 16 heads over 4,
+// head_dim 128, 178 us and 203; where they do not grow, or grow at once, both take
+// the same.
+constexpr float kHead = 4.f;
 
 // What a role needs of a unit.
 struct TileGeo {
@@ -166,18 +163,21 @@ struct Order {
   }
 };
 
-// p - kRestScale h: exact where h is p / kRestScale rounded.
-__device__ __forceinline__ float rest_of(float p, __half h) {
+// What h, p rounded, leaves of p, times kRestScale (exact; given p times that).
+__device__ __forceinline__ float rest_of(float scaled, __half h) {
   float r;
   asm("fma.rn.f32.f16 %0, %1, %2, %3;"
       : "=f"(r)
-      : "h"(__half_as_ushort(h)), "h"(__half_as_ushort(__float2half_rn(-kRestScale))), "f"(p));
+      : "h"(__half_as_ushort(h)), "h"(__half_as_ushort(__float2half_rn(-kRestScale))),
+        "f"(scaled));
   return r;
 }
-// p = 2^(s f - m) of N raw scores, added to rs, as fp16 pairs.  X2: p / kRestScale
-// as fp16 pairs, and what they leave of p.  (With a multiplication of the rest
-// instead, 4 x 300 fp32 tokens over 3000 keys take 60.2 us, head_dim 64 and 8
-// heads, and 187, head_dim 128 and 32 over 8; so 56.4 and 179.)
+// p = 2^(s f - m) of N raw scores as fp16 pairs, added to rs.  X2: and what fp16
+// leaves of them, times kRestScale.  (4 x 300 fp32 tokens over 3000 keys, 8 heads of
+// 64 / 32 over 8 of 128: 54 and 180 us; with the first part widened to fp32 and
+// subtracted before the scaling 60 and 192; with p times kRestScale from the
+// exponential on 57 and 181, and exponents near 16, whose rounding raised O's error
+// from 5.5e-7 to 6.2e-7.)
 template <bool X2, int N>
 __device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m, uint32_t* pk,
                                         uint32_t* lo, float& rs) {
@@ -191,14 +191,11 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[N], float f, float m
     f2_unpack(X, x0, x1);
     const float p0 = ex2(x0), p1 = ex2(x1);
     acc[i & 1] = f2_add(acc[i & 1], f2_pack(p0, p1));
-    if constexpr (X2) {
-      const __half2 h = __floats2half2_rn(p0 * (1.f / kRestScale), p1 * (1.f / kRestScale));
-      pk[i] = fp4::as_u32(h);
-      lo[i] = fp4::as_u32(
-          __floats2half2_rn(rest_of(p0, __low2half(h)), rest_of(p1, __high2half(h))));
-    } else {
-      pk[i] = fp4::as_u32(__floats2half2_rn(p0, p1));
-    }
+    const __half2 h = __floats2half2_rn(p0, p1);
+    pk[i] = fp4::as_u32(h);
+    if constexpr (X2)
+      lo[i] = fp4::as_u32(__floats2half2_rn(rest_of(p0 * kRestScale, __low2half(h)),
+                                            rest_of(p1 * kRestScale, __high2half(h))));
   }
   float t0, t1;
   f2_unpack(f2_add(acc[0], acc[1]), t0, t1);
@@ -522,8 +519,8 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
       };
       // O_t += P V, P in slot i, V in ring slot s, keys in groups of 16.  X2: the
       // weights' second part lies 64 columns on and has an O of its own (in the
-      // place of tile 1's): the first part is kRestScale smaller, and half as many
-      // sums are rounded at O's size.
+      // place of tile 1's): it is kRestScale times larger, and half as many sums are
+      // rounded at O's size.
       auto issue_pv = [&](int t, int i, int s, bool first, int groups) {
         const uint32_t vd = v_lo + static_cast<uint32_t>((s * C::TILE) >> 4);
 #pragma unroll
@@ -853,7 +850,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                 weights<X2>(s, f, m == -INFINITY ? 0.f : m, pk + c * 32, lo + (X2 ? c * 32 : 0),
                             rs);
               }
-              resc = resc || !(rs <= kMostSum<X2>);
+              resc = resc || !(rs <= kFusedSumLimit);
             }
             if (__any_sync(0xffffffffu, resc)) {
               float mx = -INFINITY;
@@ -862,7 +859,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
                 scores(c);
                 mx = fmaxf(mx, row_max_raw(s));
               }
-              mx = mx * f - kHead<X2>;  // -inf: no visible key
+              mx = mx * f - kHead;  // -inf: no visible key
               if (resc && mx > -INFINITY) {
                 alpha = ex2(m - mx);  // 0 when m = -inf
                 m = mx;
@@ -940,7 +937,7 @@ __global__ void __launch_bounds__(F4Cfg<D, NT, sizeof(T) == 4>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             x[i] = __float_as_uint(
-                fmaf(__uint_as_float(x[i]), kRestScale, __uint_as_float(y[i])));
+                fmaf(__uint_as_float(y[i]), 1.f / kRestScale, __uint_as_float(x[i])));
         }
       };
       tc_fence_after();
