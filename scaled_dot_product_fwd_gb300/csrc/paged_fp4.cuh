@@ -1,5 +1,5 @@
-// paged_fp4.cuh — the codes of a 4-bit paged cache as the attention kernels'
-// tensor copies see them.
+// paged_fp4.cuh — what the attention kernels over the 4-bit paged cache share:
+// the second part of fp32 calls' weights, and the codes as tensor copies see them.
 #pragma once
 
 #include <algorithm>
@@ -17,6 +17,16 @@ namespace paged {
 // most 2^3, and the second at most 2^15.)  The two hold a weight to 2^-22 of
 // itself, or to 2^-37 of the first part's unit where it is small.
 constexpr float kRestScale = 0x1p12f;
+
+// What h, p rounded, leaves of p, times kRestScale (exact; given p times that).
+__device__ __forceinline__ float rest_of(float scaled, __half h) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "h"(__half_as_ushort(h)), "h"(__half_as_ushort(__float2half_rn(-kRestScale))),
+        "f"(scaled));
+  return r;
+}
 
 // How codes reach shared memory: a tensor copy of 2^lg rows of one head at
 // coordinates {0, row, head, page}, or, where no 8 rows are sure to share a page

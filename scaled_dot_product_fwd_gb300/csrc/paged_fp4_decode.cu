@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kT, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             p[0][kg][n][h] = transpose8(fp4::as_u32(hi));
             if constexpr (kSplit)
               p[1][kg][n][h] = transpose8(
-                  fp4::as_u32(__floats2half2_rn((p0 - __low2float(hi)) * kRestScale,
-                                                (p1 - __high2float(hi)) * kRestScale)));
+                  fp4::as_u32(__floats2half2_rn(rest_of(p0 * kRestScale, __low2half(hi)),
+                                                rest_of(p1 * kRestScale, __high2half(hi)))));
           }
 #pragma unroll
       for (int kg = 0; kg < 2; ++kg) {

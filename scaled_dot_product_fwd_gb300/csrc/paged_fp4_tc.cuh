@@ -163,15 +163,6 @@ struct Order {
   }
 };
 
-// What h, p rounded, leaves of p, times kRestScale (exact; given p times that).
-__device__ __forceinline__ float rest_of(float scaled, __half h) {
-  float r;
-  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
-      : "=f"(r)
-      : "h"(__half_as_ushort(h)), "h"(__half_as_ushort(__float2half_rn(-kRestScale))),
-        "f"(scaled));
-  return r;
-}
 // p = 2^(s f - m) of N raw scores as fp16 pairs, added to rs.  X2: and what fp16
 // leaves of them, times kRestScale.  (4 x 300 fp32 tokens over 3000 keys, 8 heads of
 // 64 / 32 over 8 of 128: 54 and 180 us; with the first part widened to fp32 and
